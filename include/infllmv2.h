@@ -25,6 +25,11 @@
  * and infllmv2_sparse_attn_backward (gradients of stage 3 with the selection
  * fixed [InfLLM v2 > Training-time considerations]).
  *
+ * Beside the contiguous caches above, a cache of pages for serving many
+ * sequences from one pool, attended densely: infllmv2_paged_append_kv,
+ * infllmv2_paged_attn_decode and infllmv2_paged_evict (see there; they have
+ * shapes and types of their own).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every tensor argument is a DEVICE pointer owned by the caller (the few
@@ -85,6 +90,7 @@ extern "C" {
 #define INFLLMV2_DEVICE_BAD_KV_LEN   0x1u  /* kv_lens[b] < n_q or > max_kv_len */
 #define INFLLMV2_DEVICE_TIMEOUT      0x2u  /* a bounded mbarrier wait expired */
 #define INFLLMV2_DEVICE_BOUNDS       0x4u  /* checked build only: a caller-given index out of range */
+#define INFLLMV2_DEVICE_BAD_PAGE     0x8u  /* a page-table entry in use is outside [0, num_pages) */
 
 /* Workspace kinds for infllmv2_workspace_size. */
 #define INFLLMV2_OP_SELECT  1
@@ -92,6 +98,9 @@ extern "C" {
 #define INFLLMV2_OP_PREFILL 3
 #define INFLLMV2_OP_DECODE_STEP 4
 #define INFLLMV2_OP_BACKWARD 5
+/* For infllmv2_paged_workspace_size. */
+#define INFLLMV2_OP_PAGED_DECODE 6
+#define INFLLMV2_OP_PAGED_EVICT  7
 
 typedef struct infllmv2_params {
   int32_t batch;                 /* B */
@@ -336,6 +345,124 @@ int infllmv2_sparse_attn_backward(const infllmv2_params* p, const void* q, int32
                                   const int32_t* n_selected, const void* out, const float* lse, const void* dout,
                                   float* dq, float* dk, float* dv, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/*
+ * ---------------------------------------------------------------- pages ----
+ *
+ * A paged cache: one pool of pages of `page_size` token slots, shared by all
+ * sequences.  Slot s of sequence b is row s % page_size of page
+ * page_table[b][s / page_size]; page_table is int32 [batch, max_pages], and
+ * only the entries that cover slots [0, kv_lens[b]) are read.  kv_lens is
+ * int32 [batch], each in [0, max_pages * page_size]; a length outside sets
+ * INFLLMV2_DEVICE_BAD_KV_LEN and counts as 0.  An entry in use outside
+ * [0, num_pages) sets INFLLMV2_DEVICE_BAD_PAGE, and its page is not touched.
+ *
+ * k_pages and v_pages hold the row of (page, kv head, slot) at
+ * page * strides[0] + head * strides[1] + slot * strides[2], in elements, the
+ * head_dim values of a row consecutive: head-major and token-major storage
+ * and a buffer that holds keys and values side by side are all described so.
+ * weights and positions (both may be NULL) are contiguous [num_pages,
+ * n_kv_heads, page_size]: per slot the attention weight it has received so
+ * far, and the token's position in its sequence.  Eviction makes them
+ * differ: a sequence that has seen seq_lens[b] tokens may hold kv_lens[b] of
+ * them.  seq_lens (int32 [batch]) may be NULL: nothing was ever evicted.
+ *
+ * Supported: bf16 and fp16, head_dim 64 and 128, page_size a multiple of 16,
+ * up to 4096 sequences and 2^30 slots each, strides that are multiples of 8
+ * elements, pointers 16-byte aligned.
+ *
+ * The conventions above hold: device pointers, work enqueued on `stream`,
+ * no allocation, no synchronisation, bounded waits.  A workspace is written
+ * before it is read in every call: calls that may overlap on the GPU, graphs
+ * captured with it among them, need workspaces of their own; one stream's
+ * calls can share one.
+ */
+#define INFLLMV2_BF16 0
+#define INFLLMV2_FP16 1
+
+typedef struct infllmv2_paged_cache {
+  int32_t dtype;         /* INFLLMV2_BF16 or INFLLMV2_FP16: the pages, q, out and new rows */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;     /* token slots of a page */
+  int32_t num_pages;     /* pages of the pool */
+  int32_t reserved;      /* 0 */
+  int64_t k_strides[3];  /* elements between pages, KV heads and slots of k_pages */
+  int64_t v_strides[3];
+  void* k_pages;
+  void* v_pages;
+  float* weights;
+  int32_t* positions;
+} infllmv2_paged_cache;
+
+/* Bytes of workspace of `op` (INFLLMV2_OP_PAGED_DECODE, with group_size query
+ * heads per KV head; INFLLMV2_OP_PAGED_EVICT, which ignores group_size).  A
+ * cache with weights needs room for every score of a decode: batch *
+ * n_kv_heads * group_size * max_pages * page_size floats.  0 on invalid
+ * arguments. */
+size_t infllmv2_paged_workspace_size(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages,
+                                     int32_t group_size, int32_t op);
+
+/*
+ * Write new tokens into the pages: token t < n_new[b] of sequence b goes to
+ * slot kv_lens[b] - n_new[b] + t (kv_lens already counts the new tokens); its
+ * weight becomes 0 and its position seq_lens[b] - n_new[b] + t (seq_lens
+ * counts them too; NULL: kv_lens).
+ *   k_new, v_new  [batch, n_kv_heads, n_q, head_dim]; new_strides (host
+ *           memory, NULL for contiguous): the elements between sequences,
+ *           heads and tokens of k_new, then of v_new.  Read with ordinary
+ *           loads: they may be page-locked host memory mapped for the device.
+ *   n_new   int32 [batch], each in [0, n_q], or NULL: n_q for all.
+ * A sequence with n_new[b] outside [0, n_q] or kv_lens[b] outside
+ * [n_new[b], max_pages * page_size] is left untouched and sets
+ * INFLLMV2_DEVICE_BAD_KV_LEN; a token whose page is bad is not written.  The
+ * slots written must be pairwise different.
+ */
+int infllmv2_paged_append_kv(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages, int32_t n_q,
+                             const void* k_new, const void* v_new, const int64_t* new_strides,
+                             const int32_t* page_table, const int32_t* kv_lens, const int32_t* n_new,
+                             const int32_t* seq_lens, void* stream);
+
+/*
+ * Attention of one new token per sequence over all its slots:
+ *     z[h, s] = attn_scale q_h . k_s,  P = softmax_s(z),  out_h = sum_s P v_s,
+ *     lse_h = ln sum_s exp(z[h, s]).
+ *   q, out  [batch, 1, n_kv_heads * group_size, head_dim] in the cache's type
+ *           (heads h*G .. h*G+G-1 share KV head h); group_size in [1, 32].
+ *   lse     fp32 [batch, 1, n_kv_heads * group_size], may be NULL.
+ *   accumulate = 1: weights[slot] += sum of P over the group's heads, for
+ *           every slot attended (needs the cache's weights).  Sequences may
+ *           share pages (a common prefix); the weights of a shared slot are
+ *           then summed in an order that depends on scheduling.
+ * A sequence with kv_lens[b] = 0 gets out = 0 and lse = -inf.  Slots of bad
+ * pages, and whatever rows past kv_lens[b] hold, take no part.
+ * Workspace: infllmv2_paged_workspace_size(.., INFLLMV2_OP_PAGED_DECODE).
+ */
+int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages,
+                               int32_t group_size, const void* q, const int32_t* page_table, const int32_t* kv_lens,
+                               float attn_scale, int32_t accumulate, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Evict from every (sequence, KV head) that holds more than `budget` slots
+ * all but `budget`: kept are first the slots whose position is < n_init or
+ * >= seq_lens[b] - n_local, then those with the largest weights (equal
+ * weights: the lowest slots; a NaN weight counts as less than any number).
+ * n_init + n_local <= budget.  In place: kept slots at or past `budget` move,
+ * in ascending order, into the evicted slots below it, with their weights and
+ * positions, so a cache's slots are no longer in order of position; slots at
+ * or past `budget` are left as they were, and the pages past
+ * ceil(budget / page_size) are free.  Each KV head keeps slots of its own.
+ *   new_lens  int32 [batch]: min(kv_lens[b], budget); may be kv_lens itself.
+ * A sequence with a bad page among its slots is left as it is (new_lens =
+ * kv_lens[b]).  The pages in use must be pairwise different: a page that
+ * sequences share must not be evicted from.  max_pages * page_size <= 524288.
+ * Workspace: infllmv2_paged_workspace_size(.., INFLLMV2_OP_PAGED_EVICT).
+ */
+int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages,
+                         const int32_t* page_table, const int32_t* kv_lens, int32_t budget, int32_t n_init,
+                         int32_t n_local, const int32_t* seq_lens, int32_t* new_lens, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /*
  * The checked build.  The library can also be built with INFLLMV2_CHECKED

@@ -1,0 +1,474 @@
+"""The paged cache's operators against plain 64-bit forms (GPU).
+
+tests/paged_helpers.py derives the tolerances.  Unused pages, unused rows and
+unused table entries hold NaN or impossible page numbers in every test.
+"""
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import __graft_entry__
+    import torch
+    __graft_entry__.build()
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+@pytest.fixture(autouse=True)
+def _clean_status(dev):
+    import trainable_block_sparse_infllm_gb300 as T
+    T.get_device_status(clear=True)
+    yield
+
+
+def _status():
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    torch.cuda.synchronize()
+    return T.get_device_status(clear=True)
+
+
+def _attn(pool, group, accumulate=True, scale=None, want_lse=True, q=None, lens=None, stream=None, ws=None):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    batch = pool.table.shape[0]
+    q = pool.normal(batch, 1, pool.heads * group, pool.dim) if q is None else q
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full((batch, 1, pool.heads * group), float("nan"), device=pool.dev) if want_lse else None
+    ws = pool.workspace(T.OP_PAGED_DECODE, group) if ws is None else ws
+    T.paged_attn_decode(pool.cache, q, pool.table, pool.lens if lens is None else lens, out, lse, scale=scale,
+                        accumulate=accumulate, workspace=ws, stream=stream)
+    return q, out, lse
+
+
+EDGES = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 200, 0, 333]
+
+ATTN = [
+    # dtype, layout, heads, group, dim, page, lens
+    ("bf16", "hnd", 2, 16, 128, 64, EDGES),
+    ("bf16", "nhd", 3, 5, 128, 16, EDGES),
+    ("fp16", "pair", 1, 8, 128, 32, EDGES),
+    ("fp16", "hnd", 4, 1, 64, 48, EDGES),
+    ("bf16", "nhd", 2, 32, 128, 64, EDGES),
+    ("fp16", "nhd", 1, 17, 64, 128, EDGES),
+    ("bf16", "pair", 2, 9, 64, 256, EDGES),
+    ("bf16", "hnd", 1, 7, 128, 16, [1]),
+    ("bf16", "hnd", 1, 16, 128, 64, [0, 0, 0]),
+    ("bf16", "hnd", 2, 16, 128, 64, [40001]),            # every SM holds a piece of one unit
+    ("fp16", "nhd", 2, 4, 128, 16, [20000, 3, 9999]),
+    ("fp16", "hnd", 1, 32, 64, 80, [30011, 0, 1]),
+    ("bf16", "pair", 8, 2, 64, 32, [100 + 37 * i for i in range(60)]),   # units cut and whole, several per CTA
+]
+
+
+@pytest.mark.parametrize("dtype,layout,heads,group,dim,page,lens", ATTN)
+def test_attention(dev, dtype, layout, heads, group, dim, page, lens):
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, dtype, layout, heads, dim, page, lens, seed=len(lens) + group)
+    before = pool.weights.clone()
+    k, v = pool.k.clone(), pool.v.clone()
+    q, out, lse = _attn(pool, group)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, dim ** -0.5)
+    import torch
+    for now, then in ((pool.k, k), (pool.v, v)):   # the pages are only read
+        assert torch.equal(now.contiguous().view(torch.int16), then.contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [4, 12, 24])
+def test_attention_without_weights_or_lse(dev, dtype, group):
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, dtype, "hnd", 2, 128, 64, [70, 1000, 0, 5], seed=3, metadata=False)
+    q, out, _ = _attn(pool, group, accumulate=False, want_lse=False, scale=0.3)
+    assert _status() == 0
+    check_attend(pool, q, out, None, None, 0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_sharp_and_flat_softmax(dev, dtype):
+    """One token holds nearly all the attention and a tail of 50,000 the rest: the tail is not lost."""
+    import torch
+    from paged_helpers import Pool, check_attend
+    n = 50000
+    pool = Pool(dev, dtype, "hnd", 1, 128, 64, [n, n], seed=5)
+    q = torch.zeros((2, 1, 8, 128), dtype=pool.dtype, device=dev)
+    q[..., 0] = 8.0
+    at, row = pool.places(0, n)
+    pool.k[at, :, row] = 0.0
+    pool.k[at[100], 0, row[100], 0] = 24.0      # z = 17: the other tokens get e^-17 each
+    pool.v[at, :, row] = 1.0
+    pool.v[at[100], 0, row[100]] = 0.0          # out = the tail's share alone
+    at, row = pool.places(1, n)
+    pool.k[at, :, row] = 0.0                    # all equal
+    before = pool.weights.clone()
+    _, out, lse = _attn(pool, 8, q=q)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, 128 ** -0.5)
+    share = (n - 1) * math.exp(-8 * 24 / math.sqrt(128)) / (1 + (n - 1) * math.exp(-8 * 24 / math.sqrt(128)))
+    assert abs(out[0].double().mean().item() / share - 1) < 2.0 ** -7
+
+
+def test_large_scores(dev):
+    """Scores beyond what exp can take without its maximum: +-4000."""
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [500, 64, 1], seed=6)
+    q = pool.normal(3, 1, 32, 128) * 1000
+    before = pool.weights.clone()
+    _, out, lse = _attn(pool, 16, q=q)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, 128 ** -0.5)
+
+
+def test_nan_and_inf_stay_in_their_sequence(dev):
+    import torch
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, "bf16", "hnd", 1, 128, 16, [100, 100, 100], seed=7)
+    at, row = pool.places(1, 100)
+    pool.k[at[50], 0, row[50], 3] = float("nan")
+    before = pool.weights.clone()
+    q, out, lse = _attn(pool, 16)
+    assert _status() == 0
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    ok = [0, 2]
+    pool.table, pool.lens = pool.table[ok].contiguous(), pool.lens[ok].contiguous()
+    got = pool.weights
+    at0, row0 = pool.places(0, 100)
+    assert not torch.isnan(got[at0, :, row0]).any()
+    check_attend(pool, q[ok], out[ok], lse[ok], None, 128 ** -0.5)
+    assert before.shape == got.shape
+
+
+def test_lengths_within_the_pages(dev):
+    """kv_lens shorter than what the pages hold: a row past it takes no part."""
+    import torch
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, "bf16", "nhd", 2, 128, 64, [640, 640, 640, 640], seed=8)
+    for lens in ([0, 1, 64, 65], [639, 640, 333, 16]):
+        pool.lens = torch.tensor(lens, dtype=torch.int32, device=dev)
+        before = pool.weights.clone()
+        q, out, lse = _attn(pool, 16)
+        assert _status() == 0
+        check_attend(pool, q, out, lse, before, 128 ** -0.5)
+
+
+def test_shared_pages(dev):
+    """A common prefix: three sequences over the same pages, each adding its weights."""
+    import torch
+    from paged_helpers import Pool, attend
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [256, 256, 256], seed=9)
+    pool.table[1] = pool.table[0]
+    pool.table[2, :2] = pool.table[0, :2]
+    before = pool.weights.clone()
+    q, out, lse = _attn(pool, 16)
+    assert _status() == 0
+    (o, tol), _, added = attend(pool, q, 128 ** -0.5)
+    assert ((out.double() - o).abs() <= tol).all()
+    want, room = before.double(), torch.zeros_like(before, dtype=torch.float64)
+    for b, (x, t) in enumerate(added):
+        at, row = pool.places(b, 256)
+        want[at, :, row] += x
+        room[at, :, row] += t + 3 * 2.0 ** -24 * want[at, :, row].abs()
+    used = ~torch.isnan(want)
+    assert ((pool.weights.double() - want).abs() <= room)[used].all()
+
+
+def test_bad_lengths_and_pages(dev):
+    """A length or a page that cannot be is reported and read nowhere; other sequences are not disturbed."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, attend, check_attend
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [200, 200, 200], seed=10)
+    good = pool.lens.clone()
+    pool.lens = torch.tensor([200, -1, pool.max_pages * 64 + 1], dtype=torch.int32, device=dev)
+    q, out, lse = _attn(pool, 16, accumulate=False)
+    assert _status() == T.DEVICE_BAD_KV_LEN
+    pool.lens = torch.tensor([200, 0, 0], dtype=torch.int32, device=dev)
+    check_attend(pool, q, out, lse, None, 128 ** -0.5)
+    pool.lens = good
+    for wrong in (-1, -2, pool.k.shape[0], 2 ** 31 - 1):
+        keep = pool.table.clone()
+        pool.table[1, 1] = wrong                       # slots 64..127 are absent
+        before = pool.weights.clone()
+        q, out, lse = _attn(pool, 16)
+        assert _status() == T.DEVICE_BAD_PAGE
+        at, row = (torch.cat(x) for x in zip(pool.places(0, 200), pool.places(2, 200)))
+        assert not torch.equal(pool.weights[at, :, row], before[at, :, row])
+        # The plain form over the slots that are there.
+        k = pool.table
+        pool.table = keep.clone()
+        pool.table[1, 1], pool.table[1, 2], pool.table[1, 3] = keep[1, 2], keep[1, 3], -1
+        (o, tol), (z, ztol), _ = attend(pool, q, 128 ** -0.5, torch.tensor([200, 136, 200]))
+        assert ((out.double() - o).abs() <= tol).all() and ((lse.double() - z).abs() <= ztol).all()
+        at, row = pool.table[1].long()[:1].expand(64), torch.arange(64, device=dev)
+        assert (pool.weights[at, :, row] > before[at, :, row]).all()
+        gone = keep[1, 1].long().expand(64)
+        assert torch.equal(pool.weights[gone, :, row], before[gone, :, row])
+        assert k is not pool.table
+        pool.table = keep
+
+
+def test_stream_and_graph(dev):
+    """Enqueued on a stream of its own and captured: replays read the inputs and lengths of their time."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [700, 90, 2000], seed=11)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    before = pool.weights.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q, out, lse = _attn(pool, 16)
+    side.synchronize()
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, 128 ** -0.5)
+    ws = pool.workspace(T.OP_PAGED_DECODE, 16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.paged_attn_decode(pool.cache, q, pool.table, pool.lens, out, lse, accumulate=True, workspace=ws)
+    for lens in ([700, 90, 2000], [1, 0, 1999]):
+        pool.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(pool.normal(*q.shape))
+        before = pool.weights.clone()
+        graph.replay()
+        assert _status() == 0
+        check_attend(pool, q, out, lse, before, 128 ** -0.5)
+
+
+def test_same_result_every_time(dev):
+    import torch
+    from paged_helpers import Pool
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 16, [5000, 90, 2000, 1], seed=12)
+    first = pool.weights.clone()
+    q, out, lse = _attn(pool, 16)
+    after = pool.weights.clone()
+    for _ in range(3):
+        pool.weights.copy_(first)
+        _, o, z = _attn(pool, 16, q=q)
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16)) and torch.equal(z, lse)
+        assert torch.equal(pool.weights.view(torch.int32), after.view(torch.int32))
+
+
+# ------------------------------------------------------------------ append ------
+
+@pytest.mark.parametrize("dtype,layout,heads,dim,page", [("bf16", "hnd", 2, 128, 64), ("fp16", "nhd", 3, 64, 48),
+                                                         ("bf16", "pair", 1, 128, 16), ("bf16", "hnd", 8, 64, 128)])
+@pytest.mark.parametrize("lens,new", [([1, 2, 64, 65], None), ([5, 300, 64, 17], [5, 300, 1, 0]),
+                                      ([1000, 130, 1, 70], [999, 130, 0, 69])])
+@pytest.mark.parametrize("strided", [False, True])
+def test_append(dev, dtype, layout, heads, dim, page, lens, new, strided):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool
+    pool = Pool(dev, dtype, layout, heads, dim, page, lens, seed=13)
+    n_new = [1] * len(lens) if new is None else new
+    most = max(n_new) if new is None else max(n_new) + 3       # rows behind the last new token are not read
+    batch = len(lens)
+    k_new, v_new = (pool.normal(batch, most, heads, dim).transpose(1, 2) for _ in range(2))
+    if not strided:
+        k_new, v_new = k_new.contiguous(), v_new.contiguous()
+    seen = pool.lens + torch.arange(batch, device=dev, dtype=torch.int32) * 10 if new else None
+    want = [t.clone() for t in (pool.k, pool.v, pool.weights, pool.positions)]
+    for b, n in enumerate(lens):
+        at, row = pool.places(b, n, n - n_new[b])
+        want[0][at, :, row] = k_new[b, :, :n_new[b]].transpose(0, 1)
+        want[1][at, :, row] = v_new[b, :, :n_new[b]].transpose(0, 1)
+        want[2][at, :, row] = 0.0
+        last = n if seen is None else int(seen[b])
+        want[3][at, :, row] = torch.arange(last - n_new[b], last, dtype=torch.int32, device=dev)[:, None]
+    T.paged_append_kv(pool.cache, k_new, v_new, pool.table, pool.lens,
+                      None if new is None else torch.tensor(new, dtype=torch.int32, device=dev), seen)
+    assert _status() == 0
+    for got, w in zip((pool.k, pool.v, pool.weights, pool.positions), want):
+        bits = torch.int16 if got.element_size() == 2 else torch.int32
+        assert torch.equal(got.contiguous().view(bits), w.contiguous().view(bits))
+
+
+def test_append_bad_inputs_touch_nothing(dev):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [100, 100, 100, 100], seed=14)
+    was = [t.clone() for t in (pool.k, pool.v, pool.weights, pool.positions)]
+    k = pool.normal(4, 2, 4, 128)
+    cap = pool.max_pages * 64
+
+    def same():
+        return all(torch.equal(a.view(torch.int32), b.view(torch.int32))
+                   for a, b in zip((pool.k, pool.v, pool.weights, pool.positions), was))
+    lens = torch.tensor([3, -1, cap + 1, 0], dtype=torch.int32, device=dev)
+    T.paged_append_kv(pool.cache, k, k, pool.table, lens)
+    assert _status() == T.DEVICE_BAD_KV_LEN and same()
+    n_new = torch.tensor([-1, 5, 6, 1000], dtype=torch.int32, device=dev)
+    T.paged_append_kv(pool.cache, k, k, pool.table, pool.lens, n_new)
+    assert _status() == T.DEVICE_BAD_KV_LEN and same()
+    pool.table[:, 1] = torch.tensor([-1, pool.k.shape[0], 2 ** 31 - 1, -77], dtype=torch.int32)
+    T.paged_append_kv(pool.cache, k, k, pool.table, pool.lens)
+    assert _status() == T.DEVICE_BAD_PAGE and same()
+
+
+def test_append_from_pinned_host(dev):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool
+    pool = Pool(dev, "fp16", "hnd", 2, 128, 64, [10, 65], seed=15, metadata=False)
+    k, v = (pool.normal(2, 2, 1, 128).cpu().pin_memory() for _ in range(2))
+    T.paged_append_kv(pool.cache, k, v, pool.table, pool.lens)
+    assert _status() == 0
+    for b, n in enumerate([10, 65]):
+        at, row = pool.places(b, n, n - 1)
+        assert torch.equal(pool.k[at, :, row][0].cpu(), k[b, :, 0]) and torch.equal(pool.v[at, :, row][0].cpu(), v[b, :, 0])
+
+
+# ---------------------------------------------------------------- eviction ------
+
+def _evict(pool, budget, n_init=0, n_local=0, seq_lens=None, in_place=False):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    new = pool.lens if in_place else torch.full_like(pool.lens, -9)
+    T.paged_evict(pool.cache, pool.table, pool.lens, new, budget, n_init, n_local, seq_lens,
+                  pool.workspace(T.OP_PAGED_EVICT))
+    return new
+
+
+def _check_evict(pool, want, new):
+    import torch
+    assert new.tolist() == want[4]
+    for got, w, name in zip((pool.k, pool.v, pool.weights, pool.positions), want[:4], "k v weights positions".split()):
+        bits = torch.int16 if got.element_size() == 2 else torch.int32
+        assert torch.equal(got.cpu().contiguous().view(bits), w.contiguous().view(bits)), name
+
+
+EVICT = [
+    # dtype, layout, heads, dim, page, lens, budget, n_init, n_local
+    ("bf16", "hnd", 2, 128, 64, [65, 64, 63, 1, 0, 300], 64, 0, 0),
+    ("bf16", "hnd", 2, 128, 64, [65, 200, 2048], 64, 4, 16),
+    ("fp16", "nhd", 3, 64, 48, [1500, 47, 999], 333, 1, 100),
+    ("bf16", "pair", 1, 128, 16, [4097, 4096, 2000], 1, 0, 0),
+    ("bf16", "hnd", 2, 64, 32, [4097], 4096, 4, 256),
+    ("fp16", "hnd", 1, 128, 256, [8000, 5000], 5000, 0, 5000),
+    ("bf16", "nhd", 2, 64, 64, [20000, 12345], 8191, 64, 512),       # 4 CTAs per unit
+    ("bf16", "hnd", 1, 64, 128, [140000], 70001, 100, 1000),          # 16 CTAs, 32 keys per thread
+    ("bf16", "hnd", 1, 64, 64, [300000, 40], 1000, 0, 7),             # 16 CTAs, 64 keys per thread
+]
+
+
+@pytest.mark.parametrize("dtype,layout,heads,dim,page,lens,budget,n_init,n_local", EVICT)
+@pytest.mark.parametrize("values", ["uniform", "ties", "crowded"])
+def test_evict(dev, dtype, layout, heads, dim, page, lens, budget, n_init, n_local, values):
+    import torch
+    from paged_helpers import Pool, evict_plain
+    pool = Pool(dev, dtype, layout, heads, dim, page, lens, seed=16)
+    if values == "ties":
+        pool.weights.mul_(4).floor_()
+    elif values == "crowded":                       # nearly all in one exponent, the rest far below
+        pool.weights.copy_(torch.where(pool.weights < 0.1, pool.weights * 1e-30, 1 + pool.weights * 1e-5))
+    want = evict_plain(pool, budget, n_init, n_local)
+    new = _evict(pool, budget, n_init, n_local, in_place=values == "ties")
+    assert _status() == 0
+    _check_evict(pool, want, new)
+
+
+def test_evict_strange_weights(dev):
+    """NaN goes first, -0 ties with 0, infinities are ordinary values; positions need not be in order."""
+    import torch
+    from paged_helpers import Pool, evict_plain
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [400, 130], seed=17)
+    values = torch.tensor([float("nan"), 0.0, -0.0, float("inf"), -float("inf"), 1.0, -1.0, 1e-45, 3e38], device=dev)
+    pick = torch.randint(0, 9, pool.weights.shape, generator=pool.gen, device=dev)
+    pool.weights.copy_(values[pick])
+    pool.positions.copy_(torch.randint(0, 900, pool.positions.shape, generator=pool.gen, device=dev, dtype=torch.int32))
+    seen = torch.tensor([900, 880], dtype=torch.int32, device=dev)
+    for budget, n_init, n_local in ((100, 20, 30), (7, 3, 4), (399, 0, 0)):
+        want = evict_plain(pool, budget, n_init, n_local, seen)
+        new = _evict(pool, budget, n_init, n_local, seen)
+        assert _status() == 0
+        _check_evict(pool, want, new)
+
+
+def test_evict_leaves_a_sequence_with_a_bad_page(dev):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, evict_plain
+    for cap_lens in ([300, 300, 300], [20000, 20000, 20000]):      # one CTA per unit, and a cluster
+        pool = Pool(dev, "bf16", "hnd", 2, 64, 64, cap_lens, seed=18)
+        n = cap_lens[0]
+        keep = pool.lens.clone()
+        pool.lens = torch.tensor([n, 0, n], dtype=torch.int32, device=dev)
+        want = list(evict_plain(pool, 100))
+        want[4] = [100, n, 100]
+        pool.lens = keep
+        pool.table[1, n // 64] = pool.k.shape[0]
+        new = _evict(pool, 100)
+        assert _status() == T.DEVICE_BAD_PAGE
+        _check_evict(pool, want, new)
+        pool.lens = torch.tensor([-3, 50, pool.max_pages * 64 + 1], dtype=torch.int32, device=dev)
+        new = _evict(pool, 100)
+        assert _status() == T.DEVICE_BAD_KV_LEN
+        want[4] = [0, 50, 0]
+        _check_evict(pool, want, new)
+
+
+# --------------------------------------------------------------- together ------
+
+@pytest.mark.parametrize("dtype,layout,group", [("bf16", "hnd", 16), ("fp16", "nhd", 3)])
+def test_decode_loop_under_a_budget(dev, dtype, layout, group):
+    """Prompts in, then steps of append, attention and (every fourth) eviction, the step captured as a graph;
+    against a plain cache of lists that evicts by the library's own weights."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, check_attend, evict_plain
+    heads, dim, page, budget = 2, 128, 16, 96
+    prompts = [90, 200, 1, 0]
+    pool = Pool(dev, dtype, layout, heads, dim, page, [budget + 140] * 4, seed=19)
+    pool.weights.fill_(float("nan"))
+    seen = torch.tensor(prompts, dtype=torch.int32, device=dev)
+    pool.lens = seen.clone()
+    k, v = pool.normal(4, heads, max(prompts), dim), pool.normal(4, heads, max(prompts), dim)
+    T.paged_append_kv(pool.cache, k, v, pool.table, pool.lens, n_new=seen, seq_lens=seen)
+    k_new, v_new = pool.normal(4, heads, 1, dim), pool.normal(4, heads, 1, dim)
+    q = pool.normal(4, 1, heads * group, dim)
+    out, lse = torch.empty_like(q), torch.empty((4, 1, heads * group), device=dev)
+    ws = pool.workspace(T.OP_PAGED_DECODE, group)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.lens.add_(1)
+        seen.add_(1)
+        T.paged_append_kv(pool.cache, k_new, v_new, pool.table, pool.lens, seq_lens=seen)
+        T.paged_attn_decode(pool.cache, q, pool.table, pool.lens, out, lse, accumulate=True, workspace=ws)
+    for step in range(12):
+        k_new.copy_(pool.normal(*k_new.shape))
+        v_new.copy_(pool.normal(*v_new.shape))
+        q.copy_(pool.normal(*q.shape))
+        before = pool.weights.clone()
+        for b, n in enumerate(pool.lens.tolist()):     # what the append will do to the weights
+            at, row = pool.places(b, n + 1, n)
+            before[at, :, row] = 0.0
+        graph.replay()
+        assert _status() == 0
+        for b, n in enumerate(pool.lens.tolist()):
+            at, row = pool.places(b, n, n - 1)
+            assert torch.equal(pool.k[at, :, row][0], k_new[b, :, 0])
+            assert (pool.positions[at, :, row] == int(seen[b]) - 1).all()
+        check_attend(pool, q, out, lse, before, dim ** -0.5)
+        if step % 4 == 3:
+            want = evict_plain(pool, budget, 4, 16, seen)
+            _evict(pool, budget, 4, 16, seen, in_place=True)
+            assert _status() == 0
+            _check_evict(pool, want, pool.lens)
+            for b, n in enumerate(pool.lens.tolist()):  # what must stay has stayed
+                at, row = pool.places(b, n)
+                for h in range(heads):
+                    have = set(pool.positions[at, h, row].tolist())
+                    total = int(seen[b])
+                    assert len(have) == n
+                    assert set(range(min(4, total))) | set(range(max(0, total - 16), total)) <= have

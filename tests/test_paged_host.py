@@ -1,0 +1,155 @@
+"""Refusals of the paged cache's entry points (no GPU needed).
+
+Every call fails validation before anything touches the device; the fake
+pointers are never dereferenced.
+"""
+
+import ctypes
+
+import pytest
+
+FAKE = 0x7F0000000000
+ODD = FAKE + 8
+
+
+@pytest.fixture(scope="module")
+def L():
+    import __graft_entry__
+    __graft_entry__.build()
+    from trainable_block_sparse_infllm_gb300 import _lib
+    return _lib
+
+
+def _cache(L, **kw):
+    heads, page, dim = kw.get("n_kv_heads", 2), kw.get("page_size", 64), kw.get("head_dim", 128)
+    strides = (heads * page * dim, page * dim, dim)
+    c = L.PagedCacheStruct(dtype=L.BF16, n_kv_heads=heads, head_dim=dim, page_size=page, num_pages=10,
+                           k_strides=(ctypes.c_int64 * 3)(*strides), v_strides=(ctypes.c_int64 * 3)(*strides),
+                           k_pages=FAKE, v_pages=FAKE, weights=FAKE, positions=FAKE)
+    for k, v in kw.items():
+        setattr(c, k, (ctypes.c_int64 * 3)(*v) if k.endswith("strides") else v)
+    return c
+
+
+def _append(L, c, batch=2, max_pages=4, n_q=1, k=FAKE, v=FAKE, strides=None, table=FAKE, lens=FAKE):
+    st = None if strides is None else (ctypes.c_int64 * 6)(*strides)
+    return L.lib.infllmv2_paged_append_kv(None if c is None else ctypes.byref(c), batch, max_pages, n_q, k, v, st,
+                                          table, lens, None, None, None)
+
+
+def _attn(L, c, batch=2, max_pages=4, group=16, q=FAKE, table=FAKE, lens=FAKE, scale=0.1, accumulate=0, out=FAKE,
+          ws=FAKE, ws_bytes=1 << 40):
+    return L.lib.infllmv2_paged_attn_decode(None if c is None else ctypes.byref(c), batch, max_pages, group, q, table,
+                                            lens, scale, accumulate, out, None, ws, ws_bytes, None)
+
+
+def _evict(L, c, batch=2, max_pages=4, table=FAKE, lens=FAKE, budget=10, n_init=0, n_local=0, new=FAKE, ws=FAKE,
+           ws_bytes=1 << 40):
+    return L.lib.infllmv2_paged_evict(None if c is None else ctypes.byref(c), batch, max_pages, table, lens, budget,
+                                      n_init, n_local, None, new, ws, ws_bytes, None)
+
+
+def test_struct_matches_the_header(L):
+    assert ctypes.sizeof(L.PagedCacheStruct) == 24 + 48 + 32
+
+
+def test_bad_caches(L):
+    for call in (_append, _attn, _evict):
+        assert call(L, None) == L.INVALID_ARGUMENT
+        for field, value, code in (("dtype", 2, L.UNSUPPORTED), ("dtype", -1, L.UNSUPPORTED),
+                                   ("n_kv_heads", 0, L.INVALID_ARGUMENT), ("n_kv_heads", 2000, L.UNSUPPORTED),
+                                   ("num_pages", 0, L.INVALID_ARGUMENT), ("page_size", 0, L.INVALID_ARGUMENT),
+                                   ("k_pages", None, L.INVALID_ARGUMENT), ("v_pages", None, L.INVALID_ARGUMENT),
+                                   ("k_pages", ODD, L.UNSUPPORTED), ("v_pages", ODD, L.UNSUPPORTED),
+                                   ("weights", ODD, L.UNSUPPORTED), ("positions", ODD, L.UNSUPPORTED)):
+            c = _cache(L)
+            setattr(c, field, value)
+            assert call(L, c) == code, (call.__name__, field, value)
+        for kw in (dict(head_dim=32), dict(head_dim=256), dict(page_size=8), dict(page_size=24),
+                   dict(page_size=65536 + 16)):
+            assert call(L, _cache(L, **kw)) == L.UNSUPPORTED, kw
+        good = (2 * 64 * 128, 64 * 128, 128)
+        for bad, code in (((0, 64 * 128, 128), L.INVALID_ARGUMENT), ((good[0], -1, 128), L.INVALID_ARGUMENT),
+                          ((good[0], good[1], 132), L.UNSUPPORTED),          # not 16-byte rows
+                          ((good[0], good[1], 64), L.INVALID_ARGUMENT),      # rows overlap
+                          ((good[1], good[1], 128), L.INVALID_ARGUMENT),
+                          ((1 << 40, good[1], 128), L.UNSUPPORTED)):
+            for which in ("k_strides", "v_strides"):
+                assert call(L, _cache(L, **{which: bad})) == code, bad
+        assert call(L, _cache(L), batch=0) == L.INVALID_ARGUMENT
+        assert call(L, _cache(L), batch=4097) == L.UNSUPPORTED
+        assert call(L, _cache(L, n_kv_heads=32), batch=4096) == L.UNSUPPORTED      # 131072 units
+        assert call(L, _cache(L), max_pages=0) == L.INVALID_ARGUMENT
+        assert call(L, _cache(L), max_pages=1 << 25) == L.UNSUPPORTED              # 2^31 slots
+        assert call(L, _cache(L), table=None) == L.INVALID_ARGUMENT
+        assert call(L, _cache(L), lens=None) == L.INVALID_ARGUMENT
+
+
+def test_append_arguments(L):
+    c = _cache(L)
+    assert _append(L, c, n_q=0) == L.INVALID_ARGUMENT
+    assert _append(L, c, n_q=4 * 64 + 1) == L.INVALID_ARGUMENT
+    assert _append(L, c, k=None) == L.INVALID_ARGUMENT
+    assert _append(L, c, v=ODD) == L.UNSUPPORTED
+    assert _append(L, c, n_q=2, strides=(512, 256, 128, 512, 256, 130)) == L.UNSUPPORTED
+    assert _append(L, c, n_q=2, strides=(512, 256, 128, 512, -256, 128)) == L.INVALID_ARGUMENT
+
+
+def test_attention_arguments(L):
+    c = _cache(L)
+    assert _attn(L, c, group=0) == L.INVALID_ARGUMENT
+    assert _attn(L, c, group=33) == L.UNSUPPORTED
+    assert _attn(L, c, q=None) == L.INVALID_ARGUMENT
+    assert _attn(L, c, out=ODD) == L.UNSUPPORTED
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert _attn(L, c, scale=scale) == L.INVALID_ARGUMENT
+    assert _attn(L, c, accumulate=2) == L.INVALID_ARGUMENT
+    assert _attn(L, _cache(L, weights=None), accumulate=1) == L.INVALID_ARGUMENT
+    need = L.lib.infllmv2_paged_workspace_size(ctypes.byref(c), 2, 4, 16, L.OP_PAGED_DECODE)
+    assert need >= 2 * 2 * 16 * 4 * 64 * 4                 # a score per head and slot
+    bare = _cache(L, weights=None, positions=None)
+    assert 0 < L.lib.infllmv2_paged_workspace_size(ctypes.byref(bare), 2, 4, 16, L.OP_PAGED_DECODE) < need
+    assert _attn(L, c, ws=None) == L.WORKSPACE_TOO_SMALL
+    assert _attn(L, c, ws_bytes=need - 1) == L.WORKSPACE_TOO_SMALL
+    assert _attn(L, c, ws=ODD) == L.UNSUPPORTED
+
+
+def test_evict_arguments(L):
+    c = _cache(L)
+    assert _evict(L, _cache(L, weights=None)) == L.INVALID_ARGUMENT
+    assert _evict(L, _cache(L, positions=None)) == L.INVALID_ARGUMENT
+    assert _evict(L, c, budget=0) == L.INVALID_ARGUMENT
+    assert _evict(L, c, n_init=-1) == L.INVALID_ARGUMENT
+    assert _evict(L, c, n_local=-1) == L.INVALID_ARGUMENT
+    assert _evict(L, c, budget=10, n_init=6, n_local=5) == L.INVALID_ARGUMENT
+    assert _evict(L, c, budget=10, n_init=2 ** 31 - 1, n_local=2 ** 31 - 1) == L.INVALID_ARGUMENT
+    assert _evict(L, c, new=None) == L.INVALID_ARGUMENT
+    assert _evict(L, c, max_pages=8193) == L.UNSUPPORTED           # past 524288 slots
+    need = L.lib.infllmv2_paged_workspace_size(ctypes.byref(c), 2, 4, 0, L.OP_PAGED_EVICT)
+    assert need > 0
+    assert _evict(L, c, ws_bytes=need - 1) == L.WORKSPACE_TOO_SMALL
+    assert _evict(L, c, ws=None) == L.WORKSPACE_TOO_SMALL
+
+
+def test_workspace_size_of_bad_arguments_is_zero(L):
+    size = L.lib.infllmv2_paged_workspace_size
+    c = _cache(L)
+    assert size(None, 2, 4, 16, L.OP_PAGED_DECODE) == 0
+    assert size(ctypes.byref(c), 0, 4, 16, L.OP_PAGED_DECODE) == 0
+    assert size(ctypes.byref(c), 2, 4, 0, L.OP_PAGED_DECODE) == 0
+    assert size(ctypes.byref(c), 2, 4, 16, 99) == 0
+    assert size(ctypes.byref(c), 2, 8193, 16, L.OP_PAGED_EVICT) == 0
+
+
+def test_python_binding_refuses(L):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    k = torch.zeros((4, 2, 64, 128), dtype=torch.bfloat16)
+    with pytest.raises(T.InfLLMv2Error, match="CUDA"):
+        T.PagedCache(k, k.clone())
+    with pytest.raises(T.InfLLMv2Error, match="one shape"):
+        T.PagedCache(k, k[:3])
+    with pytest.raises(T.InfLLMv2Error, match="bf16"):
+        T.PagedCache(k.float(), k.float())
+    with pytest.raises(T.InfLLMv2Error, match="bf16"):
+        T.PagedCache(k, k.half())

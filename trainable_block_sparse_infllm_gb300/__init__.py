@@ -15,6 +15,9 @@ memory and streams.  Entry points mirror the C names:
     coarse_means, select_blocks_coarse_lse
                          the coarse-kernel LSE approximation (prefill path)
     sparse_attn_backward dq, dk, dv of stage 3 with the selection held fixed
+    PagedCache, paged_append_kv, paged_attn_decode, paged_evict
+                         a cache of pages attended densely: its append, the attention of one
+                         new token, eviction by accumulated attention weight (paged.py)
 
 Method: "MiniCPM4: Ultra-Efficient LLMs on End Devices", section "InfLLM v2:
 Trainable Sparse Attention for Both Prefilling and Decoding".
@@ -29,7 +32,10 @@ import torch
 
 from . import _lib
 from ._lib import (InfLLMv2Error, OP_BACKWARD, OP_DECODE, OP_DECODE_STEP, OP_PREFILL, OP_SELECT,  # noqa: F401
-                   Params, DEVICE_BAD_KV_LEN, DEVICE_BOUNDS, DEVICE_TIMEOUT)
+                   OP_PAGED_DECODE, OP_PAGED_EVICT, Params, DEVICE_BAD_KV_LEN, DEVICE_BAD_PAGE, DEVICE_BOUNDS,
+                   DEVICE_TIMEOUT)
+from .paged import (PagedCache, alloc_paged_workspace, paged_append_kv, paged_attn_decode, paged_evict,  # noqa: F401
+                    paged_workspace_size)
 
 __all__ = [
     "Params", "InfLLMv2Error", "make_params", "num_kernels", "max_selected", "workspace_size",
@@ -37,6 +43,8 @@ __all__ = [
     "sparse_attn_prefill", "decode_step", "coarse_means", "alloc_kcc", "select_blocks_coarse_lse",
     "sparse_attn_backward", "append_kv", "append_decode_step", "get_device_status", "OP_SELECT", "OP_DECODE", "OP_PREFILL",
     "OP_DECODE_STEP", "OP_BACKWARD", "DECODE_MAX_NQ", "is_checked_build", "test_hooks",
+    "PagedCache", "paged_workspace_size", "alloc_paged_workspace", "paged_append_kv", "paged_attn_decode",
+    "paged_evict", "OP_PAGED_DECODE", "OP_PAGED_EVICT",
 ]
 
 DECODE_MAX_NQ = 16

@@ -25,11 +25,16 @@ CUDA_ERROR = 4
 DEVICE_BAD_KV_LEN = 0x1
 DEVICE_TIMEOUT = 0x2
 DEVICE_BOUNDS = 0x4
+DEVICE_BAD_PAGE = 0x8
 OP_SELECT = 1
 OP_DECODE = 2
 OP_PREFILL = 3
 OP_DECODE_STEP = 4
 OP_BACKWARD = 5
+OP_PAGED_DECODE = 6
+OP_PAGED_EVICT = 7
+BF16 = 0
+FP16 = 1
 
 
 class InfLLMv2Error(RuntimeError):
@@ -60,6 +65,25 @@ class Params(ctypes.Structure):
 
     def __repr__(self):
         return "Params(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """Mirror of ``infllmv2_paged_cache``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("k_strides", ctypes.c_int64 * 3),
+        ("v_strides", ctypes.c_int64 * 3),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+    ]
 
 
 if not os.path.exists(LIB_PATH):
@@ -108,6 +132,17 @@ lib.infllmv2_append_decode_step.restype = ctypes.c_int
 lib.infllmv2_sparse_attn_backward.argtypes = [_P, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                               _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 lib.infllmv2_sparse_attn_backward.restype = ctypes.c_int
+_C = ctypes.POINTER(PagedCacheStruct)
+lib.infllmv2_paged_workspace_size.argtypes = [_C, _i32, _i32, _i32, _i32]
+lib.infllmv2_paged_workspace_size.restype = ctypes.c_size_t
+lib.infllmv2_paged_append_kv.argtypes = [_C, _i32, _i32, _i32, _vp, _vp, ctypes.POINTER(ctypes.c_int64), _vp, _vp,
+                                         _vp, _vp, _vp]
+lib.infllmv2_paged_append_kv.restype = ctypes.c_int
+lib.infllmv2_paged_attn_decode.argtypes = [_C, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]
+lib.infllmv2_paged_attn_decode.restype = ctypes.c_int
+lib.infllmv2_paged_evict.argtypes = [_C, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+lib.infllmv2_paged_evict.restype = ctypes.c_int
 lib.infllmv2_status_string.argtypes = [ctypes.c_int]
 lib.infllmv2_status_string.restype = ctypes.c_char_p
 lib.infllmv2_last_error.argtypes = []
@@ -122,6 +157,7 @@ EXPORTED = (
     "infllmv2_sparse_attn_decode", "infllmv2_sparse_attn_prefill", "infllmv2_decode_step",
     "infllmv2_coarse_means", "infllmv2_select_blocks_coarse_lse", "infllmv2_sparse_attn_backward",
     "infllmv2_append_kv", "infllmv2_append_decode_step",
+    "infllmv2_paged_workspace_size", "infllmv2_paged_append_kv", "infllmv2_paged_attn_decode", "infllmv2_paged_evict",
     "infllmv2_status_string",
     "infllmv2_last_error", "infllmv2_get_device_status",
 )

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "infllmv2.h"
+#include "api_common.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -29,7 +30,12 @@ namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+constexpr int kMaxDevices = 64;
+
+}  // namespace
+
+namespace infllmv2 {
+
 int fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -58,11 +64,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-constexpr int kMaxDevices = 64;
-
-// Fault-injection flags of the checked build's tests (infllmv2_test_hooks).
-std::atomic<uint32_t> g_test_flags{0};
-
 uint32_t* status_ptr() {
   static uint32_t* ptrs[kMaxDevices] = {};
   static std::mutex mu;
@@ -76,6 +77,15 @@ uint32_t* status_ptr() {
   }
   return ptrs[dev];
 }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace infllmv2
+
+namespace {
+
+// Fault-injection flags of the checked build's tests (infllmv2_test_hooks).
+std::atomic<uint32_t> g_test_flags{0};
 
 // Device address of the built-in selection scratch on the current device.  The
 // host name of a __device__ array is only a stand-in, so the address is asked
@@ -116,8 +126,6 @@ int make_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_row
   if (r != CUDA_SUCCESS) return fail(INFLLMV2_CUDA_ERROR, "tensor map for %s failed (CUresult %d)", what, (int)r);
   return INFLLMV2_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_params(const infllmv2_params* p, int32_t n_q, Shape* s) {
   if (!p) return fail(INFLLMV2_INVALID_ARGUMENT, "params is NULL");
@@ -219,13 +227,6 @@ int attn_entry(const infllmv2_params* p, const void* q, int32_t n_q, const void*
 }
 
 }  // namespace
-
-#define INFLLMV2_GUARD(...)                                                   \
-  try {                                                                       \
-    __VA_ARGS__;                                                              \
-  } catch (...) {                                                             \
-    return INFLLMV2_INVALID_ARGUMENT;                                         \
-  }
 
 extern "C" {
 
