@@ -51,7 +51,12 @@ struct PagedAttnArgs {
   float* weights;    // null: not accumulated
   float* part_o;     // [2 n][G][D]: pieces of cut units, relative to their m
   float2* part_ml;   // [2 n][32]: (m in log2 units, l)
-  int4* cut;         // [n]: the unit whose second piece starts this CTA, (unit, last CTA, first piece's slot), or -1
+  // Cut units, (unit or -1, CTA of the second piece, last CTA, first piece's
+  // slot).  unit_cut, by unit, is kept where there are no more units than CTAs
+  // or weights are summed; cta_cut, by the CTA that the second piece starts,
+  // where there are more units than CTAs.  The join goes by the shorter list.
+  int4* unit_cut;
+  int4* cta_cut;
   float* lse2;       // [B Hkv G] lse in log2 units, of units that no border cut (weights only)
   float* scores;     // [B Hkv G][cap64] z in log2 units (weights only)
   int cap64;         // cap rounded up to whole tiles
@@ -279,9 +284,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     for (int e = tid; e < heads * (kDim / 2); e += C::kThreads) out[e] = 0;
     if (a.lse)
       for (int e = tid; e < heads; e += C::kThreads) a.lse[b * heads + e] = -INFINITY;
+    if (a.unit_cut)
+      for (int h = tid; h < a.Hkv; h += C::kThreads) a.unit_cut[b * a.Hkv + h] = make_int4(-1, 0, 0, 0);
   }
   if (cta >= s.n) {
-    if (tid == 0) a.cut[cta] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && a.cta_cut) a.cta_cut[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
 
@@ -292,12 +299,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     if (lane == 0) {
       // Does the previous CTA hold the first piece of the unit that starts this one?
       const long long first = p.at - p.tile0;   // the unit's first tile
+      const bool second = p.tile0 > 0 && split_owner(s.T, s.n, first) == cta - 1;
+      const int unit = p.b * a.Hkv + p.h;
       int4 c = make_int4(-1, 0, 0, 0);
-      if (p.tile0 > 0 && split_owner(s.T, s.n, first) == cta - 1) {
-        const int last = split_owner(s.T, s.n, first + p.tiles - 1);
-        c = make_int4(p.b * a.Hkv + p.h, last, 2 * (cta - 1) + (first > split_begin(s.T, s.n, cta - 1) ? 1 : 0), 0);
-      }
-      a.cut[cta] = c;
+      if (second)
+        c = make_int4(unit, cta, split_owner(s.T, s.n, first + p.tiles - 1),
+                      2 * (cta - 1) + (first > split_begin(s.T, s.n, cta - 1) ? 1 : 0));
+      if (a.cta_cut) a.cta_cut[cta] = c;
+      if (a.unit_cut && second) a.unit_cut[unit] = c;
     }
     const int boxes = kTile / a.box;
     int stage = 0;
@@ -305,6 +314,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     bool dead = false;
     uint32_t issued = 0;
     do {
+      if (lane == 0 && a.unit_cut && p.tile0 == 0 && p.tile1 == p.tiles)
+        a.unit_cut[p.b * a.Hkv + p.h] = make_int4(-1, 0, 0, 0);
       const int32_t* row = a.table + static_cast<long long>(p.b) * a.maxp;
       // Lane i handles box i of a tile; its page is fetched one tile ahead.
       auto fetch = [&](int tile) {
@@ -601,25 +612,26 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
 
 constexpr int kJoinThreads = 256;
 
-// CTAs [0, n G): CTA i G + h joins head h of the unit whose second piece
-// starts CTA i of the pass (most CTAs find none and leave).  CTAs behind them
-// (weights only): `per` CTAs share the tiles of one CTA of the pass and add
-// each slot's weight, from the z that the pass left and the unit's lse.
+// The first `jobs` CTAs (weights only) share the tiles anew and add each slot's
+// weight, from the z that the pass left and the unit's lse.  The CTAs behind
+// them join one head of one cut unit each.
 template <bool kFp16, int kDim>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnArgs a, int ctas, int per) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnArgs a, int jobs) {
   __shared__ float red_m[8], red_l[8];
   __shared__ float4 red_o[8][kDim / 4];
   __shared__ float unit_lse2[kPagedMaxGroup];
+  __shared__ float2 red_ml[kJoinThreads / 32][kPagedMaxGroup];
   __shared__ __align__(16) int split_mem[64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  if (static_cast<int>(blockIdx.x) < ctas * a.G) {
-    const int i = blockIdx.x / a.G, h = blockIdx.x % a.G;
-    const int4 c = a.cut[i];
+  if (static_cast<int>(blockIdx.x) >= jobs) {
+    const int job = blockIdx.x - jobs, h = job % a.G;
+    const int4 c = (a.cta_cut ? a.cta_cut : a.unit_cut)[job / a.G];
     if (c.x < 0) return;
-    const int pieces = c.y - i + 2;   // CTAs i - 1 .. c.y
-    auto slot_of = [&](int j) { return j == 0 ? c.z : 2 * (i - 1 + j); };
+    const int i = c.y;
+    const int pieces = c.z - i + 2;   // CTAs i - 1 .. c.z
+    auto slot_of = [&](int j) { return j == 0 ? c.w : 2 * (i - 1 + j); };
     float mx = -INFINITY;
     for (int j = tid; j < pieces; j += kJoinThreads) mx = fmaxf(mx, a.part_ml[slot_of(j) * kPagedMaxGroup + h].x);
     mx = warp_max(mx);
@@ -633,18 +645,29 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
     const int col = tid % kLanes, part = tid / kLanes;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-#pragma unroll 4
-    for (int j = part; j < pieces; j += kPar) {
-      const int sl = slot_of(j);
-      const float2 v = a.part_ml[sl * kPagedMaxGroup + h];
-      const float f = fast_exp2(v.x - use);
-      const float4 y =
-          *reinterpret_cast<const float4*>(a.part_o + (static_cast<long long>(sl) * a.G + h) * kDim + col * 4);
-      sum += v.y * f;
-      x.x += y.x * f;
-      x.y += y.y * f;
-      x.z += y.z * f;
-      x.w += y.w * f;
+    for (int j0 = part; j0 < pieces; j0 += 4 * kPar) {   // 4 rows in flight
+      float2 v[4];
+      float4 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + e * kPar;
+        v[e] = make_float2(-INFINITY, 0.f);
+        y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < pieces) {
+          const int sl = slot_of(j);
+          v[e] = a.part_ml[sl * kPagedMaxGroup + h];
+          y[e] = *reinterpret_cast<const float4*>(a.part_o + (static_cast<long long>(sl) * a.G + h) * kDim + col * 4);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = fast_exp2(v[e].x - use);
+        sum += v[e].y * f;
+        x.x += y[e].x * f;
+        x.y += y[e].y * f;
+        x.z += y[e].z * f;
+        x.w += y[e].w * f;
+      }
     }
     if constexpr (kLanes == 16) {   // two rows per warp
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
@@ -680,48 +703,87 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   }
 
   // -------------------------------------------------------------- weights ------
-  const int job = blockIdx.x - ctas * a.G;
-  const int cta = job / per, share = job % per;
-  const Split s = make_split<kJoinThreads>(a, cta, ctas, split_mem);
-  if (cta >= s.n) return;
+  const Split s = make_split<kJoinThreads>(a, blockIdx.x, jobs, split_mem);
+  if (static_cast<int>(blockIdx.x) >= s.n) return;
   Piece p;
   first_piece(p, s, a);
   do {
     const long long unit = static_cast<long long>(p.b) * a.Hkv + p.h;
-    const long long first = p.at - p.tile0;
-    const int c0 = split_owner(s.T, s.n, first), c1 = split_owner(s.T, s.n, first + p.tiles - 1);
-    __syncthreads();
-    if (c0 == c1) {
+    const int4 c = a.unit_cut[unit];
+    __syncthreads();   // the last unit's lse has been read
+    if (c.x < 0) {
       if (tid < a.G) unit_lse2[tid] = a.lse2[unit * a.G + tid];
     } else {
-      const int slot0 = 2 * c0 + (first > split_begin(s.T, s.n, c0) ? 1 : 0);
-      for (int h = warp; h < a.G; h += kJoinThreads / 32) {
-        float mx = -INFINITY, sum = 0.f;
-        for (int j = c0 + lane; j <= c1; j += 32) {
-          const float2 v = a.part_ml[(j == c0 ? slot0 : 2 * j) * kPagedMaxGroup + h];
-          const float nm = fmaxf(mx, v.x), use = nm == -INFINITY ? 0.f : nm;
-          sum = sum * fast_exp2(mx - use) + v.y * fast_exp2(v.x - use);
-          mx = nm;
+      // The pieces' (m, l): `wide` lanes read a piece's heads, 8 loads in flight.
+      const int pieces = c.z - c.y + 2;
+      const int wide = a.G > 16 ? 32 : (a.G > 8 ? 16 : 8), rows = kJoinThreads / wide;
+      const int head = tid % wide;
+      float mx = -INFINITY, sum = 0.f;
+      for (int j0 = tid / wide; j0 < pieces; j0 += 8 * rows) {
+        float2 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + e * rows;
+          v[e] = make_float2(-INFINITY, 0.f);
+          if (j < pieces && head < a.G) v[e] = a.part_ml[(j == 0 ? c.w : 2 * (c.y - 1 + j)) * kPagedMaxGroup + head];
         }
-        const float all = warp_max(mx), use = all == -INFINITY ? 0.f : all;
-        sum = warp_sum(sum * fast_exp2(mx - use));
-        if (lane == 0) unit_lse2[h] = use + log2f(sum) - (kFp16 ? 14.f : 0.f);
+        float nm = mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nm = fmaxf(nm, v[e].x);
+        const float use = nm == -INFINITY ? 0.f : nm;
+        sum *= fast_exp2(mx - use);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += v[e].y * fast_exp2(v[e].x - use);
+        mx = nm;
+      }
+      for (int o = wide; o < 32; o <<= 1) {   // rows within the warp
+        const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+        const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
+        sum = sum * fast_exp2(mx - use) + s2 * fast_exp2(m2 - use);
+        mx = nm;
+      }
+      red_ml[warp][lane] = make_float2(mx, sum);
+      __syncthreads();
+      if (warp == 0 && lane < a.G) {
+        float all = mx;
+#pragma unroll
+        for (int j = 1; j < kJoinThreads / 32; ++j) all = fmaxf(all, red_ml[j][lane].x);
+        const float use = all == -INFINITY ? 0.f : all;
+        float l = 0.f;
+#pragma unroll
+        for (int j = 0; j < kJoinThreads / 32; ++j) l += red_ml[j][lane].y * fast_exp2(red_ml[j][lane].x - use);
+        unit_lse2[lane] = use + log2f(l) - (kFp16 ? 14.f : 0.f);
       }
     }
     __syncthreads();
     const int32_t* table = a.table + static_cast<long long>(p.b) * a.maxp;
-    const int tiles = p.tile1 - p.tile0;
-    const int s0 = (p.tile0 + static_cast<int>(static_cast<long long>(tiles) * share / per)) * kTile;
-    const int s1 = min((p.tile0 + static_cast<int>(static_cast<long long>(tiles) * (share + 1) / per)) * kTile, p.len);
-    for (int slot = s0 + tid; slot < s1; slot += kJoinThreads) {
+    const int s0 = p.tile0 * kTile, s1 = min(p.tile1 * kTile, p.len);
+    // Four slots per thread; they share a page (pages hold multiples of 16).
+    for (int slot = s0 + 4 * tid; slot < s1; slot += 4 * kJoinThreads) {
       const int page = __ldg(table + slot / a.ps);
       const float* z = a.scores + unit * a.G * a.cap64 + slot;
-      float w = 0.f;
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int h = 0; h < a.G; ++h) w += fast_exp2(z[static_cast<long long>(h) * a.cap64] - unit_lse2[h]);
+      for (int h = 0; h < a.G; ++h) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(z + static_cast<long long>(h) * a.cap64));
+        const float y = unit_lse2[h];
+        w.x += fast_exp2(x.x - y);
+        w.y += fast_exp2(x.y - y);
+        w.z += fast_exp2(x.z - y);
+        w.w += fast_exp2(x.w - y);
+      }
+      if (page < 0 || page >= a.P) continue;
       // One add per slot of a call, so that a cache's own pages sum in a fixed
       // order; pages that sequences share are summed in the order of arrival.
-      if (page >= 0 && page < a.P) atomicAdd(a.weights + paged_meta(page, p.h, slot % a.ps, a.Hkv, a.ps), w);
+      float* to = a.weights + paged_meta(page, p.h, slot % a.ps, a.Hkv, a.ps);
+      if (slot + 4 <= s1) {
+        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(w.x), "f"(w.y), "f"(w.z),
+                     "f"(w.w)
+                     : "memory");
+      } else {
+        const float e[3] = {w.x, w.y, w.z};
+        for (int i = 0; i < s1 - slot; ++i) atomicAdd(to + i, e[i]);
+      }
     }
   } while (next_piece(p, s, a));
 }
@@ -735,7 +797,7 @@ int attn_ctas(const PagedShape& s, int G) {
 }
 
 struct WsLayout {
-  size_t cut, ml, o, lse2, scores, total;
+  size_t unit_cut, cta_cut, ml, o, lse2, scores, total;
 };
 
 WsLayout ws_layout(const PagedShape& s, int G) {
@@ -743,13 +805,21 @@ WsLayout ws_layout(const PagedShape& s, int G) {
   const size_t n = attn_ctas(s, G), heads = static_cast<size_t>(s.B) * s.Hkv * G;
   const size_t cap64 = static_cast<size_t>((s.cap + kTile - 1) / kTile) * kTile;
   WsLayout w;
-  w.cut = 0;
-  w.ml = up(n * sizeof(int4));
+  const size_t units = static_cast<size_t>(s.B) * s.Hkv;
+  w.unit_cut = 0;
+  w.cta_cut = up(units * sizeof(int4));
+  w.ml = w.cta_cut + up(n * sizeof(int4));
   w.o = w.ml + up(2 * n * kPagedMaxGroup * sizeof(float2));
   w.lse2 = w.o + up(2 * n * G * s.D * sizeof(float));
   w.scores = w.lse2 + (s.weights ? up(heads * sizeof(float)) : 0);
   w.total = w.scores + (s.weights ? up(heads * cap64 * sizeof(float)) : 0);
   return w;
+}
+
+int weight_jobs(const PagedAttnArgs& a) {
+  const long long tiles = static_cast<long long>(a.B) * a.Hkv * ((a.cap + kTile - 1) / kTile);
+  const long long want = (tiles + 15) / 16, most = 10LL * device_sm_count();
+  return static_cast<int>(want < most ? want : most);
 }
 
 template <typename F, typename... A>
@@ -767,19 +837,24 @@ cudaError_t launch_pdl(F kernel, dim3 grid, int threads, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The attribute is set on every call: it belongs to the current device's copy of the kernel.
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <bool kFp16, int kDim, int kGroups, bool kStack>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, cudaStream_t st) {
   using C = AttnCfg<kDim, kGroups, kStack>;
   auto kernel = paged_attn_kernel<kFp16, kDim, kGroups, kStack>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(ctas), C::kThreads, C::kSmem, st, km, vm, a);
   if (e != cudaSuccess) return e;
-  // Two CTAs share a pass CTA's tiles in the weights' part: its loads are
-  // short and their latency is what it waits for.
-  const int per = 2;
-  const unsigned grid = static_cast<unsigned>(ctas * a.G + (a.weights ? ctas * per : 0));
-  return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(grid), kJoinThreads, 0, st, a, ctas, per);
+  // The weights' part waits for the latency of short loads: many CTAs.
+  const int jobs = a.weights ? weight_jobs(a) : 0;
+  const int cuts = a.cta_cut ? ctas : a.B * a.Hkv;
+  return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(static_cast<unsigned>(jobs + cuts * a.G)), kJoinThreads, 0, st,
+                    a, jobs);
 }
 
 template <bool kFp16, int kDim>
@@ -816,7 +891,6 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.out = out;
   a.lse = lse;
   a.weights = accumulate ? s.weights : nullptr;
-  a.cut = reinterpret_cast<int4*>(base + w.cut);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml);
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.lse2 = reinterpret_cast<float*>(base + w.lse2);
@@ -824,6 +898,9 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.cap64 = (s.cap + kTile - 1) / kTile * kTile;
   a.status = s.status;
   const int ctas = attn_ctas(s, G);
+  const bool by_unit = s.B * s.Hkv <= ctas;
+  a.unit_cut = by_unit || accumulate ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
+  a.cta_cut = by_unit ? nullptr : reinterpret_cast<int4*>(base + w.cta_cut);
   if (s.fp16)
     return s.D == 128 ? launch_g<true, 128>(k_map, v_map, a, ctas, st) : launch_g<true, 64>(k_map, v_map, a, ctas, st);
   return s.D == 128 ? launch_g<false, 128>(k_map, v_map, a, ctas, st) : launch_g<false, 64>(k_map, v_map, a, ctas, st);

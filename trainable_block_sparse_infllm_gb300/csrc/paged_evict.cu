@@ -12,12 +12,10 @@
 // Two launches:
 //  * evict_select_kernel, one cluster of C CTAs per (sequence, KV head): every
 //    thread holds kKeys consecutive slots' keys (weight order-mapped to 32
-//    bits) in registers, and the budget-th largest key is found 4 bits at a
-//    time: 16 counts per round, packed in registers, summed by redux, shared
-//    memory and, for C > 1, distributed shared memory.  Unlike a shared-memory
-//    histogram its time does not depend on how the weights are spread (sums of
-//    softmax weights crowd into a few exponents).  Ordered scans then number
-//    the holes and the movers.
+//    bits) in registers, and the budget-th largest key is found 8 bits at a
+//    time by 256-bin histograms in shared memory, for C > 1 summed through
+//    distributed shared memory.  Ordered scans then number the holes and the
+//    movers.
 //  * evict_move_kernel: the numbered moves, over the whole GPU whatever the
 //    number of (sequence, KV head) pairs; this is where the bytes are.
 #include "paged.cuh"
@@ -38,8 +36,8 @@ struct EvictArgs {
   const int32_t* seq_lens;
   int32_t* new_lens;
   int32_t* count;    // [B Hkv] rows to move; -1: a page was bad, the sequence stays
-  int32_t* hole;     // [B Hkv][most] evicted slots below the budget
-  int32_t* mover;    // [B Hkv][most] kept slots at or past it
+  int2* hole;        // [B Hkv][most] (page, row) of the evicted slots below the budget
+  int2* mover;       // [B Hkv][most] of the kept slots at or past it
   int most;          // cap / 2: min(budget, n - budget) at most
 };
 
@@ -49,8 +47,8 @@ __device__ __forceinline__ uint32_t evict_key(float w) { return w != w ? 0u : fl
 
 template <int kKeys>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int C) {
-  __shared__ uint32_t warp_hist[2][kSelWarps][8];          // 16 counts of 16 bits per warp
-  __shared__ uint32_t cta_hist[2][kMaxCluster][16];        // by rank, written by every rank
+  __shared__ __align__(16) uint32_t hist[2][256];
+  __shared__ __align__(16) uint32_t total[256];            // of the cluster
   __shared__ unsigned long long warp_tot[kSelWarps];
   __shared__ unsigned long long cta_tot[2][kMaxCluster];
   __shared__ uint32_t bad_by_rank[kMaxCluster];
@@ -59,6 +57,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = blockIdx.x / C, b = unit / s.Hkv, h = unit % s.Hkv;
   if (C > 1) cluster_arrive_relaxed();
+  if (tid < 256) hist[0][tid] = hist[1][tid] = 0;   // visible by the barrier after the loads
   pdl_wait();
   pdl_trigger();
   if (C > 1) cluster_wait();   // every CTA runs: its shared memory may be written
@@ -116,61 +115,58 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
 
-  // ---- the budget-th largest key, 4 bits per round from the top -------------
+  // ---- the budget-th largest key, 8 bits per round from the top -------------
+  // `want`: how many of the keys that match the prefix stay.  The counts are
+  // shared-memory increments; those of a warp that meet in one bin are one.
   uint32_t prefix = 0;
-  int want = a.budget;   // how many of the keys that match the prefix stay
+  int want = a.budget;
 #pragma unroll 1
-  for (int round = 0; round < 8; ++round) {
-    const int shift = 28 - 4 * round, buf = round & 1;
-    // Counts of this thread's digits, 8 bits each, digits 0-3, 4-7, 8-11, 12-15.
-    uint32_t c8[4] = {0, 0, 0, 0};
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round, buf = round & 1;
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
       const uint32_t k = key[i];
-      const bool in = i < mine && (round == 0 || (k >> (shift + 4)) == prefix);
-      const uint32_t d = (k >> shift) & 15u;
-      const uint32_t one = in ? 1u << ((d & 3) * 8) : 0u;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) c8[q] += (d >> 2) == static_cast<uint32_t>(q) ? one : 0u;
+      if (i < mine && (round == 0 || (k >> (shift + 8)) == prefix)) atomicAdd(&hist[buf][(k >> shift) & 255u], 1u);
     }
-    uint32_t sum[8];   // digits 2 j and 2 j + 1, 16 bits each
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      sum[2 * q] = __reduce_add_sync(0xffffffffu, __byte_perm(c8[q], 0, 0x4140));
-      sum[2 * q + 1] = __reduce_add_sync(0xffffffffu, __byte_perm(c8[q], 0, 0x4342));
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) warp_hist[buf][warp][j] = sum[j];
-    }
-    __syncthreads();
-    int have = 0;   // lane d < 16: keys with digit d
-    if (C == 1 || warp == 0) {
-      if (lane < 16) {
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) have += (warp_hist[buf][w][lane >> 1] >> ((lane & 1) * 16)) & 0xffffu;
-      }
-    }
-    if (C > 1) {
-      if (warp == 0) {
-        for (int r = lane >> 4; r < C; r += 2) {
-          const int v = __shfl_sync(0xffffffffu, have, lane & 15);
-          st_dsmem_u32(dsmem_addr(&cta_hist[buf][rank][lane & 15], r), v);
-        }
-      }
+    if (C > 1)
       cluster_sync();
-      have = 0;
-      if (lane < 16)
-        for (int r = 0; r < C; ++r) have += cta_hist[buf][r][lane];
+    else
+      __syncthreads();
+    if (tid < 256) hist[buf ^ 1][tid] = 0;   // the next round's (last read before the barrier above)
+    if (C > 1) {
+      // Bin tid over the cluster: each CTA sums all of it by itself.
+      if (tid < 256) {
+        uint32_t sum = 0;
+        for (int r = 0; r < C; ++r) sum += ld_dsmem_u32(dsmem_addr(&hist[buf][tid], r));
+        total[tid] = sum;
+      }
+      __syncthreads();
     }
-    // Keys with a larger digit than lane's (lanes 16.. hold 0).
-    const int incl = warp_inclusive_scan(have);
-    const int total = __shfl_sync(0xffffffffu, incl, 15);
-    const int above = total - incl;
-    const bool here = lane < 16 && above < want && above + have >= want;
-    const int d = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    want -= __shfl_sync(0xffffffffu, above, d);
-    prefix = (prefix << 4) | static_cast<uint32_t>(d);
+    // Every warp finds the bin for itself: lane l holds bins 255 - 8 l - (0..7), largest first.
+    const uint32_t* h = C > 1 ? total : hist[buf];
+    const uint4 hi = *reinterpret_cast<const uint4*>(h + 252 - 8 * lane);
+    const uint4 lo = *reinterpret_cast<const uint4*>(h + 248 - 8 * lane);
+    const int c[8] = {static_cast<int>(hi.w), static_cast<int>(hi.z), static_cast<int>(hi.y), static_cast<int>(hi.x),
+                      static_cast<int>(lo.w), static_cast<int>(lo.z), static_cast<int>(lo.y), static_cast<int>(lo.x)};
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += c[j];
+    const int incl = warp_inclusive_scan(sum);
+    int above = incl - sum;   // keys in larger bins
+    int bin = 0;
+    const bool here = above < want && incl >= want;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (above + c[j] >= want) {
+        bin = 255 - 8 * lane - j;
+        break;
+      }
+      above += c[j];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    want -= __shfl_sync(0xffffffffu, above, src);
+    prefix = (prefix << 8) | static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src));
+    __syncthreads();   // hist[buf ^ 1] is zero
   }
 
   // ---- which slots stay: larger keys, and the first `want` equal ones --------
@@ -215,9 +211,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const unsigned long long at =
       scan((static_cast<unsigned long long>(__popcll(holes)) << 32) | static_cast<unsigned long long>(__popcll(movers)), 1);
   const long long list = static_cast<long long>(unit) * a.most;
-  for (int i = static_cast<int>(at >> 32); holes; holes &= holes - 1, ++i) a.hole[list + i] = slot0 + __ffsll(holes) - 1;
+  auto place = [&](unsigned long long bits) {
+    const int slot = slot0 + __ffsll(bits) - 1;
+    return make_int2(__ldg(s.table + static_cast<long long>(b) * s.maxp + slot / s.ps), slot % s.ps);
+  };
+  for (int i = static_cast<int>(at >> 32); holes; holes &= holes - 1, ++i) a.hole[list + i] = place(holes);
   int last = static_cast<int>(at & 0xffffffffu);
-  for (; movers; movers &= movers - 1, ++last) a.mover[list + last] = slot0 + __ffsll(movers) - 1;
+  for (; movers; movers &= movers - 1, ++last) a.mover[list + last] = place(movers);
   // The unit's last thread has every mover before it.
   if (rank == C - 1 && tid == kSelThreads - 1) a.count[unit] = last;
 }
@@ -241,24 +241,27 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int n = paged_len(s.kv_lens, b, s.cap, s.status);
     a.new_lens[b] = count < 0 ? n : min(n, a.budget);
   }
-  const int32_t* table = s.table + static_cast<long long>(b) * s.maxp;
   const long long list = static_cast<long long>(unit) * a.most;
   const int step = gridDim.x * (kMoveThreads / 32) * kBatch;
-  for (int first = (blockIdx.x * (kMoveThreads / 32) + warp) * kBatch; first < count; first += step) {
+  int first = (blockIdx.x * (kMoveThreads / 32) + warp) * kBatch;
+  int2 to_next = make_int2(0, 0), from_next = make_int2(0, 0);
+  auto fetch = [&](int at) {   // one batch ahead
+    if (lane < kBatch && at + lane < count) {
+      to_next = a.hole[list + at + lane];
+      from_next = a.mover[list + at + lane];
+    }
+  };
+  fetch(first);
+  for (; first < count; first += step) {
     const int have = min(kBatch, count - first);
-    int to_page = 0, to_row = 0, from_page = 0, from_row = 0;
+    const int to_page = to_next.x, to_row = to_next.y, from_page = from_next.x, from_row = from_next.y;
+    fetch(first + step);
+    float w = 0.f;
+    int p = 0;
     if (lane < have) {
-      const int to = a.hole[list + first + lane], from = a.mover[list + first + lane];
-      to_page = __ldg(table + to / s.ps);
-      to_row = to % s.ps;
-      from_page = __ldg(table + from / s.ps);
-      from_row = from % s.ps;
-      const long long d = paged_meta(to_page, h, to_row, s.Hkv, s.ps);
       const long long f = paged_meta(from_page, h, from_row, s.Hkv, s.ps);
-      const float w = s.weights[f];
-      const int p = s.positions[f];
-      s.weights[d] = w;
-      s.positions[d] = p;
+      w = s.weights[f];
+      p = s.positions[f];
     }
     uint4 x[kSteps];
     uint16_t* dst[kSteps];
@@ -276,6 +279,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
       if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = x[i];
+    if (lane < have) {
+      const long long d = paged_meta(to_page, h, to_row, s.Hkv, s.ps);
+      s.weights[d] = w;
+      s.positions[d] = p;
+    }
   }
 }
 
@@ -351,7 +359,7 @@ bool paged_evict_supported(const PagedShape& s) { return s.cap <= kSelThreads * 
 
 size_t paged_evict_workspace_bytes(const PagedShape& s) {
   const size_t units = static_cast<size_t>(s.B) * s.Hkv;
-  return up256(units * 4) + 2 * up256(units * most_moves(s) * 4);
+  return up256(units * 4) + 2 * up256(units * most_moves(s) * sizeof(int2));
 }
 
 cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int n_local, const int32_t* seq_lens,
@@ -366,8 +374,8 @@ cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int 
   a.new_lens = new_lens;
   a.most = most_moves(s);
   a.count = static_cast<int32_t*>(ws);
-  a.hole = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(units * 4));
-  a.mover = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(units * 4) + up256(units * a.most * 4));
+  a.hole = reinterpret_cast<int2*>(static_cast<char*>(ws) + up256(units * 4));
+  a.mover = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.hole) + up256(units * a.most * sizeof(int2)));
   const EvictPlan plan = evict_plan(s.cap);
   cudaError_t e;
   switch (plan.keys) {

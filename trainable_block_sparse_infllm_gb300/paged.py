@@ -25,6 +25,7 @@ from . import _lib
 from ._lib import InfLLMv2Error
 
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16}
+_Strides = ctypes.c_int64 * 6
 
 
 def _bad(message: str):
@@ -61,12 +62,12 @@ class PagedCache:
                 raise _bad(f"{name} must be contiguous {dtype} [num_pages, n_kv_heads, page_size] on the pages' device")
         self.k_pages, self.v_pages, self.weights, self.positions = k_pages, v_pages, weights, positions
         self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
-        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.dtype, self.device, self.index = k_pages.dtype, k_pages.device, k_pages.get_device()
         self.struct = _lib.PagedCacheStruct(
             dtype=_DTYPES[k_pages.dtype], n_kv_heads=self.n_kv_heads, head_dim=self.head_dim,
             page_size=self.page_size, num_pages=self.num_pages,
-            k_strides=(ctypes.c_int64 * 3)(*k_pages.stride()[:3]),
-            v_strides=(ctypes.c_int64 * 3)(*v_pages.stride()[:3]),
+            k_strides=k_pages.stride()[:3],
+            v_strides=v_pages.stride()[:3],
             k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(),
             weights=weights.data_ptr() if weights is not None else None,
             positions=positions.data_ptr() if positions is not None else None)
@@ -75,34 +76,39 @@ class PagedCache:
 
 def _stream(cache: PagedCache, stream) -> int:
     """The stream's handle; the launch goes to the current device, which must hold the pages."""
-    if torch.cuda.current_device() != cache.device.index:
+    index = cache.index
+    if torch.cuda.current_device() != index:
         raise _bad(f"the cache lives on {cache.device}, which is not the current CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # The current stream's handle without the Stream object around it (0.1 us instead of 3).
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ints(cache: PagedCache, t: torch.Tensor | None, shape: tuple, name: str):
+# get_device() is the device's index without a device object around it, -1 on the CPU.
+
+def _ints(cache: PagedCache, t: torch.Tensor | None, batch: int, name: str):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != cache.device:
-        raise _bad(f"{name} must be contiguous int32 {list(shape)} on {cache.device}")
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != batch or not t.is_contiguous() or \
+            t.get_device() != cache.index:
+        raise _bad(f"{name} must be contiguous int32 [{batch}] on {cache.device}")
     return t.data_ptr()
 
 
-def _table(cache: PagedCache, page_table: torch.Tensor):
-    if page_table.dim() != 2:
-        raise _bad("page_table must be int32 [batch, max_pages]")
-    batch, max_pages = page_table.shape
-    return batch, max_pages, _ints(cache, page_table, (batch, max_pages), "page_table")
+def _table(cache: PagedCache, t: torch.Tensor):
+    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != cache.index:
+        raise _bad(f"page_table must be contiguous int32 [batch, max_pages] on {cache.device}")
+    batch, max_pages = t.shape
+    return batch, max_pages, t.data_ptr()
 
 
 def _workspace(cache: PagedCache, workspace: torch.Tensor | None):
     if workspace is None:
         return None, 0
-    if not workspace.is_contiguous() or workspace.device != cache.device:
+    if not workspace.is_contiguous() or workspace.get_device() != cache.index:
         raise _bad(f"workspace must be contiguous on {cache.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def paged_workspace_size(cache: PagedCache, batch: int, max_pages: int, op: int, group_size: int = 1) -> int:
@@ -127,19 +133,21 @@ def paged_append_kv(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     strides with consecutive values; pinned host tensors are accepted.
     """
     batch, max_pages, table = _table(cache, page_table)
-    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[0] != batch or \
-            k_new.shape[1] != cache.n_kv_heads or k_new.shape[3] != cache.head_dim:
+    shape = k_new.shape
+    if len(shape) != 4 or shape != v_new.shape or shape[0] != batch or shape[1] != cache.n_kv_heads or \
+            shape[3] != cache.head_dim:
         raise _bad("k_new and v_new must be [batch, n_kv_heads, n_q, head_dim]")
-    for t in (k_new, v_new):
-        if t.dtype != cache.dtype or t.stride(3) != 1:
+    kb, kh, kt, kd = k_new.stride()
+    vb, vh, vt, vd = v_new.stride()
+    for t, unit in ((k_new, kd), (v_new, vd)):
+        if t.dtype is not cache.dtype or unit != 1:
             raise _bad("k_new and v_new must have the cache's type and rows of consecutive values")
-        if t.device != cache.device and not (t.device.type == "cpu" and t.is_pinned()):
+        if t.get_device() != cache.index and (t.is_cuda or not t.is_pinned()):
             raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
-    strides = (ctypes.c_int64 * 6)(*k_new.stride()[:3], *v_new.stride()[:3])
     _lib.check(_lib.lib.infllmv2_paged_append_kv(
-        cache._ref, batch, max_pages, k_new.shape[2], k_new.data_ptr(), v_new.data_ptr(), strides, table,
-        _ints(cache, kv_lens, (batch,), "kv_lens"), _ints(cache, n_new, (batch,), "n_new"),
-        _ints(cache, seq_lens, (batch,), "seq_lens"), _stream(cache, stream)))
+        cache._ref, batch, max_pages, shape[2], k_new.data_ptr(), v_new.data_ptr(), _Strides(kb, kh, kt, vb, vh, vt), table,
+        _ints(cache, kv_lens, batch, "kv_lens"), _ints(cache, n_new, batch, "n_new"),
+        _ints(cache, seq_lens, batch, "seq_lens"), _stream(cache, stream)))
     return cache
 
 
@@ -153,22 +161,22 @@ def paged_attn_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tens
     summed over the group's heads, to the cache's weights.
     """
     batch, max_pages, table = _table(cache, page_table)
-    if q.dim() != 4 or q.shape[0] != batch or q.shape[1] != 1 or q.shape[3] != cache.head_dim or \
-            q.shape[2] == 0 or q.shape[2] % cache.n_kv_heads != 0:
+    shape = q.shape
+    heads = shape[2] if len(shape) == 4 else 0
+    if heads == 0 or shape[0] != batch or shape[1] != 1 or shape[3] != cache.head_dim or heads % cache.n_kv_heads != 0:
         raise _bad("q must be [batch, 1, n_kv_heads * group, head_dim]")
-    heads = q.shape[2]
-    if out.shape != q.shape:
+    if out.shape != shape:
         raise _bad("out must have q's shape")
     for t in (q, out):
-        if t.dtype != cache.dtype or t.device != cache.device or not t.is_contiguous():
+        if t.dtype is not cache.dtype or t.get_device() != cache.index or not t.is_contiguous():
             raise _bad("q and out must be contiguous, of the cache's type and on its device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (batch, 1, heads) or
-                            lse.device != cache.device or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (batch, 1, heads) or
+                            lse.get_device() != cache.index or not lse.is_contiguous()):
         raise _bad("lse must be contiguous fp32 [batch, 1, heads] on the cache's device")
     ws, ws_bytes = _workspace(cache, workspace)
     _lib.check(_lib.lib.infllmv2_paged_attn_decode(
         cache._ref, batch, max_pages, heads // cache.n_kv_heads, q.data_ptr(), table,
-        _ints(cache, kv_lens, (batch,), "kv_lens"), cache.head_dim ** -0.5 if scale is None else scale,
+        _ints(cache, kv_lens, batch, "kv_lens"), cache.head_dim ** -0.5 if scale is None else scale,
         1 if accumulate else 0, out.data_ptr(), lse.data_ptr() if lse is not None else None, ws, ws_bytes,
         _stream(cache, stream)))
     return out, lse
@@ -187,7 +195,7 @@ def paged_evict(cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tens
         raise _bad("new_lens is required")
     ws, ws_bytes = _workspace(cache, workspace)
     _lib.check(_lib.lib.infllmv2_paged_evict(
-        cache._ref, batch, max_pages, table, _ints(cache, kv_lens, (batch,), "kv_lens"), budget, n_init, n_local,
-        _ints(cache, seq_lens, (batch,), "seq_lens"), _ints(cache, new_lens, (batch,), "new_lens"), ws, ws_bytes,
+        cache._ref, batch, max_pages, table, _ints(cache, kv_lens, batch, "kv_lens"), budget, n_init, n_local,
+        _ints(cache, seq_lens, batch, "seq_lens"), _ints(cache, new_lens, batch, "new_lens"), ws, ws_bytes,
         _stream(cache, stream)))
     return new_lens
