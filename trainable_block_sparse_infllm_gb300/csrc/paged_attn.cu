@@ -10,9 +10,9 @@
 // the pages at the copy rate, whatever the lengths.
 //
 // Split.  The work is all 64-slot tiles of all (sequence, KV head) units, in
-// that order; CTA i takes tiles [i T / n, (i + 1) T / n), so the CTAs of any
-// ragged batch carry the same load, and one long sequence spreads over all
-// SMs.  A unit inside one CTA is finished there; of a unit that CTA borders
+// that order, each unit with a fixed cost before its tiles; the CTAs take
+// equal shares of that line, so those of any ragged batch carry the same load,
+// and one long sequence spreads over all SMs.  A unit inside one CTA is finished there; of a unit that CTA borders
 // cut, each piece leaves (m, l, sum of exp(z - m) v) in the workspace and
 // paged_join_kernel joins them.  The host needs no lengths.
 //
@@ -65,29 +65,41 @@ struct PagedAttnArgs {
 
 // ---- the split of the tiles over the CTAs ----------------------------------
 
+// The units lie one after the other on a line, each `cost` positions for its
+// fixed work (queries, merge, output) and then one for every tile; empty
+// sequences take none.  CTA i has positions [i W / n, (i + 1) W / n) and the
+// tiles in them.
 struct Split {
-  long long T;           // tiles in all
-  int n;                 // CTAs that have tiles: min(CTAs, T)
-  long long begin, end;  // this CTA's tiles
-  int b, h, tile;        // where they begin
+  long long W;           // positions
+  int n;                 // CTAs that have positions: min(CTAs, W)
+  int cost;
+  long long begin, end;  // this CTA's positions
+  int b, h;              // the unit of the first one
+  long long unit0;       // where that unit begins
 };
 
-__device__ __forceinline__ long long split_begin(long long T, int n, int i) { return i * T / n; }
-// The CTA that tile t belongs to.
-__device__ __forceinline__ int split_owner(long long T, int n, long long t) {
-  return static_cast<int>(((t + 1) * n - 1) / T);
+__device__ __forceinline__ long long split_begin(const Split& s, int i) { return i * s.W / s.n; }
+// The CTA that a position belongs to.
+__device__ __forceinline__ int split_owner(const Split& s, long long at) {
+  return static_cast<int>(((at + 1) * s.n - 1) / s.W);
 }
 
-// All threads of the CTA.  Each sums the tiles of a run of sequences; the one
-// whose run holds the CTA's first tile says where that is.
+__device__ __forceinline__ int unit_tiles(int len) { return (len + kTile - 1) / kTile; }
+
+// All threads of the CTA.  Each sums a run of sequences; the one whose run
+// holds the CTA's first position says where that is.
 template <int kThreads>
-__device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int ctas, int* shared) {
+__device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int ctas, int cost, int* shared) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+  auto width = [&](int b) {   // of one unit of sequence b
+    const int tiles = unit_tiles(paged_len(a.kv_lens, b, a.cap, a.status));
+    return tiles ? tiles + cost : 0;
+  };
   int sum = 0;   // at most 32 sequences of 2^24 tiles (4096 sequences, 2^30 slots)
-  for (int b = b0; b < b1; ++b) sum += (paged_len(a.kv_lens, b, a.cap, a.status) + kTile - 1) / kTile;
+  for (int b = b0; b < b1; ++b) sum += width(b);
   long long pre = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -103,27 +115,28 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
     if (w == warp) before = all;
     all += totals[w];
   }
-  pre += before - sum;   // tiles (of one KV head) before this thread's run
+  pre += before - sum;   // positions of one KV head before this thread's run
   Split s;
-  s.T = all * a.Hkv;
-  s.n = static_cast<int>(min(static_cast<long long>(ctas), s.T));
-  s.begin = s.end = 0;
-  s.b = s.h = s.tile = 0;
+  s.W = all * a.Hkv;
+  s.n = static_cast<int>(min(static_cast<long long>(ctas), s.W));
+  s.cost = cost;
+  s.begin = s.end = s.unit0 = 0;
+  s.b = s.h = 0;
   int* where = shared + 2 * kWarps;
   if (cta < s.n) {
-    s.begin = split_begin(s.T, s.n, cta);
-    s.end = split_begin(s.T, s.n, cta + 1);
+    s.begin = split_begin(s, cta);
+    s.end = split_begin(s, cta + 1);
     if (s.begin >= pre * a.Hkv && s.begin < (pre + sum) * a.Hkv) {
       long long rest = s.begin - pre * a.Hkv;
       for (int b = b0; b < b1; ++b) {
-        const int tiles = (paged_len(a.kv_lens, b, a.cap, a.status) + kTile - 1) / kTile;
-        if (rest < static_cast<long long>(tiles) * a.Hkv) {
+        const int w = width(b);
+        if (rest < static_cast<long long>(w) * a.Hkv) {
           where[0] = b;
-          where[1] = static_cast<int>(rest / tiles);
-          where[2] = static_cast<int>(rest % tiles);
+          where[1] = static_cast<int>(rest / w);
+          where[2] = static_cast<int>(rest % w);
           break;
         }
-        rest -= static_cast<long long>(tiles) * a.Hkv;
+        rest -= static_cast<long long>(w) * a.Hkv;
       }
     }
   }
@@ -131,48 +144,53 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
   if (cta < s.n) {
     s.b = where[0];
     s.h = where[1];
-    s.tile = where[2];
+    s.unit0 = s.begin - where[2];
   }
   return s;
 }
 
-// A piece of one unit inside a CTA's tiles.
+// The tiles of one unit in a CTA's positions.
 struct Piece {
   int b, h, len, tiles;      // the unit: its sequence, KV head, slots and tiles
   int tile0, tile1;          // the piece
-  long long at;              // its first tile among all
+  long long unit0;           // where the unit begins
 };
 
-__device__ __forceinline__ void first_piece(Piece& p, const Split& s, const PagedAttnArgs& a) {
+__device__ __forceinline__ long long tile_at(const Split& s, const Piece& p, int tile) { return p.unit0 + s.cost + tile; }
+
+// Both: false where the CTA's positions hold no (further) tile.
+__device__ __forceinline__ bool first_piece(Piece& p, const Split& s, const PagedAttnArgs& a) {
+  if (s.end == s.begin) return false;
   p.b = s.b;
   p.h = s.h;
   p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
-  p.tiles = (p.len + kTile - 1) / kTile;
-  p.tile0 = s.tile;
-  p.at = s.begin;
-  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), p.tile0 + (s.end - p.at)));
+  p.tiles = unit_tiles(p.len);
+  p.unit0 = s.unit0;
+  p.tile0 = max(0, static_cast<int>(s.begin - p.unit0) - s.cost);
+  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), s.end - tile_at(s, p, 0)));
+  return p.tile1 > p.tile0;
 }
 
 __device__ __forceinline__ bool next_piece(Piece& p, const Split& s, const PagedAttnArgs& a) {
-  p.at += p.tile1 - p.tile0;
-  if (p.at >= s.end) return false;
+  p.unit0 = tile_at(s, p, p.tiles);
+  if (p.unit0 >= s.end) return false;
   if (++p.h == a.Hkv) {
     p.h = 0;
     do {
       ++p.b;
       p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
-    } while (p.len == 0);   // tiles are left, so a sequence with slots is
-    p.tiles = (p.len + kTile - 1) / kTile;
+    } while (p.len == 0);   // positions are left, so a sequence with slots is
+    p.tiles = unit_tiles(p.len);
   }
   p.tile0 = 0;
-  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), s.end - p.at));
-  return true;
+  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), s.end - tile_at(s, p, 0)));
+  return p.tile1 > 0;
 }
 
-// Workspace slot of a cut unit's piece in CTA i: 2 i for the piece that starts
-// the CTA's tiles, 2 i + 1 for one that starts later (and so is its last).
-__device__ __forceinline__ int piece_slot(const Piece& p, const Split& s, int cta) {
-  return 2 * cta + (p.at > s.begin ? 1 : 0);
+// Workspace slot of a cut unit's piece in CTA i: 2 i for a piece that starts at
+// the CTA's first position, 2 i + 1 for one that starts later (and so is its last).
+__device__ __forceinline__ int piece_slot(const Split& s, int cta, long long at) {
+  return 2 * cta + (at > split_begin(s, cta) ? 1 : 0);
 }
 
 // ---- types ------------------------------------------------------------------
@@ -234,6 +252,10 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 
 // ---- the pass over the pages -------------------------------------------------
 
+// A unit's queries, merge and output cost a CTA about as much as this many tiles.
+template <int kDim>
+constexpr int kUnitCost = kDim == 64 ? 2 : 1;
+
 // kGroups: groups of four warps, one per 16 heads.  kStack: at most 8 heads,
 // the lo parts of the probabilities in rows 8..15.
 template <int kDim, int kGroups, bool kStack>
@@ -243,6 +265,7 @@ struct AttnCfg {
   static constexpr int kStages = (kGroups == 1 ? 98304 : 196608) / kStage;
   static constexpr int kThreads = 32 + 128 * kGroups;
   static constexpr int kPerSm = kGroups == 1 ? 2 : 1;
+  static constexpr int kCost = kUnitCost<kDim>;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kInfoOff = kBarOff + 2 * kStages * 8;
   static constexpr int kMlOff = kInfoOff + ((kStages * 4 + 15) & ~15);
@@ -274,7 +297,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
   }
   pdl_wait();
   pdl_trigger();
-  const Split s = make_split<C::kThreads>(a, cta, ctas, reinterpret_cast<int*>(smem + C::kSplitOff));
+  const Split s = make_split<C::kThreads>(a, cta, ctas, C::kCost, reinterpret_cast<int*>(smem + C::kSplitOff));
 
   // Empty sequences attend nothing: a zero row, lse = -inf.
   const long long heads = static_cast<long long>(a.Hkv) * a.G;
@@ -287,24 +310,22 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     if (a.unit_cut)
       for (int h = tid; h < a.Hkv; h += C::kThreads) a.unit_cut[b * a.Hkv + h] = make_int4(-1, 0, 0, 0);
   }
-  if (cta >= s.n) {
+  Piece p;
+  if (!first_piece(p, s, a)) {
     if (tid == 0 && a.cta_cut) a.cta_cut[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
 
   if (warp == 4 * kGroups) {
     // ------------------------------------------------ the loading warp -------
-    Piece p;
-    first_piece(p, s, a);
     if (lane == 0) {
       // Does the previous CTA hold the first piece of the unit that starts this one?
-      const long long first = p.at - p.tile0;   // the unit's first tile
-      const bool second = p.tile0 > 0 && split_owner(s.T, s.n, first) == cta - 1;
+      const long long first = tile_at(s, p, 0);
+      const bool second = p.tile0 > 0 && split_owner(s, first) == cta - 1;
       const int unit = p.b * a.Hkv + p.h;
       int4 c = make_int4(-1, 0, 0, 0);
       if (second)
-        c = make_int4(unit, cta, split_owner(s.T, s.n, first + p.tiles - 1),
-                      2 * (cta - 1) + (first > split_begin(s.T, s.n, cta - 1) ? 1 : 0));
+        c = make_int4(unit, cta, split_owner(s, tile_at(s, p, p.tiles - 1)), piece_slot(s, cta - 1, first));
       if (a.cta_cut) a.cta_cut[cta] = c;
       if (a.unit_cut && second) a.unit_cut[unit] = c;
     }
@@ -386,8 +407,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
   int stage = 0;
   uint32_t phase = 0;
   bool dead = false;
-  Piece p;
-  first_piece(p, s, a);
   bool more = true;
   while (more) {
     const long long unit = static_cast<long long>(p.b) * a.Hkv + p.h;
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       if (t4 == 0) ml[w * 16 + g + 8 * r] = make_float2(m[r], l[r]);
     }
     const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
-    const int slot = piece_slot(p, s, cta);
+    const int slot = piece_slot(s, cta, tile_at(s, p, p.tile0));
     constexpr int kRows = kStack ? 8 : 16;
     float* buf = reinterpret_cast<float*>(smem + stage * C::kStage);
     named_sync(1 + kGroups, 128 * kGroups);   // every warp is done with the stage; ml is written
@@ -611,46 +630,49 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
 // ---- the join -----------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
+constexpr int kChunk = 4 * kJoinThreads;   // slots that a CTA of the weights' part takes at once
 
-// The first `jobs` CTAs (weights only) share the tiles anew and add each slot's
-// weight, from the z that the pass left and the unit's lse.  The CTAs behind
-// them join one head of one cut unit each.
+// The first `jobs` CTAs (weights only), as many for every unit, add each slot's
+// weight, from the z that the pass left and the unit's lse: CTA y of a unit
+// takes chunks y, y + jobs / units, ... of it.  The CTAs behind them join `hp`
+// heads (a power of two up to 8) of one cut unit each.
 template <bool kFp16, int kDim>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnArgs a, int jobs) {
+__global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const PagedAttnArgs a, int jobs, int hp) {
   __shared__ float red_m[8], red_l[8];
   __shared__ float4 red_o[8][kDim / 4];
   __shared__ float unit_lse2[kPagedMaxGroup];
   __shared__ float2 red_ml[kJoinThreads / 32][kPagedMaxGroup];
-  __shared__ __align__(16) int split_mem[64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= jobs) {
-    const int job = blockIdx.x - jobs, h = job % a.G;
-    const int4 c = (a.cta_cut ? a.cta_cut : a.unit_cut)[job / a.G];
+    const int per_cut = (a.G + hp - 1) / hp, job = blockIdx.x - jobs;
+    const int4 c = (a.cta_cut ? a.cta_cut : a.unit_cut)[job / per_cut];
     if (c.x < 0) return;
-    const int i = c.y;
-    const int pieces = c.z - i + 2;   // CTAs i - 1 .. c.z
+    const int warps = 8 / hp, warp0 = warp / warps * warps;   // a head's warps
+    const int h = job % per_cut * hp + warp / warps;
+    const int i = c.y, t = tid - warp0 * 32;
+    // CTAs i - 1 .. c.z hold a piece; a head past the last one joins none.
+    const int pieces = h < a.G ? c.z - i + 2 : 0;
     auto slot_of = [&](int j) { return j == 0 ? c.w : 2 * (i - 1 + j); };
     float mx = -INFINITY;
-    for (int j = tid; j < pieces; j += kJoinThreads) mx = fmaxf(mx, a.part_ml[slot_of(j) * kPagedMaxGroup + h].x);
+    for (int j = t; j < pieces; j += warps * 32) mx = fmaxf(mx, a.part_ml[slot_of(j) * kPagedMaxGroup + h].x);
     mx = warp_max(mx);
     if (lane == 0) red_m[warp] = mx;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, red_m[j]);
+    for (int j = 0; j < warps; ++j) mx = fmaxf(mx, red_m[warp0 + j]);
     const float use = mx == -INFINITY ? 0.f : mx;
     constexpr int kLanes = kDim / 4;            // threads of a row
-    constexpr int kPar = kJoinThreads / kLanes;  // rows at once
-    const int col = tid % kLanes, part = tid / kLanes;
+    const int par = warps * 32 / kLanes;        // rows at once
+    const int col = t % kLanes, part = t / kLanes;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int j0 = part; j0 < pieces; j0 += 4 * kPar) {   // 4 rows in flight
+    for (int j0 = part; j0 < pieces; j0 += 4 * par) {   // 4 rows in flight
       float2 v[4];
       float4 y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = j0 + e * kPar;
+        const int j = j0 + e * par;
         v[e] = make_float2(-INFINITY, 0.f);
         y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j < pieces) {
@@ -679,12 +701,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
     if (lane < kLanes) red_o[warp][lane] = x;
     if (lane == 0) red_l[warp] = sum;
     __syncthreads();
-    if (tid < kLanes) {
+    if (t < kLanes && h < a.G) {
       sum = 0.f;
       x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 y = red_o[j][tid];
+      for (int j = warp0; j < warp0 + warps; ++j) {
+        const float4 y = red_o[j][t];
         sum += red_l[j];
         x.x += y.x;
         x.y += y.y;
@@ -696,21 +717,21 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
       uint2 y;
       y.x = pack_pair<kFp16>(x.x * inv, x.y * inv);
       y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + tid * 4) = y;
-      if (tid == 0 && a.lse) a.lse[head] = (use + log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + t * 4) = y;
+      if (t == 0 && a.lse) a.lse[head] = (use + log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
     }
     return;
   }
 
   // -------------------------------------------------------------- weights ------
-  const Split s = make_split<kJoinThreads>(a, blockIdx.x, jobs, split_mem);
-  if (static_cast<int>(blockIdx.x) >= s.n) return;
-  Piece p;
-  first_piece(p, s, a);
-  do {
-    const long long unit = static_cast<long long>(p.b) * a.Hkv + p.h;
+  const int units = a.B * a.Hkv;
+  const int y = blockIdx.x / units, unit_i = blockIdx.x % units, step = jobs / units;
+  const int b = unit_i / a.Hkv, kv_head = unit_i % a.Hkv;
+  const int len = paged_len(a.kv_lens, b, a.cap, a.status);
+  if (y * kChunk >= len) return;
+  const long long unit = unit_i;
+  {
     const int4 c = a.unit_cut[unit];
-    __syncthreads();   // the last unit's lse has been read
     if (c.x < 0) {
       if (tid < a.G) unit_lse2[tid] = a.lse2[unit * a.G + tid];
     } else {
@@ -756,44 +777,45 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
       }
     }
     __syncthreads();
-    const int32_t* table = a.table + static_cast<long long>(p.b) * a.maxp;
-    const int s0 = p.tile0 * kTile, s1 = min(p.tile1 * kTile, p.len);
-    // Four slots per thread; they share a page (pages hold multiples of 16).
-    for (int slot = s0 + 4 * tid; slot < s1; slot += 4 * kJoinThreads) {
-      const int page = __ldg(table + slot / a.ps);
-      const float* z = a.scores + unit * a.G * a.cap64 + slot;
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // Four slots per thread; they share a page (pages hold multiples of 16).
+  const int32_t* table = a.table + static_cast<long long>(b) * a.maxp;
+  for (int slot = y * kChunk + 4 * tid; slot < len; slot += step * kChunk) {
+    const int page = __ldg(table + slot / a.ps);
+    const float* z = a.scores + unit * a.G * a.cap64 + slot;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int h = 0; h < a.G; ++h) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(z + static_cast<long long>(h) * a.cap64));
-        const float y = unit_lse2[h];
-        w.x += fast_exp2(x.x - y);
-        w.y += fast_exp2(x.y - y);
-        w.z += fast_exp2(x.z - y);
-        w.w += fast_exp2(x.w - y);
-      }
-      if (page < 0 || page >= a.P) continue;
-      // One add per slot of a call, so that a cache's own pages sum in a fixed
-      // order; pages that sequences share are summed in the order of arrival.
-      float* to = a.weights + paged_meta(page, p.h, slot % a.ps, a.Hkv, a.ps);
-      if (slot + 4 <= s1) {
-        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(w.x), "f"(w.y), "f"(w.z),
-                     "f"(w.w)
-                     : "memory");
-      } else {
-        const float e[3] = {w.x, w.y, w.z};
-        for (int i = 0; i < s1 - slot; ++i) atomicAdd(to + i, e[i]);
-      }
+    for (int h = 0; h < a.G; ++h) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(z + static_cast<long long>(h) * a.cap64));
+      const float l = unit_lse2[h];
+      w.x += fast_exp2(x.x - l);
+      w.y += fast_exp2(x.y - l);
+      w.z += fast_exp2(x.z - l);
+      w.w += fast_exp2(x.w - l);
     }
-  } while (next_piece(p, s, a));
+    if (page < 0 || page >= a.P) continue;
+    // One add per slot of a call, so that a cache's own pages sum in a fixed
+    // order; pages that sequences share are summed in the order of arrival.
+    float* to = a.weights + paged_meta(page, kv_head, slot % a.ps, a.Hkv, a.ps);
+    if (slot + 4 <= len) {
+      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(w.x), "f"(w.y), "f"(w.z),
+                   "f"(w.w)
+                   : "memory");
+    } else {
+      atomicAdd(to, w.x);
+      if (slot + 1 < len) atomicAdd(to + 1, w.y);
+      if (slot + 2 < len) atomicAdd(to + 2, w.z);
+    }
+  }
 }
 
 // ---- host side -------------------------------------------------------------------
 
 int attn_ctas(const PagedShape& s, int G) {
-  const long long tiles = static_cast<long long>(s.B) * s.Hkv * ((s.cap + kTile - 1) / kTile);
+  const int cost = s.D == 64 ? kUnitCost<64> : kUnitCost<128>;
+  const long long positions = static_cast<long long>(s.B) * s.Hkv * ((s.cap + kTile - 1) / kTile + cost);
   const long long most = static_cast<long long>(device_sm_count()) * (G > 16 ? 1 : 2);
-  return static_cast<int>(tiles < most ? tiles : most);
+  return static_cast<int>(positions < most ? positions : most);
 }
 
 struct WsLayout {
@@ -816,10 +838,13 @@ WsLayout ws_layout(const PagedShape& s, int G) {
   return w;
 }
 
+// CTAs of the weights' part: about 16 per SM, the same number for every unit
+// and no more than its chunks.  Their loads are short, and latency is what they
+// wait for.
 int weight_jobs(const PagedAttnArgs& a) {
-  const long long tiles = static_cast<long long>(a.B) * a.Hkv * ((a.cap + kTile - 1) / kTile);
-  const long long want = (tiles + 15) / 16, most = 10LL * device_sm_count();
-  return static_cast<int>(want < most ? want : most);
+  const int units = a.B * a.Hkv, chunks = (a.cap + kChunk - 1) / kChunk;
+  const int want = (16 * device_sm_count() + units - 1) / units;
+  return units * (want < chunks ? want : chunks);
 }
 
 template <typename F, typename... A>
@@ -850,11 +875,14 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(ctas), C::kThreads, C::kSmem, st, km, vm, a);
   if (e != cudaSuccess) return e;
-  // The weights' part waits for the latency of short loads: many CTAs.
   const int jobs = a.weights ? weight_jobs(a) : 0;
+  // One CTA per head of a cut unit while that fills no more than the SMs twice
+  // (a long sequence's unit has hundreds of pieces), else up to 8 heads each.
   const int cuts = a.cta_cut ? ctas : a.B * a.Hkv;
-  return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(static_cast<unsigned>(jobs + cuts * a.G)), kJoinThreads, 0, st,
-                    a, jobs);
+  int hp = 1;
+  while (hp < 8 && cuts * ((a.G + hp - 1) / hp) > 2 * device_sm_count()) hp *= 2;
+  return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(static_cast<unsigned>(jobs + cuts * ((a.G + hp - 1) / hp))),
+                    kJoinThreads, 0, st, a, jobs, hp);
 }
 
 template <bool kFp16, int kDim>
