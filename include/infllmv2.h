@@ -368,8 +368,8 @@ int infllmv2_sparse_attn_backward(const infllmv2_params* p, const void* q, int32
  * them.  seq_lens (int32 [batch]) may be NULL: nothing was ever evicted.
  *
  * Supported: bf16 and fp16, head_dim 64 and 128, page_size a multiple of 16,
- * up to 4096 sequences and 2^30 slots each, strides that are multiples of 8
- * elements, pointers 16-byte aligned.
+ * up to 4096 sequences and 2^30 slots each, fewer than 2^31 slots in the pool,
+ * strides that are multiples of 8 elements, pointers 16-byte aligned.
  *
  * The conventions above hold: device pointers, work enqueued on `stream`,
  * no allocation, no synchronisation, bounded waits.  A workspace is written

@@ -76,6 +76,7 @@ def test_bad_caches(L):
                           ((1 << 40, good[1], 128), L.UNSUPPORTED)):
             for which in ("k_strides", "v_strides"):
                 assert call(L, _cache(L, **{which: bad})) == code, bad
+        assert call(L, _cache(L, num_pages=1 << 25)) == L.UNSUPPORTED             # 2^31 slots in the pool
         assert call(L, _cache(L), batch=0) == L.INVALID_ARGUMENT
         assert call(L, _cache(L), batch=4097) == L.UNSUPPORTED
         assert call(L, _cache(L, n_kv_heads=32), batch=4096) == L.UNSUPPORTED      # 131072 units

@@ -61,6 +61,8 @@ int check_cache(const infllmv2_paged_cache* c, int32_t batch, int32_t max_pages,
     return fail(INFLLMV2_UNSUPPORTED, "batch * n_kv_heads must be <= 65535");
   if (static_cast<int64_t>(max_pages) * c->page_size > kMaxCap)
     return fail(INFLLMV2_UNSUPPORTED, "max_pages * page_size must be <= 2^30");
+  if (static_cast<int64_t>(c->num_pages) * c->page_size > 0x7fffffffLL)
+    return fail(INFLLMV2_UNSUPPORTED, "num_pages * page_size must be < 2^31");
   if (!c->k_pages || !c->v_pages) return fail(INFLLMV2_INVALID_ARGUMENT, "k_pages or v_pages is NULL");
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->weights) || !aligned16(c->positions))
     return fail(INFLLMV2_UNSUPPORTED, "k_pages, v_pages, weights and positions must be 16-byte aligned");

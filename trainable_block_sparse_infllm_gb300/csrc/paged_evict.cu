@@ -9,15 +9,17 @@
 // never overwrites a row that is still to be read.  A decode loop that evicts
 // one token per step moves one row per step, not the cache.
 //
-// Two launches:
-//  * evict_select_kernel, one cluster of C CTAs per (sequence, KV head): every
-//    thread holds kKeys consecutive slots' keys (weight order-mapped to 32
-//    bits) in registers, and the budget-th largest key is found 8 bits at a
-//    time by 256-bin histograms in shared memory, for C > 1 summed through
-//    distributed shared memory.  Ordered scans then number the holes and the
-//    movers.
-//  * evict_move_kernel: the numbered moves, over the whole GPU whatever the
-//    number of (sequence, KV head) pairs; this is where the bytes are.
+// evict_select_kernel, one cluster of C CTAs per (sequence, KV head): every
+// thread holds kKeys consecutive slots' keys (weight order-mapped to 32 bits)
+// in registers.  The key that divides kept from evicted is found by 256-bin
+// histograms in shared memory (for C > 1 summed through distributed shared
+// memory): the first spans the keys from the smallest to the largest, each
+// further one the bin that holds the boundary, until a bin holds just the keys
+// that are still wanted.  (Digits of fixed bits would put most softmax sums
+// into the two or three bins of their exponents.)  Ordered scans then number
+// the holes and the movers, whose lists go out through shared memory, in whole
+// lines.  evict_move_kernel moves the rows over the whole GPU; with few moves
+// the selecting CTAs do it themselves and save the launch.
 #include "paged.cuh"
 #include "kernels.h"
 
@@ -36,8 +38,10 @@ struct EvictArgs {
   const int32_t* seq_lens;
   int32_t* new_lens;
   int32_t* count;    // [B Hkv] rows to move; -1: a page was bad, the sequence stays
-  int2* hole;        // [B Hkv][most] (page, row) of the evicted slots below the budget
-  int2* mover;       // [B Hkv][most] of the kept slots at or past it
+  // [B Hkv][most] evicted slots below the budget, kept slots at or past it, as
+  // page * page size + row (the pool's slots are fewer than 2^31).
+  int32_t* hole;
+  int32_t* mover;
   int most;          // cap / 2: min(budget, n - budget) at most
 };
 
@@ -45,207 +49,21 @@ struct EvictArgs {
 // of all, and -0 equals 0.
 __device__ __forceinline__ uint32_t evict_key(float w) { return w != w ? 0u : float_to_ordered(w + 0.f); }
 
-template <int kKeys>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int C) {
-  __shared__ __align__(16) uint32_t hist[2][256];
-  __shared__ __align__(16) uint32_t total[256];            // of the cluster
-  __shared__ unsigned long long warp_tot[kSelWarps];
-  __shared__ unsigned long long cta_tot[2][kMaxCluster];
-  __shared__ uint32_t bad_by_rank[kMaxCluster];
-  const PagedShape& s = a.s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int unit = blockIdx.x / C, b = unit / s.Hkv, h = unit % s.Hkv;
-  if (C > 1) cluster_arrive_relaxed();
-  if (tid < 256) hist[0][tid] = hist[1][tid] = 0;   // visible by the barrier after the loads
-  pdl_wait();
-  pdl_trigger();
-  if (C > 1) cluster_wait();   // every CTA runs: its shared memory may be written
-  const int n = paged_len(s.kv_lens, b, s.cap, s.status);
-  if (n <= a.budget) {   // the same for the whole cluster
-    if (rank == 0 && tid == 0) a.count[unit] = 0;
-    return;
-  }
-  const int seen = a.seq_lens ? __ldg(a.seq_lens + b) : n;
-  const int slot0 = (rank * kSelThreads + tid) * kKeys;
-  const int mine = max(0, min(kKeys, n - slot0));
-  uint32_t key[kKeys];
-  bool bad = false;
-  {
-    const int32_t* table = s.table + static_cast<long long>(b) * s.maxp;
-    constexpr int kPart = kKeys < 16 ? kKeys : 16;   // 16 slots at a multiple of 16 are in one page
-#pragma unroll
-    for (int c = 0; c < kKeys / kPart; ++c) {
-      const int first = slot0 + c * kPart;
-      long long at = -1;
-      if (first < n) {
-        const int page = __ldg(table + first / s.ps);
-        if (page < 0 || page >= s.P)
-          bad = true;
-        else
-          at = paged_meta(page, h, first % s.ps, s.Hkv, s.ps);
-      }
-#pragma unroll
-      for (int v = 0; v < kPart / 4; ++v) {
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        int4 p = make_int4(0, 0, 0, 0);
-        if (at >= 0) {
-          w = *reinterpret_cast<const float4*>(s.weights + at + v * 4);
-          p = *reinterpret_cast<const int4*>(s.positions + at + v * 4);
-        }
-        const float ws[4] = {w.x, w.y, w.z, w.w};
-        const int ps[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool always = ps[e] < a.n_init || ps[e] >= seen - a.n_local;
-          key[c * kPart + v * 4 + e] = always ? 0xffffffffu : evict_key(ws[e]);
-        }
-      }
-    }
-  }
-  if (bad) atomicOr(s.status, kStatusBadPage);
-  bad = __syncthreads_or(bad);
-  if (C > 1) {
-    if (tid < C) st_dsmem_u32(dsmem_addr(&bad_by_rank[rank], tid), bad ? 1u : 0u);
-    cluster_sync();
-    for (int r = 0; r < C; ++r) bad |= bad_by_rank[r] != 0;
-  }
-  if (bad) {
-    if (rank == 0 && tid == 0) a.count[unit] = -1;
-    return;
-  }
-
-  // ---- the budget-th largest key, 8 bits per round from the top -------------
-  // `want`: how many of the keys that match the prefix stay.  The counts are
-  // shared-memory increments; those of a warp that meet in one bin are one.
-  uint32_t prefix = 0;
-  int want = a.budget;
-#pragma unroll 1
-  for (int round = 0; round < 4; ++round) {
-    const int shift = 24 - 8 * round, buf = round & 1;
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const uint32_t k = key[i];
-      if (i < mine && (round == 0 || (k >> (shift + 8)) == prefix)) atomicAdd(&hist[buf][(k >> shift) & 255u], 1u);
-    }
-    if (C > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-    if (tid < 256) hist[buf ^ 1][tid] = 0;   // the next round's (last read before the barrier above)
-    if (C > 1) {
-      // Bin tid over the cluster: each CTA sums all of it by itself.
-      if (tid < 256) {
-        uint32_t sum = 0;
-        for (int r = 0; r < C; ++r) sum += ld_dsmem_u32(dsmem_addr(&hist[buf][tid], r));
-        total[tid] = sum;
-      }
-      __syncthreads();
-    }
-    // Every warp finds the bin for itself: lane l holds bins 255 - 8 l - (0..7), largest first.
-    const uint32_t* h = C > 1 ? total : hist[buf];
-    const uint4 hi = *reinterpret_cast<const uint4*>(h + 252 - 8 * lane);
-    const uint4 lo = *reinterpret_cast<const uint4*>(h + 248 - 8 * lane);
-    const int c[8] = {static_cast<int>(hi.w), static_cast<int>(hi.z), static_cast<int>(hi.y), static_cast<int>(hi.x),
-                      static_cast<int>(lo.w), static_cast<int>(lo.z), static_cast<int>(lo.y), static_cast<int>(lo.x)};
-    int sum = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += c[j];
-    const int incl = warp_inclusive_scan(sum);
-    int above = incl - sum;   // keys in larger bins
-    int bin = 0;
-    const bool here = above < want && incl >= want;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (above + c[j] >= want) {
-        bin = 255 - 8 * lane - j;
-        break;
-      }
-      above += c[j];
-    }
-    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    want -= __shfl_sync(0xffffffffu, above, src);
-    prefix = (prefix << 8) | static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src));
-    __syncthreads();   // hist[buf ^ 1] is zero
-  }
-
-  // ---- which slots stay: larger keys, and the first `want` equal ones --------
-  // Two ordered scans over all threads: the equal keys, then holes and movers.
-  auto scan = [&](unsigned long long v, int buf) {   // exclusive, over the unit's threads
-    unsigned long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (buf) __syncthreads();   // the first scan's totals have been read
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    unsigned long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w == warp) before = all;
-      all += warp_tot[w];
-    }
-    if (C > 1) {
-      if (tid < C) st_dsmem_u64(dsmem_addr(&cta_tot[buf][rank], tid), all);
-      cluster_sync();
-      for (int r = 0; r < rank; ++r) before += cta_tot[buf][r];
-    }
-    return before + inc - v;
-  };
-  int equal = 0;
-#pragma unroll
-  for (int i = 0; i < kKeys; ++i) equal += (i < mine && key[i] == prefix) ? 1 : 0;
-  int rank_eq = static_cast<int>(scan(equal, 0));
-  unsigned long long stay = 0;   // kKeys bits
-#pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
-    const bool eq = key[i] == prefix;
-    if (i < mine && (key[i] > prefix || (eq && rank_eq < want))) stay |= 1ull << i;
-    rank_eq += (i < mine && eq) ? 1 : 0;
-  }
-  const int below = max(0, min(mine, a.budget - slot0));   // slots below the budget
-  const unsigned long long below_mask = below >= 64 ? ~0ull : (1ull << below) - 1;
-  unsigned long long holes = ~stay & below_mask, movers = stay & ~below_mask;
-  const unsigned long long at =
-      scan((static_cast<unsigned long long>(__popcll(holes)) << 32) | static_cast<unsigned long long>(__popcll(movers)), 1);
-  const long long list = static_cast<long long>(unit) * a.most;
-  auto place = [&](unsigned long long bits) {
-    const int slot = slot0 + __ffsll(bits) - 1;
-    return make_int2(__ldg(s.table + static_cast<long long>(b) * s.maxp + slot / s.ps), slot % s.ps);
-  };
-  for (int i = static_cast<int>(at >> 32); holes; holes &= holes - 1, ++i) a.hole[list + i] = place(holes);
-  int last = static_cast<int>(at & 0xffffffffu);
-  for (; movers; movers &= movers - 1, ++last) a.mover[list + last] = place(movers);
-  // The unit's last thread has every mover before it.
-  if (rank == C - 1 && tid == kSelThreads - 1) a.count[unit] = last;
-}
-
-// CTA (x, unit): moves x, x + gridDim.x, ... of the unit in batches of kBatch
-// per warp.  A row of D 16-bit values takes D / 8 lanes of 16 bytes; all loads
-// of a batch are issued before its first store.
-template <int kDim>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// Moves warp, warp + warps, ... (in batches of kBatch) of a unit's `count`.  A
+// row of D 16-bit values takes D / 8 lanes of 16 bytes; all loads of a batch
+// are issued before its first store, and the next batch's places are fetched
+// meanwhile.
+template <int kDim, int kBatch>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int unit, int h, int count, int warp, int warps) {
   constexpr int kLanes = kDim / 8, kRowsAtOnce = 32 / kLanes;
-  constexpr int kBatch = 8;                              // moves: 2 kBatch rows
   constexpr int kSteps = 2 * kBatch / kRowsAtOnce;
   const PagedShape& s = a.s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.y, b = unit / s.Hkv, h = unit % s.Hkv;
-  pdl_wait();
-  pdl_trigger();
-  const int count = a.count[unit];
-  if (blockIdx.x == 0 && h == 0 && tid == 0) {
-    // The only reader of kv_lens in this launch is new_lens' writer, so the two may be one array.
-    const int n = paged_len(s.kv_lens, b, s.cap, s.status);
-    a.new_lens[b] = count < 0 ? n : min(n, a.budget);
-  }
+  const int lane = threadIdx.x & 31;
   const long long list = static_cast<long long>(unit) * a.most;
-  const int step = gridDim.x * (kMoveThreads / 32) * kBatch;
-  int first = (blockIdx.x * (kMoveThreads / 32) + warp) * kBatch;
-  int2 to_next = make_int2(0, 0), from_next = make_int2(0, 0);
-  auto fetch = [&](int at) {   // one batch ahead
+  const int step = warps * kBatch;
+  int first = warp * kBatch;
+  int to_next = 0, from_next = 0;
+  auto fetch = [&](int at) {
     if (lane < kBatch && at + lane < count) {
       to_next = a.hole[list + at + lane];
       from_next = a.mover[list + at + lane];
@@ -254,7 +72,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   fetch(first);
   for (; first < count; first += step) {
     const int have = min(kBatch, count - first);
-    const int to_page = to_next.x, to_row = to_next.y, from_page = from_next.x, from_row = from_next.y;
+    const int to_page = to_next / s.ps, to_row = to_next % s.ps;
+    const int from_page = from_next / s.ps, from_row = from_next % s.ps;
     fetch(first + step);
     float w = 0.f;
     int p = 0;
@@ -287,6 +106,310 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   }
 }
 
+__device__ __forceinline__ void count_if(bool in, uint32_t* bin) {   // no branch around the increment
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(smem_u32(bin)),
+               "r"(static_cast<uint32_t>(in))
+               : "memory");
+}
+
+constexpr uint32_t kAlways = 0xffffffffu;   // above every weight's key
+
+// What the CTAs of a cluster tell each other about their keys.
+struct EvictRange {
+  uint32_t bad, low, high, always;   // a bad page; smallest, largest key of a weight; slots that always stay
+};
+
+// kDim = 0: the moves are left to evict_move_kernel.
+template <int kKeys, int kDim>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int C) {
+  extern __shared__ int32_t stage[];                       // [kKeys kSelThreads]: holes up, movers down
+  __shared__ __align__(16) uint32_t hist[2][256];
+  __shared__ __align__(16) uint32_t total[256];            // of the cluster
+  __shared__ uint4 range_warp[kSelWarps];
+  __shared__ EvictRange range[kMaxCluster];
+  __shared__ unsigned long long warp_tot[2][kSelWarps];
+  __shared__ unsigned long long cta_tot[2][kMaxCluster];
+  const PagedShape& s = a.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / C, b = unit / s.Hkv, h = unit % s.Hkv;
+  if (C > 1) cluster_arrive_relaxed();
+  if (tid < 256) hist[0][tid] = hist[1][tid] = 0;   // visible by the barrier after the loads
+  pdl_wait();
+  pdl_trigger();
+  if (C > 1) cluster_wait();   // every CTA runs: its shared memory may be written
+  const int n = paged_len(s.kv_lens, b, s.cap, s.status);
+  const bool writes_len = kDim > 0 && rank == 0 && h == 0 && tid == 0;
+  if (n <= a.budget) {   // the same for the whole cluster
+    if (kDim == 0 && rank == 0 && tid == 0) a.count[unit] = 0;
+    if (writes_len) a.new_lens[b] = n;
+    return;
+  }
+  const int seen = a.seq_lens ? __ldg(a.seq_lens + b) : n;
+  const int slot0 = (rank * kSelThreads + tid) * kKeys;
+  // Slots at or past n get key 0.  They never stay: of equal keys the lower
+  // slots do, and more than `budget` of those exist.
+  uint32_t key[kKeys];
+  uint32_t low = kAlways, high = 0, always = 0;
+  bool bad = false;
+  constexpr int kPart = kKeys < 16 ? kKeys : 16;   // 16 slots at a multiple of 16 are in one page
+  int place[kKeys / kPart];                        // page * page size + row of a part's first slot
+  {
+    const int32_t* table = s.table + static_cast<long long>(b) * s.maxp;
+    const int local = seen - a.n_local;
+#pragma unroll
+    for (int c = 0; c < kKeys / kPart; ++c) {
+      const int first = slot0 + c * kPart;
+      long long at = -1;
+      place[c] = 0;
+      if (first < n) {
+        const int page = __ldg(table + first / s.ps), row = first % s.ps;
+        if (page < 0 || page >= s.P) {
+          bad = true;
+        } else {
+          at = paged_meta(page, h, row, s.Hkv, s.ps);
+          place[c] = page * s.ps + row;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < kPart / 4; ++v) {
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        int4 p = make_int4(0, 0, 0, 0);
+        if (at >= 0) {
+          w = *reinterpret_cast<const float4*>(s.weights + at + v * 4);
+          p = *reinterpret_cast<const int4*>(s.positions + at + v * 4);
+        }
+        const float ws[4] = {w.x, w.y, w.z, w.w};
+        const int ps[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool held = first + v * 4 + e < n, stays = ps[e] < a.n_init || ps[e] >= local;
+          const uint32_t k = evict_key(ws[e]);
+          if (held && !stays) {
+            low = min(low, k);
+            high = max(high, k);
+          }
+          always += held && stays ? 1u : 0u;
+          key[c * kPart + v * 4 + e] = held ? (stays ? kAlways : k) : 0u;
+        }
+      }
+    }
+  }
+  if (bad) atomicOr(s.status, kStatusBadPage);
+  {
+    const uint4 mine = make_uint4(__any_sync(0xffffffffu, bad), __reduce_min_sync(0xffffffffu, low),
+                                  __reduce_max_sync(0xffffffffu, high), __reduce_add_sync(0xffffffffu, always));
+    if (lane == 0) range_warp[warp] = mine;
+  }
+  __syncthreads();
+  EvictRange all_range{0, kAlways, 0, 0};
+  auto join_range = [&](uint32_t bad_, uint32_t low_, uint32_t high_, uint32_t always_) {
+    all_range.bad |= bad_;
+    all_range.low = min(all_range.low, low_);
+    all_range.high = max(all_range.high, high_);
+    all_range.always += always_;
+  };
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) join_range(range_warp[w].x, range_warp[w].y, range_warp[w].z, range_warp[w].w);
+  if (C > 1) {
+    if (tid < C) {
+      st_dsmem_u32(dsmem_addr(&range[rank].bad, tid), all_range.bad);
+      st_dsmem_u32(dsmem_addr(&range[rank].low, tid), all_range.low);
+      st_dsmem_u32(dsmem_addr(&range[rank].high, tid), all_range.high);
+      st_dsmem_u32(dsmem_addr(&range[rank].always, tid), all_range.always);
+    }
+    cluster_sync();
+    all_range = EvictRange{0, kAlways, 0, 0};
+    for (int r = 0; r < C; ++r) join_range(range[r].bad, range[r].low, range[r].high, range[r].always);
+  }
+  if (all_range.bad) {
+    if (kDim == 0 && rank == 0 && tid == 0) a.count[unit] = -1;
+    if (writes_len) a.new_lens[b] = n;
+    return;
+  }
+
+  // ---- where the boundary is ---------------------------------------------------
+  // Keys above `at + last` stay, keys below `at` go; `match` keys are between,
+  // of which the `want` largest (of equal ones the lowest slots) stay.
+  uint32_t at = kAlways, last = 0;
+  int want = a.budget, match = static_cast<int>(all_range.always);
+  if (match < want) {
+    want -= match;
+    at = all_range.low;
+    last = all_range.high - all_range.low;
+    match = n - static_cast<int>(all_range.always);
+  }
+#pragma unroll 1
+  for (int round = 0; match != want && last != 0; ++round) {
+    const int buf = round & 1;
+    const int shift = max(0, 24 - __clz(last));   // 256 bins of 2^shift keys
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const uint32_t off = key[i] - at;
+      count_if(off <= last, &hist[buf][(off >> shift) & 255u]);
+    }
+    if (C > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    if (tid < 256) hist[buf ^ 1][tid] = 0;   // the next round's (last read before the barrier above)
+    if (C > 1) {
+      // Bin tid over the cluster: each CTA sums all of it by itself.
+      if (tid < 256) {
+        uint32_t sum = 0;
+        for (int r0 = 0; r0 < C; r0 += 8) {   // 8 remote loads in flight
+          uint32_t v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = r0 + r < C ? ld_dsmem_u32(dsmem_addr(&hist[buf][tid], r0 + r)) : 0u;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) sum += v[r];
+        }
+        total[tid] = sum;
+      }
+      __syncthreads();
+    }
+    // Every warp finds the bin for itself: lane l holds bins 255 - 8 l - (0..7), largest first.
+    const uint32_t* hs = C > 1 ? total : hist[buf];
+    const uint4 hi = *reinterpret_cast<const uint4*>(hs + 252 - 8 * lane);
+    const uint4 lo = *reinterpret_cast<const uint4*>(hs + 248 - 8 * lane);
+    const int c[8] = {static_cast<int>(hi.w), static_cast<int>(hi.z), static_cast<int>(hi.y), static_cast<int>(hi.x),
+                      static_cast<int>(lo.w), static_cast<int>(lo.z), static_cast<int>(lo.y), static_cast<int>(lo.x)};
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += c[j];
+    const int incl = warp_inclusive_scan(sum);
+    int above = incl - sum;   // keys in larger bins
+    const int src = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+    int bin = 0, in_bin = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!found) {
+        if (above + c[j] >= want) {
+          found = true;
+          bin = 255 - 8 * lane - j;
+          in_bin = c[j];
+        } else {
+          above += c[j];
+        }
+      }
+    }
+    want -= __shfl_sync(0xffffffffu, above, src);
+    match = __shfl_sync(0xffffffffu, in_bin, src);
+    const uint32_t skip = static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src)) << shift;
+    at += skip;
+    last = min(last - skip, (1u << shift) - 1);
+    __syncthreads();            // hist[buf ^ 1] is zero
+  }
+
+  // ---- which slots stay, and their numbers ------------------------------------
+  // Exclusive sum over the unit's threads, in slot order, of two counts packed
+  // into 16 bits each; `cta0`: before this CTA, `cta`: this CTA's, `all`: the
+  // unit's, 32 bits each.
+  unsigned long long cta0 = 0, cta = 0, all = 0;
+  auto scan = [&](uint32_t v, int buf) {
+    uint32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    auto wide = [](uint32_t x) { return (static_cast<unsigned long long>(x >> 16) << 32) | (x & 0xffffu); };
+    if (lane == 31) warp_tot[buf][warp] = wide(inc);
+    __syncthreads();
+    unsigned long long before = 0;
+    cta = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      if (w == warp) before = cta;
+      cta += warp_tot[buf][w];
+    }
+    cta0 = 0;
+    all = cta;
+    if (C > 1) {
+      if (tid < C) st_dsmem_u64(dsmem_addr(&cta_tot[buf][rank], tid), cta);
+      cluster_sync();
+      all = 0;
+      for (int r = 0; r < C; ++r) {
+        if (r == rank) cta0 = all;
+        all += cta_tot[buf][r];
+      }
+    }
+    return before + wide(inc) - wide(v);   // within the CTA
+  };
+  int rank_eq = 0;
+  const bool ties = match > want;   // of equal keys (last = 0): the lowest slots stay
+  if (ties) {
+    uint32_t equal = 0;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) equal += key[i] == at ? 1u : 0u;
+    rank_eq = static_cast<int>(scan(equal, 0));
+    rank_eq += static_cast<int>(cta0);
+  }
+  unsigned long long stay = 0;   // kKeys bits
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const bool eq = ties && key[i] == at;
+    if (key[i] >= at && (!eq || rank_eq < want)) stay |= 1ull << i;
+    rank_eq += eq ? 1 : 0;
+  }
+  const int below = min(kKeys, a.budget - slot0);   // slots below the budget
+  const unsigned long long below_mask = below <= 0 ? 0ull : (below >= 64 ? ~0ull : (1ull << below) - 1);
+  const unsigned long long holes = ~stay & below_mask, movers = stay & ~below_mask;
+  const unsigned long long mine =
+      scan((static_cast<uint32_t>(__popcll(holes)) << 16) | static_cast<uint32_t>(__popcll(movers)), 1);
+  const int count = static_cast<int>(all & 0xffffffffu);   // as many holes as movers
+  constexpr int kSlots = kKeys * kSelThreads;
+  {
+    int32_t* up = stage + static_cast<int>(mine >> 32);
+    int32_t* down = stage + kSlots - 1 - static_cast<int>(mine & 0xffffffffu);
+#pragma unroll
+    for (int c = 0; c < kKeys / kPart; ++c) {
+      const uint32_t mask = (1u << kPart) - 1;
+      for (uint32_t x = static_cast<uint32_t>(holes >> (c * kPart)) & mask; x; x &= x - 1)
+        *up++ = place[c] + __ffs(x) - 1;
+      for (uint32_t x = static_cast<uint32_t>(movers >> (c * kPart)) & mask; x; x &= x - 1)
+        *down-- = place[c] + __ffs(x) - 1;
+    }
+  }
+  __syncthreads();
+  {
+    const int n_holes = static_cast<int>(cta >> 32), n_movers = static_cast<int>(cta & 0xffffffffu);
+    int32_t* to = a.hole + static_cast<long long>(unit) * a.most + static_cast<int>(cta0 >> 32);
+    int32_t* from = a.mover + static_cast<long long>(unit) * a.most + static_cast<int>(cta0 & 0xffffffffu);
+    for (int i = tid; i < n_holes; i += kSelThreads) to[i] = stage[i];
+    for (int i = tid; i < n_movers; i += kSelThreads) from[i] = stage[kSlots - 1 - i];
+  }
+  if constexpr (kDim == 0) {
+    if (rank == 0 && tid == 0) a.count[unit] = count;
+  } else {
+    if (C > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    if (writes_len) a.new_lens[b] = a.budget;
+    move_rows<kDim, 4>(a, unit, h, count, rank * kSelWarps + warp, C * kSelWarps);
+  }
+}
+
+// The moves over the whole GPU: CTA (x, unit).  Also writes
+// new_lens; its writer is the only reader of kv_lens in this launch, so the two
+// may be one array.
+template <int kDim>
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a) {
+  const PagedShape& s = a.s;
+  const int unit = blockIdx.y, b = unit / s.Hkv, h = unit % s.Hkv;
+  pdl_wait();
+  pdl_trigger();
+  const int count = a.count[unit];
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+    const int n = paged_len(s.kv_lens, b, s.cap, s.status);
+    a.new_lens[b] = count < 0 ? n : min(n, a.budget);
+  }
+  constexpr int kWarps = kMoveThreads / 32;
+  move_rows<kDim, 8>(a, unit, h, count, blockIdx.x * kWarps + threadIdx.x / 32, gridDim.x * kWarps);
+}
+
 struct EvictPlan {
   int keys, cluster;
 };
@@ -304,16 +427,22 @@ EvictPlan evict_plan(int cap) {
   return {keys, c};
 }
 
-template <int kKeys>
+template <int kKeys, int kDim>
 cudaError_t launch_select(const EvictArgs& a, int C, cudaStream_t st) {
-  auto kernel = evict_select_kernel<kKeys>;
+  auto kernel = evict_select_kernel<kKeys, kDim>;
+  constexpr int kSmem = kKeys * kSelThreads * 4;
   if (C > 8) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  if (kSmem > 32768) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.s.B * a.s.Hkv * C), 1, 1);
   cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -325,6 +454,17 @@ cudaError_t launch_select(const EvictArgs& a, int C, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, C);
+}
+
+template <int kDim>
+cudaError_t launch_select_any(const EvictArgs& a, EvictPlan plan, cudaStream_t st) {
+  switch (plan.keys) {
+    case 4: return launch_select<4, kDim>(a, plan.cluster, st);
+    case 8: return launch_select<8, kDim>(a, plan.cluster, st);
+    case 16: return launch_select<16, kDim>(a, plan.cluster, st);
+    case 32: return launch_select<32, kDim>(a, plan.cluster, st);
+    default: return launch_select<64, kDim>(a, plan.cluster, st);
+  }
 }
 
 template <int kDim>
@@ -359,7 +499,7 @@ bool paged_evict_supported(const PagedShape& s) { return s.cap <= kSelThreads * 
 
 size_t paged_evict_workspace_bytes(const PagedShape& s) {
   const size_t units = static_cast<size_t>(s.B) * s.Hkv;
-  return up256(units * 4) + 2 * up256(units * most_moves(s) * sizeof(int2));
+  return up256(units * 4) + 2 * up256(units * most_moves(s) * 4);
 }
 
 cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int n_local, const int32_t* seq_lens,
@@ -374,17 +514,16 @@ cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int 
   a.new_lens = new_lens;
   a.most = most_moves(s);
   a.count = static_cast<int32_t*>(ws);
-  a.hole = reinterpret_cast<int2*>(static_cast<char*>(ws) + up256(units * 4));
-  a.mover = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.hole) + up256(units * a.most * sizeof(int2)));
+  a.hole = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(units * 4));
+  a.mover = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(a.hole) + up256(units * a.most * 4));
   const EvictPlan plan = evict_plan(s.cap);
-  cudaError_t e;
-  switch (plan.keys) {
-    case 4: e = launch_select<4>(a, plan.cluster, st); break;
-    case 8: e = launch_select<8>(a, plan.cluster, st); break;
-    case 16: e = launch_select<16>(a, plan.cluster, st); break;
-    case 32: e = launch_select<32>(a, plan.cluster, st); break;
-    default: e = launch_select<64>(a, plan.cluster, st); break;
-  }
+  // The selecting CTAs move the rows themselves where a unit has no more than
+  // 64 rows to move.  new_lens over kv_lens would be read by the other KV
+  // heads' CTAs: that goes by the second launch.
+  const int moves = s.cap - budget;
+  if (new_lens != s.kv_lens && moves <= 64)
+    return s.D == 128 ? launch_select_any<128>(a, plan, st) : launch_select_any<64>(a, plan, st);
+  cudaError_t e = launch_select_any<0>(a, plan, st);
   if (e != cudaSuccess) return e;
   return s.D == 128 ? launch_move<128>(a, st) : launch_move<64>(a, st);
 }
