@@ -114,10 +114,13 @@ __device__ __forceinline__ void count_if(bool in, uint32_t* bin) {   // no branc
 
 constexpr uint32_t kAlways = 0xffffffffu;   // above every weight's key
 
-// What the CTAs of a cluster tell each other about their keys.
-struct EvictRange {
-  uint32_t bad, low, high, always;   // a bad page; smallest, largest key of a weight; slots that always stay
-};
+// What warps and CTAs tell each other about their keys, (a page is bad; the
+// smallest and largest key of a weight; slots that always stay), over the warp's
+// lanes that have one.
+__device__ __forceinline__ uint4 reduce_range(uint4 v, bool has) {
+  return make_uint4(__any_sync(0xffffffffu, has && v.x != 0), __reduce_min_sync(0xffffffffu, has ? v.y : kAlways),
+                    __reduce_max_sync(0xffffffffu, has ? v.z : 0u), __reduce_add_sync(0xffffffffu, has ? v.w : 0u));
+}
 
 // kDim = 0: the moves are left to evict_move_kernel.
 template <int kKeys, int kDim>
@@ -126,7 +129,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   __shared__ __align__(16) uint32_t hist[2][256];
   __shared__ __align__(16) uint32_t total[256];            // of the cluster
   __shared__ uint4 range_warp[kSelWarps];
-  __shared__ EvictRange range[kMaxCluster];
+  __shared__ uint4 range[kMaxCluster];
+  __shared__ int4 boundary;                                // a round's (keys above the bin, keys in it, bin)
   __shared__ unsigned long long warp_tot[2][kSelWarps];
   __shared__ unsigned long long cta_tot[2][kMaxCluster];
   const PagedShape& s = a.s;
@@ -197,32 +201,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   if (bad) atomicOr(s.status, kStatusBadPage);
   {
-    const uint4 mine = make_uint4(__any_sync(0xffffffffu, bad), __reduce_min_sync(0xffffffffu, low),
-                                  __reduce_max_sync(0xffffffffu, high), __reduce_add_sync(0xffffffffu, always));
+    const uint4 mine = reduce_range(make_uint4(bad, low, high, always), true);
     if (lane == 0) range_warp[warp] = mine;
   }
   __syncthreads();
-  EvictRange all_range{0, kAlways, 0, 0};
-  auto join_range = [&](uint32_t bad_, uint32_t low_, uint32_t high_, uint32_t always_) {
-    all_range.bad |= bad_;
-    all_range.low = min(all_range.low, low_);
-    all_range.high = max(all_range.high, high_);
-    all_range.always += always_;
-  };
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) join_range(range_warp[w].x, range_warp[w].y, range_warp[w].z, range_warp[w].w);
-  if (C > 1) {
-    if (tid < C) {
-      st_dsmem_u32(dsmem_addr(&range[rank].bad, tid), all_range.bad);
-      st_dsmem_u32(dsmem_addr(&range[rank].low, tid), all_range.low);
-      st_dsmem_u32(dsmem_addr(&range[rank].high, tid), all_range.high);
-      st_dsmem_u32(dsmem_addr(&range[rank].always, tid), all_range.always);
+  if (warp == 0) {   // the CTA's, to every CTA
+    const uint4 v = range_warp[lane % kSelWarps];
+    const uint4 sum = reduce_range(v, lane < kSelWarps);
+    if (C == 1) {
+      if (lane == 0) range[0] = sum;
+    } else if (lane < C) {
+      const uint32_t to = dsmem_addr(&range[rank], lane);
+      st_dsmem_u32(to, sum.x);
+      st_dsmem_u32(to + 4, sum.y);
+      st_dsmem_u32(to + 8, sum.z);
+      st_dsmem_u32(to + 12, sum.w);
     }
-    cluster_sync();
-    all_range = EvictRange{0, kAlways, 0, 0};
-    for (int r = 0; r < C; ++r) join_range(range[r].bad, range[r].low, range[r].high, range[r].always);
   }
-  if (all_range.bad) {
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const uint4 all_range = reduce_range(range[lane < C ? lane : 0], lane < C);
+  if (all_range.x) {
     if (kDim == 0 && rank == 0 && tid == 0) a.count[unit] = -1;
     if (writes_len) a.new_lens[b] = n;
     return;
@@ -232,12 +233,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   // Keys above `at + last` stay, keys below `at` go; `match` keys are between,
   // of which the `want` largest (of equal ones the lowest slots) stay.
   uint32_t at = kAlways, last = 0;
-  int want = a.budget, match = static_cast<int>(all_range.always);
+  int want = a.budget, match = static_cast<int>(all_range.w);
   if (match < want) {
     want -= match;
-    at = all_range.low;
-    last = all_range.high - all_range.low;
-    match = n - static_cast<int>(all_range.always);
+    at = all_range.y;
+    last = all_range.z - all_range.y;
+    match = n - static_cast<int>(all_range.w);
   }
 #pragma unroll 1
   for (int round = 0; match != want && last != 0; ++round) {
@@ -268,38 +269,38 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
       __syncthreads();
     }
-    // Every warp finds the bin for itself: lane l holds bins 255 - 8 l - (0..7), largest first.
-    const uint32_t* hs = C > 1 ? total : hist[buf];
-    const uint4 hi = *reinterpret_cast<const uint4*>(hs + 252 - 8 * lane);
-    const uint4 lo = *reinterpret_cast<const uint4*>(hs + 248 - 8 * lane);
-    const int c[8] = {static_cast<int>(hi.w), static_cast<int>(hi.z), static_cast<int>(hi.y), static_cast<int>(hi.x),
-                      static_cast<int>(lo.w), static_cast<int>(lo.z), static_cast<int>(lo.y), static_cast<int>(lo.x)};
-    int sum = 0;
+    if (warp == 0) {   // lane l holds bins 255 - 8 l - (0..7), largest first
+      const uint32_t* hs = C > 1 ? total : hist[buf];
+      const uint4 hi = *reinterpret_cast<const uint4*>(hs + 252 - 8 * lane);
+      const uint4 lo = *reinterpret_cast<const uint4*>(hs + 248 - 8 * lane);
+      const int c[8] = {static_cast<int>(hi.w), static_cast<int>(hi.z), static_cast<int>(hi.y), static_cast<int>(hi.x),
+                        static_cast<int>(lo.w), static_cast<int>(lo.z), static_cast<int>(lo.y), static_cast<int>(lo.x)};
+      int sum[8];
+      sum[0] = c[0];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum += c[j];
-    const int incl = warp_inclusive_scan(sum);
-    int above = incl - sum;   // keys in larger bins
-    const int src = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
-    int bin = 0, in_bin = 0;
-    bool found = false;
+      for (int j = 1; j < 8; ++j) sum[j] = sum[j - 1] + c[j];
+      const int incl = warp_inclusive_scan(sum[7]), above = incl - sum[7];   // above: keys in larger bins
+      if (above < want && incl >= want) {
+        int j = 0;   // bins of the lane that lie above the boundary's
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!found) {
-        if (above + c[j] >= want) {
-          found = true;
-          bin = 255 - 8 * lane - j;
-          in_bin = c[j];
-        } else {
-          above += c[j];
-        }
+        for (int e = 0; e < 7; ++e) j += above + sum[e] < want ? 1 : 0;
+        int before = above, in_bin = c[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e)
+          if (e == j) {
+            before = above + sum[e - 1];
+            in_bin = c[e];
+          }
+        boundary = make_int4(before, in_bin, 255 - 8 * lane - j, 0);
       }
     }
-    want -= __shfl_sync(0xffffffffu, above, src);
-    match = __shfl_sync(0xffffffffu, in_bin, src);
-    const uint32_t skip = static_cast<uint32_t>(__shfl_sync(0xffffffffu, bin, src)) << shift;
+    __syncthreads();   // the boundary is found; hist[buf ^ 1] is zero
+    const int4 found = boundary;
+    want -= found.x;
+    match = found.y;
+    const uint32_t skip = static_cast<uint32_t>(found.z) << shift;
     at += skip;
     last = min(last - skip, (1u << shift) - 1);
-    __syncthreads();            // hist[buf ^ 1] is zero
   }
 
   // ---- which slots stay, and their numbers ------------------------------------
