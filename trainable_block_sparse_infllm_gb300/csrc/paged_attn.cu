@@ -10,19 +10,26 @@
 // the pages at the copy rate, whatever the lengths.
 //
 // Split.  The work is all 64-slot tiles of all (sequence, KV head) units, in
-// that order, each unit with a fixed cost before its tiles; the CTAs take
-// equal shares of that line, so those of any ragged batch carry the same load,
-// and one long sequence spreads over all SMs.  A unit inside one CTA is finished there; of a unit that CTA borders
-// cut, each piece leaves (m, l, sum of exp(z - m) v) in the workspace and
-// paged_join_kernel joins them.  The host needs no lengths.
+// that order, each unit with a fixed cost before its tiles.  That line is cut
+// into chunks whatever the units' borders: one equal chunk for every CTA, so
+// that those of any ragged batch carry the same load and one long sequence
+// spreads over all SMs.  SMs do not read at one rate, though (a 32 x 32K batch
+// in equal shares took the CTAs 442 to 535 us): of a long line every CTA gets
+// four fifths of its share, and the rest goes in small chunks to whoever is
+// done, from a counter.  A unit inside one chunk is finished there; of a unit
+// that borders cut, each piece leaves (m, l, sum of exp(z - m) v) in the
+// workspace, at a place that goes by the chunk and not by the CTA, and
+// paged_join_kernel joins them in the line's order.  The host needs no lengths.
 //
 // A CTA.  One warp loads: per page piece (16, 32 or 64 rows of one page) it
-// issues one TMA box per 64 columns of K and of V, through a ring of tiles.
-// Four warps (eight for 17 to 32 heads: four per half) compute, each on its
-// own 16 slots of every tile with its own running maximum and sum, so that
-// nothing but the ring's barriers is shared until the unit's end.  The heads
-// are the 16 rows of mma.m16n8k16: at these intensities the tensor pipe idles
-// and a tcgen05 tile (128 rows) would be seven eighths empty.
+// issues one TMA box per 64 columns of K and of V, through a ring of tiles; the
+// queries of a piece come with its first tile, and what a tile is (whose, which
+// rows of it hold slots, whether a piece ends) stands beside it.  Four warps
+// (eight for 17 to 32 heads: four per half) compute, each on its own 16 slots
+// of every tile with its own running maximum and sum, so that nothing but the
+// ring's barriers is shared until the piece's end.  The heads are the 16 rows
+// of mma.m16n8k16: at these intensities the tensor pipe idles and a tcgen05
+// tile (128 rows) would be seven eighths empty.
 //
 // Types.  z, maxima, sums and accumulators are fp32.  A probability feeds the
 // product with V as two 16-bit parts (hi + lo, 16 to 22 significant bits): one
@@ -39,7 +46,10 @@ namespace infllmv2 {
 
 namespace {
 
-constexpr int kTile = 64;   // slots per tile
+// Slots per tile: 32 KB of keys and values, so that a tile's fixed cost (its
+// barriers, maxima and their exchange) is shared by as many bytes at either d.
+template <int kDim>
+constexpr int kTileOf = 8192 / kDim;
 
 struct PagedAttnArgs {
   int B, Hkv, G, ps, P, maxp, cap, box;
@@ -51,59 +61,71 @@ struct PagedAttnArgs {
   void* out;
   float* lse;
   float* weights;    // null: not accumulated
-  float* part_o;     // [2 n][G][D]: pieces of cut units, relative to their m
-  float2* part_ml;   // [2 n][32]: (m in log2 units, l)
-  // Cut units, (unit or -1, CTA of the second piece, last CTA, first piece's
-  // slot).  unit_cut, by unit, is kept where there are no more units than CTAs
-  // or weights are summed; cta_cut, by the CTA that the second piece starts,
-  // where there are more units than CTAs.  The join goes by the shorter list.
+  float* part_o;     // [2 chunks][G][D]: pieces of cut units, relative to their m
+  float2* part_ml;   // [2 chunks][32]: (m in log2 units, l)
+  // Cut units, (unit or -1, chunk of the second piece, last chunk, first
+  // piece's place).  unit_cut, by unit, is kept where there are no more units
+  // than chunks or weights are summed; chunk_cut, by the chunk that the second
+  // piece starts, where there are more units.  The join goes by the shorter list.
   int4* unit_cut;
-  int4* cta_cut;
+  int4* chunk_cut;
+  int* chunks;       // number of chunks, for the join
+  int* next;         // chunks handed out beyond the CTAs' first ones; null: none are
   float* lse2;       // [B Hkv G] lse in log2 units, of units that no border cut (weights only)
   float* scores;     // [B Hkv G][cap64] z in log2 units (weights only)
-  int cap64;         // cap rounded up to whole tiles
+  int cap64;         // scores of a head: cap rounded up to whole tiles
   int whole;         // no unit is cut: one launch
+  int tile_shift;    // log2 of the slots per tile
   uint32_t* status;
 };
 
 // ---- the split of the tiles over the CTAs ----------------------------------
 
 // The units lie one after the other on a line, each `cost` positions for its
-// fixed work (queries, merge, output) and then one for every tile; empty
-// sequences take none.  CTA i has positions [i W / n, (i + 1) W / n) and the
-// tiles in them.
+// fixed work (merge, output) and then one for every tile; empty sequences take
+// none.  Chunk k < n is [k A / n, (k + 1) A / n), and the chunks behind those
+// have `small` positions each.
 struct Split {
-  long long W;           // positions
-  int n;                 // CTAs that have positions: min(CTAs, W)
+  long long W;        // positions
+  long long A;        // of them in the first n chunks
+  int n, chunks;      // n: min(CTAs, W)
+  int small;
   int cost;
-  bool whole;            // units go whole to the CTA that has their first position
-  long long begin, end;  // this CTA's positions
-  int b, h;              // the unit of the first one
-  long long unit0;       // where that unit begins
+  bool whole;         // units go whole to the chunk that has their first position
+  int b, h;           // the unit of this CTA's first chunk's first position
+  long long unit0;    // where that unit begins
 };
 
-__device__ __forceinline__ long long split_begin(const Split& s, int i) { return i * s.W / s.n; }
-// The CTA that a position belongs to.
-__device__ __forceinline__ int split_owner(const Split& s, long long at) {
-  return static_cast<int>(((at + 1) * s.n - 1) / s.W);
+__device__ __forceinline__ long long chunk_begin(const Split& s, int k) {
+  return k <= s.n ? k * s.A / s.n : min(s.W, s.A + static_cast<long long>(k - s.n) * s.small);
+}
+// The chunk that a position belongs to.
+__device__ __forceinline__ int chunk_of(const Split& s, long long at) {
+  return static_cast<int>(at < s.A ? ((at + 1) * s.n - 1) / s.A : s.n + (at - s.A) / s.small);
 }
 
-__device__ __forceinline__ int unit_tiles(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int unit_tiles(const PagedAttnArgs& a, int len) {
+  return (len + (1 << a.tile_shift) - 1) >> a.tile_shift;
+}
+
+// Positions of one unit of sequence b.
+__device__ __forceinline__ int unit_width(const PagedAttnArgs& a, int b, int cost) {
+  const int tiles = unit_tiles(a, paged_len(a.kv_lens, b, a.cap, a.status));
+  return tiles ? tiles + cost : 0;
+}
 
 // All threads of the CTA.  Each sums a run of sequences; the one whose run
-// holds the CTA's first position says where that is.
+// holds the CTA's first position says where that is.  before[t]: positions of
+// one KV head before thread t's run; before[kThreads]: of all.
 template <int kThreads>
-__device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int ctas, int cost, int* shared) {
+__device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int ctas, int cost, long long* before,
+                                            int* shared) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
-  auto width = [&](int b) {   // of one unit of sequence b
-    const int tiles = unit_tiles(paged_len(a.kv_lens, b, a.cap, a.status));
-    return tiles ? tiles + cost : 0;
-  };
-  int sum = 0;   // at most 32 sequences of 2^24 tiles (4096 sequences, 2^30 slots)
-  for (int b = b0; b < b1; ++b) sum += width(b);
+  int sum = 0;   // at most 26 sequences of 2^24 tiles (4096 sequences, 2^30 slots)
+  for (int b = b0; b < b1; ++b) sum += unit_width(a, b, cost);
   long long pre = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -113,28 +135,38 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
   long long* totals = reinterpret_cast<long long*>(shared);   // [kWarps]
   if (lane == 31) totals[warp] = pre;
   __syncthreads();
-  long long all = 0, before = 0;
+  long long all = 0, earlier = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = all;
+    if (w == warp) earlier = all;
     all += totals[w];
   }
-  pre += before - sum;   // positions of one KV head before this thread's run
+  pre += earlier - sum;
+  before[tid] = pre;
+  if (tid == 0) before[kThreads] = all;
   Split s;
   s.W = all * a.Hkv;
   s.n = static_cast<int>(min(static_cast<long long>(ctas), s.W));
   s.cost = cost;
   s.whole = a.whole != 0;
-  s.begin = s.end = s.unit0 = 0;
+  const bool shares = a.next != nullptr && s.W >= 32LL * s.n;
+  s.A = s.W;
+  s.small = 8;
+  s.chunks = s.n;
+  if (shares) {
+    s.A -= s.W / 5;
+    s.small = max(8, static_cast<int>((s.W - s.A + 6LL * s.n - 1) / (6LL * s.n)));
+    s.chunks += static_cast<int>((s.W - s.A + s.small - 1) / s.small);
+  }
   s.b = s.h = 0;
+  s.unit0 = 0;
   int* where = shared + 2 * kWarps;
   if (cta < s.n) {
-    s.begin = split_begin(s, cta);
-    s.end = split_begin(s, cta + 1);
-    if (s.begin >= pre * a.Hkv && s.begin < (pre + sum) * a.Hkv) {
-      long long rest = s.begin - pre * a.Hkv;
+    const long long begin = chunk_begin(s, cta);
+    if (begin >= pre * a.Hkv && begin < (pre + sum) * a.Hkv) {
+      long long rest = begin - pre * a.Hkv;
       for (int b = b0; b < b1; ++b) {
-        const int w = width(b);
+        const int w = unit_width(a, b, cost);
         if (rest < static_cast<long long>(w) * a.Hkv) {
           where[0] = b;
           where[1] = static_cast<int>(rest / w);
@@ -149,12 +181,38 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
   if (cta < s.n) {
     s.b = where[0];
     s.h = where[1];
-    s.unit0 = s.begin - where[2];
+    s.unit0 = chunk_begin(s, cta) - where[2];
   }
   return s;
 }
 
-// The tiles of one unit in a CTA's positions.
+// One warp: the unit of position `at`, into s.b, s.h and s.unit0.
+template <int kThreads>
+__device__ __forceinline__ void locate(Split& s, const PagedAttnArgs& a, long long at, const long long* before) {
+  const int lane = threadIdx.x & 31, run = (a.B + kThreads - 1) / kThreads;
+  int r = 0;
+  for (int r0 = 0; r0 < kThreads; r0 += 32) {   // the run of sequences that holds it
+    const bool here = before[r0 + lane] * a.Hkv <= at && at < before[r0 + lane + 1] * a.Hkv;
+    const uint32_t hit = __ballot_sync(0xffffffffu, here);
+    if (hit) {
+      r = r0 + __ffs(hit) - 1;
+      break;
+    }
+  }
+  const int b = r * run + lane;   // a run has at most 26 sequences
+  const int w = lane < run && b < a.B ? unit_width(a, b, s.cost) : 0;
+  const int upto = warp_inclusive_scan(w);
+  const long long rest = at - before[r] * a.Hkv;
+  const bool here = static_cast<long long>(upto - w) * a.Hkv <= rest && rest < static_cast<long long>(upto) * a.Hkv;
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  const int width = __shfl_sync(0xffffffffu, w, src), first = __shfl_sync(0xffffffffu, upto - w, src);
+  const long long in = rest - static_cast<long long>(first) * a.Hkv;
+  s.b = r * run + src;
+  s.h = static_cast<int>(in / width);
+  s.unit0 = at - in % width;
+}
+
+// The tiles of one unit in a chunk [begin, end).
 struct Piece {
   int b, h, len, tiles;      // the unit: its sequence, KV head, slots and tiles
   int tile0, tile1;          // the piece
@@ -163,46 +221,43 @@ struct Piece {
 
 __device__ __forceinline__ long long tile_at(const Split& s, const Piece& p, int tile) { return p.unit0 + s.cost + tile; }
 
-__device__ __forceinline__ bool next_piece(Piece& p, const Split& s, const PagedAttnArgs& a);
-
-// Both: false where the CTA's positions hold no (further) tile.
-__device__ __forceinline__ bool first_piece(Piece& p, const Split& s, const PagedAttnArgs& a) {
-  if (s.end == s.begin) return false;
-  p.b = s.b;
-  p.h = s.h;
-  p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
-  p.tiles = unit_tiles(p.len);
-  p.unit0 = s.unit0;
-  p.tile0 = max(0, static_cast<int>(s.begin - p.unit0) - s.cost);
-  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), s.end - tile_at(s, p, 0)));
-  if (s.whole) {
-    if (p.unit0 < s.begin) return next_piece(p, s, a);
-    p.tile1 = p.tiles;
-  }
-  return p.tile1 > p.tile0;
-}
-
-__device__ __forceinline__ bool next_piece(Piece& p, const Split& s, const PagedAttnArgs& a) {
+// Both: false where the chunk holds no (further) tile.
+__device__ __forceinline__ bool next_piece(Piece& p, const Split& s, const PagedAttnArgs& a, long long end) {
   p.unit0 = tile_at(s, p, p.tiles);
-  if (p.unit0 >= s.end) return false;
+  if (p.unit0 >= end) return false;
   if (++p.h == a.Hkv) {
     p.h = 0;
     do {
       ++p.b;
       p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
     } while (p.len == 0);   // positions are left, so a sequence with slots is
-    p.tiles = unit_tiles(p.len);
+    p.tiles = unit_tiles(a, p.len);
   }
   p.tile0 = 0;
-  p.tile1 = s.whole ? p.tiles : static_cast<int>(min(static_cast<long long>(p.tiles), s.end - tile_at(s, p, 0)));
+  p.tile1 = s.whole ? p.tiles : static_cast<int>(min(static_cast<long long>(p.tiles), end - tile_at(s, p, 0)));
   return p.tile1 > 0;
 }
 
-// Workspace slot of a cut unit's piece in CTA i: 2 i for a piece that starts at
-// the CTA's first position, 2 i + 1 for one that starts later (and so is its last).
-__device__ __forceinline__ int piece_slot(const Split& s, int cta, long long at) {
-  return 2 * cta + (at > split_begin(s, cta) ? 1 : 0);
+__device__ __forceinline__ bool first_piece(Piece& p, const Split& s, const PagedAttnArgs& a, long long begin,
+                                            long long end) {
+  p.b = s.b;
+  p.h = s.h;
+  p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
+  p.tiles = unit_tiles(a, p.len);
+  p.unit0 = s.unit0;
+  p.tile0 = max(0, static_cast<int>(begin - p.unit0) - s.cost);
+  p.tile1 = static_cast<int>(min(static_cast<long long>(p.tiles), end - tile_at(s, p, 0)));
+  if (s.whole) {
+    if (p.unit0 < begin) return next_piece(p, s, a, end);
+    p.tile1 = p.tiles;
+  }
+  return p.tile1 > p.tile0;
 }
+
+// Workspace place of a cut unit's piece in chunk k whose first tile is at `at`:
+// 2 k for a piece that starts the chunk, 2 k + 1 for one that starts later (and
+// so is the chunk's last).
+__device__ __forceinline__ int piece_place(int k, long long begin, long long at) { return 2 * k + (at > begin ? 1 : 0); }
 
 // ---- types ------------------------------------------------------------------
 
@@ -257,9 +312,6 @@ __device__ __forceinline__ int by_order(PagedMapOrder o, int dim, int token, int
   return o.token == dim ? token : (o.head == dim ? head : page);
 }
 
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // Adds the weights of slots `first`, + `step`, ... (four each) of a unit, from
 // the z of its heads and their lse.
@@ -297,26 +349,42 @@ __device__ __forceinline__ void add_weights(const PagedAttnArgs& a, long long un
 
 // ---- the pass over the pages -------------------------------------------------
 
-// A unit's queries, merge and output cost a CTA about as much as this many tiles.
-template <int kDim>
-constexpr int kUnitCost = kDim == 64 ? 2 : 1;
+// A unit's merge and output cost a CTA about as much as this many tiles.
+constexpr int kUnitCost = 2;
+
+// What a stage of the ring holds.
+struct __align__(16) StageInfo {
+  uint2 valid;      // rows of each 16 that hold slots, 8 bits each
+  uint32_t flags;
+  int unit;         // b * Hkv + h
+  int place;        // where the piece's sums go if the unit is cut
+  int len, tile, b;
+};
+constexpr uint32_t kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8;   // of a piece; its unit is not cut; no more tiles
 
 // kGroups: groups of four warps, one per 16 heads.  kStack: at most 8 heads,
 // the lo parts of the probabilities in rows 8..15.
 template <int kDim, int kGroups, bool kStack>
 struct AttnCfg {
-  static constexpr int kStage = kTile * kDim * 4;   // K and V of a tile
+  static constexpr int kTile = kTileOf<kDim>;
+  static constexpr int kSub = kTile / 64;               // 16-slot parts of a tile per warp
+  static constexpr int kStage = kTile * kDim * 4;       // K and V of a tile
+  static constexpr int kQRow = kDim * 2 + 16;           // a query row, so padded that 8 rows meet all banks
+  static constexpr int kQ = 16 * kGroups * kQRow;       // the queries beside it
   // Two CTAs of at most 113 KB per SM for one group, one of at most 227 KB for two.
-  static constexpr int kStages = (kGroups == 1 ? 98304 : 196608) / kStage;
+  static constexpr int kStages = (kGroups == 1 ? 98304 : 163840) / kStage;
   static constexpr int kThreads = 32 + 128 * kGroups;
   static constexpr int kPerSm = kGroups == 1 ? 2 : 1;
-  static constexpr int kCost = kUnitCost<kDim>;
-  static constexpr int kBarOff = kStages * kStage;
-  static constexpr int kInfoOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kMlOff = kInfoOff + ((kStages * 4 + 15) & ~15);
+  static constexpr int kCost = kUnitCost;
+  static constexpr int kQOff = kStages * kStage;
+  static constexpr int kInfoOff = kQOff + kStages * kQ;
+  static constexpr int kMlOff = kInfoOff + kStages * static_cast<int>(sizeof(StageInfo));
   static constexpr int kLseOff = kMlOff + kGroups * 4 * 16 * 8;      // a whole unit's lse in log2 units
-  static constexpr int kSplitOff = kLseOff + kPagedMaxGroup * 4;
-  static constexpr int kSmem = 1024 + kSplitOff + 128;
+  static constexpr int kBeforeOff = kLseOff + kPagedMaxGroup * 4;
+  static constexpr int kSplitOff = kBeforeOff + (kThreads + 1) * 8;
+  static constexpr int kBarOff = kSplitOff + 128;
+  static constexpr int kSmem = 1024 + kBarOff + (2 * kStages + kGroups + 1) * 8;
+  static_assert(kPerSm * (kSmem + 1024) <= 233472 && kSmem <= 232448, "shared memory of an SM");
 };
 
 template <bool kFp16, int kDim, int kGroups, bool kStack>
@@ -324,11 +392,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     paged_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const PagedAttnArgs a) {
   using C = AttnCfg<kDim, kGroups, kStack>;
+  constexpr int kTile = C::kTile, kSub = C::kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
-  uint32_t* info = reinterpret_cast<uint32_t*>(smem + C::kInfoOff);   // per stage: valid rows of each 16, 8 bits each
+  uint64_t* group_bar = empty + C::kStages;   // [kGroups], then one for all computing warps
+  StageInfo* info = reinterpret_cast<StageInfo*>(smem + C::kInfoOff);
+  long long* before = reinterpret_cast<long long*>(smem + C::kBeforeOff);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
@@ -337,13 +408,16 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       mbar_init(full + i, 1);
       mbar_init(empty + i, 4 * kGroups);
     }
+    for (int i = 0; i < kGroups; ++i) mbar_init(group_bar + i, 4);
+    mbar_init(group_bar + kGroups, 4 * kGroups);
     fence_barrier_init();
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
   pdl_wait();
   pdl_trigger();
-  const Split s = make_split<C::kThreads>(a, cta, ctas, C::kCost, reinterpret_cast<int*>(smem + C::kSplitOff));
+  Split s = make_split<C::kThreads>(a, cta, ctas, C::kCost, before, reinterpret_cast<int*>(smem + C::kSplitOff));
+  if (cta == 0 && tid == 0 && a.chunks) *a.chunks = s.chunks;
 
   // Empty sequences attend nothing: a zero row, lse = -inf.
   const long long heads = static_cast<long long>(a.Hkv) * a.G;
@@ -356,85 +430,133 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     if (a.unit_cut)
       for (int h = tid; h < a.Hkv; h += C::kThreads) a.unit_cut[b * a.Hkv + h] = make_int4(-1, 0, 0, 0);
   }
-  Piece p;
-  if (!first_piece(p, s, a)) {
-    if (tid == 0 && a.cta_cut) a.cta_cut[cta] = make_int4(-1, 0, 0, 0);
-    return;
-  }
+  if (cta >= s.n) return;
 
   if (warp == 4 * kGroups) {
     // ------------------------------------------------ the loading warp -------
-    if (lane == 0) {
-      // Does the previous CTA hold the first piece of the unit that starts this one?
-      const long long first = tile_at(s, p, 0);
-      const bool second = p.tile0 > 0 && split_owner(s, first) == cta - 1;
-      const int unit = p.b * a.Hkv + p.h;
-      int4 c = make_int4(-1, 0, 0, 0);
-      if (second)
-        c = make_int4(unit, cta, split_owner(s, tile_at(s, p, p.tiles - 1)), piece_slot(s, cta - 1, first));
-      if (a.cta_cut) a.cta_cut[cta] = c;
-      if (a.unit_cut && second) a.unit_cut[unit] = c;
-    }
     const int boxes = kTile / a.box;
     int stage = 0;
     uint32_t phase = 0;
     bool dead = false;
     uint32_t issued = 0;
-    do {
-      if (lane == 0 && a.unit_cut && p.tile0 == 0 && p.tile1 == p.tiles)
-        a.unit_cut[p.b * a.Hkv + p.h] = make_int4(-1, 0, 0, 0);
-      const int32_t* row = a.table + static_cast<long long>(p.b) * a.maxp;
-      // Lane i handles box i of a tile; its page is fetched one tile ahead.
-      auto fetch = [&](int tile) {
-        const int slot = tile * kTile + lane * a.box;
-        return (lane < boxes && tile < p.tile1 && slot < p.len) ? __ldg(row + slot / a.ps) : -1;
-      };
-      int page_next = fetch(p.tile0);
-      for (int t = p.tile0; t < p.tile1 && !dead; ++t) {
-        const int page = page_next;
-        page_next = fetch(t + 1);
-        const int slot = t * kTile + lane * a.box;
-        const bool ok = page >= 0 && page < a.P;
-        // The slots of an entry that names no page count as absent.
-        if (!ok && lane < boxes && slot < p.len) atomicOr(a.status, kStatusBadPage);
-        const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-        if (!mbar_wait(empty + stage, phase ^ 1, a.status)) {
-          dead = true;
-          break;
-        }
-        uint8_t* dst = smem + stage * C::kStage;
-        if (lane == 0) {
-          uint32_t v = 0;
+    int chunk = cta;
+    while (true) {
+      const long long begin = chunk_begin(s, chunk), end = chunk_begin(s, chunk + 1);
+      Piece p;
+      bool have = first_piece(p, s, a, begin, end);
+      // Does the chunk before hold the first piece of the unit that starts this one?
+      const bool later = have && p.tile0 > 0;
+      const int cut_unit = p.b * a.Hkv + p.h, cut_tiles = p.tiles;
+      const long long cut_at = tile_at(s, p, 0);
+      while (have && !dead) {
+        const int unit = p.b * a.Hkv + p.h;
+        const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
+        if (lane == 0 && a.unit_cut && whole) a.unit_cut[unit] = make_int4(-1, 0, 0, 0);
+        const int32_t* row = a.table + static_cast<long long>(p.b) * a.maxp;
+        // Lane i handles box i of a tile; its page is fetched one tile ahead.
+        auto fetch = [&](int tile) {
+          const int slot = tile * kTile + lane * a.box;
+          return (lane < boxes && tile < p.tile1 && slot < p.len) ? __ldg(row + slot / a.ps) : -1;
+        };
+        int page_next = fetch(p.tile0);
+        // The unit's queries, 16 bytes per lane and step, on their way while the
+        // first page entry is.
+        constexpr int kQSteps = kGroups * kDim / 16;
+        uint4 qv[kQSteps];
+        {
+          const uint4* q = static_cast<const uint4*>(a.q) + static_cast<long long>(unit) * a.G * (kDim / 8);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int left = p.len - (t * kTile + w * 16);
-            if ((oks >> (w * 16 / a.box)) & 1u) v |= static_cast<uint32_t>(max(0, min(16, left))) << (8 * w);
-          }
-          info[stage] = v;
-          mbar_arrive_expect_tx(full + stage, __popc(oks) * a.box * kDim * 4);
+          for (int i = 0; i < kQSteps; ++i)
+            if (i * 32 + lane < a.G * (kDim / 8)) qv[i] = __ldg(q + i * 32 + lane);
         }
-        __syncwarp();
-        if (ok) {
-          const int in_page = slot % a.ps;
-          const int k1 = by_order(a.ko, 1, in_page, p.h, page), k2 = by_order(a.ko, 2, in_page, p.h, page),
-                    k3 = by_order(a.ko, 3, in_page, p.h, page);
-          const int v1 = by_order(a.vo, 1, in_page, p.h, page), v2 = by_order(a.vo, 2, in_page, p.h, page),
-                    v3 = by_order(a.vo, 3, in_page, p.h, page);
+        const int place = piece_place(chunk, begin, tile_at(s, p, p.tile0));
+        for (int t = p.tile0; t < p.tile1; ++t) {
+          const int page = page_next;
+          page_next = fetch(t + 1);
+          const int slot = t * kTile + lane * a.box;
+          const bool ok = page >= 0 && page < a.P;
+          // The slots of an entry that names no page count as absent.
+          if (!ok && lane < boxes && slot < p.len) atomicOr(a.status, kStatusBadPage);
+          const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+          if (!mbar_wait(empty + stage, phase ^ 1, a.status)) {
+            dead = true;
+            break;
+          }
+          uint8_t* dst = smem + stage * C::kStage;
+          if (lane == 0) {
+            StageInfo x;
+            uint32_t valid[2] = {0, 0};
+            const int box_shift = 31 - __clz(a.box);
 #pragma unroll
-          for (int c = 0; c < kDim / 64; ++c) {
-            tma_load_4d(dst + c * kTile * 128 + lane * a.box * 128, &k_map, c * 64, k1, k2, k3, full + stage);
-            tma_load_4d(dst + kTile * kDim * 2 + c * kTile * 128 + lane * a.box * 128, &v_map, c * 64, v1, v2, v3,
-                        full + stage);
+            for (int w = 0; w < kTile / 16; ++w) {
+              const int left = p.len - (t * kTile + w * 16);
+              if ((oks >> (w * 16 >> box_shift)) & 1u)
+                valid[w >> 2] |= static_cast<uint32_t>(max(0, min(16, left))) << (8 * (w & 3));
+            }
+            x.valid = make_uint2(valid[0], valid[1]);
+            x.flags = (t == p.tile0 ? kFirst : 0) | (t + 1 == p.tile1 ? kLast : 0) | (whole ? kWhole : 0);
+            x.unit = unit;
+            x.place = place;
+            x.len = p.len;
+            x.tile = t;
+            x.b = p.b;
+            info[stage] = x;
+          }
+          if (t == p.tile0) {
+#pragma unroll
+            for (int i = 0; i < kQSteps; ++i) {
+              const int e = i * 32 + lane;
+              if (e < a.G * (kDim / 8))
+                *reinterpret_cast<uint4*>(smem + C::kQOff + stage * C::kQ + e / (kDim / 8) * C::kQRow +
+                                          e % (kDim / 8) * 16) = qv[i];
+            }
+          }
+          __syncwarp();   // the arrival releases what every lane has written
+          if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(oks) * a.box * kDim * 4);
+          __syncwarp();
+          if (ok) {
+            const int in_page = slot % a.ps;
+            const int k1 = by_order(a.ko, 1, in_page, p.h, page), k2 = by_order(a.ko, 2, in_page, p.h, page),
+                      k3 = by_order(a.ko, 3, in_page, p.h, page);
+            const int v1 = by_order(a.vo, 1, in_page, p.h, page), v2 = by_order(a.vo, 2, in_page, p.h, page),
+                      v3 = by_order(a.vo, 3, in_page, p.h, page);
+#pragma unroll
+            for (int c = 0; c < kDim / 64; ++c) {
+              tma_load_4d(dst + c * kTile * 128 + lane * a.box * 128, &k_map, c * 64, k1, k2, k3, full + stage);
+              tma_load_4d(dst + kTile * kDim * 2 + c * kTile * 128 + lane * a.box * 128, &v_map, c * 64, v1, v2, v3,
+                          full + stage);
+            }
+          }
+          ++issued;
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        ++issued;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        if (!dead) have = next_piece(p, s, a, end);
       }
-    } while (!dead && next_piece(p, s, a));
-    if (dead) {
+      if (lane == 0) {   // the chunk's loads are on their way: note the cut
+        int4 c = make_int4(-1, 0, 0, 0);
+        if (later && cut_at < begin && chunk_of(s, cut_at) == chunk - 1)
+          c = make_int4(cut_unit, chunk, chunk_of(s, cut_at + cut_tiles - 1),
+                        piece_place(chunk - 1, chunk_begin(s, chunk - 1), cut_at));
+        if (a.chunk_cut) a.chunk_cut[chunk] = c;
+        if (a.unit_cut && c.x >= 0) a.unit_cut[c.x] = c;
+      }
+      if (dead || s.chunks == s.n) break;
+      int next = 0;
+      if (lane == 0) next = s.n + atomicAdd(a.next, 1);
+      chunk = __shfl_sync(0xffffffffu, next, 0);
+      if (chunk >= s.chunks) break;
+      locate<C::kThreads>(s, a, chunk_begin(s, chunk), before);
+    }
+    if (!dead && !mbar_wait(empty + stage, phase ^ 1, a.status)) dead = true;
+    if (!dead) {
+      if (lane == 0) {
+        info[stage].flags = kEnd;
+        mbar_arrive(full + stage);
+      }
+    } else {
       // A wait gave up: nothing more is issued, and the copies in flight land
       // (or are waited for as long) before this warp leaves.
       const uint32_t from = issued > C::kStages ? issued - C::kStages : 0;
@@ -452,117 +574,145 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
   float* unit_lse2 = reinterpret_cast<float*>(smem + C::kLseOff);
   const bool row0 = head0 + g < a.G, row1 = !kStack && head0 + g + 8 < a.G;
   int stage = 0;
-  uint32_t phase = 0;
-  bool dead = false;
-  bool more = true;
-  while (more) {
-    const long long unit = static_cast<long long>(p.b) * a.Hkv + p.h;
-    // The group's queries as A fragments, rows beyond G zero.
-    uint32_t qf[kDim / 16][4];
-    {
-      const uint32_t* q = static_cast<const uint32_t*>(a.q) + (unit * a.G + head0) * (kDim / 2);
+  uint32_t phase = 0, group_phase = 0, all_phase = 0;
+  // Barriers of warps, bounded like every wait: a warp that gave up is missed
+  // for a while, not for ever.
+  auto sync = [&](uint64_t* bar, uint32_t& parity) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    const bool ok = mbar_wait(bar, parity, a.status);
+    parity ^= 1;
+    return ok;
+  };
+  uint32_t qf[kDim / 16][4];
+  float o[kDim / 8][4];
+  float m[2], l[2];
+
+  while (mbar_wait(full + stage, phase, a.status)) {
+    const uint4 head = *reinterpret_cast<const uint4*>(&info[stage]);   // valid, flags, unit
+    const uint32_t flags = head.z;
+    if (flags & kEnd) break;
+    if (flags & kFirst) {
+      // The group's queries as A fragments, rows beyond G zero.
+      const uint8_t* q = smem + C::kQOff + stage * C::kQ + (head0 + g) * C::kQRow + t4 * 4;
 #pragma unroll
       for (int kk = 0; kk < kDim / 16; ++kk) {
-        const int c = kk * 8 + t4;
-        qf[kk][0] = row0 ? __ldg(q + g * (kDim / 2) + c) : 0u;
-        qf[kk][1] = row1 ? __ldg(q + (g + 8) * (kDim / 2) + c) : 0u;
-        qf[kk][2] = row0 ? __ldg(q + g * (kDim / 2) + c + 4) : 0u;
-        qf[kk][3] = row1 ? __ldg(q + (g + 8) * (kDim / 2) + c + 4) : 0u;
+        qf[kk][0] = row0 ? *reinterpret_cast<const uint32_t*>(q + kk * 32) : 0u;
+        qf[kk][1] = row1 ? *reinterpret_cast<const uint32_t*>(q + 8 * C::kQRow + kk * 32) : 0u;
+        qf[kk][2] = row0 ? *reinterpret_cast<const uint32_t*>(q + kk * 32 + 16) : 0u;
+        qf[kk][3] = row1 ? *reinterpret_cast<const uint32_t*>(q + 8 * C::kQRow + kk * 32 + 16) : 0u;
       }
-    }
-    float o[kDim / 8][4];
 #pragma unroll
-    for (int i = 0; i < kDim / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    for (int t = p.tile0; t < p.tile1; ++t) {
-      if (!dead) dead = !mbar_wait(full + stage, phase, a.status);
-      const int valid = dead ? 0 : static_cast<int>((info[stage] >> (8 * w)) & 0xffu);
+      for (int i = 0; i < kDim / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+    }
+    // This warp's parts of the tile: slots (w kSub + sub) 16 .. + 15.
+    int valid[kSub];
+    bool any = false;
+#pragma unroll
+    for (int sub = 0; sub < kSub; ++sub) {
+      const int part = w * kSub + sub;
+      valid[sub] = static_cast<int>(((part < 4 ? head.x : head.y) >> (8 * (part & 3))) & 0xffu);
+      any = any || valid[sub] > 0;
+    }
+    if (any) {
       const uint32_t ks = smem_u32(smem + stage * C::kStage);
       const uint32_t vs = ks + kTile * kDim * 2;
-      if (valid > 0) {
-        if (valid < 16) {
-          // Slots past `valid` hold nothing: their probability will be 0, and
-          // their V rows, whatever the page holds there, have to read as 0.
-          for (int e = lane; e < (16 - valid) * (kDim / 8); e += 32) {
-            const int row = w * 16 + valid + e / (kDim / 8);
-            *reinterpret_cast<uint4*>(smem + stage * C::kStage + kTile * kDim * 2 +
-                                      swz128_offset(row, e % (kDim / 8), kTile)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();   // before the stage is loaded again
-          __syncwarp();
+      const int row0w = w * kSub * 16;
+      float z[kSub][2][4];
+#pragma unroll
+      for (int sub = 0; sub < kSub; ++sub) {
+        float even[2][4] = {}, odd[2][4] = {};   // two sums each: half the dependent products
+        const int row = row0w + sub * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+        for (int kk = 0; kk < kDim / 16; kk += 2) {
+          uint32_t r[4];
+          ldmatrix_x4(r, ks + swz128_offset(row, kk * 2 + ((lane >> 3) & 1), kTile));
+          mma_16816<kFp16>(even[0], qf[kk], r[0], r[1]);
+          mma_16816<kFp16>(even[1], qf[kk], r[2], r[3]);
+          ldmatrix_x4(r, ks + swz128_offset(row, kk * 2 + 2 + ((lane >> 3) & 1), kTile));
+          mma_16816<kFp16>(odd[0], qf[kk + 1], r[0], r[1]);
+          mma_16816<kFp16>(odd[1], qf[kk + 1], r[2], r[3]);
         }
-        float z[2][4];
-        {
-          float even[2][4] = {}, odd[2][4] = {};   // two sums each: half the dependent products
-          const int row = w * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-          for (int kk = 0; kk < kDim / 16; kk += 2) {
-            uint32_t r[4];
-            ldmatrix_x4(r, ks + swz128_offset(row, kk * 2 + ((lane >> 3) & 1), kTile));
-            mma_16816<kFp16>(even[0], qf[kk], r[0], r[1]);
-            mma_16816<kFp16>(even[1], qf[kk], r[2], r[3]);
-            ldmatrix_x4(r, ks + swz128_offset(row, kk * 2 + 2 + ((lane >> 3) & 1), kTile));
-            mma_16816<kFp16>(odd[0], qf[kk + 1], r[0], r[1]);
-            mma_16816<kFp16>(odd[1], qf[kk + 1], r[2], r[3]);
-          }
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int e = 0; e < 4; ++e) z[sub][j][e] = even[j][e] + odd[j][e];   // unscaled
+      }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[j][e] = even[j][e] + odd[j][e];   // unscaled
+      for (int sub = 0; sub < kSub; ++sub) {
+        if (valid[sub] == 16) continue;
+        // Slots past `valid` hold nothing: their probability is to be 0, and
+        // their V rows, whatever the page (or the stage, where no page was
+        // loaded) holds there, have to read as 0.
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j * 8 + 2 * t4 + (e & 1) >= valid[sub]) z[sub][j][e] = -INFINITY;
+        for (int e = lane; e < (16 - valid[sub]) * (kDim / 8); e += 32) {
+          const int row = row0w + sub * 16 + valid[sub] + e / (kDim / 8);
+          *reinterpret_cast<uint4*>(smem + stage * C::kStage + kTile * kDim * 2 +
+                                    swz128_offset(row, e % (kDim / 8), kTile)) = make_uint4(0, 0, 0, 0);
         }
-        if (valid < 16) {
+        fence_proxy_async_smem();   // before the stage is loaded again
+        __syncwarp();
+      }
+      if (a.weights) {
+        float* sc = a.scores + (static_cast<long long>(head.w) * a.G + head0) * a.cap64 + info[stage].tile * kTile +
+                    row0w + 2 * t4;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+        for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j * 8 + 2 * t4 + (e & 1) >= valid) z[j][e] = -INFINITY;
-        }
-        if (a.weights) {
-          float* sc = a.scores + (unit * a.G + head0) * a.cap64 + t * kTile + w * 16 + 2 * t4;
-          if (row0) {
-            float* r = sc + static_cast<long long>(g) * a.cap64;
-            *reinterpret_cast<float2*>(r) = make_float2(z[0][0] * a.scale2, z[0][1] * a.scale2);
-            *reinterpret_cast<float2*>(r + 8) = make_float2(z[1][0] * a.scale2, z[1][1] * a.scale2);
-          }
-          if (row1) {
-            float* r = sc + static_cast<long long>(g + 8) * a.cap64;
-            *reinterpret_cast<float2*>(r) = make_float2(z[0][2] * a.scale2, z[0][3] * a.scale2);
-            *reinterpret_cast<float2*>(r + 8) = make_float2(z[1][2] * a.scale2, z[1][3] * a.scale2);
-          }
-        }
-        float alpha[2];
-        float base[2];
+          for (int r = 0; r < 2; ++r)
+            if (r == 0 ? row0 : row1) {
+              float* to = sc + static_cast<long long>(g + 8 * r) * a.cap64 + sub * 16;
 #pragma unroll
-        for (int r = 0; r < (kStack ? 1 : 2); ++r) {
-          float mx = fmaxf(fmaxf(z[0][2 * r], z[0][2 * r + 1]), fmaxf(z[1][2 * r], z[1][2 * r + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx = fmaxf(mx * a.scale2, m[r]);
-          const float use = mx == -INFINITY ? 0.f : mx;
-          alpha[r] = fast_exp2(m[r] - use);
-          m[r] = mx;
-          base[r] = kFp16 ? use - 14.f : use;   // fp16: probabilities times 2^14
-        }
-        if constexpr (kStack) alpha[1] = alpha[0];
-        const bool changed = alpha[0] != 1.f || alpha[1] != 1.f;
-        if (__any_sync(0xffffffffu, changed)) {
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float2*>(to + 8 * j) =
+                    make_float2(z[sub][j][2 * r] * a.scale2, z[sub][j][2 * r + 1] * a.scale2);
+            }
+      }
+      float alpha[2];
+      float base[2];
 #pragma unroll
-          for (int i = 0; i < kDim / 8; ++i) {
-            o[i][0] *= alpha[0];
-            o[i][1] *= alpha[0];
-            o[i][2] *= alpha[1];
-            o[i][3] *= alpha[1];
-          }
+      for (int r = 0; r < (kStack ? 1 : 2); ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub)
+          mx = fmaxf(mx, fmaxf(fmaxf(z[sub][0][2 * r], z[sub][0][2 * r + 1]),
+                               fmaxf(z[sub][1][2 * r], z[sub][1][2 * r + 1])));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx = fmaxf(mx * a.scale2, m[r]);
+        const float use = mx == -INFINITY ? 0.f : mx;
+        alpha[r] = fast_exp2(m[r] - use);
+        m[r] = mx;
+        base[r] = kFp16 ? use - 14.f : use;   // fp16: probabilities times 2^14
+        l[r] *= alpha[r];
+      }
+      if constexpr (kStack) alpha[1] = alpha[0];
+      const bool changed = alpha[0] != 1.f || alpha[1] != 1.f;
+      if (__any_sync(0xffffffffu, changed)) {
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
         }
+      }
+#pragma unroll
+      for (int sub = 0; sub < kSub; ++sub) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int r = 0; r < (kStack ? 1 : 2); ++r) {
-          const float p0 = fast_exp2(fmaf(z[0][2 * r], a.scale2, -base[r]));
-          const float p1 = fast_exp2(fmaf(z[0][2 * r + 1], a.scale2, -base[r]));
-          const float p2 = fast_exp2(fmaf(z[1][2 * r], a.scale2, -base[r]));
-          const float p3 = fast_exp2(fmaf(z[1][2 * r + 1], a.scale2, -base[r]));
-          l[r] = l[r] * alpha[r] + ((p0 + p1) + (p2 + p3));
+          const float p0 = fast_exp2(fmaf(z[sub][0][2 * r], a.scale2, -base[r]));
+          const float p1 = fast_exp2(fmaf(z[sub][0][2 * r + 1], a.scale2, -base[r]));
+          const float p2 = fast_exp2(fmaf(z[sub][1][2 * r], a.scale2, -base[r]));
+          const float p3 = fast_exp2(fmaf(z[sub][1][2 * r + 1], a.scale2, -base[r]));
+          l[r] += (p0 + p1) + (p2 + p3);
           split_pair<kFp16>(p0, p1, hi[r], lo[r]);
           split_pair<kFp16>(p2, p3, hi[2 + r], lo[2 + r]);
         }
@@ -570,33 +720,32 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           hi[1] = lo[0];
           hi[3] = lo[2];
         }
-        {
-          const int row = w * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+        const int row = row0w + sub * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-          for (int dn = 0; dn < kDim / 16; ++dn) {
-            uint32_t r[4];
-            ldmatrix_x4_trans(r, vs + swz128_offset(row, dn * 2 + (lane >> 4), kTile));
-            mma_16816<kFp16>(o[2 * dn], hi, r[0], r[1]);
-            mma_16816<kFp16>(o[2 * dn + 1], hi, r[2], r[3]);
-            if constexpr (!kStack) {
-              mma_16816<kFp16>(o[2 * dn], lo, r[0], r[1]);
-              mma_16816<kFp16>(o[2 * dn + 1], lo, r[2], r[3]);
-            }
+        for (int dn = 0; dn < kDim / 16; ++dn) {
+          uint32_t r[4];
+          ldmatrix_x4_trans(r, vs + swz128_offset(row, dn * 2 + (lane >> 4), kTile));
+          mma_16816<kFp16>(o[2 * dn], hi, r[0], r[1]);
+          mma_16816<kFp16>(o[2 * dn + 1], hi, r[2], r[3]);
+          if constexpr (!kStack) {
+            mma_16816<kFp16>(o[2 * dn], lo, r[0], r[1]);
+            mma_16816<kFp16>(o[2 * dn + 1], lo, r[2], r[3]);
           }
         }
       }
-      if (t + 1 < p.tile1) {   // the piece's last stage is held: it is the merge's scratch
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + stage);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+    }
+    if (!(flags & kLast)) {   // the piece's last stage is held: it is the merge's scratch
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
       }
+      continue;
     }
 
     // ---- the four warps' partials merge in the last stage's memory ----------
-    // [4 warps][16 rows (8 stacked)][kDim] fp32, 64 kDim * 4 bytes at most: a stage.
+    // [4 warps][16 rows (8 stacked)][kDim] fp32, 256 kDim bytes at most: a stage or half of one.
     if constexpr (kStack) {
 #pragma unroll
       for (int i = 0; i < kDim / 8; ++i) {
@@ -610,11 +759,12 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (t4 == 0) ml[w * 16 + g + 8 * r] = make_float2(m[r], l[r]);
     }
-    const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
-    const int slot = piece_slot(s, cta, tile_at(s, p, p.tile0));
+    const bool whole = (flags & kWhole) != 0;
     constexpr int kRows = kStack ? 8 : 16;
     float* buf = reinterpret_cast<float*>(smem + stage * C::kStage);
-    named_sync(1 + kGroups, 128 * kGroups);   // every warp is done with the stage; ml is written
+    bool ok = sync(group_bar + kGroups, all_phase);   // every warp is done with the stage; ml is written
+    const long long unit = info[stage].unit;
+    const int place = info[stage].place;
 #pragma unroll
     for (int turn = 0; turn < kGroups; ++turn) {
       if (turn == group) {
@@ -632,20 +782,20 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
             *reinterpret_cast<float2*>(to + ((i * 8 + 2 * t4) ^ ((row & 3) << 3))) =
                 make_float2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
         }
-        named_sync(1 + group, 128);
+        ok = sync(group_bar + group, group_phase) && ok;
         const int gt = tid - group * 128;
         const int rows = min(kRows, a.G - head0);
         for (int e = gt; e < rows * (kDim / 4); e += 128) {
           const int row = e / (kDim / 4), c = (e % (kDim / 4)) * 4;
           const float* from = buf + row * kDim + (c ^ ((row & 3) << 3));
-          float4 x = *reinterpret_cast<const float4*>(from);
+          float4 y = *reinterpret_cast<const float4*>(from);
 #pragma unroll
           for (int i = 1; i < 4; ++i) {
-            const float4 y = *reinterpret_cast<const float4*>(from + i * kRows * kDim);
-            x.x += y.x;
-            x.y += y.y;
-            x.z += y.z;
-            x.w += y.w;
+            const float4 z = *reinterpret_cast<const float4*>(from + i * kRows * kDim);
+            y.x += z.x;
+            y.y += z.y;
+            y.z += z.z;
+            y.w += z.w;
           }
           float mx = fmaxf(fmaxf(ml[row].x, ml[16 + row].x), fmaxf(ml[32 + row].x, ml[48 + row].x));
           const float use = mx == -INFINITY ? 0.f : mx;
@@ -655,10 +805,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           const long long head = unit * a.G + head0 + row;
           if (whole) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            uint2 y;
-            y.x = pack_pair<kFp16>(x.x * inv, x.y * inv);
-            y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + c) = y;
+            uint2 z;
+            z.x = pack_pair<kFp16>(y.x * inv, y.y * inv);
+            z.y = pack_pair<kFp16>(y.z * inv, y.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + c) = z;
             if (c == 0) {
               // fp16 probabilities, and so the sum, carry a factor 2^14.
               const float lse2 = use + log2f(sum) - (kFp16 ? 14.f : 0.f);
@@ -669,24 +819,26 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
                 a.lse2[head] = lse2;
             }
           } else {
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * a.G + head0 + row) * kDim + c) = x;
-            if (c == 0) a.part_ml[slot * kPagedMaxGroup + head0 + row] = make_float2(mx, sum);
+            *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(place) * a.G + head0 + row) * kDim + c) = y;
+            if (c == 0) a.part_ml[place * kPagedMaxGroup + head0 + row] = make_float2(mx, sum);
           }
         }
         fence_proxy_async_smem();   // the next tile lands here through the async proxy
       }
-      if (kGroups > 1) named_sync(1 + kGroups, 128 * kGroups);
+      if (kGroups > 1) ok = sync(group_bar + kGroups, all_phase) && ok;
     }
-    if (kGroups == 1) named_sync(1 + group, 128);   // ml is read before the next piece writes it
+    if (kGroups == 1) ok = sync(group_bar + group, group_phase) && ok;   // ml is read before the next piece writes it
     // (The barrier also orders the z that every warp has stored and the lse.)
     if (a.whole && a.weights)
-      add_weights(a, unit, p.b, p.h, p.len, 4 * tid, 4 * 128 * kGroups, unit_lse2);
+      add_weights(a, unit, info[stage].b, info[stage].unit - info[stage].b * a.Hkv, info[stage].len, 4 * tid,
+                  4 * 128 * kGroups, unit_lse2);
+    if (!ok) break;
+    __syncwarp();
     if (lane == 0) mbar_arrive(empty + stage);
     if (++stage == C::kStages) {
       stage = 0;
       phase ^= 1;
     }
-    more = next_piece(p, s, a);
   }
 }
 
@@ -710,12 +862,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= jobs) {
     const int per_cut = (a.G + hp - 1) / hp, job = blockIdx.x - jobs;
-    const int4 c = (a.cta_cut ? a.cta_cut : a.unit_cut)[job / per_cut];
+    if (a.chunk_cut && job / per_cut >= *a.chunks) return;
+    const int4 c = (a.chunk_cut ? a.chunk_cut : a.unit_cut)[job / per_cut];
     if (c.x < 0) return;
     const int warps = 8 / hp, warp0 = warp / warps * warps;   // a head's warps
     const int h = job % per_cut * hp + warp / warps;
     const int i = c.y, t = tid - warp0 * 32;
-    // CTAs i - 1 .. c.z hold a piece; a head past the last one joins none.
+    // Chunks i - 1 .. c.z hold a piece; a head past the last one joins none.
     const int pieces = h < a.G ? c.z - i + 2 : 0;
     auto slot_of = [&](int j) { return j == 0 ? c.w : 2 * (i - 1 + j); };
     float mx = -INFINITY;
@@ -844,6 +997,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
   add_weights(a, unit, b, kv_head, len, y * kChunk + 4 * tid, step * kChunk, unit_lse2);
 }
 
+// The count of chunks handed out starts at 0.
+__global__ void paged_counter_kernel(int* next) {
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) *next = 0;
+}
+
 // ---- host side -------------------------------------------------------------------
 
 // Caches of up to this many slots are attended without cuts, in one launch.  Two
@@ -852,30 +1012,48 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
 // 12.1 against 10.1 and 8.5 us.
 constexpr int kWholeCap = 256;
 
+int unit_tiles_of(const PagedShape& s) {
+  const int tile = s.D == 64 ? kTileOf<64> : kTileOf<128>;
+  return (s.cap + tile - 1) / tile;
+}
+
 int attn_ctas(const PagedShape& s, int G) {
-  const int cost = s.D == 64 ? kUnitCost<64> : kUnitCost<128>;
-  const long long positions = static_cast<long long>(s.B) * s.Hkv * ((s.cap + kTile - 1) / kTile + cost);
+  const long long positions = static_cast<long long>(s.B) * s.Hkv * (unit_tiles_of(s) + kUnitCost);
   const long long most = static_cast<long long>(device_sm_count()) * (G > 16 ? 1 : 2);
   return static_cast<int>(positions < most ? positions : most);
 }
 
+// Scores of a head: the capacity in whole tiles.
+size_t score_row(const PagedShape& s) {
+  return static_cast<size_t>(unit_tiles_of(s)) * (s.D == 64 ? kTileOf<64> : kTileOf<128>);
+}
+
+// Small chunks are handed out where the line is long enough for the SMs' rates
+// to matter: 128 tiles of the capacity for every CTA.
+bool hands_out(const PagedShape& s, int ctas) {
+  return static_cast<long long>(s.B) * s.Hkv * unit_tiles_of(s) >= 128LL * ctas;
+}
+
+// Chunks at most: see make_split.
+int most_chunks(const PagedShape& s, int ctas) { return hands_out(s, ctas) ? 7 * ctas : ctas; }
+
 struct WsLayout {
-  size_t unit_cut, cta_cut, ml, o, lse2, scores, total;
+  size_t counts, unit_cut, chunk_cut, ml, o, lse2, scores, total;
 };
 
 WsLayout ws_layout(const PagedShape& s, int G) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t n = attn_ctas(s, G), heads = static_cast<size_t>(s.B) * s.Hkv * G;
-  const size_t cap64 = static_cast<size_t>((s.cap + kTile - 1) / kTile) * kTile;
+  const size_t n = most_chunks(s, attn_ctas(s, G)), units = static_cast<size_t>(s.B) * s.Hkv, heads = units * G;
+  const size_t row = score_row(s);
   WsLayout w;
-  const size_t units = static_cast<size_t>(s.B) * s.Hkv;
-  w.unit_cut = 0;
-  w.cta_cut = up(units * sizeof(int4));
-  w.ml = w.cta_cut + up(n * sizeof(int4));
+  w.counts = 0;
+  w.unit_cut = 256;
+  w.chunk_cut = w.unit_cut + up(units * sizeof(int4));
+  w.ml = w.chunk_cut + up(n * sizeof(int4));
   w.o = w.ml + up(2 * n * kPagedMaxGroup * sizeof(float2));
   w.lse2 = w.o + up(2 * n * G * s.D * sizeof(float));
   w.scores = w.lse2 + (s.weights ? up(heads * sizeof(float)) : 0);
-  w.total = w.scores + (s.weights ? up(heads * cap64 * sizeof(float)) : 0);
+  w.total = w.scores + (s.weights ? up(heads * row * sizeof(float)) : 0);
   return w;
 }
 
@@ -904,7 +1082,8 @@ cudaError_t launch_pdl(F kernel, dim3 grid, int threads, size_t smem, cudaStream
 }
 
 template <bool kFp16, int kDim, int kGroups, bool kStack>
-cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, int most,
+                   cudaStream_t st) {
   using C = AttnCfg<kDim, kGroups, kStack>;
   auto kernel = paged_attn_kernel<kFp16, kDim, kGroups, kStack>;
   static std::atomic<uint64_t> allowed{0};   // devices whose copy of the kernel has the attribute
@@ -916,12 +1095,16 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
+  if (a.next) {
+    e = launch_pdl(paged_counter_kernel, dim3(1), 32, 0, st, a.next);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(kernel, dim3(ctas), C::kThreads, C::kSmem, st, km, vm, a);
   if (e != cudaSuccess || a.whole) return e;
   const int jobs = a.weights ? weight_jobs(a) : 0;
   // One CTA per head of a cut unit while that fills no more than the SMs twice
   // (a long sequence's unit has hundreds of pieces), else up to 8 heads each.
-  const int cuts = a.cta_cut ? ctas : a.B * a.Hkv;
+  const int cuts = a.chunk_cut ? most : a.B * a.Hkv;
   int hp = 1;
   while (hp < 8 && cuts * ((a.G + hp - 1) / hp) > 2 * device_sm_count()) hp *= 2;
   return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(static_cast<unsigned>(jobs + cuts * ((a.G + hp - 1) / hp))),
@@ -929,10 +1112,11 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
 }
 
 template <bool kFp16, int kDim>
-cudaError_t launch_g(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, cudaStream_t st) {
-  if (a.G > 16) return launch<kFp16, kDim, 2, false>(km, vm, a, ctas, st);
-  if (a.G > 8) return launch<kFp16, kDim, 1, false>(km, vm, a, ctas, st);
-  return launch<kFp16, kDim, 1, true>(km, vm, a, ctas, st);
+cudaError_t launch_g(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, int most,
+                     cudaStream_t st) {
+  if (a.G > 16) return launch<kFp16, kDim, 2, false>(km, vm, a, ctas, most, st);
+  if (a.G > 8) return launch<kFp16, kDim, 1, false>(km, vm, a, ctas, most, st);
+  return launch<kFp16, kDim, 1, true>(km, vm, a, ctas, most, st);
 }
 
 }  // namespace
@@ -966,17 +1150,22 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.lse2 = reinterpret_cast<float*>(base + w.lse2);
   a.scores = reinterpret_cast<float*>(base + w.scores);
-  a.cap64 = (s.cap + kTile - 1) / kTile * kTile;
+  a.cap64 = static_cast<int>(score_row(s));
+  a.tile_shift = s.D == 64 ? 7 : 6;
+  static_assert(kTileOf<64> == 128 && kTileOf<128> == 64, "tile_shift");
   a.status = s.status;
-  const int ctas = attn_ctas(s, G);
-  const bool by_unit = s.B * s.Hkv <= ctas;
-  // Short caches are not cut: see kWholeCap.
-  a.whole = s.cap <= kWholeCap;
-  a.unit_cut = a.whole ? nullptr : by_unit || accumulate ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
-  a.cta_cut = a.whole || by_unit ? nullptr : reinterpret_cast<int4*>(base + w.cta_cut);
+  const int ctas = attn_ctas(s, G), most = most_chunks(s, ctas);
+  const bool by_unit = s.B * s.Hkv <= most;
+  a.whole = s.cap <= kWholeCap;   // then nothing is cut and nothing joined
+  a.unit_cut = !a.whole && (by_unit || accumulate) ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
+  a.chunk_cut = !a.whole && !by_unit ? reinterpret_cast<int4*>(base + w.chunk_cut) : nullptr;
+  a.chunks = a.whole ? nullptr : reinterpret_cast<int*>(base + w.counts);
+  a.next = !a.whole && hands_out(s, ctas) ? reinterpret_cast<int*>(base + w.counts) + 1 : nullptr;
   if (s.fp16)
-    return s.D == 128 ? launch_g<true, 128>(k_map, v_map, a, ctas, st) : launch_g<true, 64>(k_map, v_map, a, ctas, st);
-  return s.D == 128 ? launch_g<false, 128>(k_map, v_map, a, ctas, st) : launch_g<false, 64>(k_map, v_map, a, ctas, st);
+    return s.D == 128 ? launch_g<true, 128>(k_map, v_map, a, ctas, most, st)
+                      : launch_g<true, 64>(k_map, v_map, a, ctas, most, st);
+  return s.D == 128 ? launch_g<false, 128>(k_map, v_map, a, ctas, most, st)
+                    : launch_g<false, 64>(k_map, v_map, a, ctas, most, st);
 }
 
 }  // namespace infllmv2
