@@ -871,23 +871,28 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
     // Chunks i - 1 .. c.z hold a piece; a head past the last one joins none.
     const int pieces = h < a.G ? c.z - i + 2 : 0;
     auto slot_of = [&](int j) { return j == 0 ? c.w : 2 * (i - 1 + j); };
-    float mx = -INFINITY;
-    for (int j = t; j < pieces; j += warps * 32) mx = fmaxf(mx, a.part_ml[slot_of(j) * kPagedMaxGroup + h].x);
-    mx = warp_max(mx);
-    if (lane == 0) red_m[warp] = mx;
-    __syncthreads();
-    for (int j = 0; j < warps; ++j) mx = fmaxf(mx, red_m[warp0 + j]);
-    const float use = mx == -INFINITY ? 0.f : mx;
     constexpr int kLanes = kDim / 4;            // threads of a row
     const int par = warps * 32 / kLanes;        // rows at once
     const int col = t % kLanes, part = t / kLanes;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int j0 = part; j0 < pieces; j0 += 4 * par) {   // 4 rows in flight
-      float2 v[4];
-      float4 y[4];
+    float mx = -INFINITY, sum = 0.f;
+    // Merges a sum relative to 2^m2 into (mx, sum, x).
+    auto merge = [&](float m2, float s2, float4 x2) {
+      const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
+      const float f = fast_exp2(mx - use), f2 = fast_exp2(m2 - use);
+      mx = nm;
+      sum = sum * f + s2 * f2;
+      x.x = x.x * f + x2.x * f2;
+      x.y = x.y * f + x2.y * f2;
+      x.z = x.z * f + x2.z * f2;
+      x.w = x.w * f + x2.w * f2;
+    };
+    constexpr int kAhead = 8;   // rows in flight
+    for (int j0 = part; j0 < pieces; j0 += kAhead * par) {
+      float2 v[kAhead];
+      float4 y[kAhead];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kAhead; ++e) {
         const int j = j0 + e * par;
         v[e] = make_float2(-INFINITY, 0.f);
         y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -898,36 +903,23 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float f = fast_exp2(v[e].x - use);
-        sum += v[e].y * f;
-        x.x += y[e].x * f;
-        x.y += y[e].y * f;
-        x.z += y[e].z * f;
-        x.w += y[e].w * f;
-      }
+      for (int e = 0; e < kAhead; ++e) merge(v[e].x, v[e].y, y[e]);
     }
     if constexpr (kLanes == 16) {   // two rows per warp
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      x.x += __shfl_xor_sync(0xffffffffu, x.x, 16);
-      x.y += __shfl_xor_sync(0xffffffffu, x.y, 16);
-      x.z += __shfl_xor_sync(0xffffffffu, x.z, 16);
-      x.w += __shfl_xor_sync(0xffffffffu, x.w, 16);
+      const float m2 = __shfl_xor_sync(0xffffffffu, mx, 16), s2 = __shfl_xor_sync(0xffffffffu, sum, 16);
+      const float4 x2 = make_float4(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16),
+                                    __shfl_xor_sync(0xffffffffu, x.z, 16), __shfl_xor_sync(0xffffffffu, x.w, 16));
+      merge(m2, s2, x2);
     }
     if (lane < kLanes) red_o[warp][lane] = x;
-    if (lane == 0) red_l[warp] = sum;
+    if (lane == 0) {
+      red_m[warp] = mx;
+      red_l[warp] = sum;
+    }
     __syncthreads();
     if (t < kLanes && h < a.G) {
-      sum = 0.f;
-      x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j = warp0; j < warp0 + warps; ++j) {
-        const float4 y = red_o[j][t];
-        sum += red_l[j];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-      }
+      for (int j = warp0 + 1; j < warp0 + warps; ++j) merge(red_m[j], red_l[j], red_o[j][t]);
+      const float use = mx == -INFINITY ? 0.f : mx;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long head = static_cast<long long>(c.x) * a.G + h;
       uint2 y;
