@@ -48,8 +48,8 @@ namespace {
 
 // Slots per tile: 32 KB of keys and values, so that a tile's fixed cost (its
 // barriers, maxima and their exchange) is shared by as many bytes at either d.
-template <int kDim>
-constexpr int kTileOf = 8192 / kDim;
+template <int kDim, int kGroups>
+constexpr int kTileOf = kGroups == 2 ? 128 : 8192 / kDim;
 
 struct PagedAttnArgs {
   int B, Hkv, G, ps, P, maxp, cap, box;
@@ -366,13 +366,13 @@ constexpr uint32_t kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8;   // of a piece;
 // the lo parts of the probabilities in rows 8..15.
 template <int kDim, int kGroups, bool kStack>
 struct AttnCfg {
-  static constexpr int kTile = kTileOf<kDim>;
+  static constexpr int kTile = kTileOf<kDim, kGroups>;
   static constexpr int kSub = kTile / 64;               // 16-slot parts of a tile per warp
   static constexpr int kStage = kTile * kDim * 4;       // K and V of a tile
   static constexpr int kQRow = kDim * 2 + 16;           // a query row, so padded that 8 rows meet all banks
   static constexpr int kQ = 16 * kGroups * kQRow;       // the queries beside it
   // Two CTAs of at most 113 KB per SM for one group, one of at most 227 KB for two.
-  static constexpr int kStages = (kGroups == 1 ? 98304 : 163840) / kStage;
+  static constexpr int kStages = (kGroups == 1 ? 98304 : 196608) / kStage;
   static constexpr int kThreads = 32 + 128 * kGroups;
   static constexpr int kPerSm = kGroups == 1 ? 2 : 1;
   static constexpr int kCost = kUnitCost;
@@ -1004,30 +1004,35 @@ __global__ void paged_counter_kernel(int* next) {
 // 12.1 against 10.1 and 8.5 us.
 constexpr int kWholeCap = 256;
 
-int unit_tiles_of(const PagedShape& s) {
-  const int tile = s.D == 64 ? kTileOf<64> : kTileOf<128>;
-  return (s.cap + tile - 1) / tile;
+int tile_shift_of(const PagedShape& s, int G) {
+  static_assert(kTileOf<128, 1> == 64 && kTileOf<64, 1> == 128 && kTileOf<128, 2> == 128 && kTileOf<64, 2> == 128, "");
+  return s.D == 128 && G <= 16 ? 6 : 7;
+}
+
+int unit_tiles_of(const PagedShape& s, int G) {
+  const int shift = tile_shift_of(s, G);
+  return (s.cap + (1 << shift) - 1) >> shift;
 }
 
 int attn_ctas(const PagedShape& s, int G) {
-  const long long positions = static_cast<long long>(s.B) * s.Hkv * (unit_tiles_of(s) + kUnitCost);
+  const long long positions = static_cast<long long>(s.B) * s.Hkv * (unit_tiles_of(s, G) + kUnitCost);
   const long long most = static_cast<long long>(device_sm_count()) * (G > 16 ? 1 : 2);
   return static_cast<int>(positions < most ? positions : most);
 }
 
 // Scores of a head: the capacity in whole tiles.
-size_t score_row(const PagedShape& s) {
-  return static_cast<size_t>(unit_tiles_of(s)) * (s.D == 64 ? kTileOf<64> : kTileOf<128>);
+size_t score_row(const PagedShape& s, int G) {
+  return static_cast<size_t>(unit_tiles_of(s, G)) << tile_shift_of(s, G);
 }
 
 // Small chunks are handed out where the line is long enough for the SMs' rates
 // to matter: 128 tiles of the capacity for every CTA.
-bool hands_out(const PagedShape& s, int ctas) {
-  return static_cast<long long>(s.B) * s.Hkv * unit_tiles_of(s) >= 128LL * ctas;
+bool hands_out(const PagedShape& s, int G, int ctas) {
+  return static_cast<long long>(s.B) * s.Hkv * unit_tiles_of(s, G) >= 128LL * ctas;
 }
 
 // Chunks at most: see make_split.
-int most_chunks(const PagedShape& s, int ctas) { return hands_out(s, ctas) ? 7 * ctas : ctas; }
+int most_chunks(const PagedShape& s, int G, int ctas) { return hands_out(s, G, ctas) ? 7 * ctas : ctas; }
 
 struct WsLayout {
   size_t counts, unit_cut, chunk_cut, ml, o, lse2, scores, total;
@@ -1035,8 +1040,8 @@ struct WsLayout {
 
 WsLayout ws_layout(const PagedShape& s, int G) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t n = most_chunks(s, attn_ctas(s, G)), units = static_cast<size_t>(s.B) * s.Hkv, heads = units * G;
-  const size_t row = score_row(s);
+  const size_t n = most_chunks(s, G, attn_ctas(s, G)), units = static_cast<size_t>(s.B) * s.Hkv, heads = units * G;
+  const size_t row = score_row(s, G);
   WsLayout w;
   w.counts = 0;
   w.unit_cut = 256;
@@ -1142,17 +1147,16 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.lse2 = reinterpret_cast<float*>(base + w.lse2);
   a.scores = reinterpret_cast<float*>(base + w.scores);
-  a.cap64 = static_cast<int>(score_row(s));
-  a.tile_shift = s.D == 64 ? 7 : 6;
-  static_assert(kTileOf<64> == 128 && kTileOf<128> == 64, "tile_shift");
+  a.cap64 = static_cast<int>(score_row(s, G));
+  a.tile_shift = tile_shift_of(s, G);
   a.status = s.status;
-  const int ctas = attn_ctas(s, G), most = most_chunks(s, ctas);
+  const int ctas = attn_ctas(s, G), most = most_chunks(s, G, ctas);
   const bool by_unit = s.B * s.Hkv <= most;
   a.whole = s.cap <= kWholeCap;   // then nothing is cut and nothing joined
   a.unit_cut = !a.whole && (by_unit || accumulate) ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
   a.chunk_cut = !a.whole && !by_unit ? reinterpret_cast<int4*>(base + w.chunk_cut) : nullptr;
   a.chunks = a.whole ? nullptr : reinterpret_cast<int*>(base + w.counts);
-  a.next = !a.whole && hands_out(s, ctas) ? reinterpret_cast<int*>(base + w.counts) + 1 : nullptr;
+  a.next = !a.whole && hands_out(s, G, ctas) ? reinterpret_cast<int*>(base + w.counts) + 1 : nullptr;
   if (s.fp16)
     return s.D == 128 ? launch_g<true, 128>(k_map, v_map, a, ctas, most, st)
                       : launch_g<true, 64>(k_map, v_map, a, ctas, most, st);

@@ -26,6 +26,9 @@ from ._lib import InfLLMv2Error
 
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16}
 _Strides = ctypes.c_int64 * 6
+_append = _lib.lib.infllmv2_paged_append_kv
+_attn = _lib.lib.infllmv2_paged_attn_decode
+_evict = _lib.lib.infllmv2_paged_evict
 
 
 def _bad(message: str):
@@ -62,6 +65,7 @@ class PagedCache:
                 raise _bad(f"{name} must be contiguous {dtype} [num_pages, n_kv_heads, page_size] on the pages' device")
         self.k_pages, self.v_pages, self.weights, self.positions = k_pages, v_pages, weights, positions
         self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self.scale = self.head_dim ** -0.5
         self.dtype, self.device, self.index = k_pages.dtype, k_pages.device, k_pages.get_device()
         self.struct = _lib.PagedCacheStruct(
             dtype=_DTYPES[k_pages.dtype], n_kv_heads=self.n_kv_heads, head_dim=self.head_dim,
@@ -74,33 +78,35 @@ class PagedCache:
         self._ref = ctypes.byref(self.struct)
 
 
+# Each call's arguments are looked at in one expression; only where it fails do
+# the functions named _refuse_* find out what is wrong.  get_device() is a
+# tensor's device index without a device object around it, -1 on the CPU.
+
 def _stream(cache: PagedCache, stream) -> int:
     """The stream's handle; the launch goes to the current device, which must hold the pages."""
-    index = cache.index
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != cache.index:
         raise _bad(f"the cache lives on {cache.device}, which is not the current CUDA device")
     if stream is None:
         # The current stream's handle without the Stream object around it (0.1 us instead of 3).
-        return torch._C._cuda_getCurrentRawStream(index)
+        return torch._C._cuda_getCurrentRawStream(cache.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# get_device() is the device's index without a device object around it, -1 on the CPU.
-
-def _ints(cache: PagedCache, t: torch.Tensor | None, batch: int, name: str):
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != batch or not t.is_contiguous() or \
-            t.get_device() != cache.index:
-        raise _bad(f"{name} must be contiguous int32 [{batch}] on {cache.device}")
-    return t.data_ptr()
-
-
-def _table(cache: PagedCache, t: torch.Tensor):
+def _refuse_table(cache: PagedCache, page_table: torch.Tensor, **ints: torch.Tensor | None) -> None:
+    t = page_table
     if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != cache.index:
         raise _bad(f"page_table must be contiguous int32 [batch, max_pages] on {cache.device}")
-    batch, max_pages = t.shape
-    return batch, max_pages, t.data_ptr()
+    for name, t in ints.items():
+        if t is None and name in ("n_new", "seq_lens"):
+            continue
+        if t is None or t.dtype is not torch.int32 or t.shape != page_table.shape[:1] or not t.is_contiguous() or \
+                t.get_device() != cache.index:
+            raise _bad(f"{name} must be contiguous int32 [{page_table.shape[0]}] on {cache.device}")
+
+
+def _optional_ints(cache: PagedCache, t: torch.Tensor | None, batch: int) -> bool:
+    return t is None or (t.dtype is torch.int32 and t.dim() == 1 and t.numel() == batch and t.is_contiguous() and
+                         t.get_device() == cache.index)
 
 
 def _workspace(cache: PagedCache, workspace: torch.Tensor | None):
@@ -132,22 +138,32 @@ def paged_append_kv(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     ``seq_lens``, the tokens each sequence has seen (default: kv_lens).  Any
     strides with consecutive values; pinned host tensors are accepted.
     """
-    batch, max_pages, table = _table(cache, page_table)
-    shape = k_new.shape
+    index, dtype, shape = cache.index, cache.dtype, k_new.shape
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous() or \
+            page_table.get_device() != index:
+        _refuse_table(cache, page_table)
+    batch, max_pages = page_table.shape
+    if not (kv_lens.dtype is torch.int32 and kv_lens.dim() == 1 and kv_lens.numel() == batch and
+            kv_lens.is_contiguous() and kv_lens.get_device() == index and _optional_ints(cache, n_new, batch) and
+            _optional_ints(cache, seq_lens, batch)):
+        _refuse_table(cache, page_table, kv_lens=kv_lens, n_new=n_new, seq_lens=seq_lens)
     if len(shape) != 4 or shape != v_new.shape or shape[0] != batch or shape[1] != cache.n_kv_heads or \
             shape[3] != cache.head_dim:
         raise _bad("k_new and v_new must be [batch, n_kv_heads, n_q, head_dim]")
     kb, kh, kt, kd = k_new.stride()
     vb, vh, vt, vd = v_new.stride()
-    for t, unit in ((k_new, kd), (v_new, vd)):
-        if t.dtype is not cache.dtype or unit != 1:
-            raise _bad("k_new and v_new must have the cache's type and rows of consecutive values")
-        if t.get_device() != cache.index and (t.is_cuda or not t.is_pinned()):
-            raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
-    _lib.check(_lib.lib.infllmv2_paged_append_kv(
-        cache._ref, batch, max_pages, shape[2], k_new.data_ptr(), v_new.data_ptr(), _Strides(kb, kh, kt, vb, vh, vt), table,
-        _ints(cache, kv_lens, batch, "kv_lens"), _ints(cache, n_new, batch, "n_new"),
-        _ints(cache, seq_lens, batch, "seq_lens"), _stream(cache, stream)))
+    if k_new.dtype is not dtype or v_new.dtype is not dtype or kd != 1 or vd != 1:
+        raise _bad("k_new and v_new must have the cache's type and rows of consecutive values")
+    if k_new.get_device() != index or v_new.get_device() != index:
+        for t in (k_new, v_new):
+            if t.get_device() != index and (t.is_cuda or not t.is_pinned()):
+                raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
+    rc = _append(cache._ref, batch, max_pages, shape[2], k_new.data_ptr(), v_new.data_ptr(),
+                 _Strides(kb, kh, kt, vb, vh, vt), page_table.data_ptr(), kv_lens.data_ptr(),
+                 None if n_new is None else n_new.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
+                 _stream(cache, stream))
+    if rc:
+        _lib.check(rc)
     return cache
 
 
@@ -160,25 +176,30 @@ def paged_attn_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tens
     1 / sqrt(head_dim).  ``accumulate``: add each slot's attention weight,
     summed over the group's heads, to the cache's weights.
     """
-    batch, max_pages, table = _table(cache, page_table)
-    shape = q.shape
+    index, dtype, shape = cache.index, cache.dtype, q.shape
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous() or \
+            page_table.get_device() != index:
+        _refuse_table(cache, page_table)
+    batch, max_pages = page_table.shape
+    if not (kv_lens.dtype is torch.int32 and kv_lens.dim() == 1 and kv_lens.numel() == batch and
+            kv_lens.is_contiguous() and kv_lens.get_device() == index):
+        _refuse_table(cache, page_table, kv_lens=kv_lens)
     heads = shape[2] if len(shape) == 4 else 0
     if heads == 0 or shape[0] != batch or shape[1] != 1 or shape[3] != cache.head_dim or heads % cache.n_kv_heads != 0:
         raise _bad("q must be [batch, 1, n_kv_heads * group, head_dim]")
-    if out.shape != shape:
-        raise _bad("out must have q's shape")
-    for t in (q, out):
-        if t.dtype is not cache.dtype or t.get_device() != cache.index or not t.is_contiguous():
-            raise _bad("q and out must be contiguous, of the cache's type and on its device")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (batch, 1, heads) or
-                            lse.get_device() != cache.index or not lse.is_contiguous()):
+    if out.shape != shape or q.dtype is not dtype or out.dtype is not dtype or q.get_device() != index or \
+            out.get_device() != index or not q.is_contiguous() or not out.is_contiguous():
+        raise _bad("q and out must have one shape, be contiguous, of the cache's type and on its device")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.dim() != 3 or lse.numel() != batch * heads or
+                            lse.shape[0] != batch or lse.shape[2] != heads or lse.get_device() != index or
+                            not lse.is_contiguous()):
         raise _bad("lse must be contiguous fp32 [batch, 1, heads] on the cache's device")
     ws, ws_bytes = _workspace(cache, workspace)
-    _lib.check(_lib.lib.infllmv2_paged_attn_decode(
-        cache._ref, batch, max_pages, heads // cache.n_kv_heads, q.data_ptr(), table,
-        _ints(cache, kv_lens, batch, "kv_lens"), cache.head_dim ** -0.5 if scale is None else scale,
-        1 if accumulate else 0, out.data_ptr(), lse.data_ptr() if lse is not None else None, ws, ws_bytes,
-        _stream(cache, stream)))
+    rc = _attn(cache._ref, batch, max_pages, heads // cache.n_kv_heads, q.data_ptr(), page_table.data_ptr(),
+               kv_lens.data_ptr(), cache.scale if scale is None else scale, 1 if accumulate else 0, out.data_ptr(),
+               None if lse is None else lse.data_ptr(), ws, ws_bytes, _stream(cache, stream))
+    if rc:
+        _lib.check(rc)
     return out, lse
 
 
@@ -190,12 +211,19 @@ def paged_evict(cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tens
     The first ``n_init`` and newest ``n_local`` positions always stay.
     ``new_lens`` (int32 [batch], may be kv_lens) receives the lengths after it.
     """
-    batch, max_pages, table = _table(cache, page_table)
-    if new_lens is None:
-        raise _bad("new_lens is required")
+    index = cache.index
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous() or \
+            page_table.get_device() != index:
+        _refuse_table(cache, page_table)
+    batch, max_pages = page_table.shape
+    if kv_lens is None or new_lens is None or not (
+            _optional_ints(cache, kv_lens, batch) and _optional_ints(cache, new_lens, batch) and
+            _optional_ints(cache, seq_lens, batch)):
+        _refuse_table(cache, page_table, kv_lens=kv_lens, new_lens=new_lens, seq_lens=seq_lens)
     ws, ws_bytes = _workspace(cache, workspace)
-    _lib.check(_lib.lib.infllmv2_paged_evict(
-        cache._ref, batch, max_pages, table, _ints(cache, kv_lens, batch, "kv_lens"), budget, n_init, n_local,
-        _ints(cache, seq_lens, batch, "seq_lens"), _ints(cache, new_lens, batch, "new_lens"), ws, ws_bytes,
-        _stream(cache, stream)))
+    rc = _evict(cache._ref, batch, max_pages, page_table.data_ptr(), kv_lens.data_ptr(), budget, n_init, n_local,
+                None if seq_lens is None else seq_lens.data_ptr(), new_lens.data_ptr(), ws, ws_bytes,
+                _stream(cache, stream))
+    if rc:
+        _lib.check(rc)
     return new_lens
