@@ -453,7 +453,8 @@ int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch,
  * positions, so a cache's slots are no longer in order of position; slots at
  * or past `budget` are left as they were, and the pages past
  * ceil(budget / page_size) are free.  Each KV head keeps slots of its own.
- *   new_lens  int32 [batch]: min(kv_lens[b], budget); may be kv_lens itself.
+ *   new_lens  int32 [batch]: min(kv_lens[b], budget); kv_lens itself, or an
+ *           array apart from kv_lens and seq_lens.
  * A sequence with a bad page among its slots is left as it is (new_lens =
  * kv_lens[b]).  The pages in use must be pairwise different: a page that
  * sequences share must not be evicted from.  max_pages * page_size <= 524288.

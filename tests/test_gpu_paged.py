@@ -82,6 +82,95 @@ def test_attention(dev, dtype, layout, heads, group, dim, page, lens):
         assert torch.equal(now.contiguous().view(torch.int16), then.contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype,layout,heads,group,dim,page,lens,spare", [
+    # A capacity at which the end of the line goes out in small chunks: by unit, and (more units than chunks) by chunk.
+    ("bf16", "hnd", 4, 2, 128, 64, [16000, 0, 1, 9999] + [8000 + 77 * i for i in range(16)], 600),
+    ("fp16", "nhd", 16, 1, 64, 32, [100 + 13 * (i % 97) for i in range(160)], 200),
+    ("bf16", "pair", 2, 32, 128, 256, [20000 + 999 * i for i in range(9)], 600),
+    # The same capacity, but too few slots in use for that.
+    ("bf16", "hnd", 4, 2, 128, 64, [5, 640, 0, 64] * 5, 600),
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_lines(dev, dtype, layout, heads, group, dim, page, lens, spare, accumulate):
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, dtype, layout, heads, dim, page, lens, spare_entries=spare, seed=21, metadata=accumulate)
+    before = pool.weights.clone() if accumulate else None
+    q, out, lse = _attn(pool, group, accumulate=accumulate)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, dim ** -0.5)
+
+
+@pytest.mark.parametrize("heads,group,dim,lens", [(2, 16, 128, [256, 255, 1, 0, 129]), (8, 4, 64, [17 * i % 257 for i in range(90)]),
+                                                  (1, 32, 128, [200, 256, 33])])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_short_caches_in_one_launch(dev, heads, group, dim, lens, accumulate):
+    """A page table of at most 256 slots: no unit is cut."""
+    from paged_helpers import Pool, check_attend
+    pool = Pool(dev, "bf16", "hnd", heads, dim, 64, lens, spare_entries=0, seed=22, metadata=accumulate)
+    assert pool.max_pages * 64 <= 256
+    before = pool.weights.clone() if accumulate else None
+    q, out, lse = _attn(pool, group, accumulate=accumulate)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, dim ** -0.5)
+
+
+def test_a_pool_past_32_bit_offsets(dev):
+    """Pages whose rows lie beyond 2^32 elements of the pool, for all three operators."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, check_attend, evict_plain
+    small = Pool(dev, "bf16", "hnd", 8, 128, 64, [300, 64, 1], seed=23)
+    P = 70000                                    # 70000 * 8 * 64 * 128 elements: 4.6e9
+    shift = P - small.k.shape[0]
+    k = torch.empty((P, 8, 64, 128), dtype=torch.bfloat16, device=dev)
+    v = torch.empty_like(k)
+    weights, positions = torch.zeros((P, 8, 64), device=dev), torch.zeros((P, 8, 64), dtype=torch.int32, device=dev)
+    k[shift:], v[shift:], weights[shift:], positions[shift:] = small.k, small.v, small.weights, small.positions
+    big = T.PagedCache(k, v, weights, positions)
+    table = torch.where((small.table >= 0) & (small.table < P), small.table + shift, small.table)
+    q = small.normal(3, 1, 32, 128)
+    out, lse = torch.empty_like(q), torch.empty((3, 1, 32), device=dev)
+    before = small.weights.clone()
+    T.paged_attn_decode(big, q, table, small.lens, out, lse, accumulate=True,
+                        workspace=T.alloc_paged_workspace(big, table, T.OP_PAGED_DECODE, 4))
+    assert _status() == 0
+    small.weights.copy_(weights[shift:])
+    check_attend(small, q, out, lse, before, 128 ** -0.5)
+    k_new = small.normal(3, 8, 1, 128)
+    T.paged_append_kv(big, k_new, k_new, table, small.lens)
+    for b, n in enumerate(small.lens.tolist()):
+        at, row = small.places(b, n, n - 1)
+        small.k[at, :, row] = k_new[b].transpose(0, 1)
+        small.v[at, :, row] = k_new[b].transpose(0, 1)
+        small.weights[at, :, row] = 0.0
+        small.positions[at, :, row] = n - 1
+    want = evict_plain(small, 100)
+    new = torch.empty_like(small.lens)
+    T.paged_evict(big, table, small.lens, new, 100, workspace=T.alloc_paged_workspace(big, table, T.OP_PAGED_EVICT))
+    assert _status() == 0
+    small.k, small.v, small.weights, small.positions = k[shift:], v[shift:], weights[shift:], positions[shift:]
+    _check_evict(small, want, new)
+
+
+def test_two_streams_at_once(dev):
+    """Two calls that overlap, each with a workspace of its own."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, check_attend
+    pools = [Pool(dev, "bf16", "hnd", 2, 128, 64, [30000, 500], seed=24 + i) for i in range(2)]
+    qs = [p.normal(2, 1, 32, 128) for p in pools]
+    before = [p.weights.clone() for p in pools]
+    outs = [(torch.empty_like(q), torch.empty((2, 1, 32), device=dev)) for q in qs]
+    wss = [p.workspace(T.OP_PAGED_DECODE, 16) for p in pools]
+    streams = [torch.cuda.Stream() for _ in pools]
+    torch.cuda.synchronize()
+    for p, q, (out, lse), ws, st in zip(pools, qs, outs, wss, streams):
+        T.paged_attn_decode(p.cache, q, p.table, p.lens, out, lse, accumulate=True, workspace=ws, stream=st)
+    assert _status() == 0
+    for p, q, (out, lse), w in zip(pools, qs, outs, before):
+        check_attend(p, q, out, lse, w, 128 ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("group", [4, 12, 24])
 def test_attention_without_weights_or_lse(dev, dtype, group):
@@ -373,6 +462,17 @@ def test_evict(dev, dtype, layout, heads, dim, page, lens, budget, n_init, n_loc
         pool.weights.copy_(torch.where(pool.weights < 0.1, pool.weights * 1e-30, 1 + pool.weights * 1e-5))
     want = evict_plain(pool, budget, n_init, n_local)
     new = _evict(pool, budget, n_init, n_local, in_place=values == "ties")
+    assert _status() == 0
+    _check_evict(pool, want, new)
+
+
+@pytest.mark.parametrize("most,budget", [(67, 40), (500, 100), (1000, 999), (2000, 700), (4000, 100)])
+def test_evict_many_short(dev, most, budget):
+    """More (sequence, KV head) units than the SMs hold CTAs of 512 threads."""
+    from paged_helpers import Pool, evict_plain
+    pool = Pool(dev, "bf16", "hnd", 8, 64, 16, [(most * (i + 1)) // 40 for i in range(40)], spare_entries=1, seed=25)
+    want = evict_plain(pool, budget, 2, 7)
+    new = _evict(pool, budget, 2, 7)
     assert _status() == 0
     _check_evict(pool, want, new)
 

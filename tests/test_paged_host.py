@@ -43,10 +43,10 @@ def _attn(L, c, batch=2, max_pages=4, group=16, q=FAKE, table=FAKE, lens=FAKE, s
                                             lens, scale, accumulate, out, None, ws, ws_bytes, None)
 
 
-def _evict(L, c, batch=2, max_pages=4, table=FAKE, lens=FAKE, budget=10, n_init=0, n_local=0, new=FAKE, ws=FAKE,
-           ws_bytes=1 << 40):
+def _evict(L, c, batch=2, max_pages=4, table=FAKE, lens=FAKE, budget=10, n_init=0, n_local=0, seen=None, new=FAKE,
+           ws=FAKE, ws_bytes=1 << 40):
     return L.lib.infllmv2_paged_evict(None if c is None else ctypes.byref(c), batch, max_pages, table, lens, budget,
-                                      n_init, n_local, None, new, ws, ws_bytes, None)
+                                      n_init, n_local, seen, new, ws, ws_bytes, None)
 
 
 def test_struct_matches_the_header(L):
@@ -125,6 +125,7 @@ def test_evict_arguments(L):
     assert _evict(L, c, budget=10, n_init=6, n_local=5) == L.INVALID_ARGUMENT
     assert _evict(L, c, budget=10, n_init=2 ** 31 - 1, n_local=2 ** 31 - 1) == L.INVALID_ARGUMENT
     assert _evict(L, c, new=None) == L.INVALID_ARGUMENT
+    assert _evict(L, c, seen=FAKE + 64, new=FAKE + 64) == L.INVALID_ARGUMENT
     assert _evict(L, c, max_pages=8193) == L.UNSUPPORTED           # past 524288 slots
     need = L.lib.infllmv2_paged_workspace_size(ctypes.byref(c), 2, 4, 0, L.OP_PAGED_EVICT)
     assert need > 0

@@ -256,6 +256,7 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
     if (static_cast<int64_t>(n_init) + n_local > budget)
       return fail(INFLLMV2_INVALID_ARGUMENT, "budget %d < n_init %d + n_local %d", budget, n_init, n_local);
     if (!new_lens) return fail(INFLLMV2_INVALID_ARGUMENT, "new_lens is NULL");
+    if (new_lens == seq_lens) return fail(INFLLMV2_INVALID_ARGUMENT, "new_lens must not be seq_lens");
     if (!paged_evict_supported(s))
       return fail(INFLLMV2_UNSUPPORTED, "eviction takes max_pages * page_size <= 524288 (got %d)", s.cap);
     if ((rc = check_workspace(paged_evict_workspace_bytes(s), workspace, workspace_bytes))) return rc;

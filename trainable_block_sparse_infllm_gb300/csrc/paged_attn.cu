@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
 
   if (warp == 4 * kGroups) {
     // ------------------------------------------------ the loading warp -------
+    fence_proxy_async_global();   // rows that earlier kernels stored are read by TMA
     const int boxes = kTile / a.box;
     int stage = 0;
     uint32_t phase = 0;

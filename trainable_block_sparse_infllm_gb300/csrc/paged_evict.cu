@@ -28,7 +28,7 @@ namespace infllmv2 {
 namespace {
 
 constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kShortThreads = 128;   // of a CTA for a short cache among many
 constexpr int kMoveThreads = 256;
 constexpr int kMaxCluster = 16;
 
@@ -123,9 +123,10 @@ __device__ __forceinline__ uint4 reduce_range(uint4 v, bool has) {
 }
 
 // kDim = 0: the moves are left to evict_move_kernel.
-template <int kKeys, int kDim>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int C) {
-  extern __shared__ int32_t stage[];                       // [kKeys kSelThreads]: holes up, movers down
+template <int kThreads, int kKeys, int kDim>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a, int C) {
+  constexpr int kSelWarps = kThreads / 32;
+  extern __shared__ int32_t stage[];                       // [kKeys kThreads]: holes up, movers down
   __shared__ __align__(16) uint32_t hist[2][256];
   __shared__ __align__(16) uint32_t total[256];            // of the cluster
   __shared__ uint4 range_warp[kSelWarps];
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = blockIdx.x / C, b = unit / s.Hkv, h = unit % s.Hkv;
   if (C > 1) cluster_arrive_relaxed();
-  if (tid < 256) hist[0][tid] = hist[1][tid] = 0;   // visible by the barrier after the loads
+  for (int i = tid; i < 256; i += kThreads) hist[0][i] = hist[1][i] = 0;   // visible by the barrier after the loads
   pdl_wait();
   pdl_trigger();
   if (C > 1) cluster_wait();   // every CTA runs: its shared memory may be written
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
   const int seen = a.seq_lens ? __ldg(a.seq_lens + b) : n;
-  const int slot0 = (rank * kSelThreads + tid) * kKeys;
+  const int slot0 = (rank * kThreads + tid) * kKeys;
   // Slots at or past n get key 0.  They never stay: of equal keys the lower
   // slots do, and more than `budget` of those exist.
   uint32_t key[kKeys];
@@ -253,9 +254,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       cluster_sync();
     else
       __syncthreads();
-    if (tid < 256) hist[buf ^ 1][tid] = 0;   // the next round's (last read before the barrier above)
+    // The next round's (last read before the barrier above).
+    for (int i = tid; i < 256; i += kThreads) hist[buf ^ 1][i] = 0;
     if (C > 1) {
-      // Bin tid over the cluster: each CTA sums all of it by itself.
+      // Bin tid over the cluster: each CTA sums all of it by itself.  (Clusters
+      // have at least 256 threads per CTA.)
       if (tid < 256) {
         uint32_t sum = 0;
         for (int r0 = 0; r0 < C; r0 += 8) {   // 8 remote loads in flight
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const unsigned long long mine =
       scan((static_cast<uint32_t>(__popcll(holes)) << 16) | static_cast<uint32_t>(__popcll(movers)), 1);
   const int count = static_cast<int>(all & 0xffffffffu);   // as many holes as movers
-  constexpr int kSlots = kKeys * kSelThreads;
+  constexpr int kSlots = kKeys * kThreads;
   {
     int32_t* up = stage + static_cast<int>(mine >> 32);
     int32_t* down = stage + kSlots - 1 - static_cast<int>(mine & 0xffffffffu);
@@ -378,8 +381,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int n_holes = static_cast<int>(cta >> 32), n_movers = static_cast<int>(cta & 0xffffffffu);
     int32_t* to = a.hole + static_cast<long long>(unit) * a.most + static_cast<int>(cta0 >> 32);
     int32_t* from = a.mover + static_cast<long long>(unit) * a.most + static_cast<int>(cta0 & 0xffffffffu);
-    for (int i = tid; i < n_holes; i += kSelThreads) to[i] = stage[i];
-    for (int i = tid; i < n_movers; i += kSelThreads) from[i] = stage[kSlots - 1 - i];
+    for (int i = tid; i < n_holes; i += kThreads) to[i] = stage[i];
+    for (int i = tid; i < n_movers; i += kThreads) from[i] = stage[kSlots - 1 - i];
   }
   if constexpr (kDim == 0) {
     if (rank == 0 && tid == 0) a.count[unit] = count;
@@ -412,26 +415,32 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const Evict
 }
 
 struct EvictPlan {
-  int keys, cluster;
+  int threads, keys, cluster;
 };
 
-// Slots per thread and CTAs per unit.  One CTA holds 512 x 4, 8 or 16 slots;
-// longer caches take clusters of up to 16 CTAs, and past 131072 slots more
-// keys per thread.
-EvictPlan evict_plan(int cap) {
-  if (cap <= kSelThreads * 4) return {4, 1};
-  if (cap <= kSelThreads * 8) return {8, 1};
+// Threads per CTA, slots per thread and CTAs per unit.  A cache of up to 8192
+// slots takes one CTA of 512 threads with 4, 8 or 16 slots each.  With more
+// units than the SMs hold such CTAs at once, caches of up to 4096 slots take
+// CTAs of 128 threads with up to 32, more of which share an SM (468 units of
+// 844 slots: 29.2 us with 512 threads, 16.8 us with 128; 800 units of 4000: 113
+// and 109 us; but 800 of 6000: 165 and 179 us).  Longer caches take clusters of
+// up to 16 CTAs, and past 131072 slots more slots per thread.
+EvictPlan evict_plan(int cap, long long units) {
+  if (cap <= 4096 && units > 2 * device_sm_count())
+    return {kShortThreads, cap <= 512 ? 4 : (cap <= 1024 ? 8 : (cap <= 2048 ? 16 : 32)), 1};
+  if (cap <= 2048) return {kSelThreads, 4, 1};
+  if (cap <= 4096) return {kSelThreads, 8, 1};
   int c = 1;
   while (c < kMaxCluster && cap > kSelThreads * 16 * c) c *= 2;
   int keys = 16;
   while (keys < 64 && cap > kSelThreads * keys * c) keys *= 2;
-  return {keys, c};
+  return {kSelThreads, keys, c};
 }
 
-template <int kKeys, int kDim>
+template <int kThreads, int kKeys, int kDim>
 cudaError_t launch_select(const EvictArgs& a, int C, cudaStream_t st) {
-  auto kernel = evict_select_kernel<kKeys, kDim>;
-  constexpr int kSmem = kKeys * kSelThreads * 4;
+  auto kernel = evict_select_kernel<kThreads, kKeys, kDim>;
+  constexpr int kSmem = kKeys * kThreads * 4;
   if (C > 8) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -442,7 +451,7 @@ cudaError_t launch_select(const EvictArgs& a, int C, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.s.B * a.s.Hkv * C), 1, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -459,12 +468,18 @@ cudaError_t launch_select(const EvictArgs& a, int C, cudaStream_t st) {
 
 template <int kDim>
 cudaError_t launch_select_any(const EvictArgs& a, EvictPlan plan, cudaStream_t st) {
+  if (plan.threads == kShortThreads) {
+    if (plan.keys == 4) return launch_select<kShortThreads, 4, kDim>(a, 1, st);
+    if (plan.keys == 8) return launch_select<kShortThreads, 8, kDim>(a, 1, st);
+    if (plan.keys == 16) return launch_select<kShortThreads, 16, kDim>(a, 1, st);
+    return launch_select<kShortThreads, 32, kDim>(a, 1, st);
+  }
   switch (plan.keys) {
-    case 4: return launch_select<4, kDim>(a, plan.cluster, st);
-    case 8: return launch_select<8, kDim>(a, plan.cluster, st);
-    case 16: return launch_select<16, kDim>(a, plan.cluster, st);
-    case 32: return launch_select<32, kDim>(a, plan.cluster, st);
-    default: return launch_select<64, kDim>(a, plan.cluster, st);
+    case 4: return launch_select<kSelThreads, 4, kDim>(a, plan.cluster, st);
+    case 8: return launch_select<kSelThreads, 8, kDim>(a, plan.cluster, st);
+    case 16: return launch_select<kSelThreads, 16, kDim>(a, plan.cluster, st);
+    case 32: return launch_select<kSelThreads, 32, kDim>(a, plan.cluster, st);
+    default: return launch_select<kSelThreads, 64, kDim>(a, plan.cluster, st);
   }
 }
 
@@ -517,7 +532,7 @@ cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int 
   a.count = static_cast<int32_t*>(ws);
   a.hole = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(units * 4));
   a.mover = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(a.hole) + up256(units * a.most * 4));
-  const EvictPlan plan = evict_plan(s.cap);
+  const EvictPlan plan = evict_plan(s.cap, static_cast<long long>(units));
   // The selecting CTAs move the rows themselves where a unit has no more than
   // 64 rows to move.  new_lens over kv_lens would be read by the other KV
   // heads' CTAs: that goes by the second launch.

@@ -76,6 +76,7 @@ class PagedCache:
             weights=weights.data_ptr() if weights is not None else None,
             positions=positions.data_ptr() if positions is not None else None)
         self._ref = ctypes.byref(self.struct)
+        self._new_strides = (None, None)
 
 
 # Each call's arguments are looked at in one expression; only where it fails do
@@ -150,16 +151,17 @@ def paged_append_kv(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
     if len(shape) != 4 or shape != v_new.shape or shape[0] != batch or shape[1] != cache.n_kv_heads or \
             shape[3] != cache.head_dim:
         raise _bad("k_new and v_new must be [batch, n_kv_heads, n_q, head_dim]")
-    kb, kh, kt, kd = k_new.stride()
-    vb, vh, vt, vd = v_new.stride()
-    if k_new.dtype is not dtype or v_new.dtype is not dtype or kd != 1 or vd != 1:
+    strides = (k_new.stride(), v_new.stride())
+    if k_new.dtype is not dtype or v_new.dtype is not dtype or strides[0][3] != 1 or strides[1][3] != 1:
         raise _bad("k_new and v_new must have the cache's type and rows of consecutive values")
     if k_new.get_device() != index or v_new.get_device() != index:
         for t in (k_new, v_new):
             if t.get_device() != index and (t.is_cuda or not t.is_pinned()):
                 raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
+    if cache._new_strides[0] != strides:   # a loop's appends have the same: no new array each time
+        cache._new_strides = (strides, _Strides(*strides[0][:3], *strides[1][:3]))
     rc = _append(cache._ref, batch, max_pages, shape[2], k_new.data_ptr(), v_new.data_ptr(),
-                 _Strides(kb, kh, kt, vb, vh, vt), page_table.data_ptr(), kv_lens.data_ptr(),
+                 cache._new_strides[1], page_table.data_ptr(), kv_lens.data_ptr(),
                  None if n_new is None else n_new.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
                  _stream(cache, stream))
     if rc:
