@@ -1055,12 +1055,12 @@ WsLayout ws_layout(const PagedShape& s, int G) {
   return w;
 }
 
-// CTAs of the weights' part: about 16 per SM, the same number for every unit
+// CTAs of the weights' part: about 8 per SM, the same number for every unit
 // and no more than its chunks.  Their loads are short, and latency is what they
 // wait for.
 int weight_jobs(const PagedAttnArgs& a) {
   const int units = a.B * a.Hkv, chunks = (a.cap + kChunk - 1) / kChunk;
-  const int want = (16 * device_sm_count() + units - 1) / units;
+  const int want = (8 * device_sm_count() + units - 1) / units;
   return units * (want < chunks ? want : chunks);
 }
 
