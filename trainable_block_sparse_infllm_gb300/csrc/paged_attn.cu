@@ -9,8 +9,8 @@
 // even 32 heads to a KV head give 32 FLOPs per byte.  The aim is one pass over
 // the pages at the copy rate, whatever the lengths.
 //
-// Split.  The work is all 64-slot tiles of all (sequence, KV head) units, in
-// that order, each unit with a fixed cost before its tiles.  That line is cut
+// Split.  The work is all tiles (64 or 128 slots) of all (sequence, KV head)
+// units, in that order, each unit with a fixed cost before its tiles.  That line is cut
 // into chunks whatever the units' borders: one equal chunk for every CTA, so
 // that those of any ragged batch carry the same load and one long sequence
 // spreads over all SMs.  SMs do not read at one rate, though (a 32 x 32K batch
@@ -25,9 +25,9 @@
 // issues one TMA box per 64 columns of K and of V, through a ring of tiles; the
 // queries of a piece come with its first tile, and what a tile is (whose, which
 // rows of it hold slots, whether a piece ends) stands beside it.  Four warps
-// (eight for 17 to 32 heads: four per half) compute, each on its own 16 slots
-// of every tile with its own running maximum and sum, so that nothing but the
-// ring's barriers is shared until the piece's end.  The heads are the 16 rows
+// (eight for 17 to 32 heads: four per half) compute, each on its own quarter of
+// every tile's slots with its own running maximum and sum, so that nothing but
+// the ring's barriers is shared until the piece's end.  The heads are the 16 rows
 // of mma.m16n8k16: at these intensities the tensor pipe idles and a tcgen05
 // tile (128 rows) would be seven eighths empty.
 //
@@ -35,8 +35,16 @@
 // product with V as two 16-bit parts (hi + lo, 16 to 22 significant bits): one
 // rounding of it to bf16 would cost as much again as the output's own.  With
 // up to 8 heads the lo parts fill the rows 8..15 that would be empty; with
-// more they are a second product.  fp16 probabilities are scaled by 2^14, so
+// more they are a second product (a unit of 256 slots, d 128, alone on its SM:
+// 7.0 us a call with 8 heads, 8.0 with 16).  fp16 probabilities are scaled by 2^14, so
 // that the long tail of a sharp softmax stays above fp16's smallest number.
+//
+// Measured (GB300, bf16 unless said): 32 sequences of 16K to 32K, 8 KV heads of
+// 8, with weights: the pass 505 us (3.3 GB: 6.6 TB/s, 98% of the copy rate, its
+// scores' 0.2 GB included), the join and weights 43 us.  64 ragged of up to 8K,
+// fp16, token-major pages of 16, with weights: 179 us (6.4 TB/s) and 18 us.  One
+// of 128K, 2 KV heads of 16, with weights: 28 us (134 MB; 4 us until the first
+// tiles land, and CTAs of 13 or 14 tiles) and 9 us.
 #include <atomic>
 
 #include "paged.cuh"
@@ -47,7 +55,11 @@ namespace infllmv2 {
 namespace {
 
 // Slots per tile: 32 KB of keys and values, so that a tile's fixed cost (its
-// barriers, maxima and their exchange) is shared by as many bytes at either d.
+// barriers, maxima and their exchange) is shared by as many bytes at either d:
+// 96 short sequences at d 64 took 84 us with 64 slots and 70 with 128.  With two
+// groups (17 to 32 heads) 128 slots at either: each warp then has two
+// independent parts to overlap; 4 x 60K slots, 8 KV heads of 32, d 128, took
+// 248 us with 64 slots and 168 with 128.
 template <int kDim, int kGroups>
 constexpr int kTileOf = kGroups == 2 ? 128 : 8192 / kDim;
 
@@ -1027,7 +1039,9 @@ size_t score_row(const PagedShape& s, int G) {
 }
 
 // Small chunks are handed out where the line is long enough for the SMs' rates
-// to matter: 128 tiles of the capacity for every CTA.
+// to matter more than the counter's launch: 128 tiles of the capacity for every
+// CTA.  32 x 32K (430 tiles per CTA): 572 us in equal shares, 552 handed out; 64
+// ragged (215): 205 and 201; 96 short (81): 70.5 and 70.9, and 2 us of the host.
 bool hands_out(const PagedShape& s, int G, int ctas) {
   return static_cast<long long>(s.B) * s.Hkv * unit_tiles_of(s, G) >= 128LL * ctas;
 }
