@@ -89,6 +89,7 @@ def test_attention(dev, dtype, layout, heads, group, dim, page, lens):
     ("bf16", "pair", 2, 32, 128, 256, [20000 + 999 * i for i in range(9)], 600),
     # The same capacity, but too few slots in use for that.
     ("bf16", "hnd", 4, 2, 128, 64, [5, 640, 0, 64] * 5, 600),
+    ("bf16", "hnd", 4, 2, 128, 64, [0] * 20, 600),
 ])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_long_lines(dev, dtype, layout, heads, group, dim, page, lens, spare, accumulate):

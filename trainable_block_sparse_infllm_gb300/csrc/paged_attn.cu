@@ -108,12 +108,19 @@ struct Split {
   long long unit0;    // where that unit begins
 };
 
+// a / b for a >= 0, b > 0: in 32 bits where that does (a 64-bit division is a
+// hundred instructions, and every CTA starts with a few).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 __device__ __forceinline__ long long chunk_begin(const Split& s, int k) {
-  return k <= s.n ? k * s.A / s.n : min(s.W, s.A + static_cast<long long>(k - s.n) * s.small);
+  return k <= s.n ? quotient(k * s.A, s.n) : min(s.W, s.A + static_cast<long long>(k - s.n) * s.small);
 }
 // The chunk that a position belongs to.
 __device__ __forceinline__ int chunk_of(const Split& s, long long at) {
-  return static_cast<int>(at < s.A ? ((at + 1) * s.n - 1) / s.A : s.n + (at - s.A) / s.small);
+  return static_cast<int>(at < s.A ? quotient((at + 1) * s.n - 1, s.A) : s.n + quotient(at - s.A, s.small));
 }
 
 __device__ __forceinline__ int unit_tiles(const PagedAttnArgs& a, int len) {
@@ -161,7 +168,7 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
   s.n = static_cast<int>(min(static_cast<long long>(ctas), s.W));
   s.cost = cost;
   s.whole = a.whole != 0;
-  const bool shares = a.next != nullptr && s.W >= 32LL * s.n;
+  const bool shares = a.next != nullptr && s.n > 0 && s.W >= 32LL * s.n;
   s.A = s.W;
   s.small = 8;
   s.chunks = s.n;
@@ -181,8 +188,8 @@ __device__ __forceinline__ Split make_split(const PagedAttnArgs& a, int cta, int
         const int w = unit_width(a, b, cost);
         if (rest < static_cast<long long>(w) * a.Hkv) {
           where[0] = b;
-          where[1] = static_cast<int>(rest / w);
-          where[2] = static_cast<int>(rest % w);
+          where[1] = static_cast<int>(quotient(rest, w));
+          where[2] = static_cast<int>(rest - static_cast<long long>(where[1]) * w);
           break;
         }
         rest -= static_cast<long long>(w) * a.Hkv;
@@ -220,8 +227,8 @@ __device__ __forceinline__ void locate(Split& s, const PagedAttnArgs& a, long lo
   const int width = __shfl_sync(0xffffffffu, w, src), first = __shfl_sync(0xffffffffu, upto - w, src);
   const long long in = rest - static_cast<long long>(first) * a.Hkv;
   s.b = r * run + src;
-  s.h = static_cast<int>(in / width);
-  s.unit0 = at - in % width;
+  s.h = static_cast<int>(quotient(in, width));
+  s.unit0 = at - (in - static_cast<long long>(s.h) * width);
 }
 
 // The tiles of one unit in a chunk [begin, end).
