@@ -333,6 +333,56 @@ def test_stream_and_graph(dev):
         check_attend(pool, q, out, lse, before, 128 ** -0.5)
 
 
+def test_two_graphs_share_a_workspace(dev):
+    """Captured with one workspace and replayed in turn on one stream: nothing is kept from one to the next."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, check_attend
+    pools = [Pool(dev, "bf16", "hnd", 2, 128, 64, lens, seed=30 + i)
+             for i, lens in enumerate(([9000, 90, 2000], [1, 12000, 0]))]
+    ws = max((p.workspace(T.OP_PAGED_DECODE, 16) for p in pools), key=lambda w: w.numel())
+    qs = [p.normal(3, 1, 32, 128) for p in pools]
+    outs = [(torch.empty_like(q), torch.empty((3, 1, 32), device=dev)) for q in qs]
+    graphs = []
+    for p, q, (out, lse) in zip(pools, qs, outs):
+        T.paged_attn_decode(p.cache, q, p.table, p.lens, out, lse, accumulate=True, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            T.paged_attn_decode(p.cache, q, p.table, p.lens, out, lse, accumulate=True, workspace=ws)
+    before = [p.weights.clone() for p in pools]
+    for _ in range(3):
+        for p, w in zip(pools, before):
+            p.weights.copy_(w)
+        for g in graphs:
+            g.replay()
+    assert _status() == 0
+    for p, q, (out, lse), w in zip(pools, qs, outs, before):
+        check_attend(p, q, out, lse, w, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("lens,budget", [([300, 64, 1, 777], 64), ([40000, 9000], 5000), ([4097, 4096], 4096)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_in_a_graph(dev, lens, budget, in_place):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, evict_plain
+    pool = Pool(dev, "bf16", "hnd", 2, 64, 64, lens, seed=32)
+    start = [t.clone() for t in (pool.k, pool.v, pool.weights, pool.positions, pool.lens)]
+    want = evict_plain(pool, budget, 2, 9)
+    new = pool.lens if in_place else torch.empty_like(pool.lens)
+    ws = pool.workspace(T.OP_PAGED_EVICT)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.paged_evict(pool.cache, pool.table, pool.lens, new, budget, 2, 9, workspace=ws)
+    for _ in range(2):
+        for t, was in zip((pool.k, pool.v, pool.weights, pool.positions, pool.lens), start):
+            t.copy_(was)
+        graph.replay()
+        assert _status() == 0
+        _check_evict(pool, want, new)
+
+
 def test_same_result_every_time(dev):
     import torch
     from paged_helpers import Pool
