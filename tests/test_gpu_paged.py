@@ -101,6 +101,30 @@ def test_long_lines(dev, dtype, layout, heads, group, dim, page, lens, spare, ac
     check_attend(pool, q, out, lse, before, dim ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,heads,group,dim,page,lens", [
+    ("bf16", 2, 16, 128, 64, [1000]), ("fp16", 1, 8, 128, 16, [512, 1, 0, 300]), ("bf16", 4, 3, 64, 48, [2000, 129]),
+    ("bf16", 2, 32, 128, 64, [1100, 5]), ("fp16", 8, 20, 64, 128, [640, 1]), ("bf16", 4, 16, 128, 32, [2500, 64, 65, 3000]),
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_clusters(dev, dtype, heads, group, dim, page, lens, accumulate):
+    """Few units of a few thousand slots: each by a cluster that joins its pieces itself; again with a bad page."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, attend, check_attend
+    pool = Pool(dev, dtype, "nhd", heads, dim, page, lens, seed=26, metadata=accumulate)
+    before = pool.weights.clone() if accumulate else None
+    q, out, lse = _attn(pool, group, accumulate=accumulate)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, dim ** -0.5)
+    last = (lens[0] - 1) // page
+    pool.table[0, last] = pool.k.shape[0]            # the first sequence's last page is absent
+    left = torch.tensor([last * page] + lens[1:])
+    before = pool.weights.clone() if accumulate else None
+    q, out, lse = _attn(pool, group, accumulate=accumulate)
+    assert _status() == T.DEVICE_BAD_PAGE
+    check_attend(pool, q, out, lse, before, dim ** -0.5, lens=left)
+
+
 @pytest.mark.parametrize("heads,group,dim,lens", [(2, 16, 128, [256, 255, 1, 0, 129]), (8, 4, 64, [17 * i % 257 for i in range(90)]),
                                                   (1, 32, 128, [200, 256, 33])])
 @pytest.mark.parametrize("accumulate", [False, True])

@@ -21,6 +21,11 @@
 // workspace, at a place that goes by the chunk and not by the CTA, and
 // paged_join_kernel joins them in the line's order.  The host needs no lengths.
 //
+// Where the capacity is small the second launch costs more than the balance
+// gives.  Then each unit goes to a cluster of 4 or 8 CTAs, which joins its
+// pieces itself behind the cluster's barrier (cluster_size has the rule), or,
+// of many caches of up to 256 slots, whole to one CTA.
+//
 // A CTA.  One warp loads: per page piece (16, 32 or 64 rows of one page) it
 // issues one TMA box per 64 columns of K and of V, through a ring of tiles; the
 // queries of a piece come with its first tile, and what a tile is (whose, which
@@ -87,6 +92,7 @@ struct PagedAttnArgs {
   float* scores;     // [B Hkv G][cap64] z in log2 units (weights only)
   int cap64;         // scores of a head: cap rounded up to whole tiles
   int whole;         // no unit is cut: one launch
+  int cluster;       // CTAs of a cluster per unit, which join their pieces themselves: one launch; 0: none
   int tile_shift;    // log2 of the slots per tile
   uint32_t* status;
 };
@@ -273,6 +279,19 @@ __device__ __forceinline__ bool first_piece(Piece& p, const Split& s, const Page
   return p.tile1 > p.tile0;
 }
 
+// A cluster's unit and the piece of CTA `cta` in it; false where it has no tile.
+__device__ __forceinline__ bool cluster_piece(Piece& p, const PagedAttnArgs& a, int cta) {
+  const int unit = cta / a.cluster, rank = cta % a.cluster;
+  p.b = unit / a.Hkv;
+  p.h = unit % a.Hkv;
+  p.len = paged_len(a.kv_lens, p.b, a.cap, a.status);
+  p.tiles = unit_tiles(a, p.len);
+  p.tile0 = p.tiles * rank / a.cluster;
+  p.tile1 = p.tiles * (rank + 1) / a.cluster;
+  p.unit0 = 0;
+  return p.tile1 > p.tile0;
+}
+
 // Workspace place of a cut unit's piece in chunk k whose first tile is at `at`:
 // 2 k for a piece that starts the chunk, 2 k + 1 for one that starts later (and
 // so is the chunk's last).
@@ -435,7 +454,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
   }
   pdl_wait();
   pdl_trigger();
-  Split s = make_split<C::kThreads>(a, cta, ctas, C::kCost, before, reinterpret_cast<int*>(smem + C::kSplitOff));
+  Split s = {};
+  if (a.cluster)
+    __syncthreads();   // the barriers are set up
+  else
+    s = make_split<C::kThreads>(a, cta, ctas, C::kCost, before, reinterpret_cast<int*>(smem + C::kSplitOff));
   if (cta == 0 && tid == 0 && a.chunks) *a.chunks = s.chunks;
 
   // Empty sequences attend nothing: a zero row, lse = -inf.
@@ -449,7 +472,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     if (a.unit_cut)
       for (int h = tid; h < a.Hkv; h += C::kThreads) a.unit_cut[b * a.Hkv + h] = make_int4(-1, 0, 0, 0);
   }
-  if (cta >= s.n) return;
+  if (cta >= s.n && !a.cluster) return;
 
   if (warp == 4 * kGroups) {
     // ------------------------------------------------ the loading warp -------
@@ -461,9 +484,16 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     uint32_t issued = 0;
     int chunk = cta;
     while (true) {
-      const long long begin = chunk_begin(s, chunk), end = chunk_begin(s, chunk + 1);
+      long long begin = 0, end = 0;
       Piece p;
-      bool have = first_piece(p, s, a, begin, end);
+      bool have;
+      if (a.cluster) {
+        have = cluster_piece(p, a, cta);
+      } else {
+        begin = chunk_begin(s, chunk);
+        end = chunk_begin(s, chunk + 1);
+        have = first_piece(p, s, a, begin, end);
+      }
       // Does the chunk before hold the first piece of the unit that starts this one?
       const bool later = have && p.tile0 > 0;
       const int cut_unit = p.b * a.Hkv + p.h, cut_tiles = p.tiles;
@@ -489,7 +519,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           for (int i = 0; i < kQSteps; ++i)
             if (i * 32 + lane < a.G * (kDim / 8)) qv[i] = __ldg(q + i * 32 + lane);
         }
-        const int place = piece_place(chunk, begin, tile_at(s, p, p.tile0));
+        const int place = a.cluster ? cta : piece_place(chunk, begin, tile_at(s, p, p.tile0));
         for (int t = p.tile0; t < p.tile1; ++t) {
           const int page = page_next;
           page_next = fetch(t + 1);
@@ -553,8 +583,9 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
             phase ^= 1;
           }
         }
-        if (!dead) have = next_piece(p, s, a, end);
+        if (!dead) have = !a.cluster && next_piece(p, s, a, end);
       }
+      if (a.cluster) break;
       if (lane == 0) {   // the chunk's loads are on their way: note the cut
         int4 c = make_int4(-1, 0, 0, 0);
         if (later && cut_at < begin && chunk_of(s, cut_at) == chunk - 1)
@@ -583,6 +614,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       for (uint32_t i = from; i < issued; ++i)
         mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, a.status);
     }
+    __syncwarp();
+    if (a.cluster) cluster_sync();   // with the computing warps' below
     return;
   }
 
@@ -833,7 +866,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
               // fp16 probabilities, and so the sum, carry a factor 2^14.
               const float lse2 = use + log2f(sum) - (kFp16 ? 14.f : 0.f);
               if (a.lse) a.lse[head] = lse2 * 0.6931471805599453f;
-              if (a.whole)
+              if (a.whole || a.cluster)
                 unit_lse2[head0 + row] = lse2;
               else if (a.weights)
                 a.lse2[head] = lse2;
@@ -860,6 +893,73 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       phase ^= 1;
     }
   }
+  if (a.cluster == 0) return;
+
+  // ---- a cluster joins its unit ---------------------------------------------
+  // The pieces lie in the workspace; the cluster's barrier orders them.
+  cluster_sync();
+  Piece p;
+  const bool mine = cluster_piece(p, a, cta);
+  const int unit = cta / a.cluster, rank = cta % a.cluster;
+  int pieces = 0;
+  for (int r = 0; r < a.cluster; ++r)
+    pieces += p.tiles * (r + 1) / a.cluster > p.tiles * r / a.cluster ? 1 : 0;
+  if (pieces > 1) {
+    auto has = [&](int r) { return p.tiles * (r + 1) / a.cluster > p.tiles * r / a.cluster; };
+    // Head rank + C i is joined by warp i of CTA `rank`.
+    for (int h = rank + a.cluster * warp; h < a.G; h += a.cluster * 4 * kGroups) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mx = -INFINITY, sum = 0.f;
+      for (int r0 = 0; r0 < a.cluster; r0 += 8) {   // 8 pieces in flight
+        float2 v[8];
+        float4 y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = make_float2(-INFINITY, 0.f);
+          y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r0 + e < a.cluster && has(r0 + e)) {
+            const long long at = unit * a.cluster + r0 + e;
+            v[e] = __ldcg(a.part_ml + at * kPagedMaxGroup + h);
+            if (lane < kDim / 4) y[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (at * a.G + h) * kDim) + lane);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float nm = fmaxf(mx, v[e].x), use = nm == -INFINITY ? 0.f : nm;
+          const float f = fast_exp2(mx - use), f2 = fast_exp2(v[e].x - use);
+          mx = nm;
+          sum = sum * f + v[e].y * f2;
+          x.x = x.x * f + y[e].x * f2;
+          x.y = x.y * f + y[e].y * f2;
+          x.z = x.z * f + y[e].z * f2;
+          x.w = x.w * f + y[e].w * f2;
+        }
+      }
+      const float use = mx == -INFINITY ? 0.f : mx;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long head = static_cast<long long>(unit) * a.G + h;
+      if (lane < kDim / 4) {
+        uint2 y;
+        y.x = pack_pair<kFp16>(x.x * inv, x.y * inv);
+        y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + lane * 4) = y;
+      }
+      if (lane == 0 && a.lse) a.lse[head] = (use + log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
+    }
+    if (a.weights && tid < a.G) {
+      float mx = -INFINITY, sum = 0.f;
+      for (int r = 0; r < a.cluster; ++r) {
+        if (!has(r)) continue;
+        const float2 v = __ldcg(a.part_ml + static_cast<long long>(unit * a.cluster + r) * kPagedMaxGroup + tid);
+        const float nm = fmaxf(mx, v.x), use = nm == -INFINITY ? 0.f : nm;
+        sum = sum * fast_exp2(mx - use) + v.y * fast_exp2(v.x - use);
+        mx = nm;
+      }
+      unit_lse2[tid] = (mx == -INFINITY ? 0.f : mx) + log2f(sum) - (kFp16 ? 14.f : 0.f);
+    }
+  }
+  if (a.weights && mine && sync(group_bar + kGroups, all_phase))
+    add_weights(a, unit, p.b, p.h, min(p.len, p.tile1 * kTile), p.tile0 * kTile + 4 * tid, 4 * 128 * kGroups, unit_lse2);
 }
 
 // ---- the join -----------------------------------------------------------------
@@ -1018,10 +1118,10 @@ __global__ void paged_counter_kernel(int* next) {
 
 // ---- host side -------------------------------------------------------------------
 
-// Caches of up to this many slots are attended without cuts, in one launch.  Two
-// KV heads of 256 slots (16 heads each, d 128): 9.0 us a call from Python and
-// 8.4 us on the GPU without cuts, 9.8 and 8.2 us with them; 512 slots: 12.4 and
-// 12.1 against 10.1 and 8.5 us.
+// Where clusters do not serve, caches of up to this many slots are attended
+// without cuts, in one launch (256 units of 128 to 256 slots, 16 heads, d 128:
+// 11.4 us without cuts, 17.5 with them; of 256 to 512 slots 21.4 and 22.7, and
+// with fewer units of those cuts win).
 constexpr int kWholeCap = 256;
 
 int tile_shift_of(const PagedShape& s, int G) {
@@ -1038,6 +1138,27 @@ int attn_ctas(const PagedShape& s, int G) {
   const long long positions = static_cast<long long>(s.B) * s.Hkv * (unit_tiles_of(s, G) + kUnitCost);
   const long long most = static_cast<long long>(device_sm_count()) * (G > 16 ? 1 : 2);
   return static_cast<int>(positions < most ? positions : most);
+}
+
+// CTAs of a cluster for each unit, or 0 where the line is split over all CTAs.
+// A cluster joins its unit itself, which saves the second launch, but its few
+// CTAs have to suffice.  With 8 or 4 CTAs of d 128, 16 heads, calls from Python:
+// 2 units of 512 / 1024 / 2048 slots 8.1 / 8.6 / 10.0 us against 9.5 / 9.7 / 9.7;
+// 16 units of 512 / 2048 / 4096 / 8192 slots 8.5 / 11.0 / 15.1 / 22.6 against
+// 11.2 / 12.8 / 16.7 / 22.5; so two tiles per CTA, or eight where half the SMs
+// have a CTA.  Clusters that fill more than half of the GPU's CTAs do not all
+// fit its processing clusters at once (32 units of 512 slots: 11.6 us with 8
+// CTAs each, 8.7 with 4).
+int cluster_size(const PagedShape& s, int G) {
+  const int tiles = unit_tiles_of(s, G), sms = device_sm_count();
+  const long long units = static_cast<long long>(s.B) * s.Hkv;
+  if (tiles < 3) return 0;
+  for (int c = 8; c >= 4; c /= 2) {
+    const long long ctas = units * c;
+    if (2 * tiles <= c || 2 * ctas > sms * (G > 16 ? 1 : 2)) continue;
+    return tiles <= c * (2 * ctas >= sms ? 8 : 2) ? c : 0;
+  }
+  return 0;
 }
 
 // Scores of a head: the capacity in whole tiles.
@@ -1086,17 +1207,21 @@ int weight_jobs(const PagedAttnArgs& a) {
 }
 
 template <typename F, typename... A>
-cudaError_t launch_pdl(F kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_pdl(F kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1115,11 +1240,12 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
     if (dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   if (a.next) {
-    e = launch_pdl(paged_counter_kernel, dim3(1), 32, 0, st, a.next);
+    e = launch_pdl(paged_counter_kernel, dim3(1), 32, 0, st, 0, a.next);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(kernel, dim3(ctas), C::kThreads, C::kSmem, st, km, vm, a);
-  if (e != cudaSuccess || a.whole) return e;
+  e = launch_pdl(kernel, dim3(a.cluster ? a.B * a.Hkv * a.cluster : ctas), C::kThreads, C::kSmem, st, a.cluster, km, vm,
+                 a);
+  if (e != cudaSuccess || a.whole || a.cluster) return e;
   const int jobs = a.weights ? weight_jobs(a) : 0;
   // One CTA per head of a cut unit while that fills no more than the SMs twice
   // (a long sequence's unit has hundreds of pieces), else up to 8 heads each.
@@ -1127,7 +1253,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
   int hp = 1;
   while (hp < 8 && cuts * ((a.G + hp - 1) / hp) > 2 * device_sm_count()) hp *= 2;
   return launch_pdl(paged_join_kernel<kFp16, kDim>, dim3(static_cast<unsigned>(jobs + cuts * ((a.G + hp - 1) / hp))),
-                    kJoinThreads, 0, st, a, jobs, hp);
+                    kJoinThreads, 0, st, 0, a, jobs, hp);
 }
 
 template <bool kFp16, int kDim>
@@ -1174,11 +1300,13 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.status = s.status;
   const int ctas = attn_ctas(s, G), most = most_chunks(s, G, ctas);
   const bool by_unit = s.B * s.Hkv <= most;
-  a.whole = s.cap <= kWholeCap;   // then nothing is cut and nothing joined
-  a.unit_cut = !a.whole && (by_unit || accumulate) ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
-  a.chunk_cut = !a.whole && !by_unit ? reinterpret_cast<int4*>(base + w.chunk_cut) : nullptr;
-  a.chunks = a.whole ? nullptr : reinterpret_cast<int*>(base + w.counts);
-  a.next = !a.whole && hands_out(s, G, ctas) ? reinterpret_cast<int*>(base + w.counts) + 1 : nullptr;
+  a.cluster = cluster_size(s, G);
+  a.whole = !a.cluster && s.cap <= kWholeCap;   // then nothing is cut and nothing joined
+  const bool joins = !a.whole && !a.cluster;   // a second launch does
+  a.unit_cut = joins && (by_unit || accumulate) ? reinterpret_cast<int4*>(base + w.unit_cut) : nullptr;
+  a.chunk_cut = joins && !by_unit ? reinterpret_cast<int4*>(base + w.chunk_cut) : nullptr;
+  a.chunks = !joins ? nullptr : reinterpret_cast<int*>(base + w.counts);
+  a.next = joins && hands_out(s, G, ctas) ? reinterpret_cast<int*>(base + w.counts) + 1 : nullptr;
   if (s.fp16)
     return s.D == 128 ? launch_g<true, 128>(k_map, v_map, a, ctas, most, st)
                       : launch_g<true, 64>(k_map, v_map, a, ctas, most, st);
