@@ -11,7 +11,7 @@
 //
 // Measured (GB300): 8 prompts of up to 8192 tokens, 4 KV heads, 37,700 tokens in
 // all, 25.9 us, 93% of the copy rate; one token of each of 64 sequences, 8 KV
-// heads, 2.4 us in a graph, 7.2 us a call from Python.
+// heads, 2.4 us in a graph, 7.0 us a call from Python.
 #include "paged.cuh"
 
 namespace infllmv2 {
