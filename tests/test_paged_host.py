@@ -155,3 +155,72 @@ def test_python_binding_refuses(L):
         T.PagedCache(k.float(), k.float())
     with pytest.raises(T.InfLLMv2Error, match="bf16"):
         T.PagedCache(k, k.half())
+
+
+def _binding_on_cpu(monkeypatch, calls):
+    """The binding with a cache of CPU tensors and a recorder in place of the C append: (token rows' address, strides)."""
+    import torch
+    from trainable_block_sparse_infllm_gb300 import paged
+
+    class Cache(paged.PagedCache):
+        def __init__(self):
+            self.n_kv_heads, self.head_dim, self.dtype, self.index = 2, 64, torch.bfloat16, -1
+            self.device, self._ref = torch.device("cpu"), None
+            self._new_strides = (None, None)
+
+    def append(ref, batch, max_pages, n_q, k, v, strides, *rest):
+        calls.append((k, tuple(strides)))
+        return 0
+    monkeypatch.setattr(paged, "_append", append)
+    monkeypatch.setattr(paged, "_stream", lambda cache, stream: 0)
+    table, lens = torch.zeros((2, 4), dtype=torch.int32), torch.full((2,), 8, dtype=torch.int32)
+    # A prompt thread's rows are token-major, a decode thread's head-major.
+    token_major = torch.zeros((2, 8, 2, 64), dtype=torch.bfloat16).transpose(1, 2)
+    head_major = torch.zeros((2, 2, 1, 64), dtype=torch.bfloat16)
+    rows = (token_major, head_major)
+    want = {r.data_ptr(): (*r.stride()[:3], *r.stride()[:3]) for r in rows}
+    return Cache, (lambda cache, r: paged.paged_append_kv(cache, r, r, table, lens)), rows, want
+
+
+def test_append_passes_its_own_strides_when_another_call_comes_between(L, monkeypatch):
+    """Another thread's append may run between any two steps of this one: at every look at what the cache keeps."""
+    calls = []
+    Cache, append, (mine, other), want = _binding_on_cpu(monkeypatch, calls)
+
+    class Interrupted(Cache):
+        inside = False
+
+        @property
+        def _new_strides(self):
+            if not self.inside:
+                self.inside = True
+                append(self, other)
+                self.inside = False
+            return self.kept
+
+        @_new_strides.setter
+        def _new_strides(self, pair):
+            self.kept = pair
+    cache = Interrupted()
+    for _ in range(3):
+        append(cache, mine)
+    assert calls and all(strides == want[k] for k, strides in calls)
+
+
+def test_append_from_two_threads(L, monkeypatch):
+    import sys
+    import threading
+    calls = []
+    Cache, append, rows, want = _binding_on_cpu(monkeypatch, calls)
+    cache = Cache()
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=lambda r=r: [append(cache, r) for _ in range(20000)]) for r in rows]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert len(calls) == 40000 and all(strides == want[k] for k, strides in calls)

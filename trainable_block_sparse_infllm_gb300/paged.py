@@ -158,10 +158,13 @@ def paged_append_kv(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor,
         for t in (k_new, v_new):
             if t.get_device() != index and (t.is_cuda or not t.is_pinned()):
                 raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
-    if cache._new_strides[0] != strides:   # a loop's appends have the same: no new array each time
-        cache._new_strides = (strides, _Strides(*strides[0][:3], *strides[1][:3]))
+    # A loop's appends have the same strides: no new array each time.  The pair is read once and never
+    # changed, so that calls from several threads each pass their own.
+    kept = cache._new_strides
+    if kept[0] != strides:
+        cache._new_strides = kept = (strides, _Strides(*strides[0][:3], *strides[1][:3]))
     rc = _append(cache._ref, batch, max_pages, shape[2], k_new.data_ptr(), v_new.data_ptr(),
-                 cache._new_strides[1], page_table.data_ptr(), kv_lens.data_ptr(),
+                 kept[1], page_table.data_ptr(), kv_lens.data_ptr(),
                  None if n_new is None else n_new.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
                  _stream(cache, stream))
     if rc:
