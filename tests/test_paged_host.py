@@ -224,3 +224,87 @@ def test_append_from_two_threads(L, monkeypatch):
     finally:
         sys.setswitchinterval(interval)
     assert len(calls) == 40000 and all(strides == want[k] for k, strides in calls)
+
+
+def _cut_check(tmp_path):
+    """The join's check of a cut unit's record, compiled for the host."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, lib = tmp_path / "rules.cc", tmp_path / "rules.so"
+    src.write_text('#include "paged_rules.h"\nextern "C" int ok(int u, int s, int l, int p, int units, int most) '
+                   "{ return infllmv2::cut_in_range(u, s, l, p, units, most); }\n")
+    csrc = os.path.join(root, "trainable_block_sparse_infllm_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", csrc, str(src), "-o", str(lib)], check=True)
+    return ctypes.CDLL(str(lib)).ok
+
+
+def test_join_follows_no_record_out_of_the_workspace(tmp_path):
+    """Whatever an unwritten record holds: a unit that is none is not written, a place that is none not read."""
+    import random
+    ok = _cut_check(tmp_path)
+    rng = random.Random(3)
+    units, most = 7, 40
+    edge = [-2 ** 31, -78, -2, -1, 0, 1, 2, 6, 7, 8, 38, 39, 40, 41, 79, 80, 81, 2 ** 30, 2 ** 31 - 1]
+    taken = 0
+    for _ in range(200000):
+        u, s, l, p = (rng.choice(edge) if rng.random() < 0.7 else rng.randrange(-3, 90) for _ in range(4))
+        if not ok(u, s, l, p, units, most):
+            continue
+        taken += 1
+        places = [p] + [2 * k for k in range(s, l + 1)]      # what the join reads for the record
+        assert 0 <= u < units and len(places) == l - s + 2 >= 2
+        assert 0 <= min(places) and max(places) < 2 * most and len(set(places)) == len(places)
+    assert taken > 0
+
+
+def _split(lens, heads, tile, ctas, cost, counter):
+    """The line of tiles cut into chunks, as csrc/paged_attn.cu words it: (chunks, {unit: [(place, first, last tile)]})."""
+    width = [-(-n // tile) + cost if n else 0 for n in lens]
+    W = sum(width) * heads
+    n = min(ctas, W)
+    borders = [k * W // n for k in range(n + 1)] if n else [0]
+    if counter and n and W >= 32 * n:
+        A = W - W // 5
+        small = max(8, (W - A + 6 * n - 1) // (6 * n))
+        borders = [k * A // n for k in range(n + 1)]
+        borders += list(range(A + small, W, small)) + [W]
+    pieces, at, k = {}, 0, 0
+    for b, w in enumerate(width):
+        for h in range(heads if w else 0):
+            first = at + cost
+            while k + 1 < len(borders) and borders[k + 1] <= first:
+                k += 1
+            t = 0
+            while t < w - cost:
+                end = min(w - cost, borders[k + 1] - first)
+                pieces.setdefault(b * heads + h, []).append((2 * k + (first + t > borders[k]), t, end))
+                t = end
+                if first + t >= borders[k + 1]:
+                    k += 1
+            at += w
+    return len(borders) - 1, pieces
+
+
+@pytest.mark.parametrize("lens,heads,ctas,counter", [
+    ([40001], 2, 304, False), ([100 + 37 * i for i in range(60)], 8, 304, False), ([9, 0, 70000, 0, 1], 1, 152, False),
+    ([20000 + 300 * i for i in range(32)], 8, 304, True), ([600] * 400, 3, 304, True), ([1 + i % 97 for i in range(4096)], 15, 304, True),
+    ([0, 0, 131072, 5], 4, 152, True)])
+def test_join_follows_every_record_of_a_pass(tmp_path, lens, heads, ctas, counter):
+    ok = _cut_check(tmp_path)
+    chunks, pieces = _split(lens, heads, 64, ctas, 2, counter)
+    most = 7 * ctas if counter else ctas
+    assert chunks <= most
+    seen = set()
+    cut = 0
+    for unit, parts in pieces.items():
+        assert [p[1] for p in parts[1:]] == [p[2] for p in parts[:-1]] and parts[0][1] == 0
+        if len(parts) == 1:
+            continue
+        cut += 1
+        second, last = parts[1][0] // 2, parts[-1][0] // 2
+        assert [p[0] for p in parts[1:]] == [2 * k for k in range(second, last + 1)]
+        assert ok(unit, second, last, parts[0][0], len(lens) * heads, most)
+        assert not seen & {p[0] for p in parts}              # no two pieces at one place
+        seen |= {p[0] for p in parts}
+    assert cut > 0

@@ -54,6 +54,7 @@
 
 #include "paged.cuh"
 #include "kernels.h"
+#include "paged_rules.h"
 
 namespace infllmv2 {
 
@@ -87,6 +88,7 @@ struct PagedAttnArgs {
   int4* unit_cut;
   int4* chunk_cut;
   int* chunks;       // number of chunks, for the join
+  int most;          // chunks that the workspace has room for
   int* next;         // chunks handed out beyond the CTAs' first ones; null: none are
   float* lse2;       // [B Hkv G] lse in log2 units, of units that no border cut (weights only)
   float* scores;     // [B Hkv G][cap64] z in log2 units (weights only)
@@ -982,9 +984,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= jobs) {
     const int per_cut = (a.G + hp - 1) / hp, job = blockIdx.x - jobs;
-    if (a.chunk_cut && job / per_cut >= *a.chunks) return;
-    const int4 c = (a.chunk_cut ? a.chunk_cut : a.unit_cut)[job / per_cut];
-    if (c.x < 0) return;
+    const int at = job / per_cut;
+    if (a.chunk_cut && at >= *a.chunks) return;
+    const int4 c = (a.chunk_cut ? a.chunk_cut : a.unit_cut)[at];
+    if ((a.chunk_cut ? c.y : c.x) != at || !cut_in_range(c.x, c.y, c.z, c.w, a.B * a.Hkv, a.most)) return;
     const int warps = 8 / hp, warp0 = warp / warps * warps;   // a head's warps
     const int h = job % per_cut * hp + warp / warps;
     const int i = c.y, t = tid - warp0 * 32;
@@ -1062,6 +1065,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
     const int4 c = a.unit_cut[unit];
     if (c.x < 0) {
       if (tid < a.G) unit_lse2[tid] = a.lse2[unit * a.G + tid];
+    } else if (c.x != unit_i || !cut_in_range(c.x, c.y, c.z, c.w, units, a.most)) {
+      return;
     } else {
       // The pieces' (m, l): `wide` lanes read a piece's heads, 8 loads in flight.
       const int pieces = c.z - c.y + 2;
@@ -1300,6 +1305,7 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.status = s.status;
   const int ctas = attn_ctas(s, G), most = most_chunks(s, G, ctas);
   const bool by_unit = s.B * s.Hkv <= most;
+  a.most = most;
   a.cluster = cluster_size(s, G);
   a.whole = !a.cluster && s.cap <= kWholeCap;   // then nothing is cut and nothing joined
   const bool joins = !a.whole && !a.cluster;   // a second launch does
