@@ -226,23 +226,25 @@ def test_append_from_two_threads(L, monkeypatch):
     assert len(calls) == 40000 and all(strides == want[k] for k, strides in calls)
 
 
-def _cut_check(tmp_path):
-    """The join's check of a cut unit's record, compiled for the host."""
+def _rules(tmp_path):
+    """The attention kernel's rules for waits that gave up, compiled for the host."""
     import os
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     src, lib = tmp_path / "rules.cc", tmp_path / "rules.so"
     src.write_text('#include "paged_rules.h"\nextern "C" int ok(int u, int s, int l, int p, int units, int most) '
-                   "{ return infllmv2::cut_in_range(u, s, l, p, units, most); }\n")
+                   "{ return infllmv2::cut_in_range(u, s, l, p, units, most); }\n"
+                   'extern "C" unsigned first(unsigned issued, unsigned stages, int freed) '
+                   "{ return infllmv2::first_in_flight(issued, stages, freed != 0); }\n")
     csrc = os.path.join(root, "trainable_block_sparse_infllm_gb300", "csrc")
     subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", csrc, str(src), "-o", str(lib)], check=True)
-    return ctypes.CDLL(str(lib)).ok
+    return ctypes.CDLL(str(lib))
 
 
 def test_join_follows_no_record_out_of_the_workspace(tmp_path):
     """Whatever an unwritten record holds: a unit that is none is not written, a place that is none not read."""
     import random
-    ok = _cut_check(tmp_path)
+    ok = _rules(tmp_path).ok
     rng = random.Random(3)
     units, most = 7, 40
     edge = [-2 ** 31, -78, -2, -1, 0, 1, 2, 6, 7, 8, 38, 39, 40, 41, 79, 80, 81, 2 ** 30, 2 ** 31 - 1]
@@ -291,7 +293,7 @@ def _split(lens, heads, tile, ctas, cost, counter):
     ([20000 + 300 * i for i in range(32)], 8, 304, True), ([600] * 400, 3, 304, True), ([1 + i % 97 for i in range(4096)], 15, 304, True),
     ([0, 0, 131072, 5], 4, 152, True)])
 def test_join_follows_every_record_of_a_pass(tmp_path, lens, heads, ctas, counter):
-    ok = _cut_check(tmp_path)
+    ok = _rules(tmp_path).ok
     chunks, pieces = _split(lens, heads, 64, ctas, 2, counter)
     most = 7 * ctas if counter else ctas
     assert chunks <= most
@@ -308,3 +310,24 @@ def test_join_follows_every_record_of_a_pass(tmp_path, lens, heads, ctas, counte
         assert not seen & {p[0] for p in parts}              # no two pieces at one place
         seen |= {p[0] for p in parts}
     assert cut > 0
+
+
+@pytest.mark.parametrize("stages", [3, 6])
+def test_the_loading_warp_waits_for_every_copy_in_flight(tmp_path, stages):
+    """Whoever gave up: each copy that may not have landed is waited for, and no wait is for a phase gone by."""
+    first = _rules(tmp_path).first
+    for issued in range(0, 5 * stages + 1):
+        for freed in (0, 1):
+            # Known to have landed: what was consumed before the last copy's stage was taken again, and
+            # (freed: the end's stage) one more; the computing warps may have left with all others on their way.
+            known = max(0, issued - stages + freed)
+            waited = list(range(first(issued, stages, freed), issued))
+            assert set(range(known, issued)) <= set(waited)
+            for landed in range(known, issued + 1):          # copies land in order here
+                # Phases that each stage's barrier has completed; the end arrives on the next one's.
+                phases = [sum(1 for i in range(landed) if i % stages == s) for s in range(stages)]
+                if freed:
+                    phases[issued % stages] += 1
+                for i in waited:
+                    passes = phases[i % stages] % 2 != (i // stages) % 2
+                    assert passes == (i < landed)

@@ -604,18 +604,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       locate<C::kThreads>(s, a, chunk_begin(s, chunk), before);
     }
     if (!dead && !mbar_wait(empty + stage, phase ^ 1, a.status)) dead = true;
-    if (!dead) {
-      if (lane == 0) {
-        info[stage].flags = kEnd;
-        mbar_arrive(full + stage);
-      }
-    } else {
-      // A wait gave up: nothing more is issued, and the copies in flight land
-      // (or are waited for as long) before this warp leaves.
-      const uint32_t from = issued > C::kStages ? issued - C::kStages : 0;
-      for (uint32_t i = from; i < issued; ++i)
-        mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, a.status);
+    if (!dead && lane == 0) {
+      info[stage].flags = kEnd;
+      mbar_arrive(full + stage);
     }
+    // Whatever gave up, here or in the computing warps, this warp does not leave
+    // before the copies in flight have landed (or as long a wait for them).
+    for (uint32_t i = first_in_flight(issued, C::kStages, !dead); i < issued; ++i)
+      mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, a.status);
     __syncwarp();
     if (a.cluster) cluster_sync();   // with the computing warps' below
     return;

@@ -22,4 +22,11 @@ INFLLMV2_HD bool cut_in_range(int unit, int second, int last, int place, int uni
          place / 2 == second - 1;
 }
 
+// The oldest of `issued` copies through a ring of `stages` that may still be in
+// flight.  `freed`: the next stage's copy has been consumed, so it has landed.
+INFLLMV2_HD unsigned first_in_flight(unsigned issued, unsigned stages, bool freed) {
+  const unsigned most = stages - (freed ? 1 : 0);
+  return issued > most ? issued - most : 0;
+}
+
 }  // namespace infllmv2
