@@ -647,3 +647,46 @@ def test_decode_loop_under_a_budget(dev, dtype, layout, group):
                     total = int(seen[b])
                     assert len(have) == n
                     assert set(range(min(4, total))) | set(range(max(0, total - 16), total)) <= have
+
+
+# ------------------------------------------------------------ large scores ------
+
+HUGE = {"fp16": (60000.0, [60000, 45024, 52000, 38016, 47008, 64992, 35008, 57984]),
+        "bf16": (163840.0, [163840, 204800, 139264, 188416, 344064, 155648, 237568, 253952])}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group", [(128, 8), (128, 16), (64, 24)])
+@pytest.mark.parametrize("n,spare", [(200, 0), (300, 2), (5000, 2)])      # uncut, clusters, joined
+def test_scores_of_any_finite_size(dev, dtype, dim, group, n, spare):
+    """Scores of 10^8 and more, exact in fp32: equal ones share the attention, smaller ones get none.
+
+    One dimension holds all of q and k, so a score is one exact product.  p is then 1 / (number of largest
+    scores) or 0: what is left of the helper's tolerances is 2^-16 + 2^-19 of the magnitudes and the output's
+    rounding; for lse three roundings of relative 2^-24 and the logarithm's, below 2^-20 |lse| + 2^-20.
+    """
+    import torch
+    from paged_helpers import Pool
+    q0, keys = HUGE[dtype]
+    batch = len(keys)
+    pool = Pool(dev, dtype, "hnd", 1, dim, 64, [n] * batch, spare_entries=spare, seed=40, metadata=False)
+    q = torch.zeros((batch, 1, group, dim), dtype=pool.dtype, device=dev)
+    q[..., 0] = q0
+    scale = dim ** -0.5
+    want = torch.empty((batch, dim), dtype=torch.float64, device=dev)
+    mag = torch.empty_like(want)
+    top = torch.arange(n, device=dev) % 3 != 1
+    for b, key in enumerate(keys):
+        at, row = pool.places(b, n)
+        pool.k[at, :, row] = 0.0
+        pool.k[at, 0, row, 0] = torch.where(top, float(key), key * 0.5).to(pool.dtype)
+        v = pool.v[at, 0, row].double()[top]
+        want[b], mag[b] = v.mean(dim=0), v.abs().mean(dim=0)
+    _, out, lse = _attn(pool, group, accumulate=False, q=q)
+    assert _status() == 0
+    info = torch.finfo(pool.dtype)
+    tol = (2.0 ** -16 + 2.0 ** -19) * mag + info.eps / 2 * 1.001 * want.abs() + info.tiny * info.eps / 2
+    assert torch.isfinite(out).all()
+    assert ((out[:, 0].double() - want[:, None]).abs() <= tol[:, None]).all()
+    z = q0 * torch.tensor(keys, dtype=torch.float64, device=dev) * scale + math.log(int(top.sum()))
+    assert ((lse[:, 0].double() - z[:, None]).abs() <= 2.0 ** -20 * z[:, None].abs() + 2.0 ** -20).all()

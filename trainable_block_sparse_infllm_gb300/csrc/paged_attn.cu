@@ -36,7 +36,11 @@
 // of mma.m16n8k16: at these intensities the tensor pipe idles and a tcgen05
 // tile (128 rows) would be seven eighths empty.
 //
-// Types.  z, maxima, sums and accumulators are fp32.  A probability feeds the
+// Types.  z, maxima, sums and accumulators are fp32.  Maxima are those of the
+// unscaled scores, and a score is scaled after the maximum is taken off: of the
+// largest that leaves 0, whatever its size.  (exp2(z scale - m), with m the rounded
+// product, is 2^(half a step of m), which passes fp16's range from scores of 2^25
+// and fp32's from 2^31.)  A probability feeds the
 // product with V as two 16-bit parts (hi + lo, 16 to 22 significant bits): one
 // rounding of it to bf16 would cost as much again as the output's own.  With
 // up to 8 heads the lo parts fill the rows 8..15 that would be empty; with
@@ -80,7 +84,7 @@ struct PagedAttnArgs {
   float* lse;
   float* weights;    // null: not accumulated
   float* part_o;     // [2 chunks][G][D]: pieces of cut units, relative to their m
-  float2* part_ml;   // [2 chunks][32]: (m in log2 units, l)
+  float2* part_ml;   // [2 chunks][32]: (m of the unscaled scores, l)
   // Cut units, (unit or -1, chunk of the second piece, last chunk, first
   // piece's place).  unit_cut, by unit, is kept where there are no more units
   // than chunks or weights are summed; chunk_cut, by the chunk that the second
@@ -337,6 +341,13 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
   } else {
     return pack_bf16x2(x, y);
   }
+}
+
+// lse in log2 units of a sum relative to the maximum m of the unscaled scores.
+// fp16 probabilities, and so their sum, carry a factor 2^14.
+template <bool kFp16>
+__device__ __forceinline__ float lse_of(float m, float sum, float scale2) {
+  return fmaf(m, scale2, log2f(sum) - (kFp16 ? 14.f : 0.f));
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int c1, int c2, int c3,
@@ -736,11 +747,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
                                fmaxf(z[sub][1][2 * r], z[sub][1][2 * r + 1])));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx = fmaxf(mx * a.scale2, m[r]);
-        const float use = mx == -INFINITY ? 0.f : mx;
-        alpha[r] = fast_exp2(m[r] - use);
+        mx = fmaxf(mx, m[r]);
+        base[r] = mx == -INFINITY ? 0.f : mx;
+        alpha[r] = fast_exp2((m[r] - base[r]) * a.scale2);
         m[r] = mx;
-        base[r] = kFp16 ? use - 14.f : use;   // fp16: probabilities times 2^14
         l[r] *= alpha[r];
       }
       if constexpr (kStack) alpha[1] = alpha[0];
@@ -759,10 +769,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int r = 0; r < (kStack ? 1 : 2); ++r) {
-          const float p0 = fast_exp2(fmaf(z[sub][0][2 * r], a.scale2, -base[r]));
-          const float p1 = fast_exp2(fmaf(z[sub][0][2 * r + 1], a.scale2, -base[r]));
-          const float p2 = fast_exp2(fmaf(z[sub][1][2 * r], a.scale2, -base[r]));
-          const float p3 = fast_exp2(fmaf(z[sub][1][2 * r + 1], a.scale2, -base[r]));
+          constexpr float kUp = kFp16 ? 14.f : 0.f;   // fp16: probabilities times 2^14
+          const float p0 = fast_exp2(fmaf(z[sub][0][2 * r] - base[r], a.scale2, kUp));
+          const float p1 = fast_exp2(fmaf(z[sub][0][2 * r + 1] - base[r], a.scale2, kUp));
+          const float p2 = fast_exp2(fmaf(z[sub][1][2 * r] - base[r], a.scale2, kUp));
+          const float p3 = fast_exp2(fmaf(z[sub][1][2 * r + 1] - base[r], a.scale2, kUp));
           l[r] += (p0 + p1) + (p2 + p3);
           split_pair<kFp16>(p0, p1, hi[r], lo[r]);
           split_pair<kFp16>(p2, p3, hi[2 + r], lo[2 + r]);
@@ -824,7 +835,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           const int row = g + 8 * r;
           float mx = fmaxf(fmaxf(ml[row].x, ml[16 + row].x), fmaxf(ml[32 + row].x, ml[48 + row].x));
           if (mx == -INFINITY) mx = 0.f;
-          const float f = fast_exp2(m[r] - mx);
+          const float f = fast_exp2((m[r] - mx) * a.scale2);
           float* to = buf + (w * kRows + row) * kDim;
           // Columns are permuted by row so that the 8 rows of a store meet
           // different banks.
@@ -852,7 +863,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           const float use = mx == -INFINITY ? 0.f : mx;
           float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum += ml[i * 16 + row].y * fast_exp2(ml[i * 16 + row].x - use);
+          for (int i = 0; i < 4; ++i) sum += ml[i * 16 + row].y * fast_exp2((ml[i * 16 + row].x - use) * a.scale2);
           const long long head = unit * a.G + head0 + row;
           if (whole) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -861,8 +872,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
             z.y = pack_pair<kFp16>(y.z * inv, y.w * inv);
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + c) = z;
             if (c == 0) {
-              // fp16 probabilities, and so the sum, carry a factor 2^14.
-              const float lse2 = use + log2f(sum) - (kFp16 ? 14.f : 0.f);
+              const float lse2 = lse_of<kFp16>(use, sum, a.scale2);
               if (a.lse) a.lse[head] = lse2 * 0.6931471805599453f;
               if (a.whole || a.cluster)
                 unit_lse2[head0 + row] = lse2;
@@ -924,7 +934,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float nm = fmaxf(mx, v[e].x), use = nm == -INFINITY ? 0.f : nm;
-          const float f = fast_exp2(mx - use), f2 = fast_exp2(v[e].x - use);
+          const float f = fast_exp2((mx - use) * a.scale2), f2 = fast_exp2((v[e].x - use) * a.scale2);
           mx = nm;
           sum = sum * f + v[e].y * f2;
           x.x = x.x * f + y[e].x * f2;
@@ -942,7 +952,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + lane * 4) = y;
       }
-      if (lane == 0 && a.lse) a.lse[head] = (use + log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
+      if (lane == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2) * 0.6931471805599453f;
     }
     if (a.weights && tid < a.G) {
       float mx = -INFINITY, sum = 0.f;
@@ -950,10 +960,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         if (!has(r)) continue;
         const float2 v = __ldcg(a.part_ml + static_cast<long long>(unit * a.cluster + r) * kPagedMaxGroup + tid);
         const float nm = fmaxf(mx, v.x), use = nm == -INFINITY ? 0.f : nm;
-        sum = sum * fast_exp2(mx - use) + v.y * fast_exp2(v.x - use);
+        sum = sum * fast_exp2((mx - use) * a.scale2) + v.y * fast_exp2((v.x - use) * a.scale2);
         mx = nm;
       }
-      unit_lse2[tid] = (mx == -INFINITY ? 0.f : mx) + log2f(sum) - (kFp16 ? 14.f : 0.f);
+      unit_lse2[tid] = lse_of<kFp16>(mx == -INFINITY ? 0.f : mx, sum, a.scale2);
     }
   }
   if (a.weights && mine && sync(group_bar + kGroups, all_phase))
@@ -995,10 +1005,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
     const int col = t % kLanes, part = t / kLanes;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float mx = -INFINITY, sum = 0.f;
-    // Merges a sum relative to 2^m2 into (mx, sum, x).
+    // Merges a sum relative to the maximum m2 into (mx, sum, x).
     auto merge = [&](float m2, float s2, float4 x2) {
       const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
-      const float f = fast_exp2(mx - use), f2 = fast_exp2(m2 - use);
+      const float f = fast_exp2((mx - use) * a.scale2), f2 = fast_exp2((m2 - use) * a.scale2);
       mx = nm;
       sum = sum * f + s2 * f2;
       x.x = x.x * f + x2.x * f2;
@@ -1045,7 +1055,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
       y.x = pack_pair<kFp16>(x.x * inv, x.y * inv);
       y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + t * 4) = y;
-      if (t == 0 && a.lse) a.lse[head] = (use + log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
+      if (t == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2) * 0.6931471805599453f;
     }
     return;
   }
@@ -1081,15 +1091,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
 #pragma unroll
         for (int e = 0; e < 8; ++e) nm = fmaxf(nm, v[e].x);
         const float use = nm == -INFINITY ? 0.f : nm;
-        sum *= fast_exp2(mx - use);
+        sum *= fast_exp2((mx - use) * a.scale2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += v[e].y * fast_exp2(v[e].x - use);
+        for (int e = 0; e < 8; ++e) sum += v[e].y * fast_exp2((v[e].x - use) * a.scale2);
         mx = nm;
       }
       for (int o = wide; o < 32; o <<= 1) {   // rows within the warp
         const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
         const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
-        sum = sum * fast_exp2(mx - use) + s2 * fast_exp2(m2 - use);
+        sum = sum * fast_exp2((mx - use) * a.scale2) + s2 * fast_exp2((m2 - use) * a.scale2);
         mx = nm;
       }
       red_ml[warp][lane] = make_float2(mx, sum);
@@ -1101,8 +1111,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
         const float use = all == -INFINITY ? 0.f : all;
         float l = 0.f;
 #pragma unroll
-        for (int j = 0; j < kJoinThreads / 32; ++j) l += red_ml[j][lane].y * fast_exp2(red_ml[j][lane].x - use);
-        unit_lse2[lane] = use + log2f(l) - (kFp16 ? 14.f : 0.f);
+        for (int j = 0; j < kJoinThreads / 32; ++j) l += red_ml[j][lane].y * fast_exp2((red_ml[j][lane].x - use) * a.scale2);
+        unit_lse2[lane] = lse_of<kFp16>(use, l, a.scale2);
       }
     }
     __syncthreads();
