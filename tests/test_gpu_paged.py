@@ -690,3 +690,42 @@ def test_scores_of_any_finite_size(dev, dtype, dim, group, n, spare):
     assert ((out[:, 0].double() - want[:, None]).abs() <= tol[:, None]).all()
     z = q0 * torch.tensor(keys, dtype=torch.float64, device=dev) * scale + math.log(int(top.sum()))
     assert ((lse[:, 0].double() - z[:, None]).abs() <= 2.0 ** -20 * z[:, None].abs() + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group", [(128, 4), (64, 16), (128, 20)])
+@pytest.mark.parametrize("n,spare", [(200, 0), (1000, 2), (5000, 2)])     # uncut, clusters, joined
+def test_weights_of_large_scores(dev, dtype, dim, group, n, spare):
+    """Scores around 4000 to 6000 that are exact in fp32: a call's weights are the softmax's and sum to the heads.
+
+    Two dimensions hold q and k: an offset of about 45,000 and a whole number in [-64, 64), so z - m is exact.
+    Relative errors in units of 2^-24: the scale in base 2 and its product, 3 |x| ln 2 < 48 for |x| < 23.1, in a
+    slot's term and again in the sum it is divided by; 4 for each exp2, merges included, 20 in all; fewer than 80
+    additions in a row in the sum; 32 over the heads; the division and products, 4.  Together below 256, 2^-16.
+    """
+    import torch
+    from paged_helpers import Pool
+    heads, batch = 2, 2
+    pool = Pool(dev, dtype, "nhd", heads, dim, 64, [n] * batch, spare_entries=spare, seed=41)
+    q = torch.zeros((batch, 1, heads * group, dim), dtype=pool.dtype, device=dev)
+    q[..., 0] = 200.0 + torch.arange(heads * group, device=dev) % 50      # each head an lse of its own
+    q[..., 1] = 8.0
+    scale = float(torch.tensor(dim ** -0.5, dtype=torch.float32))
+    small = torch.randint(-64, 64, (batch, n, heads), generator=pool.gen, device=dev)
+    want = torch.full_like(pool.weights, float("nan"), dtype=torch.float64)
+    for b in range(batch):
+        at, row = pool.places(b, n)
+        pool.k[at, :, row] = 0.0
+        pool.k[at, :, row, 0] = 214.0
+        pool.k[at, :, row, 1] = (small[b] / 8).to(pool.dtype)
+        pool.weights[at, :, row] = 0.0
+        want[at, :, row] = group * torch.softmax(small[b].double() * scale, dim=0)
+    _attn(pool, group, q=q, scale=scale)
+    assert _status() == 0
+    used = ~torch.isnan(want)
+    got = pool.weights.double()
+    off = ((got - want).abs() / want)[used].max().item()
+    assert off <= 2.0 ** -16, f"weights off by {off} of their value"
+    for b in range(batch):
+        at, row = pool.places(b, n)
+        assert ((got[at, :, row].sum(dim=0) / group - 1).abs() <= 2.0 ** -16).all()

@@ -94,8 +94,8 @@ struct PagedAttnArgs {
   int* chunks;       // number of chunks, for the join
   int most;          // chunks that the workspace has room for
   int* next;         // chunks handed out beyond the CTAs' first ones; null: none are
-  float* lse2;       // [B Hkv G] lse in log2 units, of units that no border cut (weights only)
-  float* scores;     // [B Hkv G][cap64] z in log2 units (weights only)
+  float2* unit_ml;   // [B Hkv G] (m, 1 / l) of units that no border cut (weights only)
+  float* scores;     // [B Hkv G][cap64] z, unscaled (weights only)
   int cap64;         // scores of a head: cap rounded up to whole tiles
   int whole;         // no unit is cut: one launch
   int cluster;       // CTAs of a cluster per unit, which join their pieces themselves: one launch; 0: none
@@ -343,11 +343,17 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
   }
 }
 
-// lse in log2 units of a sum relative to the maximum m of the unscaled scores.
-// fp16 probabilities, and so their sum, carry a factor 2^14.
+// lse of a sum relative to the maximum m of the unscaled scores.  fp16
+// probabilities, and so their sum, carry a factor 2^14.
 template <bool kFp16>
 __device__ __forceinline__ float lse_of(float m, float sum, float scale2) {
-  return fmaf(m, scale2, log2f(sum) - (kFp16 ? 14.f : 0.f));
+  return fmaf(m, scale2, log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
+}
+
+// What add_weights needs of a head; nothing attended weighs nothing.
+template <bool kFp16>
+__device__ __forceinline__ float2 m_and_inverse(float m, float sum) {
+  return make_float2(m == -INFINITY ? 0.f : m, sum == 0.f ? 0.f : (kFp16 ? 16384.f : 1.f) / sum);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int c1, int c2, int c3,
@@ -365,9 +371,11 @@ __device__ __forceinline__ int by_order(PagedMapOrder o, int dim, int token, int
 
 
 // Adds the weights of slots `first`, + `step`, ... (four each) of a unit, from
-// the z of its heads and their lse.
+// the z of its heads and their (m, 1 / l): exp(scale (z - m)) / l as for the
+// output.  (exp2(z - lse) with an lse of one float loses what lse's size takes
+// from it: at |lse| = 4000 every weight of a head was off by up to 1.7e-4.)
 __device__ __forceinline__ void add_weights(const PagedAttnArgs& a, long long unit, int b, int kv_head, int len, int first,
-                                            int step, const float* lse2) {
+                                            int step, const float2* ml) {
   const int32_t* table = a.table + static_cast<long long>(b) * a.maxp;
   for (int slot = first; slot < len; slot += step) {   // the four share a page (pages hold multiples of 16)
     const int page = __ldg(table + slot / a.ps);
@@ -376,11 +384,11 @@ __device__ __forceinline__ void add_weights(const PagedAttnArgs& a, long long un
 #pragma unroll 8
     for (int h = 0; h < a.G; ++h) {
       const float4 x = __ldcs(reinterpret_cast<const float4*>(z + static_cast<long long>(h) * a.cap64));
-      const float l = lse2[h];
-      w.x += fast_exp2(x.x - l);
-      w.y += fast_exp2(x.y - l);
-      w.z += fast_exp2(x.z - l);
-      w.w += fast_exp2(x.w - l);
+      const float2 y = ml[h];
+      w.x += fast_exp2((x.x - y.x) * a.scale2) * y.y;
+      w.y += fast_exp2((x.y - y.x) * a.scale2) * y.y;
+      w.z += fast_exp2((x.z - y.x) * a.scale2) * y.y;
+      w.w += fast_exp2((x.w - y.x) * a.scale2) * y.y;
     }
     if (page < 0 || page >= a.P) continue;
     // One add per slot of a call, so that a cache's own pages sum in a fixed
@@ -430,8 +438,8 @@ struct AttnCfg {
   static constexpr int kQOff = kStages * kStage;
   static constexpr int kInfoOff = kQOff + kStages * kQ;
   static constexpr int kMlOff = kInfoOff + kStages * static_cast<int>(sizeof(StageInfo));
-  static constexpr int kLseOff = kMlOff + kGroups * 4 * 16 * 8;      // a whole unit's lse in log2 units
-  static constexpr int kBeforeOff = kLseOff + kPagedMaxGroup * 4;
+  static constexpr int kUnitOff = kMlOff + kGroups * 4 * 16 * 8;     // a whole unit's (m, 1 / l)
+  static constexpr int kBeforeOff = kUnitOff + kPagedMaxGroup * 8;
   static constexpr int kSplitOff = kBeforeOff + (kThreads + 1) * 8;
   static constexpr int kBarOff = kSplitOff + 128;
   static constexpr int kSmem = 1024 + kBarOff + (2 * kStages + kGroups + 1) * 8;
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
   const int g = lane >> 2, t4 = lane & 3;          // rows g and g + 8; columns 2 t4, 2 t4 + 1
   const int head0 = group * 16;                    // first head of the group within the KV head's
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff) + group * 64;   // [4 warps][16 rows]
-  float* unit_lse2 = reinterpret_cast<float*>(smem + C::kLseOff);
+  float2* unit_ml = reinterpret_cast<float2*>(smem + C::kUnitOff);
   const bool row0 = head0 + g < a.G, row1 = !kStack && head0 + g + 8 < a.G;
   int stage = 0;
   uint32_t phase = 0, group_phase = 0, all_phase = 0;
@@ -732,8 +740,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
               float* to = sc + static_cast<long long>(g + 8 * r) * a.cap64 + sub * 16;
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<float2*>(to + 8 * j) =
-                    make_float2(z[sub][j][2 * r] * a.scale2, z[sub][j][2 * r + 1] * a.scale2);
+                *reinterpret_cast<float2*>(to + 8 * j) = make_float2(z[sub][j][2 * r], z[sub][j][2 * r + 1]);
             }
       }
       float alpha[2];
@@ -872,12 +879,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
             z.y = pack_pair<kFp16>(y.z * inv, y.w * inv);
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + c) = z;
             if (c == 0) {
-              const float lse2 = lse_of<kFp16>(use, sum, a.scale2);
-              if (a.lse) a.lse[head] = lse2 * 0.6931471805599453f;
+              if (a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2);
               if (a.whole || a.cluster)
-                unit_lse2[head0 + row] = lse2;
+                unit_ml[head0 + row] = m_and_inverse<kFp16>(mx, sum);
               else if (a.weights)
-                a.lse2[head] = lse2;
+                a.unit_ml[head] = m_and_inverse<kFp16>(mx, sum);
             }
           } else {
             *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(place) * a.G + head0 + row) * kDim + c) = y;
@@ -892,7 +898,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     // (The barrier also orders the z that every warp has stored and the lse.)
     if (a.whole && a.weights)
       add_weights(a, unit, info[stage].b, info[stage].unit - info[stage].b * a.Hkv, info[stage].len, 4 * tid,
-                  4 * 128 * kGroups, unit_lse2);
+                  4 * 128 * kGroups, unit_ml);
     if (!ok) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + stage);
@@ -952,7 +958,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + lane * 4) = y;
       }
-      if (lane == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2) * 0.6931471805599453f;
+      if (lane == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2);
     }
     if (a.weights && tid < a.G) {
       float mx = -INFINITY, sum = 0.f;
@@ -963,11 +969,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         sum = sum * fast_exp2((mx - use) * a.scale2) + v.y * fast_exp2((v.x - use) * a.scale2);
         mx = nm;
       }
-      unit_lse2[tid] = lse_of<kFp16>(mx == -INFINITY ? 0.f : mx, sum, a.scale2);
+      unit_ml[tid] = m_and_inverse<kFp16>(mx, sum);
     }
   }
   if (a.weights && mine && sync(group_bar + kGroups, all_phase))
-    add_weights(a, unit, p.b, p.h, min(p.len, p.tile1 * kTile), p.tile0 * kTile + 4 * tid, 4 * 128 * kGroups, unit_lse2);
+    add_weights(a, unit, p.b, p.h, min(p.len, p.tile1 * kTile), p.tile0 * kTile + 4 * tid, 4 * 128 * kGroups, unit_ml);
 }
 
 // ---- the join -----------------------------------------------------------------
@@ -976,14 +982,14 @@ constexpr int kJoinThreads = 256;
 constexpr int kChunk = 4 * kJoinThreads;   // slots that a CTA of the weights' part takes at once
 
 // The first `jobs` CTAs (weights only), as many for every unit, add each slot's
-// weight, from the z that the pass left and the unit's lse: CTA y of a unit
+// weight, from the z that the pass left and the unit's (m, l): CTA y of a unit
 // takes chunks y, y + jobs / units, ... of it.  The CTAs behind them join `hp`
 // heads (a power of two up to 8) of one cut unit each.
 template <bool kFp16, int kDim>
 __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const PagedAttnArgs a, int jobs, int hp) {
   __shared__ float red_m[8], red_l[8];
   __shared__ float4 red_o[8][kDim / 4];
-  __shared__ float unit_lse2[kPagedMaxGroup];
+  __shared__ float2 unit_ml[kPagedMaxGroup];
   __shared__ float2 red_ml[kJoinThreads / 32][kPagedMaxGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -1055,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
       y.x = pack_pair<kFp16>(x.x * inv, x.y * inv);
       y.y = pack_pair<kFp16>(x.z * inv, x.w * inv);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * kDim + t * 4) = y;
-      if (t == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2) * 0.6931471805599453f;
+      if (t == 0 && a.lse) a.lse[head] = lse_of<kFp16>(use, sum, a.scale2);
     }
     return;
   }
@@ -1070,7 +1076,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
   {
     const int4 c = a.unit_cut[unit];
     if (c.x < 0) {
-      if (tid < a.G) unit_lse2[tid] = a.lse2[unit * a.G + tid];
+      if (tid < a.G) unit_ml[tid] = a.unit_ml[unit * a.G + tid];
     } else if (c.x != unit_i || !cut_in_range(c.x, c.y, c.z, c.w, units, a.most)) {
       return;
     } else {
@@ -1112,12 +1118,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
         float l = 0.f;
 #pragma unroll
         for (int j = 0; j < kJoinThreads / 32; ++j) l += red_ml[j][lane].y * fast_exp2((red_ml[j][lane].x - use) * a.scale2);
-        unit_lse2[lane] = lse_of<kFp16>(use, l, a.scale2);
+        unit_ml[lane] = m_and_inverse<kFp16>(all, l);
       }
     }
     __syncthreads();
   }
-  add_weights(a, unit, b, kv_head, len, y * kChunk + 4 * tid, step * kChunk, unit_lse2);
+  add_weights(a, unit, b, kv_head, len, y * kChunk + 4 * tid, step * kChunk, unit_ml);
 }
 
 // The count of chunks handed out starts at 0.
@@ -1189,7 +1195,7 @@ bool hands_out(const PagedShape& s, int G, int ctas) {
 int most_chunks(const PagedShape& s, int G, int ctas) { return hands_out(s, G, ctas) ? 7 * ctas : ctas; }
 
 struct WsLayout {
-  size_t counts, unit_cut, chunk_cut, ml, o, lse2, scores, total;
+  size_t counts, unit_cut, chunk_cut, ml, o, unit_ml, scores, total;
 };
 
 WsLayout ws_layout(const PagedShape& s, int G) {
@@ -1202,8 +1208,8 @@ WsLayout ws_layout(const PagedShape& s, int G) {
   w.chunk_cut = w.unit_cut + up(units * sizeof(int4));
   w.ml = w.chunk_cut + up(n * sizeof(int4));
   w.o = w.ml + up(2 * n * kPagedMaxGroup * sizeof(float2));
-  w.lse2 = w.o + up(2 * n * G * s.D * sizeof(float));
-  w.scores = w.lse2 + (s.weights ? up(heads * sizeof(float)) : 0);
+  w.unit_ml = w.o + up(2 * n * G * s.D * sizeof(float));
+  w.scores = w.unit_ml + (s.weights ? up(heads * sizeof(float2)) : 0);
   w.total = w.scores + (s.weights ? up(heads * row * sizeof(float)) : 0);
   return w;
 }
@@ -1304,7 +1310,7 @@ cudaError_t launch_paged_attn(const PagedShape& s, int G, const CUtensorMap& k_m
   a.weights = accumulate ? s.weights : nullptr;
   a.part_ml = reinterpret_cast<float2*>(base + w.ml);
   a.part_o = reinterpret_cast<float*>(base + w.o);
-  a.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  a.unit_ml = reinterpret_cast<float2*>(base + w.unit_ml);
   a.scores = reinterpret_cast<float*>(base + w.scores);
   a.cap64 = static_cast<int>(score_row(s, G));
   a.tile_shift = tile_shift_of(s, G);
