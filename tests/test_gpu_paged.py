@@ -729,3 +729,97 @@ def test_weights_of_large_scores(dev, dtype, dim, group, n, spare):
     for b in range(batch):
         at, row = pool.places(b, n)
         assert ((got[at, :, row].sum(dim=0) / group - 1).abs() <= 2.0 ** -16).all()
+
+
+# ----------------------------------------------------- infinities in attended rows ------
+
+STRANGE = [("bf16", 128, 4), ("fp16", 128, 4), ("bf16", 64, 16), ("fp16", 64, 16), ("bf16", 128, 24), ("fp16", 64, 20)]
+
+
+def _check_weights(pool, q, before, scale, skip=()):
+    """The added weights of all sequences but those in `skip`, within the helper's tolerance."""
+    from paged_helpers import attend
+    _, _, added = attend(pool, q, scale)
+    for b, (x, tol) in enumerate(added):
+        if b in skip:
+            continue
+        at, row = pool.places(b, x.shape[0])
+        want = before[at, :, row].double() + x
+        room = tol + 2.0 ** -24 * want.abs()
+        assert ((pool.weights[at, :, row].double() - want).abs() <= room).all()
+
+
+@pytest.mark.parametrize("dtype,dim,group", STRANGE)
+@pytest.mark.parametrize("n,spare", [(200, 0), (1000, 2), (9000, 2)])     # uncut, clusters, joined
+def test_infinite_values(dev, dtype, dim, group, n, spare):
+    """An infinity in an attended value row fills its column of out, two of both signs make NaN, and no more."""
+    import torch
+    from paged_helpers import Pool, attend
+    pool = Pool(dev, dtype, "hnd", 2, dim, 64, [n, n, n], spare_entries=spare, seed=42)
+    at, row = pool.places(1, n)
+    inf = float("inf")
+    put = [(3, 7, inf), (n // 2, 7, inf), (n - 1, 20, -inf), (5, 33, inf), (n - 2, 33, -inf), (n // 3, 50, float("nan"))]
+    for slot, column, value in put:
+        pool.v[at[slot], :, row[slot], column] = value
+    before = pool.weights.clone()
+    q, out, lse = _attn(pool, group)
+    assert _status() == 0
+    got = out[1, 0]
+    assert (got[:, 7] == inf).all() and (got[:, 20] == -inf).all()
+    assert torch.isnan(got[:, 33]).all() and torch.isnan(got[:, 50]).all()
+    for slot, column, _ in put:                      # the rest is as with zeros there
+        pool.v[at[slot], :, row[slot], column] = 0.0
+    (o, tol), (z, z_tol), _ = attend(pool, q, dim ** -0.5)
+    strange = torch.zeros(o.shape, dtype=torch.bool, device=dev)
+    strange[1, 0, :, [7, 20, 33, 50]] = True
+    assert (((out.double() - o).abs() <= tol) | strange).all()
+    assert ((lse.double() - z).abs() <= z_tol).all()
+    _check_weights(pool, q, before, dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,dim,group", STRANGE)
+@pytest.mark.parametrize("n,spare", [(200, 0), (1000, 2), (9000, 2)])
+def test_infinite_keys(dev, dtype, dim, group, n, spare):
+    """A score of -inf takes no part; one of +inf makes its own sequence's heads NaN and no other's."""
+    import torch
+    from paged_helpers import Pool, attend
+    pool = Pool(dev, dtype, "hnd", 2, dim, 64, [n, n, n], spare_entries=spare, seed=43)
+    q = pool.normal(3, 1, 2 * group, dim)
+    q[..., 11] = q[..., 11].abs() + 0.5
+    (at, row), (at2, row2) = pool.places(0, n), pool.places(1, n)
+    gone = torch.arange(n, device=dev) % 7 == 3
+    pool.k[at[gone], :, row[gone], 11] = -float("inf")
+    pool.k[at2[n // 2], :, row2[n // 2], 11] = float("inf")
+    before = pool.weights.clone()
+    _, out, lse = _attn(pool, group, q=q)
+    assert _status() == 0
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.equal(pool.weights[at[gone], :, row[gone]], before[at[gone], :, row[gone]])
+    # Sequence 0 in the plain form: over the slots that are left, moved to the front of a table of their own.
+    left = int((~gone).sum())
+    kept = [t[at[~gone], :, row[~gone]].clone() for t in (pool.k, pool.v, before, pool.weights)]
+    head, first = pool.places(0, left)
+    for t, x in zip((pool.k, pool.v, before, pool.weights), kept):
+        t[head, :, first] = x
+    pool.k[at2[n // 2], :, row2[n // 2], 11] = 0.0
+    pool.lens = torch.tensor([left, n, n], dtype=torch.int32, device=dev)
+    (o, tol), (z, z_tol), _ = attend(pool, q, dim ** -0.5)
+    for b in (0, 2):
+        assert ((out[b].double() - o[b]).abs() <= tol[b]).all() and ((lse[b].double() - z[b]).abs() <= z_tol[b]).all()
+    _check_weights(pool, q, before, dim ** -0.5, skip=(1,))
+
+
+@pytest.mark.parametrize("dtype,dim,group", STRANGE)
+def test_nan_leaves_other_sequences_weights(dev, dtype, dim, group):
+    import torch
+    from paged_helpers import Pool
+    pool = Pool(dev, dtype, "nhd", 2, dim, 16, [100, 100, 100], seed=44)
+    at, row = pool.places(1, 100)
+    pool.k[at[50], 1, row[50], 3] = float("nan")     # one KV head of one sequence
+    before = pool.weights.clone()
+    q, out, lse = _attn(pool, group)
+    assert _status() == 0
+    assert torch.isnan(out[1, 0, group:]).all() and torch.isnan(lse[1, 0, group:]).all()
+    assert torch.isfinite(out[:, :, :group]).all() and torch.isfinite(out[[0, 2]]).all()
+    pool.k[at[50], 1, row[50], 3] = 0.0
+    _check_weights(pool, q, before, dim ** -0.5, skip=(1,))

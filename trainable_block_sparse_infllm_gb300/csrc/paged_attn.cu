@@ -41,7 +41,7 @@
 // largest that leaves 0, whatever its size.  (exp2(z scale - m), with m the rounded
 // product, is 2^(half a step of m), which passes fp16's range from scores of 2^25
 // and fp32's from 2^31.)  A probability feeds the
-// product with V as two 16-bit parts (hi + lo, 16 to 22 significant bits): one
+// product with V as two 16-bit parts (hi + lo, to 2^-16 of it or better): one
 // rounding of it to bf16 would cost as much again as the output's own.  With
 // up to 8 heads the lo parts fill the rows 8..15 that would be empty; with
 // more they are a second product (a unit of 256 slots, d 128, alone on its SM:
@@ -318,18 +318,25 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
   }
 }
 
-// Two floats as 16-bit parts: hi = their roundings, lo = the rest's.
+// Two probabilities as 16-bit parts, x = hi + lo to 2^-16 (bf16) or 2^-19 (fp16).
+// Both parts of a positive x are positive: with hi the nearest, lo would be zero
+// or negative as often as not, and an infinite v in an attended row would end as
+// 0 * inf or inf - inf.  (In fp16 lo is positive from x = 2^-14 on, a probability
+// of 2^-28; in bf16 from 2^-110 on.)
 template <bool kFp16>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
   if constexpr (kFp16) {
-    const __half2 h = __floats2half2_rn(x, y);
+    const __half2 h = __hmul2(__floats2half2_rn(x, y), __float2half2_rn(1.f - 0x1p-9f));   // 1 to 5 steps below x
     const float2 f = __half22float2(h);
     const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&l);
   } else {
-    hi = pack_bf16x2(x, y);
-    lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+    const uint32_t bx = __float_as_uint(x), by = __float_as_uint(y);
+    hi = __byte_perm(bx, by, 0x7632);   // cut off
+    constexpr float kAbove = 1.f + 0x1p-23f;
+    lo = pack_bf16x2(fmaf(x, kAbove, -__uint_as_float(bx & 0xffff0000u)),
+                     fmaf(y, kAbove, -__uint_as_float(by & 0xffff0000u)));
   }
 }
 
