@@ -823,3 +823,100 @@ def test_nan_leaves_other_sequences_weights(dev, dtype, dim, group):
     assert torch.isfinite(out[:, :, :group]).all() and torch.isfinite(out[[0, 2]]).all()
     pool.k[at[50], 1, row[50], 3] = 0.0
     _check_weights(pool, q, before, dim ** -0.5, skip=(1,))
+
+
+# -------------------------------------- more sequences than a CTA has threads ------
+
+@pytest.mark.parametrize("batch,dtype,heads,group,dim,page,high,spare", [
+    (161, "bf16", 2, 8, 64, 16, 300, 0),        # equal chunks; 160 threads
+    (161, "fp16", 2, 4, 128, 64, 4000, 100),    # chunks from the counter
+    (289, "bf16", 2, 20, 128, 16, 400, 0),      # equal chunks; 288 threads
+    (289, "bf16", 1, 20, 64, 32, 4500, 150),    # chunks from the counter
+    (4096, "bf16", 2, 4, 64, 16, 60, 40),       # chunks from the counter, more units than chunks
+    (4096, "fp16", 1, 3, 128, 16, 100, 12),     # equal chunks, more units than chunks
+    (4096, "bf16", 1, 24, 64, 16, 80, 12),
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_many_sequences(dev, batch, dtype, heads, group, dim, page, high, spare, accumulate):
+    """A thread of the split then has a run of sequences: empty ones at the runs' borders and whole runs of them."""
+    import random
+    from paged_helpers import Pool, check_attend
+    rng = random.Random(batch + group)
+    run = -(-batch // (288 if group > 16 else 160))
+    lens = [rng.randrange(1, high + 1) for _ in range(batch)]
+    for first in range(0, batch, run):
+        kind = rng.randrange(6)
+        for b in range(first, min(first + run, batch)):
+            if kind == 0 or (kind == 1 and b == first) or (kind == 2 and b == first + run - 1):
+                lens[b] = 0
+    lens[0], lens[-1], lens[1] = 0, high, high
+    pool = Pool(dev, dtype, "hnd", heads, dim, page, lens, spare_entries=spare, seed=45, metadata=accumulate)
+    before = pool.weights.clone() if accumulate else None
+    q, out, lse = _attn(pool, group, accumulate=accumulate)
+    assert _status() == 0
+    check_attend(pool, q, out, lse, before, dim ** -0.5)
+
+
+# ----------------------------------------------------- eviction in one launch ------
+
+def _one_launch(pool, budget, n_init=0, n_local=0):
+    """An eviction of at most 64 slots of the capacity, new_lens apart from kv_lens: the selecting CTAs move the rows."""
+    assert 0 < pool.max_pages * pool.page - budget <= 64
+    return _evict(pool, budget, n_init, n_local)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype,cap,page,budget,n_init,n_local", [
+    ("bf16", 320, 64, 256, 4, 16), ("fp16", 2048, 16, 1984, 0, 100), ("bf16", 4096, 64, 4033, 3, 0),
+    ("fp16", 4160, 64, 4096, 4, 256),                                              # 512 threads, 4 to 16 keys
+    ("bf16", 8208, 16, 8150, 64, 512), ("bf16", 33024, 256, 33000, 0, 1),        # clusters of 2 and 8
+    ("bf16", 140032, 64, 139970, 100, 1000), ("fp16", 262208, 64, 262150, 0, 7),   # of 16, 32 and 64 keys
+])
+@pytest.mark.parametrize("values", ["uniform", "ties"])
+def test_evict_in_one_launch(dev, dtype, cap, page, budget, n_init, n_local, values, dim):
+    from paged_helpers import Pool, evict_plain
+    lens = [cap, budget + 1, budget, 7, 0] if cap < 10000 else [cap, budget + 1]
+    pool = Pool(dev, dtype, "nhd", 2, dim, page, lens, spare_entries=0, seed=46)
+    if values == "ties":
+        pool.weights.mul_(4).floor_()
+    want = evict_plain(pool, budget, n_init, n_local)
+    new = _one_launch(pool, budget, n_init, n_local)
+    assert _status() == 0
+    _check_evict(pool, want, new)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("cap,budget", [(512, 460), (1024, 961), (2048, 2000), (4096, 4032)])
+def test_evict_many_short_in_one_launch(dev, cap, budget, dim):
+    """More units than the SMs hold CTAs of 512 threads: CTAs of 128."""
+    from paged_helpers import Pool, evict_plain
+    lens = [cap - 3 * i for i in range(39)] + [cap]
+    pool = Pool(dev, "bf16", "hnd", 8, dim, 16, lens, spare_entries=0, seed=47)
+    pool.weights.mul_(50).floor_()
+    want = evict_plain(pool, budget, 2, 7)
+    new = _one_launch(pool, budget, 2, 7)
+    assert _status() == 0
+    _check_evict(pool, want, new)
+
+
+@pytest.mark.parametrize("cap,page", [(320, 64), (16400, 16)])     # one CTA per unit, and a cluster
+def test_evict_in_one_launch_leaves_a_bad_page(dev, cap, page):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from paged_helpers import Pool, evict_plain
+    budget = cap - 60
+    pool = Pool(dev, "bf16", "hnd", 2, 128, page, [cap, cap, cap], spare_entries=0, seed=48)
+    keep = pool.lens.clone()
+    pool.lens = torch.tensor([cap, 0, cap], dtype=torch.int32, device=dev)
+    want = list(evict_plain(pool, budget))
+    want[4] = [budget, cap, budget]
+    pool.lens = keep
+    pool.table[1, cap // page - 1] = pool.k.shape[0]
+    new = _one_launch(pool, budget)
+    assert _status() == T.DEVICE_BAD_PAGE
+    _check_evict(pool, want, new)
+    pool.lens = torch.tensor([-3, 50, cap + 1], dtype=torch.int32, device=dev)
+    new = _one_launch(pool, budget)
+    assert _status() == T.DEVICE_BAD_KV_LEN
+    want[4] = [0, 50, 0]
+    _check_evict(pool, want, new)
