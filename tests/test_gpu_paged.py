@@ -920,3 +920,17 @@ def test_evict_in_one_launch_leaves_a_bad_page(dev, cap, page):
     assert _status() == T.DEVICE_BAD_KV_LEN
     want[4] = [0, 50, 0]
     _check_evict(pool, want, new)
+
+
+@pytest.mark.parametrize("slack", [65, 127, 128, 129])
+def test_evict_around_the_largest_one_launch(dev, slack):
+    """The border between one launch and two, by the capacity past the budget: every slot of it to be moved."""
+    from paged_helpers import Pool, evict_plain
+    cap = 1024
+    pool = Pool(dev, "bf16", "hnd", 2, 128, 64, [cap, cap - 1, cap - slack], spare_entries=0, seed=49)
+    at, row = pool.places(0, cap, cap - slack)
+    pool.weights[at, :, row] += 2.0
+    want = evict_plain(pool, cap - slack, 1, 3)
+    new = _evict(pool, cap - slack, 1, 3)
+    assert _status() == 0
+    _check_evict(pool, want, new)

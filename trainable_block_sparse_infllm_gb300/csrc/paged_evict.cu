@@ -425,6 +425,16 @@ struct EvictPlan {
   int threads, keys, cluster;
 };
 
+// Moves of a unit up to which the selecting CTAs make them.  d 128, pages of 16,
+// every slot past the budget to be moved, in a graph, one against two launches:
+// 128 moves: 11.5 and 10.7 us (2 units of 4096), 12.0 and 12.9 (32 of 4096), 17.2
+// and 20.4 (256 of 4096), 14.3 and 19.9 (32 of 16384), 178 and 168 (800 of 16384);
+// 256 moves: 14.9 and 10.7, 15.6 and 13.8, 23.8 and 24.5, 14.4 and 20.6, 197 and
+// 191; 512 moves: 19.5 and 11.6, 21.0 and 17.4, 33.2 and 33.6, 18.0 and 23.1, 240
+// and 229.  With one of them to be moved: 7.1 and 8.5, 8.0 and 10.2, 10.3 and 14.9,
+// 11.6 and 16.1, 141 and 134.
+constexpr int kFewMoves = 128;
+
 // Threads per CTA, slots per thread and CTAs per unit.  A cache of up to 8192
 // slots takes one CTA of 512 threads with 4, 8 or 16 slots each.  With more
 // units than the SMs hold such CTAs at once, caches of up to 4096 slots take
@@ -540,13 +550,12 @@ cudaError_t launch_paged_evict(const PagedShape& s, int budget, int n_init, int 
   a.hole = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + up256(units * 4));
   a.mover = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(a.hole) + up256(units * a.most * 4));
   const EvictPlan plan = evict_plan(s.cap, static_cast<long long>(units));
-  // The selecting CTAs move the rows themselves where a unit has no more than
-  // 64 rows to move: one slot of 4097 (16 sequences, 2 KV heads) took 11.5 us in
-  // one launch and 14.4 in two, but 32 ragged sequences 134 us of kernels in one
-  // and 124 in two.  new_lens over kv_lens would be read by the other KV heads'
-  // CTAs: that goes by the second launch.
-  const int moves = s.cap - budget;
-  if (new_lens != s.kv_lens && moves <= 64)
+  // The selecting CTAs move the rows themselves, without a second launch, where
+  // the page table has room for at most kFewMoves slots past the budget (the host
+  // does not know the lengths, so this bounds a unit's moves).  new_lens over
+  // kv_lens would be read by the other KV heads' CTAs: that goes by the second
+  // launch.
+  if (new_lens != s.kv_lens && s.cap - budget <= kFewMoves)
     return s.D == 128 ? launch_select_any<128>(a, plan, st) : launch_select_any<64>(a, plan, st);
   cudaError_t e = launch_select_any<0>(a, plan, st);
   if (e != cudaSuccess) return e;
