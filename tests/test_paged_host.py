@@ -331,3 +331,11 @@ def test_the_loading_warp_waits_for_every_copy_in_flight(tmp_path, stages):
                 for i in waited:
                     passes = phases[i % stages] % 2 != (i // stages) % 2
                     assert passes == (i < landed)
+
+
+def test_a_scale_past_fp32_in_base_2_is_refused(L):
+    """scale log2(e) has to be finite as well: beyond that every score would come out NaN."""
+    c = _cache(L)
+    for scale in (2.4e38, 3.4e38):
+        assert _attn(L, c, scale=scale) == L.INVALID_ARGUMENT
+    assert _attn(L, c, scale=2.3e38, ws_bytes=0) == L.WORKSPACE_TOO_SMALL      # past the check

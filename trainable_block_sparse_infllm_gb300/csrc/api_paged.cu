@@ -224,8 +224,9 @@ int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch,
     if ((rc = check_group(group_size))) return rc;
     if (!q || !out) return fail(INFLLMV2_INVALID_ARGUMENT, "q or out is NULL");
     if (!aligned16(q) || !aligned16(out)) return fail(INFLLMV2_UNSUPPORTED, "q and out must be 16-byte aligned");
-    if (!(std::isfinite(attn_scale) && attn_scale > 0.f))
-      return fail(INFLLMV2_INVALID_ARGUMENT, "attn_scale must be finite and > 0");
+    const float scale2 = attn_scale * 1.4426950408889634f;
+    if (!(std::isfinite(scale2) && scale2 > 0.f))
+      return fail(INFLLMV2_INVALID_ARGUMENT, "attn_scale must be > 0 and finite, also times log2(e)");
     if (accumulate != 0 && accumulate != 1) return fail(INFLLMV2_INVALID_ARGUMENT, "accumulate must be 0 or 1");
     if (accumulate && !s.weights) return fail(INFLLMV2_INVALID_ARGUMENT, "accumulate needs the cache's weights");
     if ((rc = check_workspace(paged_attn_workspace_bytes(s, group_size), workspace, workspace_bytes))) return rc;
@@ -236,9 +237,8 @@ int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch,
     PagedMapOrder ko, vo;
     if ((rc = make_pool_map(&km, &ko, s, s.k, s.kst, box, "k_pages"))) return rc;
     if ((rc = make_pool_map(&vm, &vo, s, s.v, s.vst, box, "v_pages"))) return rc;
-    const cudaError_t e =
-        launch_paged_attn(s, group_size, km, ko, vm, vo, box, q, attn_scale * 1.4426950408889634f, accumulate != 0,
-                          out, lse, workspace, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_paged_attn(s, group_size, km, ko, vm, vo, box, q, scale2, accumulate != 0, out, lse,
+                                            workspace, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn_decode");
     return INFLLMV2_OK;
   });
