@@ -339,3 +339,12 @@ def test_a_scale_past_fp32_in_base_2_is_refused(L):
     for scale in (2.4e38, 3.4e38):
         assert _attn(L, c, scale=scale) == L.INVALID_ARGUMENT
     assert _attn(L, c, scale=2.3e38, ws_bytes=0) == L.WORKSPACE_TOO_SMALL      # past the check
+
+
+def test_strides_that_pass_64_bits_are_refused(L):
+    """Extents are computed in 64 bits: strides whose rows would wrap around must not look as if they did not overlap."""
+    far = (1 << 39) - 8
+    for which in ("k_strides", "v_strides"):
+        c = _cache(L, num_pages=(1 << 27) - 1, page_size=16, **{which: (far, 16 * 128, 128)})     # 2^66 elements
+        for call in (_append, _attn, _evict):
+            assert call(L, c) == L.UNSUPPORTED

@@ -24,7 +24,8 @@ int check_strides(const int64_t st[3], const int64_t n[3], const char* what) {
 }
 
 // No two of the pool's rows overlap: sorted by stride, each dimension steps
-// over the extent of the ones below it.
+// over the extent of the ones below it.  Extents past 2^56 elements, which no
+// address space holds, are refused before they could wrap around.
 int check_layout(const int64_t st[3], const int64_t n[3], int d, const char* what) {
   int order[3] = {0, 1, 2};
   for (int i = 0; i < 3; ++i)
@@ -39,6 +40,8 @@ int check_layout(const int64_t st[3], const int64_t n[3], int d, const char* wha
     const int x = order[i];
     if (n[x] <= 1) continue;
     if (st[x] < extent) return fail(INFLLMV2_INVALID_ARGUMENT, "%s: rows overlap (strides)", what);
+    if (st[x] > ((1ll << 56) - extent) / (n[x] - 1))
+      return fail(INFLLMV2_UNSUPPORTED, "%s: strides span too much", what);
     extent = st[x] * (n[x] - 1) + extent;
   }
   return INFLLMV2_OK;
