@@ -357,6 +357,25 @@ __device__ __forceinline__ float lse_of(float m, float sum, float scale2) {
   return fmaf(m, scale2, log2f(sum) - (kFp16 ? 14.f : 0.f)) * 0.6931471805599453f;
 }
 
+// Merges the sum l2 relative to the maximum m2 (of unscaled scores; -inf where
+// nothing was attended) into (m, l); returns what the two sides' other sums are to
+// be multiplied by.
+__device__ __forceinline__ float2 merge_ml(float& m, float& l, float m2, float l2, float scale2) {
+  const float top = fmaxf(m, m2), use = top == -INFINITY ? 0.f : top;
+  const float f = fast_exp2((m - use) * scale2), f2 = fast_exp2((m2 - use) * scale2);
+  m = top;
+  l = l * f + l2 * f2;
+  return make_float2(f, f2);
+}
+__device__ __forceinline__ void merge_sums(float& m, float& l, float4& x, float m2, float l2, const float4& x2,
+                                           float scale2) {
+  const float2 f = merge_ml(m, l, m2, l2, scale2);
+  x.x = x.x * f.x + x2.x * f.y;
+  x.y = x.y * f.x + x2.y * f.y;
+  x.z = x.z * f.x + x2.z * f.y;
+  x.w = x.w * f.x + x2.w * f.y;
+}
+
 // What add_weights needs of a head; nothing attended weighs nothing.
 template <bool kFp16>
 __device__ __forceinline__ float2 m_and_inverse(float m, float sum) {
@@ -414,6 +433,9 @@ __device__ __forceinline__ void add_weights(const PagedAttnArgs& a, long long un
 }
 
 // ---- the pass over the pages -------------------------------------------------
+
+// CTAs of a cluster, at most (cluster_size picks 8 or 4).
+constexpr int kMaxCluster = 8;
 
 // A unit's merge and output cost a CTA about as much as this many tiles.
 constexpr int kUnitCost = 2;
@@ -931,31 +953,20 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
     for (int h = rank + a.cluster * warp; h < a.G; h += a.cluster * 4 * kGroups) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       float mx = -INFINITY, sum = 0.f;
-      for (int r0 = 0; r0 < a.cluster; r0 += 8) {   // 8 pieces in flight
-        float2 v[8];
-        float4 y[8];
+      float2 v[kMaxCluster];   // all pieces in flight
+      float4 y[kMaxCluster];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = make_float2(-INFINITY, 0.f);
-          y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r0 + e < a.cluster && has(r0 + e)) {
-            const long long at = unit * a.cluster + r0 + e;
-            v[e] = __ldcg(a.part_ml + at * kPagedMaxGroup + h);
-            if (lane < kDim / 4) y[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (at * a.G + h) * kDim) + lane);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float nm = fmaxf(mx, v[e].x), use = nm == -INFINITY ? 0.f : nm;
-          const float f = fast_exp2((mx - use) * a.scale2), f2 = fast_exp2((v[e].x - use) * a.scale2);
-          mx = nm;
-          sum = sum * f + v[e].y * f2;
-          x.x = x.x * f + y[e].x * f2;
-          x.y = x.y * f + y[e].y * f2;
-          x.z = x.z * f + y[e].z * f2;
-          x.w = x.w * f + y[e].w * f2;
+      for (int r = 0; r < kMaxCluster; ++r) {
+        v[r] = make_float2(-INFINITY, 0.f);
+        y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < a.cluster && has(r)) {
+          const long long at = unit * a.cluster + r;
+          v[r] = __ldcg(a.part_ml + at * kPagedMaxGroup + h);
+          if (lane < kDim / 4) y[r] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (at * a.G + h) * kDim) + lane);
         }
       }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) merge_sums(mx, sum, x, v[r].x, v[r].y, y[r], a.scale2);
       const float use = mx == -INFINITY ? 0.f : mx;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long head = static_cast<long long>(unit) * a.G + h;
@@ -972,9 +983,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
       for (int r = 0; r < a.cluster; ++r) {
         if (!has(r)) continue;
         const float2 v = __ldcg(a.part_ml + static_cast<long long>(unit * a.cluster + r) * kPagedMaxGroup + tid);
-        const float nm = fmaxf(mx, v.x), use = nm == -INFINITY ? 0.f : nm;
-        sum = sum * fast_exp2((mx - use) * a.scale2) + v.y * fast_exp2((v.x - use) * a.scale2);
-        mx = nm;
+        merge_ml(mx, sum, v.x, v.y, a.scale2);
       }
       unit_ml[tid] = m_and_inverse<kFp16>(mx, sum);
     }
@@ -1018,17 +1027,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
     const int col = t % kLanes, part = t / kLanes;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float mx = -INFINITY, sum = 0.f;
-    // Merges a sum relative to the maximum m2 into (mx, sum, x).
-    auto merge = [&](float m2, float s2, float4 x2) {
-      const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
-      const float f = fast_exp2((mx - use) * a.scale2), f2 = fast_exp2((m2 - use) * a.scale2);
-      mx = nm;
-      sum = sum * f + s2 * f2;
-      x.x = x.x * f + x2.x * f2;
-      x.y = x.y * f + x2.y * f2;
-      x.z = x.z * f + x2.z * f2;
-      x.w = x.w * f + x2.w * f2;
-    };
     constexpr int kAhead = 8;   // rows in flight
     for (int j0 = part; j0 < pieces; j0 += kAhead * par) {
       float2 v[kAhead];
@@ -1045,13 +1043,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
         }
       }
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) merge(v[e].x, v[e].y, y[e]);
+      for (int e = 0; e < kAhead; ++e) merge_sums(mx, sum, x, v[e].x, v[e].y, y[e], a.scale2);
     }
     if constexpr (kLanes == 16) {   // two rows per warp
       const float m2 = __shfl_xor_sync(0xffffffffu, mx, 16), s2 = __shfl_xor_sync(0xffffffffu, sum, 16);
       const float4 x2 = make_float4(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16),
                                     __shfl_xor_sync(0xffffffffu, x.z, 16), __shfl_xor_sync(0xffffffffu, x.w, 16));
-      merge(m2, s2, x2);
+      merge_sums(mx, sum, x, m2, s2, x2, a.scale2);
     }
     if (lane < kLanes) red_o[warp][lane] = x;
     if (lane == 0) {
@@ -1060,7 +1058,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
     }
     __syncthreads();
     if (t < kLanes && h < a.G) {
-      for (int j = warp0 + 1; j < warp0 + warps; ++j) merge(red_m[j], red_l[j], red_o[j][t]);
+      for (int j = warp0 + 1; j < warp0 + warps; ++j)
+        merge_sums(mx, sum, x, red_m[j], red_l[j], red_o[j][t], a.scale2);
       const float use = mx == -INFINITY ? 0.f : mx;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long head = static_cast<long long>(c.x) * a.G + h;
@@ -1111,9 +1110,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join_kernel(const Paged
       }
       for (int o = wide; o < 32; o <<= 1) {   // rows within the warp
         const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
-        const float nm = fmaxf(mx, m2), use = nm == -INFINITY ? 0.f : nm;
-        sum = sum * fast_exp2((mx - use) * a.scale2) + s2 * fast_exp2((m2 - use) * a.scale2);
-        mx = nm;
+        merge_ml(mx, sum, m2, s2, a.scale2);
       }
       red_ml[warp][lane] = make_float2(mx, sum);
       __syncthreads();
@@ -1177,7 +1174,7 @@ int cluster_size(const PagedShape& s, int G) {
   const int tiles = unit_tiles_of(s, G), sms = device_sm_count();
   const long long units = static_cast<long long>(s.B) * s.Hkv;
   if (tiles < 3) return 0;
-  for (int c = 8; c >= 4; c /= 2) {
+  for (int c = kMaxCluster; c >= 4; c /= 2) {
     const long long ctas = units * c;
     if (2 * tiles <= c || 2 * ctas > sms * (G > 16 ? 1 : 2)) continue;
     return tiles <= c * (2 * ctas >= sms ? 8 : 2) ? c : 0;
