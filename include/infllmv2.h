@@ -416,7 +416,7 @@ size_t infllmv2_paged_workspace_size(const infllmv2_paged_cache* cache, int32_t 
  * A sequence with n_new[b] outside [0, n_q] or kv_lens[b] outside
  * [n_new[b], max_pages * page_size] is left untouched and sets
  * INFLLMV2_DEVICE_BAD_KV_LEN; a token whose page is bad is not written.  The
- * slots written must be pairwise different.
+ * slots written must be pairwise different, and k_new and v_new apart from them.
  */
 int infllmv2_paged_append_kv(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages, int32_t n_q,
                              const void* k_new, const void* v_new, const int64_t* new_strides,
@@ -435,7 +435,11 @@ int infllmv2_paged_append_kv(const infllmv2_paged_cache* cache, int32_t batch, i
  *           share pages (a common prefix); the weights of a shared slot are
  *           then summed in an order that depends on scheduling.
  * A sequence with kv_lens[b] = 0 gets out = 0 and lse = -inf.  Slots of bad
- * pages, and whatever rows past kv_lens[b] hold, take no part.
+ * pages, and whatever rows past kv_lens[b] hold, take no part.  Infinities and
+ * NaN in attended rows act as in the formula, in their own sequence and KV head
+ * only, but for an infinity in a value row whose probability is below 2^-28
+ * (fp16; bf16: 2^-110) of the largest: it may give NaN instead.
+ *   attn_scale  > 0, and finite in fp32 also times log2(e).
  * Workspace: infllmv2_paged_workspace_size(.., INFLLMV2_OP_PAGED_DECODE).
  */
 int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch, int32_t max_pages,
@@ -454,7 +458,8 @@ int infllmv2_paged_attn_decode(const infllmv2_paged_cache* cache, int32_t batch,
  * or past `budget` are left as they were, and the pages past
  * ceil(budget / page_size) are free.  Each KV head keeps slots of its own.
  *   new_lens  int32 [batch]: min(kv_lens[b], budget); kv_lens itself, or an
- *           array apart from kv_lens and seq_lens.
+ *           array apart from kv_lens and seq_lens (with which a page table of at
+ *           most 128 slots past the budget takes one launch instead of two).
  * A sequence with a bad page among its slots is left as it is (new_lens =
  * kv_lens[b]).  The pages in use must be pairwise different: a page that
  * sequences share must not be evicted from.  max_pages * page_size <= 524288.

@@ -40,19 +40,21 @@
 // unscaled scores, and a score is scaled after the maximum is taken off: of the
 // largest that leaves 0, whatever its size.  (exp2(z scale - m), with m the rounded
 // product, is 2^(half a step of m), which passes fp16's range from scores of 2^25
-// and fp32's from 2^31.)  A probability feeds the
-// product with V as two 16-bit parts (hi + lo, to 2^-16 of it or better): one
-// rounding of it to bf16 would cost as much again as the output's own.  With
-// up to 8 heads the lo parts fill the rows 8..15 that would be empty; with
-// more they are a second product (a unit of 256 slots, d 128, alone on its SM:
-// 7.0 us a call with 8 heads, 8.0 with 16).  fp16 probabilities are scaled by 2^14, so
-// that the long tail of a sharp softmax stays above fp16's smallest number.
+// and fp32's from 2^31.)  A probability feeds the product with V as two 16-bit
+// parts (hi + lo, to 2^-16 of it or better): one rounding of it to bf16 would cost
+// as much again as the output's own, and against 2^-16 the output's own is all that
+// is seen: bf16 outputs are 0.00167 (relative 2-norm) from the formula in 64 bits
+// with 24-bit probabilities and with these, and 0.3% of them are the neighbouring
+// value.  With up to 8 heads the lo parts fill the rows 8..15 that would be empty;
+// with more they are a second product (a unit of 256 slots, d 128, cut over the
+// SMs: 7.9 us a call with 8 heads, 8.8 with 16).  fp16 probabilities are scaled by
+// 2^14, so that the long tail of a sharp softmax stays above fp16's smallest number.
 //
 // Measured (GB300, bf16 unless said): 32 sequences of 16K to 32K, 8 KV heads of
-// 8, with weights: the pass 505 us (3.3 GB: 6.6 TB/s, 98% of the copy rate, its
-// scores' 0.2 GB included), the join and weights 43 us.  64 ragged of up to 8K,
-// fp16, token-major pages of 16, with weights: 179 us (6.4 TB/s) and 18 us.  One
-// of 128K, 2 KV heads of 16, with weights: 28 us (134 MB; 4 us until the first
+// 8, with weights: the pass 500 us (3.3 GB: 6.6 TB/s, 99% of the copy rate, its
+// scores' 0.2 GB included), the join and weights 46 us.  64 ragged of up to 8K,
+// fp16, token-major pages of 16, with weights: 179 us (6.4 TB/s) and 21 us.  One
+// of 128K, 2 KV heads of 16, with weights: 30 us (134 MB; 4 us until the first
 // tiles land, and CTAs of 13 or 14 tiles) and 9 us.
 #include <atomic>
 
@@ -69,7 +71,7 @@ namespace {
 // 96 short sequences at d 64 took 84 us with 64 slots and 70 with 128.  With two
 // groups (17 to 32 heads) 128 slots at either: each warp then has two
 // independent parts to overlap; 4 x 60K slots, 8 KV heads of 32, d 128, took
-// 248 us with 64 slots and 168 with 128.
+// 248 us with 64 slots and 168 with 128 (where 48 bytes of a thread spill).
 template <int kDim, int kGroups>
 constexpr int kTileOf = kGroups == 2 ? 128 : 8192 / kDim;
 
@@ -1163,13 +1165,13 @@ int attn_ctas(const PagedShape& s, int G) {
 
 // CTAs of a cluster for each unit, or 0 where the line is split over all CTAs.
 // A cluster joins its unit itself, which saves the second launch, but its few
-// CTAs have to suffice.  With 8 or 4 CTAs of d 128, 16 heads, calls from Python:
-// 2 units of 512 / 1024 / 2048 slots 8.1 / 8.6 / 10.0 us against 9.5 / 9.7 / 9.7;
-// 16 units of 512 / 2048 / 4096 / 8192 slots 8.5 / 11.0 / 15.1 / 22.6 against
-// 11.2 / 12.8 / 16.7 / 22.5; so two tiles per CTA, or eight where half the SMs
-// have a CTA.  Clusters that fill more than half of the GPU's CTAs do not all
-// fit its processing clusters at once (32 units of 512 slots: 11.6 us with 8
-// CTAs each, 8.7 with 4).
+// CTAs have to suffice.  With 8 or 4 CTAs, d 128, 16 heads, calls from Python,
+// clusters against the split: 2 units of 512 / 1024 / 2048 / 4096 slots 8.0 / 8.6 /
+// 10.1 / 12.9 us against 9.6 / 9.8 / 9.8 / 10.2; 16 units of 512 / 2048 / 4096 / 8192
+// slots 8.6 / 11.0 / 15.0 / 22.5 against 11.6 / 13.2 / 17.2 / 22.9; so two tiles per
+// CTA, or eight where half the SMs have a CTA.  Clusters that fill more than half
+// of the GPU's CTAs do not all fit its processing clusters at once (32 units of
+// 512 slots: 11.2 us with 8 CTAs each, 8.9 with 4).
 int cluster_size(const PagedShape& s, int G) {
   const int tiles = unit_tiles_of(s, G), sms = device_sm_count();
   const long long units = static_cast<long long>(s.B) * s.Hkv;

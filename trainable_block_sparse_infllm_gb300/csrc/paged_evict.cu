@@ -18,14 +18,15 @@
 // that are still wanted.  (Digits of fixed bits would put most softmax sums
 // into the two or three bins of their exponents.)  Ordered scans then number
 // the holes and the movers, whose lists go out through shared memory, in whole
-// lines.  evict_move_kernel moves the rows over the whole GPU; with few moves
-// the selecting CTAs do it themselves and save the launch.
+// lines.  evict_move_kernel moves the rows over the whole GPU; where the capacity
+// past the budget allows few moves (kFewMoves) the selecting CTAs do it themselves
+// and save the launch.
 //
 // Measured (GB300): 32 sequences of 2K to 16K, 8 KV heads, pages of 16, to 4096:
 // selection 33 us (barriers and shared-memory counts; 2 CTAs per unit, 1.7
-// waves), moves 87 us (454 MB of rows and 50 MB of their weights' and positions'
-// sectors: 5.8 TB/s, 86% of the copy rate, in rows of 256 bytes).  One of 128K to
-// 32K, 2 KV heads: 17 and 11.7 us.  One slot of each of 16 sequences of 4097, 2 KV
+// waves), moves 89 us (454 MB of rows and 50 MB of their weights' and positions'
+// sectors: 5.7 TB/s, 85% of the copy rate, in rows of 256 bytes).  One of 128K to
+// 32K, 2 KV heads: 17 and 12 us.  One slot of each of 16 sequences of 4097, 2 KV
 // heads: 8.7 us, one launch.
 #include "paged.cuh"
 #include "kernels.h"
