@@ -471,6 +471,192 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
                          size_t workspace_bytes, void* stream);
 
 /*
+ * The page tables and the token maps of one step, from its requests' lengths.
+ * Sequence b holds kv_lens[b] tokens and gets n_new[b] more (0: none).  It owns
+ * the first held[b] entries of its row of page_table, and needs
+ * ceil((kv_lens[b] + n_new[b]) / page_size); the call takes the pages it lacks
+ * from the free pages and gives back those it no longer needs: all of them for
+ * kv_lens[b] = n_new[b] = 0 (a finished sequence), the ones past the budget after
+ * an eviction.  No page may be owned twice.
+ *   page_table  int32 [batch, max_pages], in/out; entries past held[b] are left
+ *           as they were.
+ *   held    int32 [batch], in/out.
+ *   free_pages, n_free  int32 [num_pages] and [1], in/out: a stack of
+ *           n_free[0] free pages.  Pages are taken from its top, sequence by
+ *           sequence; once it is empty, of those given back, in order; the rest
+ *           of those go onto it.  Entries from n_free[0] on are left as they were.
+ *   seq_lens  int32 [batch], the tokens each sequence has seen, without the new
+ *           ones, or NULL: kv_lens.
+ *   new_lens  int32 [batch]: kv_lens + n_new; may be kv_lens or n_new.
+ *   starts  int32 [batch + 1]: sequence b's new tokens are tokens starts[b] ..
+ *           starts[b + 1] - 1 of the step.
+ *   slots, positions  int32 [max_tokens], each may be NULL: of every token of the
+ *           step its slot in the pool, page * page_size + row, and its position,
+ *           seq_lens[b] + t; past the last token -1 and 0.
+ *   missing int32 [1]: 0, or the number of free pages that lack, or -1: a length,
+ *           held[b] or n_free is out of range (a row has max_pages entries), or
+ *           the step has more than max_tokens tokens; then also
+ *           INFLLMV2_DEVICE_BAD_KV_LEN.  Where it is not 0 nothing is taken or
+ *           given back, new_lens is kv_lens, every start 0 and every slot -1: the
+ *           step is empty.
+ * Page sizes, batch and pool as for the paged cache (any page size from 1 on).
+ */
+int infllmv2_paged_reserve(int32_t page_size, int32_t num_pages, int32_t batch, int32_t max_pages,
+                           int32_t* page_table, int32_t* held, int32_t* free_pages, int32_t* n_free,
+                           const int32_t* kv_lens, const int32_t* n_new, const int32_t* seq_lens, int32_t* new_lens,
+                           int32_t* starts, int32_t max_tokens, int32_t* slots, int32_t* positions, int32_t* missing,
+                           void* stream);
+
+/*
+ * Write the tokens of a packed step into the pages: row t of k_new and v_new
+ * [tokens, n_kv_heads, head_dim] goes to slot slots[t] (page * page_size + row;
+ * below 0: nowhere); the slot's weight becomes 0 and its position positions[t].
+ *   strides (host memory, NULL for contiguous): the elements between tokens and
+ *           heads of k_new, then of v_new.  Read with ordinary loads: they may be
+ *           page-locked host memory mapped for the device.
+ *   positions  int32 [tokens]; NULL only where the cache has none.
+ * A slot past the pool is not written and sets INFLLMV2_DEVICE_BAD_PAGE.  The
+ * slots written must be pairwise different, and k_new and v_new apart from them.
+ */
+int infllmv2_paged_append_packed(const infllmv2_paged_cache* cache, int32_t tokens, const void* k_new,
+                                 const void* v_new, const int64_t* strides, const int32_t* slots,
+                                 const int32_t* positions, void* stream);
+
+/*
+ * --------------------------------------------------------- packed steps ----
+ *
+ * The tokens of several sequences one after the other: starts int32 [batch + 1],
+ * sequence b's are rows starts[b] .. starts[b + 1] - 1 of tensors [tokens, heads,
+ * head_dim] with any strides between tokens and heads (multiples of 16 bytes; the
+ * values of a head are consecutive), as views of one projection's output have.
+ * Rows of no sequence are neither read into a result nor written.
+ */
+
+/*
+ * The frequencies of rotary positions: pair i of rotary_dim / 2 turns by
+ * base^(-2 i / rotary_dim) radians per position, scaled for contexts longer than
+ * the trained original_len by
+ *   INFLLMV2_ROTARY_PLAIN    nothing;
+ *   INFLLMV2_ROTARY_LINEAR   all divided by factor;
+ *   INFLLMV2_ROTARY_BASE     base times factor^(d / (d - 2)), so that the slowest
+ *           pair is divided by factor and the fastest stays (d = rotary_dim > 2);
+ *   INFLLMV2_ROTARY_PARTS    pairs that turn more than fast_turns times in
+ *           original_len positions stay, those that turn less than slow_turns times
+ *           are divided by factor, a linear ramp over the pairs' index between
+ *           (its ends rounded outwards); values times 0.1 ln(factor) + 1
+ *           (Peng et al. 2023, "YaRN");
+ *   INFLLMV2_ROTARY_FACTORS  pair i divided by factors[i]; values times
+ *           sqrt(1 + ln(factor) / ln(original_len)) (Ding et al. 2024, "LongRoPE").
+ * Host code: turns and scale are host memory.  turns[i] is 2^64 times the turns
+ * per position, scale what infllmv2_rotary multiplies the values by.
+ */
+#define INFLLMV2_ROTARY_PLAIN 0
+#define INFLLMV2_ROTARY_LINEAR 1
+#define INFLLMV2_ROTARY_BASE 2
+#define INFLLMV2_ROTARY_PARTS 3
+#define INFLLMV2_ROTARY_FACTORS 4
+
+typedef struct infllmv2_rotary_config {
+  int32_t rotary_dim;    /* even, 2 .. 512 */
+  int32_t scaling;       /* INFLLMV2_ROTARY_* */
+  double base;           /* > 1 */
+  double factor;         /* >= 1 */
+  int32_t original_len;  /* > 1; read by PARTS and FACTORS */
+  int32_t reserved;      /* 0 */
+  double fast_turns, slow_turns;   /* PARTS: fast > slow > 0 (32 and 1) */
+  const double* factors; /* FACTORS: rotary_dim / 2 divisors, >= 1 */
+} infllmv2_rotary_config;
+
+int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* turns, float* scale);
+
+/*
+ * Rotary positions of a packed step's queries and keys: of every head the first
+ * rotary_dim values are pairs (x, y), value i with i + rotary_dim / 2, or
+ * (interleaved) 2 i with 2 i + 1.  Pair i of token t becomes
+ *     scale (x cos a - y sin a, x sin a + y cos a),  a = 2 pi positions[t] turns[i] / 2^64,
+ * with transpose = 1 the same with -a: the gradient of the inputs from that of
+ * the outputs.  The other head_dim - rotary_dim values are copied.
+ *   q, k    INFLLMV2_BF16, INFLLMV2_FP16 or INFLLMV2_FP32 (dtype); k may be NULL.
+ *           Strides in elements between tokens and heads.  out may be in, with the
+ *           same strides; otherwise the two must not overlap.
+ *   positions  int32 [tokens], any value.
+ *   turns   device memory, [rotary_dim / 2], from infllmv2_rotary_frequencies.
+ * head_dim and rotary_dim: multiples of 16, rotary_dim <= head_dim <= 512.
+ * Angles are exact to 2^-32 turn whatever the position.
+ */
+#define INFLLMV2_FP32 2
+
+typedef struct infllmv2_rotary_rows {
+  const void* in;
+  void* out;
+  int64_t in_strides[2];   /* elements between tokens and heads */
+  int64_t out_strides[2];
+  int32_t heads;
+  int32_t reserved;        /* 0 */
+} infllmv2_rotary_rows;
+
+int infllmv2_rotary(int32_t dtype, int32_t tokens, int32_t head_dim, const infllmv2_rotary_rows* q,
+                    const infllmv2_rotary_rows* k, const int32_t* positions, int32_t rotary_dim,
+                    const uint64_t* turns, float scale, int32_t interleaved, int32_t transpose, void* stream);
+
+/*
+ * Causal attention over packed sequences with grouped heads.  Sequence b has the
+ * query rows q_starts[b] .. q_starts[b + 1] - 1 and the key rows k_starts[b] ..
+ * k_starts[b + 1] - 1; the last of each are the same token, so query i of n_q
+ * attends the keys j <= n_k - n_q + i of n_k (more keys than queries: tokens
+ * of earlier steps come first).  Of its n_kv_heads * group_size heads the ones
+ * h * group_size .. (h + 1) * group_size - 1 share KV head h:
+ *     z_j = scale q . k_j,  P = softmax_j(z),  out = sum_j P_j v_j,
+ *     lse = ln sum_j exp(z_j).
+ * A row that attends no key (n_k < n_q) gets out = 0 and lse = -inf.  Rows of other
+ * sequences and of none take no part, whatever they hold.  Within a sequence,
+ * infinities and NaN act as in the formula, and what a query does not attend
+ * does not reach it.
+ *   dtype   INFLLMV2_BF16 or INFLLMV2_FP16: q, k, v, out and the gradients.
+ *   head_dim 64 or 128; group_size 1 .. 32; up to 4096 sequences; fewer than
+ *           2^31 / (n_kv_heads * group_size) tokens.
+ *   strides elements between tokens and heads, multiples of 8; rows of one tensor
+ *           must not overlap.  Pointers 16-byte aligned.
+ *   q_starts, k_starts  int32 [batch + 1], not descending, within [0, q_tokens] and
+ *           [0, k_tokens]; k_starts NULL: q_starts.  A sequence whose starts are out of
+ *           range or descend sets INFLLMV2_DEVICE_BAD_KV_LEN and counts as empty.
+ *   scale   > 0, and finite in fp32 also times log2(e).
+ * lse is contiguous fp32 [q_tokens, heads] and may be NULL in the forward call.
+ */
+typedef struct infllmv2_packed_attn_args {
+  int32_t dtype, batch, n_kv_heads, group_size, head_dim, q_tokens, k_tokens;
+  float scale;
+  const void* q;   /* [q_tokens, n_kv_heads * group_size, head_dim] */
+  const void* k;   /* [k_tokens, n_kv_heads, head_dim] */
+  const void* v;
+  int64_t q_strides[2], k_strides[2], v_strides[2];
+  const int32_t* q_starts;
+  const int32_t* k_starts;
+} infllmv2_packed_attn_args;
+
+int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const int64_t* out_strides, float* lse,
+                         void* stream);
+
+/*
+ * Its gradient: for the upstream gradient dout of out,
+ *     P = exp(z - lse),  D = rowsum(dout * out),  dS = P * (dout . v - D),
+ *     dq = scale sum_j dS k_j,  dk_j = scale sum dS q,  dv_j = sum P dout,
+ * the sums for a key over all queries of all heads of its group that attend it.
+ * Every row of a sequence is written, in an order of sums that does not change from
+ * run to run; keys that no query attends get 0.
+ *   out, lse  as the forward call on the same arguments wrote them.
+ *   grad_strides (host memory): between tokens and heads of out, dout, dq, dk, dv.
+ *   P and dS enter the sums in the type of q: a non-finite dout or q row reaches every
+ *           key row of its own sequence and KV head, a non-finite key every query row.
+ * Workspace: infllmv2_packed_workspace_size(args) bytes (D and lse of each row).  Written before
+ * it is read in every call: calls that may overlap on the GPU need their own.
+ */
+size_t infllmv2_packed_workspace_size(const infllmv2_packed_attn_args* args);
+int infllmv2_packed_attn_backward(const infllmv2_packed_attn_args* args, const void* out, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, const int64_t* grad_strides,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The checked build.  The library can also be built with INFLLMV2_CHECKED
  * (libinfllmv2_checked.so), in place of a memory checker.  It verifies
  * every index that comes from the caller before use (each counted

@@ -18,6 +18,10 @@ memory and streams.  Entry points mirror the C names:
     PagedCache, paged_append_kv, paged_attn_decode, paged_evict
                          a cache of pages attended densely: its append, the attention of one
                          new token, eviction by accumulated attention weight (paged.py)
+    PageTables, paged_reserve, paged_append_packed, rotary, packed_attn, packed_attn_backward
+                         a packed step of several sequences: its page tables and token maps, its
+                         rotary positions, causal attention and its gradient, its write into the
+                         pages (packed.py)
 
 Method: "MiniCPM4: Ultra-Efficient LLMs on End Devices", section "InfLLM v2:
 Trainable Sparse Attention for Both Prefilling and Decoding".
@@ -36,6 +40,10 @@ from ._lib import (InfLLMv2Error, OP_BACKWARD, OP_DECODE, OP_DECODE_STEP, OP_PRE
                    DEVICE_TIMEOUT)
 from .paged import (PagedCache, alloc_paged_workspace, paged_append_kv, paged_attn_decode, paged_evict,  # noqa: F401
                     paged_workspace_size)
+from ._lib import ROTARY_BASE, ROTARY_FACTORS, ROTARY_LINEAR, ROTARY_PARTS, ROTARY_PLAIN  # noqa: F401
+from .packed import (PageTables, RotaryPlan, alloc_packed_workspace, alloc_page_tables, alloc_rotary_plan,  # noqa: F401
+                     packed_attn, packed_attn_backward, packed_workspace_size, paged_append_packed, paged_reserve,
+                     rotary, rotary_frequencies)
 
 __all__ = [
     "Params", "InfLLMv2Error", "make_params", "num_kernels", "max_selected", "workspace_size",
@@ -45,6 +53,9 @@ __all__ = [
     "OP_DECODE_STEP", "OP_BACKWARD", "DECODE_MAX_NQ", "is_checked_build", "test_hooks",
     "PagedCache", "paged_workspace_size", "alloc_paged_workspace", "paged_append_kv", "paged_attn_decode",
     "paged_evict", "OP_PAGED_DECODE", "OP_PAGED_EVICT",
+    "PageTables", "alloc_page_tables", "paged_reserve", "paged_append_packed", "RotaryPlan", "rotary_frequencies",
+    "alloc_rotary_plan", "rotary", "packed_attn", "packed_attn_backward", "packed_workspace_size",
+    "alloc_packed_workspace", "ROTARY_PLAIN", "ROTARY_LINEAR", "ROTARY_BASE", "ROTARY_PARTS", "ROTARY_FACTORS",
 ]
 
 DECODE_MAX_NQ = 16

@@ -35,6 +35,12 @@ OP_PAGED_DECODE = 6
 OP_PAGED_EVICT = 7
 BF16 = 0
 FP16 = 1
+FP32 = 2
+ROTARY_PLAIN = 0
+ROTARY_LINEAR = 1
+ROTARY_BASE = 2
+ROTARY_PARTS = 3
+ROTARY_FACTORS = 4
 
 
 class InfLLMv2Error(RuntimeError):
@@ -83,6 +89,63 @@ class PagedCacheStruct(ctypes.Structure):
         ("v_pages", ctypes.c_void_p),
         ("weights", ctypes.c_void_p),
         ("positions", ctypes.c_void_p),
+    ]
+
+
+class RotaryConfig(ctypes.Structure):
+    """Mirror of ``infllmv2_rotary_config``."""
+
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("fast_turns", ctypes.c_double),
+        ("slow_turns", ctypes.c_double),
+        ("factors", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class RotaryRows(ctypes.Structure):
+    """Mirror of ``infllmv2_rotary_rows``."""
+
+    _fields_ = [
+        ("x_in", ctypes.c_void_p),
+        ("x_out", ctypes.c_void_p),
+        ("in_token", ctypes.c_int64),
+        ("in_head", ctypes.c_int64),
+        ("out_token", ctypes.c_int64),
+        ("out_head", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class PackedAttnArgs(ctypes.Structure):
+    """Mirror of ``infllmv2_packed_attn_args``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("q_tokens", ctypes.c_int32),
+        ("k_tokens", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_token", ctypes.c_int64),
+        ("q_head", ctypes.c_int64),
+        ("k_token", ctypes.c_int64),
+        ("k_head", ctypes.c_int64),
+        ("v_token", ctypes.c_int64),
+        ("v_head", ctypes.c_int64),
+        ("q_starts", ctypes.c_void_p),
+        ("k_starts", ctypes.c_void_p),
     ]
 
 
@@ -143,6 +206,25 @@ lib.infllmv2_paged_attn_decode.argtypes = [_C, _i32, _i32, _i32, _vp, _vp, _vp, 
 lib.infllmv2_paged_attn_decode.restype = ctypes.c_int
 lib.infllmv2_paged_evict.argtypes = [_C, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 lib.infllmv2_paged_evict.restype = ctypes.c_int
+lib.infllmv2_paged_reserve.argtypes = [_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+                                       _vp, _vp, _vp]
+lib.infllmv2_paged_reserve.restype = ctypes.c_int
+lib.infllmv2_paged_append_packed.argtypes = [_C, _i32, _vp, _vp, ctypes.POINTER(ctypes.c_int64), _vp, _vp, _vp]
+lib.infllmv2_paged_append_packed.restype = ctypes.c_int
+lib.infllmv2_rotary_frequencies.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(ctypes.c_uint64),
+                                            ctypes.POINTER(ctypes.c_float)]
+lib.infllmv2_rotary_frequencies.restype = ctypes.c_int
+_R = ctypes.POINTER(RotaryRows)
+lib.infllmv2_rotary.argtypes = [_i32, _i32, _i32, _R, _R, _vp, _i32, _vp, ctypes.c_float, _i32, _i32, _vp]
+lib.infllmv2_rotary.restype = ctypes.c_int
+_A = ctypes.POINTER(PackedAttnArgs)
+lib.infllmv2_packed_attn.argtypes = [_A, _vp, ctypes.POINTER(ctypes.c_int64), _vp, _vp]
+lib.infllmv2_packed_attn.restype = ctypes.c_int
+lib.infllmv2_packed_workspace_size.argtypes = [_A]
+lib.infllmv2_packed_workspace_size.restype = ctypes.c_size_t
+lib.infllmv2_packed_attn_backward.argtypes = [_A, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int64), _vp,
+                                              ctypes.c_size_t, _vp]
+lib.infllmv2_packed_attn_backward.restype = ctypes.c_int
 lib.infllmv2_status_string.argtypes = [ctypes.c_int]
 lib.infllmv2_status_string.restype = ctypes.c_char_p
 lib.infllmv2_last_error.argtypes = []
@@ -158,6 +240,8 @@ EXPORTED = (
     "infllmv2_coarse_means", "infllmv2_select_blocks_coarse_lse", "infllmv2_sparse_attn_backward",
     "infllmv2_append_kv", "infllmv2_append_decode_step",
     "infllmv2_paged_workspace_size", "infllmv2_paged_append_kv", "infllmv2_paged_attn_decode", "infllmv2_paged_evict",
+    "infllmv2_paged_reserve", "infllmv2_paged_append_packed", "infllmv2_rotary_frequencies", "infllmv2_rotary",
+    "infllmv2_packed_attn", "infllmv2_packed_workspace_size", "infllmv2_packed_attn_backward",
     "infllmv2_status_string",
     "infllmv2_last_error", "infllmv2_get_device_status",
 )

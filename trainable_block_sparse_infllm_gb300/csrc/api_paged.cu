@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "api_common.h"
+#include "packed.h"
 #include "paged.h"
 
 using namespace infllmv2;
@@ -270,6 +271,68 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
     const cudaError_t e = launch_paged_evict(s, budget, n_init, n_local, seq_lens, new_lens, workspace,
                                              static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged_evict");
+    return INFLLMV2_OK;
+  });
+}
+
+int infllmv2_paged_append_packed(const infllmv2_paged_cache* cache, int32_t tokens, const void* k_new,
+                                 const void* v_new, const int64_t* strides, const int32_t* slots,
+                                 const int32_t* positions, void* stream) {
+  INFLLMV2_GUARD({
+    PagedShape s = {};
+    int rc = check_cache(cache, 1, 1, &s);
+    if (rc) return rc;
+    if (tokens < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "tokens must be >= 1 (got %d)", tokens);
+    if (!k_new || !v_new || !slots) return fail(INFLLMV2_INVALID_ARGUMENT, "k_new, v_new or slots is NULL");
+    if (!aligned16(k_new) || !aligned16(v_new))
+      return fail(INFLLMV2_UNSUPPORTED, "k_new and v_new must be 16-byte aligned");
+    if (s.positions && !positions)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "a cache with positions needs those of the new tokens");
+    const int64_t n[2] = {tokens, s.Hkv};
+    const long long whole[2] = {static_cast<long long>(s.Hkv) * s.D, s.D};
+    long long st[4];
+    for (int i = 0; i < 4; ++i) {
+      st[i] = n[i & 1] > 1 ? (strides ? strides[i] : whole[i & 1]) : 0;
+      if (st[i] < 0) return fail(INFLLMV2_INVALID_ARGUMENT, "strides must be >= 0");
+      if (st[i] % 8 != 0) return fail(INFLLMV2_UNSUPPORTED, "strides must be multiples of 8 elements");
+      if (st[i] > (1ll << 56) / n[i & 1]) return fail(INFLLMV2_UNSUPPORTED, "strides span too much");
+    }
+    s.status = status_ptr();
+    if (!s.status) return fail(INFLLMV2_CUDA_ERROR, "no device status word (no current CUDA device?)");
+    const PackedAppend a{k_new, v_new, st[0], st[1], st[2], st[3], tokens, slots, positions};
+    const cudaError_t e = launch_paged_append_packed(s, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged_append_packed");
+    return INFLLMV2_OK;
+  });
+}
+
+int infllmv2_paged_reserve(int32_t page_size, int32_t num_pages, int32_t batch, int32_t max_pages,
+                           int32_t* page_table, int32_t* held, int32_t* free_pages, int32_t* n_free,
+                           const int32_t* kv_lens, const int32_t* n_new, const int32_t* seq_lens, int32_t* new_lens,
+                           int32_t* starts, int32_t max_tokens, int32_t* slots, int32_t* positions, int32_t* missing,
+                           void* stream) {
+  INFLLMV2_GUARD({
+    if (page_size < 1 || num_pages < 1 || batch < 1 || max_pages < 1)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "page_size, num_pages, batch and max_pages must be >= 1");
+    if (batch > kPagedMaxBatch)
+      return fail(INFLLMV2_UNSUPPORTED, "at most %d sequences (got %d)", kPagedMaxBatch, batch);
+    if (page_size > 65536) return fail(INFLLMV2_UNSUPPORTED, "page_size must be <= 65536 (got %d)", page_size);
+    if (static_cast<int64_t>(max_pages) * page_size > kMaxCap)
+      return fail(INFLLMV2_UNSUPPORTED, "max_pages * page_size must be <= 2^30");
+    if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL)
+      return fail(INFLLMV2_UNSUPPORTED, "num_pages * page_size must be < 2^31");
+    if (max_tokens < 0) return fail(INFLLMV2_INVALID_ARGUMENT, "max_tokens must be >= 0 (got %d)", max_tokens);
+    if (max_tokens > kMaxCap) return fail(INFLLMV2_UNSUPPORTED, "max_tokens must be <= 2^30 (got %d)", max_tokens);
+    if (!page_table || !held || !free_pages || !n_free || !kv_lens || !n_new || !new_lens || !starts || !missing)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "a required array is NULL");
+    if (new_lens == seq_lens || new_lens == held || starts == kv_lens || starts == n_new || starts == seq_lens)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "new_lens and starts must be apart from seq_lens, held and the lengths");
+    uint32_t* status = status_ptr();
+    if (!status) return fail(INFLLMV2_CUDA_ERROR, "no device status word (no current CUDA device?)");
+    const ReserveArgs a{batch, max_pages, page_size, num_pages, max_tokens, page_table, held, free_pages, n_free,
+                        kv_lens, n_new, seq_lens, new_lens, starts, slots, positions, missing, status};
+    const cudaError_t e = launch_paged_reserve(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged_reserve");
     return INFLLMV2_OK;
   });
 }

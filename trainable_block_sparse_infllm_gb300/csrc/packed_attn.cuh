@@ -1,0 +1,218 @@
+// What the packed attention kernels share: which sequence and tile a CTA works
+// on, 3D and 4D TMA loads, and packing of probabilities.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "packed_attn.h"
+#include "tc.cuh"
+
+namespace infllmv2 {
+namespace packed {
+
+// A sequence's rows.  One whose starts are out of range or descend is empty.
+struct Sequence {
+  int q0, n_q, k0, n_k;
+};
+
+__device__ __forceinline__ Sequence sequence(const PackedAttnShape& s, int b, bool* bad) {
+  Sequence r;
+  r.q0 = __ldg(s.q_starts + b);
+  r.k0 = __ldg(s.k_starts + b);
+  const int q1 = __ldg(s.q_starts + b + 1), k1 = __ldg(s.k_starts + b + 1);
+  if (r.q0 < 0 || q1 < r.q0 || q1 > s.Tq || r.k0 < 0 || k1 < r.k0 || k1 > s.Tk) {
+    *bad = true;
+    return {0, 0, 0, 0};
+  }
+  r.n_q = q1 - r.q0;
+  r.n_k = k1 - r.k0;
+  return r;
+}
+
+// Tiles of `step` tokens cut from the sequences' queries (of_keys: keys).  A
+// tile's level is its index among the queries' tiles, or that of the keys' tiles
+// counted from the last: either way causal work grows with it.  The order of all
+// tiles goes down the levels, sequence by sequence within one, so that the CTAs
+// that start last have the least to do.  Finds the sequence and level of tile `i`
+// of that order, the same for all threads of the CTA; false past the last tile.
+// `scratch`: 4 ints of shared memory.
+__device__ __forceinline__ int tile_count(const PackedAttnShape& s, int b, int step, bool of_keys, bool* bad) {
+  const Sequence q = sequence(s, b, bad);
+  return ((of_keys ? q.n_k : q.n_q) + step - 1) / step;
+}
+
+__device__ __forceinline__ bool find_tile(const PackedAttnShape& s, int i, int step, bool of_keys, int* scratch,
+                                          int* b_out, int* level_out) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  if (s.B == 1) {
+    const int n = tile_count(s, 0, step, of_keys, &bad);
+    if (bad && i == 0 && threadIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
+    *b_out = 0;
+    *level_out = n - 1 - i;
+    return i < n;
+  }
+  // One warp: lane l holds the counts of sequences l, l + 32, ... (the first in a
+  // register).  at_least(t) = tiles with index >= t.
+  if (threadIdx.x < 32) {
+    const int first = lane < s.B ? tile_count(s, lane, step, of_keys, &bad) : 0;
+    auto at_least = [&](int t) {
+      unsigned sum = max(first - t, 0);
+      for (int b = lane + 32; b < s.B; b += 32) sum += max(tile_count(s, b, step, of_keys, &bad) - t, 0);
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, sum));
+    };
+    int most = first;
+    for (int b = lane + 32; b < s.B; b += 32) most = max(most, tile_count(s, b, step, of_keys, &bad));
+    most = __reduce_max_sync(0xffffffffu, most);
+    int lo = 0, hi = most;   // at_least(lo) > i >= at_least(hi), if there is such a tile
+    const bool found = at_least(0) > i;
+    while (found && hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at_least(mid) > i) lo = mid; else hi = mid;
+    }
+    int b = 0;
+    if (found) {
+      int rank = i - at_least(lo + 1);   // among the sequences that have a tile of level `lo`
+      for (int base = 0; base < s.B; base += 32) {
+        const bool has = base + lane < s.B &&
+                         (base == 0 ? first : tile_count(s, base + lane, step, of_keys, &bad)) > lo;
+        const unsigned mask = __ballot_sync(0xffffffffu, has);
+        const int n = __popc(mask);
+        if (rank < n) {
+          b = base + static_cast<int>(__fns(mask, 0, rank + 1));
+          break;
+        }
+        rank -= n;
+      }
+    }
+    if (bad && i == 0) atomicOr(s.status, kStatusBadKvLen);
+    if (lane == 0) {
+      scratch[0] = found;
+      scratch[1] = b;
+      scratch[2] = lo;
+    }
+  }
+  __syncthreads();
+  *b_out = scratch[1];
+  *level_out = scratch[2];
+  return scratch[0] != 0;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (kFp16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return pack_bf16x2(lo, hi);
+}
+
+template <bool kFp16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (kFp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool kFp16>
+constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
+  return kFp16 ? tc::idesc_fp16(M, N, a_mn, b_mn) : tc::idesc_bf16(M, N, a_mn, b_mn);
+}
+
+// One product of a 128-row A by D-step K extent: both operands K-major tiles of
+// [rows][kD] in boxes of 64 columns x 128 rows.
+template <int kD>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id) {
+#pragma unroll
+  for (int k = 0; k < kD / 16; ++k) {
+    const uint64_t off = static_cast<uint64_t>(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+    tc::mma_ss(d_tmem, a + off, b + off, id, k > 0 ? 1u : 0u);
+  }
+}
+
+// D += A B over 128 rows of B: A [128 x 128] two to a 32-bit column of tensor
+// memory, the columns of its second half kHalf behind the first's, B the
+// [128][kD] tile read along its rows (MN-major).
+template <int kHalf = 32>
+__device__ __forceinline__ void mma_cols(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    tc::mma_ts(d_tmem, a_tmem + kHalf * (k >> 2) + 8 * (k & 3), b + static_cast<uint64_t>((k * 2048) >> 4), id,
+               accumulate || k > 0 ? 1u : 0u);
+}
+
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) { return tc::sdesc_sw128(saddr, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr) { return tc::sdesc_sw128(saddr, 16384, 1024); }
+
+// One warp: clears rows [from, 128) of a [128][kD] tile, so that a zero
+// probability never multiplies what lies behind a sequence's end.
+template <int kD>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
+  const int lane = threadIdx.x & 31;
+  for (int e = lane; e < (128 - from) * (kD / 8); e += 32) {
+    const int row = from + e / (kD / 8), c = e % (kD / 8);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Two warps (half 0 and 1): looks through the 64 rows [64 half, 64 half + 64) of a
+// [128][kD] tile.  Rows from `valid` on are cleared; so are the ones with an
+// infinity or NaN, and their bits set in flags[0 .. 3].
+template <int kD, bool kFp16>
+__device__ __forceinline__ void check_rows(uint8_t* tile, int half, int valid, uint32_t* flags) {
+  constexpr uint32_t kExponent = kFp16 ? 0x7c007c00u : 0x7f807f80u;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int row = 64 * half + 32 * k + lane;
+    uint8_t* at = tile + row * 128;
+    uint32_t most = 0u;   // the largest exponent of each 16-bit lane
+#pragma unroll
+    for (int c = 0; c < kD / 8; ++c) {   // (in an order without bank conflicts)
+      const uint4 u = *reinterpret_cast<const uint4*>(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
+      most = __vmaxu2(__vmaxu2(most, __vmaxu2(u.x & kExponent, u.y & kExponent)),
+                      __vmaxu2(u.z & kExponent, u.w & kExponent));
+    }
+    const bool odd = ((most ^ kExponent) & 0xffffu) == 0u || ((most ^ kExponent) >> 16) == 0u;
+    const uint32_t mask = __ballot_sync(0xffffffffu, odd && row < valid);
+    if (lane == 0) flags[2 * half + k] = mask;
+    if (odd || row >= valid) {
+#pragma unroll
+      for (int c = 0; c < kD / 8; ++c)
+        *reinterpret_cast<uint4*>(at + (c >> 3) * 16384 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+}  // namespace packed
+}  // namespace infllmv2

@@ -62,6 +62,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// The same with fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // ---------------------------------------------------------------- MMA -----
 
 // D[tmem] (+)= A[smem] * B[smem]; issued by a single thread.
