@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlags);
   uint8_t* ring = smem + 2 * kTile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
   pdl_trigger();
@@ -166,53 +166,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       flags + 4 * (j - partial));
         if (lane == 0) mbar_arrive(&bars[L::kChecked + j - partial]);
       }
-    } else if (warp == kMmaWarp && lane == 0 && n > 0) {
+    } else if (warp == kMmaWarp && n > 0) {
       // --------------------------------------------------------- products
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
       const uint64_t q_desc = packed::desc_rows(smem_u32(smem));
       const uint64_t k_desc = packed::desc_rows(smem_u32(ring));
       const uint64_t v_desc = packed::desc_cols(smem_u32(ring));
+      const bool issuer = packed::elect_one();
       bool ok = true;
       auto wait = [&](int bar, int phase) {
-        if (ok) ok = mbar_wait(&bars[bar], phase & 1, s.status);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
         tc::fence_after_sync();
       };
       auto scores = [&](int x, int j) {   // S of half x and key tile j
-        packed::mma_rows<kD>(tmem + x * 128, q_desc + ((x * kTile) >> 4),
-                             k_desc + (((2 * j) % kStages * kTile) >> 4), kIdS);
-        tc::commit(&bars[L::kSFull + x]);
+        if (issuer) {
+          packed::mma_rows<kD>(tmem + x * 128, q_desc + ((x * kTile) >> 4),
+                               k_desc + (((2 * j) % kStages * kTile) >> 4), kIdS);
+          tc::commit(&bars[L::kSFull + x]);
+        }
+        __syncwarp();
       };
       wait(L::kFull, 0);
+#pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (n_tiles[x] == 0) continue;
         wait(L::kQFull + x, 0);
         if (ok) scores(x, 0);
       }
-      if (ok) tc::commit(&bars[L::kEmpty]);
+      if (ok && issuer) tc::commit(&bars[L::kEmpty]);
+      __syncwarp();
       for (int j = 0; j < n && ok; ++j) {
         const int vi = 2 * j + 1, ki = 2 * j + 2;
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (j >= n_tiles[x]) continue;
+          if (j >= n_tiles[x] || !ok) continue;
           if (j < partial) {
             wait(L::kFull + vi % kStages, vi / kStages);
           } else {
             wait(L::kChecked + j - partial, 0);
           }
           wait(L::kPFull + x, j);
-          if (!ok) break;
-          packed::mma_cols(tmem + kColO + x * kD, tmem + x * 128, v_desc + ((vi % kStages * kTile) >> 4), kIdO, j > 0);
+          if (!ok) continue;
+          if (issuer)
+            packed::mma_cols(tmem + kColO + x * kD, tmem + x * 128, v_desc + ((vi % kStages * kTile) >> 4), kIdO,
+                             j > 0);
+          __syncwarp();
           if (j + 1 < n_tiles[x]) {
             wait(L::kFull + ki % kStages, ki / kStages);
-            if (!ok) break;
-            scores(x, j + 1);
+            if (ok) scores(x, j + 1);
           } else {
-            tc::commit(&bars[L::kODone + x]);
+            if (issuer) tc::commit(&bars[L::kODone + x]);
+            __syncwarp();
           }
         }
-        if (!ok) break;
-        tc::commit(&bars[L::kEmpty + vi % kStages]);
-        if (j + 1 < n) tc::commit(&bars[L::kEmpty + ki % kStages]);
+        if (ok && issuer) {
+          tc::commit(&bars[L::kEmpty + vi % kStages]);
+          if (j + 1 < n) tc::commit(&bars[L::kEmpty + ki % kStages]);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();

@@ -136,6 +136,20 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
   return kFp16 ? tc::idesc_fp16(M, N, a_mn, b_mn) : tc::idesc_bf16(M, N, a_mn, b_mn);
 }
 
+// One lane of a converged warp, in a form from which the compiler knows that the
+// rest of the warp's work stays uniform.  Products are issued so: the whole warp
+// runs the issuer's loop, which keeps descriptors and addresses in uniform
+// registers, where tcgen05.mma takes them from; in a branch of lane 0 each product
+// moved them there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// The warp's index, uniform for the compiler too.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
 // One product of a 128-row A by D-step K extent: both operands K-major tiles of
 // [rows][kD] in boxes of 64 columns x 128 rows.
 template <int kD>
