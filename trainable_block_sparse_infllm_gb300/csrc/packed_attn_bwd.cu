@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* scratch = reinterpret_cast<int*>(smem + L::kScratch);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
   uint8_t* ring = smem + L::kRing;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
   pdl_trigger();
@@ -136,16 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars[L::kCleared]);
       }
       mbar_wait(&bars[L::kQFull], 0, s.status);
-    } else if (warp == kMmaWarp && lane == 0 && n > 0) {
+    } else if (warp == kMmaWarp && n > 0) {
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
       const uint64_t q_desc = packed::desc_rows(smem_u32(smem));
       const uint64_t do_desc = packed::desc_rows(smem_u32(smem + kTile));
       const uint64_t rows_desc = packed::desc_rows(smem_u32(ring));
       const uint64_t cols_desc = packed::desc_cols(smem_u32(ring));
+      const bool issuer = packed::elect_one();
       bool ok = true;
       auto wait = [&](int bar, int phase) {
-        if (ok) ok = mbar_wait(&bars[bar], phase & 1, s.status);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
         tc::fence_after_sync();
       };
       auto stage = [&](int i) { return static_cast<uint64_t>((i % kStages * kTile) >> 4); };
@@ -153,18 +154,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(L::kFull + (2 * j) % kStages, 2 * j / kStages);
         if (clears && j == steps - 1) wait(L::kCleared, 0);
         if (!ok) return;
-        packed::mma_rows<kD>(tmem + kDqS, q_desc, rows_desc + stage(2 * j), kIdS);
-        tc::commit(&bars[L::kSFull]);
+        if (issuer) {
+          packed::mma_rows<kD>(tmem + kDqS, q_desc, rows_desc + stage(2 * j), kIdS);
+          tc::commit(&bars[L::kSFull]);
+        }
+        __syncwarp();
         wait(L::kFull + (2 * j + 1) % kStages, (2 * j + 1) / kStages);
         if (!ok) return;
-        packed::mma_rows<kD>(tmem + kDqDp, do_desc, rows_desc + stage(2 * j + 1), kIdS);
-        tc::commit(&bars[L::kDpFull]);
-        tc::commit(&bars[L::kEmpty + (2 * j + 1) % kStages]);
+        if (issuer) {
+          packed::mma_rows<kD>(tmem + kDqDp, do_desc, rows_desc + stage(2 * j + 1), kIdS);
+          tc::commit(&bars[L::kDpFull]);
+          tc::commit(&bars[L::kEmpty + (2 * j + 1) % kStages]);
+        }
+        __syncwarp();
       };
       wait(L::kQFull, 0);
       if (ok) scores(0);
       for (int j = 0; j < steps && ok; ++j) {
-        if (j < back) tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
+        if (j < back && issuer) tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
+        __syncwarp();
         if (j + 1 < steps) {
           wait(L::kFree, j);   // both score buffers are in registers
           if (ok) scores(j + 1);
@@ -173,9 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = j - back;
         wait(L::kDsFull + (i & 1), i >> 1);
         if (!ok) break;
-        packed::mma_cols(tmem + kDqAcc, tmem + kDqDs + (i & 1) * 64, cols_desc + stage(2 * j), kIdO, i > 0);
-        tc::commit(&bars[L::kDqDone + (i & 1)]);
-        tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
+        if (issuer) {
+          packed::mma_cols(tmem + kDqAcc, tmem + kDqDs + (i & 1) * 64, cols_desc + stage(2 * j), kIdO, i > 0);
+          tc::commit(&bars[L::kDqDone + (i & 1)]);
+          tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
   uint8_t* ring = smem + L::kRing;
   float* rows = reinterpret_cast<float*>(smem + L::kRows);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
   pdl_trigger();
@@ -441,16 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kRowsFull + buf]);
       }
-    } else if (warp == kMmaWarp && lane == 0 && n > 0) {
+    } else if (warp == kMmaWarp && n > 0) {
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
       const uint64_t k_desc = packed::desc_rows(smem_u32(smem));
       const uint64_t v_desc = packed::desc_rows(smem_u32(smem + kTile));
       const uint64_t rows_desc = packed::desc_rows(smem_u32(ring));
       const uint64_t cols_desc = packed::desc_cols(smem_u32(ring));
+      const bool issuer = packed::elect_one();
       bool ok = true;
       auto wait = [&](int bar, int phase) {
-        if (ok) ok = mbar_wait(&bars[bar], phase & 1, s.status);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
         tc::fence_after_sync();
       };
       auto stage = [&](int i) { return static_cast<uint64_t>((i % kStages * kTile) >> 4); };
@@ -461,13 +473,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto scores = [&](int i) {
         if (!loaded(2 * i)) return;
-        packed::mma_rows<kD>(tmem + kKvS, k_desc, rows_desc + stage(2 * i), kIdS);
-        tc::commit(&bars[L::kSFull]);
+        if (issuer) {
+          packed::mma_rows<kD>(tmem + kKvS, k_desc, rows_desc + stage(2 * i), kIdS);
+          tc::commit(&bars[L::kSFull]);
+        }
+        __syncwarp();
       };
       auto inner = [&](int i) {
         if (!loaded(2 * i + 1)) return;
-        packed::mma_rows<kD>(tmem + kKvDp, v_desc, rows_desc + stage(2 * i + 1), kIdS);
-        tc::commit(&bars[L::kDpFull]);
+        if (issuer) {
+          packed::mma_rows<kD>(tmem + kKvDp, v_desc, rows_desc + stage(2 * i + 1), kIdS);
+          tc::commit(&bars[L::kDpFull]);
+        }
+        __syncwarp();
       };
       wait(L::kKvFull, 0);
       if (ok) scores(0);
@@ -475,16 +493,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n && ok; ++i) {
         wait(L::kPFull, i);
         if (!ok) break;
-        packed::mma_cols<64>(tmem + kKvDv, tmem + kKvS, cols_desc + stage(2 * i + 1), kIdO, i > 0);
-        tc::commit(&bars[L::kEmpty + (2 * i + 1) % kStages]);
+        if (issuer) {
+          packed::mma_cols<64>(tmem + kKvDv, tmem + kKvS, cols_desc + stage(2 * i + 1), kIdO, i > 0);
+          tc::commit(&bars[L::kEmpty + (2 * i + 1) % kStages]);
+        }
+        __syncwarp();
         if (i + 1 < n) scores(i + 1);
         wait(L::kDsFull, i);
         if (!ok) break;
-        packed::mma_cols<64>(tmem + kKvDk, tmem + kKvDp, cols_desc + stage(2 * i), kIdO, i > 0);
-        tc::commit(&bars[L::kEmpty + (2 * i) % kStages]);
+        if (issuer) {
+          packed::mma_cols<64>(tmem + kKvDk, tmem + kKvDp, cols_desc + stage(2 * i), kIdO, i > 0);
+          tc::commit(&bars[L::kEmpty + (2 * i) % kStages]);
+        }
+        __syncwarp();
         if (i + 1 < n) inner(i + 1);
       }
-      if (ok) tc::commit(&bars[L::kDone]);
+      if (ok && issuer) tc::commit(&bars[L::kDone]);
     }
     __syncwarp();
   } else {
