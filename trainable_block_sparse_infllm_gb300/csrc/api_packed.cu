@@ -268,7 +268,8 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
     PackedAttnMaps maps = {};
     if ((rc = attn_maps(&maps, args, c))) return rc;
     const PackedAttnOut to{out, {o.token, o.head}, lse};
-    const PackedAttnIn in{args->q, args->k, args->v, {c.q.token, c.q.head}, {c.k.token, c.k.head}, {c.v.token, c.v.head}};
+    const PackedAttnIn in{args->q, args->k, args->v, {c.q.token, c.q.head}, {c.k.token, c.k.head},
+                          {c.v.token, c.v.head}};
     const cudaError_t e = launch_packed_attn(c.s, c.D, c.fp16, maps, in, to, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "packed_attn");
     return INFLLMV2_OK;

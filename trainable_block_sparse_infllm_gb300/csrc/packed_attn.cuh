@@ -219,6 +219,21 @@ __device__ __forceinline__ void check_rows(uint8_t* tile, int half, int valid, u
   __syncwarp();
 }
 
+// Where float4 c4 of row `row` lies in a table of fp32 rows of kD in shared
+// memory: a warp's 32 rows meet different banks.
+template <int kD>
+__device__ __forceinline__ int swizzled(int row, int c4) {
+  return row * (kD / 4) + (c4 ^ (row & (kD / 4 - 1)));
+}
+
+__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));

@@ -24,6 +24,7 @@
 // the tiles that TMA brought.  Two warpgroups share a tile's columns.
 #include <algorithm>
 
+#include "kernels.h"
 #include "packed_attn.cuh"
 
 namespace infllmv2 {
@@ -352,7 +353,8 @@ constexpr uint32_t kKvS = 0, kKvDp = 128, kKvDv = 256, kKvDk = 384;
 
 template <int kD, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
-    packed_dkv_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnGrads g) {
+    packed_dkv_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnGrads g,
+                      const int ctas) {
   using L = DkvLayout<kD>;
   constexpr int kTile = L::kTile, kStages = L::kStages;
   constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off again: from dout . v - D for dS, from dv
@@ -363,22 +365,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
   uint8_t* ring = smem + L::kRing;
   float* rows = reinterpret_cast<float*>(smem + L::kRows);
+  float4* parts = reinterpret_cast<float4*>(ring);   // at the end: this CTA's dv and dk, 2 x 128 rows of kD
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
   pdl_trigger();
   const int tile_tokens = packed_tile_tokens(s.G), tile_rows = tile_tokens * s.G;
-  const int h = static_cast<int>(blockIdx.x) % s.Hkv;
+  const int rank = static_cast<int>(blockIdx.x) % ctas, unit = static_cast<int>(blockIdx.x) / ctas;
+  const int h = unit % s.Hkv;
   int b, level;
-  if (!packed::find_tile(s, static_cast<int>(blockIdx.x) / s.Hkv, 128, true, scratch, &b, &level)) return;
+  if (!packed::find_tile(s, unit / s.Hkv, 128, true, scratch, &b, &level)) return;   // the same for the whole cluster
   bool bad = false;
   const packed::Sequence seq = packed::sequence(s, b, &bad);
   const int key0 = ((seq.n_k + 127) / 128 - 1 - level) * 128;
   const int before = seq.n_k - seq.n_q;
   const int t0 = max(key0 - before, 0);   // the first query that attends the tile's first key
-  const int n = (max(seq.n_q - t0, 0) + tile_tokens - 1) / tile_tokens;   // row tiles
+  // Row tiles: of all of them this CTA takes rank, rank + ctas, ...
+  const int n_all = (max(seq.n_q - t0, 0) + tile_tokens - 1) / tile_tokens;
+  const int n = (n_all - rank + ctas - 1) / ctas;
+  auto tile_token = [&](int i) { return t0 + (rank + i * ctas) * tile_tokens; };   // of its i-th tile
   // Rows of the last tile that hold no query of the sequence meet P = dS = 0.
-  const int last_rows = (seq.n_q - t0 - (n - 1) * tile_tokens) * s.G;
+  const int last_rows = (seq.n_q - tile_token(n - 1)) * s.G;
   const bool clears = n > 0 && last_rows < tile_rows;
 
   if (tid == 0) {
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&bars[L::kFull + st], tile_rows * kD * 2);
           for (int c = 0; c < kD / 64; ++c)
             packed::tma_load_4d(smem_u32(ring + st * kTile + c * 16384), issued & 1 ? &maps.dout : &maps.q, c * 64, 0,
-                                h, seq.q0 + t0 + (issued >> 1) * tile_tokens, &bars[L::kFull + st]);
+                                h, seq.q0 + tile_token(issued >> 1), &bars[L::kFull + st]);
         }
       }
       issued = __shfl_sync(0xffffffffu, issued, 0);
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars[L::kRowsFree + buf], (i / 2 - 1) & 1, s.status))) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = lane + 32 * k, token = t0 + i * tile_tokens + r / s.G;
+          const int r = lane + 32 * k, token = tile_token(i) + r / s.G;
           float2 v = make_float2(INFINITY, 0.f);
           if (r < tile_rows && token < seq.n_q)
             v = __ldg(g.rows + static_cast<long long>(seq.q0 + token) * (s.Hkv * s.G) + h * s.G + r % s.G);
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int i = 0; i < n; ++i) {
       // Rows of tokens before key - before do not attend the key.
-      const int token0 = t0 + i * tile_tokens;
+      const int token0 = tile_token(i);
       const int from = (key - before - token0) * s.G - 64 * half;
       const bool masked = warp_last - before > token0;
       const float4* lse2 = reinterpret_cast<const float4*>(rows + (i & 1) * 256 + 64 * half);
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
     }
     if (n > 0) wait(L::kDone, 0);
-    // ---- the first warpgroup writes dv, the second dk ----
+    // ---- the first warpgroup has dv, the second dk ----
     const bool active = key < seq.n_k;
     const PackedStride st = half ? g.dk_st : g.dv_st;
     uint16_t* to = static_cast<uint16_t*>(half ? g.dk : g.dv) + static_cast<long long>(seq.k0 + key) * st.token +
@@ -603,7 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld32(lane_addr + (half ? kKvDk : kKvDv) + 32 * c, w);
         tc::wait_ld();
       }
-      if (active) {
+      if (ctas > 1) {   // into this CTA's ring, which is free now
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          parts[packed::swizzled<kD>(half * 128 + (tid & 127), 8 * c + i)] =
+              make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
+                          __uint_as_float(w[4 * i + 3]));
+      } else if (active) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t p[4];
@@ -616,6 +629,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (ctas > 1) {
+    // ---- every CTA sums its share of the rows over the cluster, in the order of the ranks ----
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8) {   // (the others have given registers away)
+      const int share = 2 * 128 / ctas;   // rows of dv, then of dk
+      for (int e = tid; e < share * (kD / 4); e += 256) {
+        const int row = rank * share + e / (kD / 4), c4 = e % (kD / 4);
+        const int which = row >> 7, key = key0 + (row & 127);
+        if (key >= seq.n_k) continue;
+        const float4* mine = parts + packed::swizzled<kD>(row, c4);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < ctas; ++c) {
+          const float4 x = packed::ld_dsmem_f32x4(dsmem_addr(mine, static_cast<uint32_t>(c)));
+          sum.x += x.x;
+          sum.y += x.y;
+          sum.z += x.z;
+          sum.w += x.w;
+        }
+        const PackedStride st = which ? g.dk_st : g.dv_st;
+        const float scale = which ? s.scale : kDown;
+        uint16_t* to = static_cast<uint16_t*>(which ? g.dk : g.dv) + static_cast<long long>(seq.k0 + key) * st.token +
+                       h * st.head + 4 * c4;
+        *reinterpret_cast<uint2*>(to) = make_uint2(packed::pack2<kFp16>(sum.x * scale, sum.y * scale),
+                                                   packed::pack2<kFp16>(sum.z * scale, sum.w * scale));
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while another reads its ring
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -624,22 +667,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename Kernel>
-cudaError_t launch_one(Kernel kernel, int bytes, long long ctas, const PackedAttnShape& s, const PackedAttnMaps& maps,
-                       const PackedAttnGrads& g, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <typename Kernel, typename... More>
+cudaError_t launch_one(Kernel kernel, int bytes, long long units, int ctas, cudaStream_t st, const More&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(units * ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, maps, s, g);
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = ctas;
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Tiles of `step` tokens of B sequences with `tokens` in all: at most one partly filled one each.
@@ -649,11 +695,23 @@ long long most_tiles(int tokens, int step, int B) {
 
 template <int kD, bool kFp16>
 cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const PackedAttnGrads& g, cudaStream_t st) {
-  const cudaError_t e = launch_one(packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
-                                   most_tiles(s.Tq, packed_tile_tokens(s.G), s.B) * s.Hkv, s, maps, g, st);
+  const cudaError_t e =
+      launch_one(packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
+                 most_tiles(s.Tq, packed_tile_tokens(s.G), s.B) * s.Hkv, 1, st, maps, s, g);
   if (e != cudaSuccess) return e;
-  return launch_one(packed_dkv_kernel<kD, kFp16>, DkvLayout<kD>::kBytes, most_tiles(s.Tk, 128, s.B) * s.Hkv, s, maps,
-                    g, st);
+  // CTAs per tile of keys.  Causal tiles differ by the whole length of the sequence, so
+  // units that are few leave SMs idle behind the longest: one 8K sequence with 2 KV
+  // heads took 1.42 ms with clusters of 4, 1.53 with 2, 1.76 with 8 (which few SMs
+  // of a GPC are left over for) and 2.52 alone.  16 documents (640 units) took
+  // 0.57 ms alone and 0.62 with 2: enough units, and the join costs a few row tiles.
+  const long long units = ((s.Tk + s.B - 1) / s.B + 127) / 128 * static_cast<long long>(s.B) * s.Hkv;
+  const long long row_tiles = static_cast<long long>(s.Tq) * s.G / 128 / s.B;
+  const int sms = device_sm_count();
+  int ctas = 1;
+  while (ctas < 4 && units * ctas < 2 * sms && row_tiles >= 12 * ctas) ctas *= 2;
+  if (ctas == 4 && units * 8 <= sms && row_tiles >= 48) ctas = 8;
+  return launch_one(packed_dkv_kernel<kD, kFp16>, DkvLayout<kD>::kBytes, most_tiles(s.Tk, 128, s.B) * s.Hkv, ctas, st,
+                    maps, s, g, ctas);
 }
 
 }  // namespace
