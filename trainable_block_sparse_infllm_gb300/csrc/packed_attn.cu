@@ -6,26 +6,33 @@
 // in base 2: with m >= the row's scores (up to 2^8, see below), x = sum 2^(z - m) v
 // and l = sum 2^(z - m) are kept per row, and out = x / l.  One pass over the keys.
 //
-// A CTA takes two adjacent tiles (256 rows) of one sequence and KV head, and walks
-// the keys in tiles of 128 up to the last one that a row attends:
+// A unit is two adjacent tiles (256 rows) of one sequence and KV head; it walks the
+// keys in tiles of 128 up to the last one that a row attends.  A CTA stays on its SM
+// and takes one unit after another, the longest first; while a unit's last tiles are
+// finished the next one's copies and first scores are under way.
 //   warps 0-3, 4-7  softmax of the first and second tile; a thread is a row.  S
 //              comes from tensor memory, P (16 bits) goes back over it, which makes
 //              it the A operand of P V.  The running maximum moves only when it
 //              grows by more than 2^8, which is rare, so x is rarely rescaled.
 //   warp 8     issues the products of both tiles in turn: while one tile's softmax
 //              runs, the other's P V and next Q K^T keep the tensor cores busy.
-//              P V of key tile j before S of j + 1 in issue order: S overwrites P.
-//   warp 9     TMA: both Q tiles, then K_0, V_0, K_1, V_1, ... through a ring.
+//   warp 9     finds the units; TMA: both Q tiles, then K_0, V_0, K_1, V_1, ...
+//              through a ring that goes on from unit to unit.
 //   warps 10, 11  look through the V tiles that some row attends in part (at most
 //              three): a zero probability must meet no infinity or NaN.  Rows behind
 //              the sequence's end are cleared; a row of the sequence that holds one is
 //              cleared too, and the rows that attend it add it at the end, one by one.
+// Jobs (a tile's scores for one tile of keys, then P V) go through the score buffers
+// in tensor memory in turn, columns of 128: two for D = 128 and three for D = 64,
+// beside two accumulators of D.  S of job k goes out right after P V of job k - 2 or
+// k - 3, whose P it overwrites; with three the next scores of a tile are done before
+// its softmax is, which is what bounds D = 64.
 // Few queries against many keys (drafted tokens, a short chunk after a long past)
 // leave most SMs without a unit: its key tiles are then divided over a cluster,
 // whose CTAs join their (m, l, x) through distributed shared memory.
-// Tensor memory: two S / P buffers of 128 columns and two accumulators of D.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kernels.h"
 #include "packed_attn.cuh"
@@ -43,21 +50,34 @@ constexpr float kLazy = 8.0f;   // log2 of how far scores may pass the running m
 // small probabilities could add up to; its largest value leaves room for 2^(6 + 8).
 template <bool kFp16>
 constexpr float kTop = kFp16 ? 6.0f : 0.0f;
-constexpr uint32_t kColO = 256;
 
 template <int kD>
 struct Layout {
   static constexpr int kTile = kD / 64 * 16384;   // 128 rows of kD
   static constexpr int kStages = kRing / kTile;
+  static constexpr int kBuffers = kD == 64 ? 3 : 2;   // of scores
+  static constexpr uint32_t kColO = 128 * kBuffers;
   static constexpr int kBars = 2 * kTile + kRing;
-  // Barriers: Q of each tile, ring full and empty, V tiles attended in part, before and after they were
-  // looked through, then S, P and O of each tile.
-  static constexpr int kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kPartial = kEmpty + kStages,
-                       kChecked = kPartial + kMaxPartial, kSFull = kChecked + kMaxPartial, kPFull = kSFull + 2,
-                       kODone = kPFull + 2, kNumBars = kODone + 2;
-  static constexpr int kScratch = kBars + 8 * kNumBars;
-  static constexpr int kFlags = kScratch + 32;   // [kMaxPartial][4]: rows of those tiles that were cleared
-  static constexpr int kBytes = kFlags + kMaxPartial * 16 + 1024;   // and slack to align the tiles
+  // Barriers: a unit found and done with; Q of each tile full and free; ring full and empty; V tiles
+  // attended in part, before and after they were looked through; of each score buffer S and P; of each
+  // tile P V (three, in turn) and x read; kSplit: all products.
+  static constexpr int kUnit = 0, kUnitFree = kUnit + 2, kQFull = kUnitFree + 2, kQFree = kQFull + 2,
+                       kFull = kQFree + 2, kEmpty = kFull + kStages, kPartial = kEmpty + kStages,
+                       kChecked = kPartial + kMaxPartial, kSFull = kChecked + kMaxPartial,
+                       kPFull = kSFull + kBuffers, kPvDone = kPFull + kBuffers, kOFree = kPvDone + 6, kAllDone = kOFree + 2, kNumBars = kAllDone + 1;
+  static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 32 bytes each
+  static constexpr int kFlags = kUnits + 2 * 32;   // of each unit [kMaxPartial][4]: rows that were cleared
+  static constexpr int kSlot = kFlags + 2 * kMaxPartial * 16;
+  static constexpr int kBytes = kSlot + 16 + 1024;   // and slack to align the tiles
+};
+
+// What the roles need to know of a unit.  All tile indexes count from key tile j0.
+struct Unit {
+  packed::Sequence seq;
+  int t0, h;             // its first query and its KV head
+  int before;            // query t attends keys 0 .. before + t
+  int j0, n_tiles[2], n;
+  int partial, looked;   // the first key tile that some row attends in part, and that is looked through
 };
 
 template <int kD, bool kFp16>
@@ -72,18 +92,19 @@ __device__ __forceinline__ float dot(const uint16_t* q, const uint16_t* k) {
   return z;
 }
 
-// kSplit: a unit's key tiles are divided over a cluster of `ctas` CTAs.
+// kSplit: one unit per cluster of `ctas` CTAs, among which its key tiles are divided.
 template <int kD, bool kFp16, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnIn in,
                        const PackedAttnOut o, const int ctas) {
   using L = Layout<kD>;
-  constexpr int kTile = L::kTile, kStages = L::kStages;
+  constexpr int kTile = L::kTile, kStages = L::kStages, kBuffers = L::kBuffers;
+  constexpr uint32_t kColO = L::kColO;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  int* scratch = reinterpret_cast<int*>(smem + L::kScratch);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
+  int4* units = reinterpret_cast<int4*>(smem + L::kUnits);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlags);
   uint8_t* ring = smem + 2 * kTile;
   // kSplit, at the end, over the ring: x of this CTA's 256 rows, their (m, l), and the weights of the share it joins.
@@ -91,45 +112,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* sums = reinterpret_cast<float2*>(ring + 256 * kD * 4);
   float* weights = reinterpret_cast<float*>(sums + 256);   // [256 / ctas][16]
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
-
-  pdl_wait();
-  pdl_trigger();
   const int tile_tokens = packed_tile_tokens(s.G);
   const int rank = kSplit ? static_cast<int>(blockIdx.x) % ctas : 0;
-  const int index = kSplit ? static_cast<int>(blockIdx.x) / ctas : static_cast<int>(blockIdx.x);
-  const int h = index % s.Hkv;
-  int b, unit;
-  if (!packed::find_tile(s, index / s.Hkv, 2 * tile_tokens, false, scratch, &b, &unit)) return;   // the whole cluster
-  bool bad = false;
-  const packed::Sequence seq = packed::sequence(s, b, &bad);
-  const int t0 = unit * 2 * tile_tokens;   // the CTA's first query
-  const int before = seq.n_k - seq.n_q;    // query t attends keys 0 .. before + t
-  // Key tiles of each half: up to its last query's own key.
-  int n_tiles[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int first = t0 + x * tile_tokens, last = min(first + tile_tokens, seq.n_q) - 1;
-    n_tiles[x] = last < first ? 0 : (max(before + last + 1, 0) + 127) / 128;
-  }
-  int j0 = 0;   // this CTA's first key tile; all tile indexes below count from it
-  if (kSplit) {
-    const int all = max(n_tiles[0], n_tiles[1]);
-    j0 = rank * all / ctas;
-    const int j1 = (rank + 1) * all / ctas;
-    n_tiles[0] = max(min(n_tiles[0], j1) - j0, 0);
-    n_tiles[1] = max(min(n_tiles[1], j1) - j0, 0);
-  }
-  const int n = max(n_tiles[0], n_tiles[1]);
-  const int partial = max(before + t0 + 1, 0) / 128 - j0;   // the first key tile that some row attends in part
-  const int looked = max(partial, 0);                        // the first of this CTA's that is looked through
 
   if (tid == 0) {
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
     for (int i = 0; i < L::kNumBars; ++i) {
-      const bool by_warps = i == L::kPFull || i == L::kPFull + 1;
-      mbar_init(&bars[i], by_warps ? 4 : i >= L::kChecked && i < L::kChecked + kMaxPartial ? 2 : 1);
+      int count = 1;
+      if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
+      if ((i >= L::kPFull && i < L::kPFull + kBuffers) || (i >= L::kOFree && i < L::kOFree + 2)) count = 4;
+      if (i >= L::kChecked && i < L::kChecked + kMaxPartial) count = 2;
+      mbar_init(&bars[i], count);
     }
     fence_barrier_init();
   }
@@ -141,54 +136,147 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  // A unit from where it lies: (sequence, index of its two tiles, KV head).
+  auto unit_of = [&](int4 at) {
+    Unit u;
+    bool bad = false;
+    u.seq = packed::sequence(s, at.x, &bad);
+    u.t0 = at.y * 2 * tile_tokens;
+    u.h = at.z;
+    u.before = u.seq.n_k - u.seq.n_q;
+    u.j0 = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {   // each half: up to its last query's own key
+      const int first = u.t0 + x * tile_tokens, last = min(first + tile_tokens, u.seq.n_q) - 1;
+      u.n_tiles[x] = last < first ? 0 : (max(u.before + last + 1, 0) + 127) / 128;
+    }
+    if (kSplit) {
+      const int all = max(u.n_tiles[0], u.n_tiles[1]), j1 = (rank + 1) * all / ctas;
+      u.j0 = rank * all / ctas;
+      u.n_tiles[0] = max(min(u.n_tiles[0], j1) - u.j0, 0);
+      u.n_tiles[1] = max(min(u.n_tiles[1], j1) - u.j0, 0);
+    }
+    u.n = max(u.n_tiles[0], u.n_tiles[1]);
+    u.partial = max(u.before + u.t0 + 1, 0) / 128 - u.j0;
+    u.looked = max(u.partial, 0);
+    return u;
+  };
+  // The next unit, for the warps that do not find it: false past the last one, or after a wait that gave up.
+  auto next_unit = [&](int k, bool* ok, Unit* u) {
+    if (*ok) *ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnit + (k & 1)], (k >> 1) & 1, s.status));
+    if (!*ok) return false;
+    int4 at = units[2 * (k & 1)];
+    at.x = __shfl_sync(0xffffffffu, at.x, 0);   // (uniform for the compiler, so that the roles' loops are)
+    if (at.x < 0) return false;
+    at.y = __shfl_sync(0xffffffffu, at.y, 0);
+    at.z = __shfl_sync(0xffffffffu, at.z, 0);
+    *u = unit_of(at);
+    return true;
+  };
+  auto unit_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[L::kUnitFree + (k & 1)]);
+  };
+  Unit u;
+  bool any = false;   // a softmax warp: the CTA had a unit (kSplit: its only one)
 
   if (warp >= 8) {
     packed::regs_down<72>();
-    if (warp == kTmaWarp && n > 0) {
-      // ------------------------------------------------------------ loads
-      int issued = 0;
-      if (lane == 0) {
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------- units and loads
+      packed::Walker walker;
+      bool bad = false, ok = true;
+      walker.start(s, 2 * tile_tokens, false, &bad);
+      int issued = 0, seen = 0, q_uses[2] = {0, 0};   // ring copies, V tiles looked through, Q tiles
+      const int stride = kSplit ? 1 : static_cast<int>(gridDim.x);
+      for (int k = 0;; ++k) {
+        // Unit number k of this CTA: down the order of all and back, so that none gets the longest of each round.
+        int i = kSplit ? static_cast<int>(blockIdx.x) / ctas : static_cast<int>(blockIdx.x);
+        if (!kSplit) i = k * stride + (k & 1 ? stride - 1 - i : i);
+        int4 at = make_int4(-1, 0, i % s.Hkv, 0);
+        int b, level;
+        if (!(kSplit && k > 0) && walker.find(s, i / s.Hkv, 2 * tile_tokens, false, &b, &level, &bad)) {
+          at.x = b;
+          at.y = level;
+        }
+        if (k >= 2 && ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnitFree + (k & 1)], ((k >> 1) - 1) & 1, s.status));
+        if (!ok) at.x = -1;
+        if (lane == 0) {
+          units[2 * (k & 1)] = at;
+          mbar_arrive(&bars[L::kUnit + (k & 1)]);
+        }
+        __syncwarp();
+        if (at.x < 0) break;
+        u = unit_of(at);
         const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (n_tiles[x] == 0) continue;
-          mbar_arrive_expect_tx(&bars[L::kQFull + x], row_bytes);
-          for (int c = 0; c < kD / 64; ++c)
-            packed::tma_load_4d(smem_u32(smem + x * kTile + c * 16384), &maps.q, c * 64, 0, h,
-                                seq.q0 + t0 + x * tile_tokens, &bars[L::kQFull + x]);
-        }
-        for (; issued < 2 * n; ++issued) {
-          const int st = issued % kStages;
-          if (issued >= kStages && !mbar_wait(&bars[L::kEmpty + st], (issued / kStages - 1) & 1, s.status)) break;
-          // A V tile to be looked through lands on a barrier of its own; its stage's only counts the turn.
-          const int j = issued >> 1;
-          uint64_t* bar = &bars[L::kFull + st];
-          if ((issued & 1) && j >= partial) {
-            mbar_arrive(bar);
-            bar = &bars[L::kPartial + j - partial];
+          if (u.n_tiles[x] == 0) continue;
+          if (q_uses[x] > 0 && ok)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kQFree + x], (q_uses[x] - 1) & 1, s.status));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars[L::kQFull + x], row_bytes);
+            for (int c = 0; c < kD / 64; ++c)
+              packed::tma_load_4d(smem_u32(smem + x * kTile + c * 16384), &maps.q, c * 64, 0, u.h,
+                                  u.seq.q0 + u.t0 + x * tile_tokens, &bars[L::kQFull + x]);
           }
-          mbar_arrive_expect_tx(bar, kTile);
-          for (int c = 0; c < kD / 64; ++c)
-            packed::tma_load_3d(smem_u32(ring + st * kTile + c * 16384), issued & 1 ? &maps.v : &maps.k, c * 64,
-                                seq.k0 + (j0 + j) * 128, h, bar);
+          ++q_uses[x];
         }
+        for (int i2 = 0; i2 < 2 * u.n && ok; ++i2) {
+          const int st = issued % kStages, j = i2 >> 1;
+          if (issued >= kStages)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kEmpty + st], (issued / kStages - 1) & 1, s.status));
+          if (!ok) break;
+          // A V tile to be looked through lands on a barrier of its own; its stage's only counts the turn.
+          uint64_t* bar = &bars[L::kFull + st];
+          const bool looks = (i2 & 1) && j >= u.looked;
+          if (lane == 0) {
+            if (looks) {
+              mbar_arrive(bar);
+              bar = &bars[L::kPartial + seen % kMaxPartial];
+            }
+            mbar_arrive_expect_tx(bar, kTile);
+            for (int c = 0; c < kD / 64; ++c)
+              packed::tma_load_3d(smem_u32(ring + st * kTile + c * 16384), i2 & 1 ? &maps.v : &maps.k, c * 64,
+                                  u.seq.k0 + (u.j0 + j) * 128, u.h, bar);
+          }
+          seen += looks;
+          ++issued;
+        }
+        __syncwarp();
       }
-      issued = __shfl_sync(0xffffffffu, issued, 0);
-      // The CTA outlives its copies, also after a wait that gave up.  (The last copy
-      // of a stage is its barrier's newest phase here.)
+      if (bad && blockIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
+      // The CTA outlives its copies, also after a wait that gave up.  (Each barrier's last copy is its
+      // newest phase here.)
       for (int i = max(0, issued - kStages); i < issued; ++i)
         mbar_wait(&bars[L::kFull + i % kStages], (i / kStages) & 1, s.status);
-      for (int j = looked; 2 * j + 1 < issued; ++j) mbar_wait(&bars[L::kPartial + j - partial], 0, s.status);
+      for (int i = max(0, seen - kMaxPartial); i < seen; ++i)
+        mbar_wait(&bars[L::kPartial + i % kMaxPartial], (i / kMaxPartial) & 1, s.status);
       for (int x = 0; x < 2; ++x)
-        if (n_tiles[x] > 0) mbar_wait(&bars[L::kQFull + x], 0, s.status);
+        if (q_uses[x] > 0) mbar_wait(&bars[L::kQFull + x], (q_uses[x] - 1) & 1, s.status);
     } else if (warp >= kCheckWarp) {
       // ---------------------------------------------- V attended in part
-      for (int j = looked; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[L::kPartial + j - partial], 0, s.status))) break;
-        packed::check_rows<kD, kFp16>(ring + (2 * j + 1) % kStages * kTile, warp - kCheckWarp,
-                                      seq.n_k - (j0 + j) * 128, flags + 4 * (j - partial));
-        if (lane == 0) mbar_arrive(&bars[L::kChecked + j - partial]);
+      bool ok = true;
+      int copies = 0, seen = 0;
+      for (int k = 0; next_unit(k, &ok, &u); ++k) {
+        for (int j = u.looked; j < u.n && ok; ++j, ++seen) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kPartial + seen % kMaxPartial], (seen / kMaxPartial) & 1,
+                                                 s.status));
+          if (!ok) break;
+          packed::check_rows<kD, kFp16>(ring + (copies + 2 * j + 1) % kStages * kTile, warp - kCheckWarp,
+                                        u.seq.n_k - (u.j0 + j) * 128,
+                                        flags + ((k & 1) * kMaxPartial + j - u.looked) * 4);
+          if (lane == 0) mbar_arrive(&bars[L::kChecked + seen % kMaxPartial]);
+        }
+        copies += 2 * u.n;
+        unit_done(k);
       }
-    } else if (warp == kMmaWarp && n > 0) {
+    } else if (warp == kMmaWarp) {
       // --------------------------------------------------------- products
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
@@ -201,52 +289,154 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
         tc::fence_after_sync();
       };
-      auto scores = [&](int x, int j) {   // S of half x and key tile j
-        if (issuer) {
-          packed::mma_rows<kD>(tmem + x * 128, q_desc + ((x * kTile) >> 4),
-                               k_desc + (((2 * j) % kStages * kTile) >> 4), kIdS);
-          tc::commit(&bars[L::kSFull + x]);
-        }
-        __syncwarp();
+      auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+      // Where the scores' and the P V stream are: stage and phase in the ring (every other place is a K),
+      // score buffer and phase.  They go on from unit to unit.
+      struct Stream {
+        int stage, stage_phase, buffer, buffer_phase;
       };
-      wait(L::kFull, 0);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (n_tiles[x] == 0) continue;
-        wait(L::kQFull + x, 0);
-        if (ok) scores(x, 0);
-      }
-      if (ok && issuer) tc::commit(&bars[L::kEmpty]);
-      __syncwarp();
-      for (int j = 0; j < n && ok; ++j) {
-        const int vi = 2 * j + 1, ki = 2 * j + 2;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (j >= n_tiles[x] || !ok) continue;
-          if (j < partial) {
-            wait(L::kFull + vi % kStages, vi / kStages);
-          } else {
-            wait(L::kChecked + j - partial, 0);
-          }
-          wait(L::kPFull + x, j);
-          if (!ok) continue;
-          if (issuer)
-            packed::mma_cols(tmem + kColO + x * kD, tmem + x * 128, v_desc + ((vi % kStages * kTile) >> 4), kIdO,
-                             j > 0);
-          __syncwarp();
-          if (j + 1 < n_tiles[x]) {
-            wait(L::kFull + ki % kStages, ki / kStages);
-            if (ok) scores(x, j + 1);
-          } else {
-            if (issuer) tc::commit(&bars[L::kODone + x]);
+      Stream ss = {0, 0, 0, 0}, sv = {1, 0, 0, 0};
+      auto next_tile = [](Stream& t) {
+        t.stage += 2;
+        if (t.stage >= kStages) {
+          t.stage -= kStages;
+          t.stage_phase ^= 1;
+        }
+      };
+      auto next_buffer = [](Stream& t) {
+        if (++t.buffer == kBuffers) {
+          t.buffer = 0;
+          t.buffer_phase ^= 1;
+        }
+      };
+      // Of each half: its units and its P V barrier's turn; and V tiles looked through.  (After a wait that
+      // gave up nothing waits any more; what is issued then stays within this CTA's memory.)
+      int used[2] = {0, 0}, turn[2] = {0, 0}, look = 0, look_phase = 0;
+      auto next_turn = [&](int& t) { t = t == 2 ? 0 : t + 1; };
+      auto values = [&](bool checked) {   // this tile's V is there
+        if (!checked) {
+          wait(L::kFull + sv.stage, sv.stage_phase);
+          return;
+        }
+        wait(L::kChecked + look, look_phase);
+        if (++look == kMaxPartial) {
+          look = 0;
+          look_phase ^= 1;
+        }
+      };
+      for (int k = 0; next_unit(k, &ok, &u); ++k) {
+        const int n0 = uniform(u.n_tiles[0]), n1 = uniform(u.n_tiles[1]), looked = uniform(u.looked);
+        const int n = max(n0, n1);
+        if constexpr (kBuffers == 2) {
+          // A buffer for each half; both in turn, each P V followed by the half's next scores.
+          auto scores = [&](auto half, bool first, bool last) {
+            constexpr int x = decltype(half)::value;
+            if (first) wait(L::kQFull + x, used[x]);
+            if (issuer) {
+              packed::mma_rows<kD>(tmem + x * 128, q_desc + (x * kTile >> 4),
+                                   k_desc + static_cast<uint64_t>(ss.stage * (kTile >> 4)), kIdS);
+              tc::commit(&bars[L::kSFull + x]);
+              if (last) tc::commit(&bars[L::kQFree + x]);
+            }
             __syncwarp();
+          };
+          auto job = [&](auto half, int j, int mine) {
+            constexpr int x = decltype(half)::value;
+            if (j == 0 && used[x] > 0) wait(L::kOFree + x, used[x] - 1);   // the last unit's x has been read
+            wait(L::kPFull + x, x ? ss.buffer_phase : sv.buffer_phase);
+            if (x) {
+              ss.buffer_phase ^= 1;
+            } else {
+              sv.buffer_phase ^= 1;
+            }
+            if (issuer) {
+              packed::mma_cols(tmem + kColO + x * kD, tmem + x * 128,
+                               v_desc + static_cast<uint64_t>(sv.stage * (kTile >> 4)), kIdO, j > 0);
+              if (j + 1 == mine) tc::commit(&bars[L::kPvDone + 3 * x + turn[x]]);
+            }
+            __syncwarp();
+            if (j + 1 < mine) scores(half, false, j + 2 == mine);
+          };
+          using Half0 = std::integral_constant<int, 0>;
+          using Half1 = std::integral_constant<int, 1>;
+          if (n > 0) wait(L::kFull + ss.stage, ss.stage_phase);
+          if (n0 > 0) scores(Half0(), true, n0 == 1);
+          if (n1 > 0) scores(Half1(), true, n1 == 1);
+          for (int j = 0; j < n; ++j) {
+            if (issuer) tc::commit(&bars[L::kEmpty + ss.stage]);   // K of tile j
+            __syncwarp();
+            next_tile(ss);
+            values(j >= looked);
+            if (j + 1 < n) wait(L::kFull + ss.stage, ss.stage_phase);
+            if (j < n0) job(Half0(), j, n0);
+            if (j < n1) job(Half1(), j, n1);
+            if (issuer) tc::commit(&bars[L::kEmpty + sv.stage]);
+            __syncwarp();
+            next_tile(sv);
+          }
+          if (n0 > 0) next_turn(turn[0]);
+          if (n1 > 0) next_turn(turn[1]);
+        } else {
+          // The unit's jobs: the halves in turn, then what the longer one has more.
+          const int both = min(n0, n1), total = n0 + n1, longer = n1 > n0 ? 1 : 0;
+          int xs = both > 0 ? 0 : longer, js = 0, xv = xs, jv = 0;
+          auto next_job = [&](int& x, int& j) {   // true where the tile of keys changes
+            if (x == 0 && j < both) {
+              x = 1;
+              return false;
+            }
+            ++j;
+            x = j < both ? 0 : longer;
+            return true;
+          };
+          bool fresh = true;   // a tile of keys that no scores have been issued for
+          auto scores = [&](bool last) {
+            const int x = xs, j = js;
+            if (j == 0) wait(L::kQFull + x, x ? used[1] : used[0]);
+            if (fresh) wait(L::kFull + ss.stage, ss.stage_phase);
+            const bool q_free = j + 1 == (x ? n1 : n0);
+            fresh = next_job(xs, js) || last;   // K's last reader
+            if (issuer) {
+              packed::mma_rows<kD>(tmem + ss.buffer * 128, q_desc + (x ? kTile >> 4 : 0),
+                                   k_desc + static_cast<uint64_t>(ss.stage * (kTile >> 4)), kIdS);
+              tc::commit(&bars[L::kSFull + ss.buffer]);
+              if (fresh) tc::commit(&bars[L::kEmpty + ss.stage]);
+              if (q_free) tc::commit(&bars[L::kQFree + x]);
+            }
+            __syncwarp();
+            next_buffer(ss);
+            if (fresh) next_tile(ss);
+          };
+          for (int i = 0; i < min(total, kBuffers); ++i) scores(i + 1 == total);
+          bool opens = true;   // a tile whose V has not been waited for
+          for (int i = 0; i < total; ++i) {
+            const int x = xv, j = jv;
+            if (opens) values(j >= looked);
+            opens = next_job(xv, jv) || i + 1 == total;   // V's last reader
+            if (j == 0 && (x ? used[1] : used[0]) > 0) wait(L::kOFree + x, (x ? used[1] : used[0]) - 1);
+            wait(L::kPFull + sv.buffer, sv.buffer_phase);
+            if (issuer) {
+              packed::mma_cols(tmem + kColO + (x ? kD : 0), tmem + sv.buffer * 128,
+                               v_desc + static_cast<uint64_t>(sv.stage * (kTile >> 4)), kIdO, j > 0);
+              tc::commit(&bars[L::kPvDone + (x ? 3 + turn[1] : turn[0])]);
+              if (opens) tc::commit(&bars[L::kEmpty + sv.stage]);
+            }
+            __syncwarp();
+            if (i + kBuffers < total) scores(i + kBuffers + 1 == total);
+            next_buffer(sv);
+            if (x) {
+              next_turn(turn[1]);
+            } else {
+              next_turn(turn[0]);
+            }
+            if (opens) next_tile(sv);
           }
         }
-        if (ok && issuer) {
-          tc::commit(&bars[L::kEmpty + vi % kStages]);
-          if (j + 1 < n) tc::commit(&bars[L::kEmpty + ki % kStages]);
-        }
+        if (kSplit && issuer) tc::commit(&bars[L::kAllDone]);
         __syncwarp();
+        used[0] += n0 > 0;
+        used[1] += n1 > 0;
+        unit_done(k);
       }
     }
     __syncwarp();
@@ -255,143 +445,177 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed::regs_up<216>();
     const int x = warp >> 2;
     const int r = tid & 127;
-    const int token = t0 + x * tile_tokens + r / s.G;   // in the sequence
-    const bool active = r < tile_tokens * s.G && token < seq.n_q;
-    const int limit = active ? before + token + 1 - j0 * 128 : 0;   // keys 0 .. limit - 1, from tile j0 on
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + x * 128, o_addr = lane_addr + kColO + x * kD;
-    const int mine = x ? n_tiles[1] : n_tiles[0];
-    // Key tiles before this one need no mask in any row of the warp.
-    const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
-    float m = -INFINITY, l = 0.f;
+    const uint32_t o_addr = lane_addr + kColO + x * kD;
+    const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
     bool ok = true;
-    for (int j = 0; j < mine; ++j) {
-      // (A warp whose wait gave up goes on without waiting; the status word has the error.)
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kSFull + x], j & 1, s.status));
-      tc::fence_after_sync();
-      uint32_t z[128];
+    int jobs = 0, done = 0, used = 0;   // of all units before: jobs, this half's, and its units
+    for (int k = 0; next_unit(k, &ok, &u); ++k) {
+      any = true;
+      const int token = u.t0 + x * tile_tokens + r / s.G;   // in the sequence
+      const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
+      const int limit = active ? u.before + token + 1 - u.j0 * 128 : 0;   // keys 0 .. limit - 1, from tile j0 on
+      const int mine = x ? u.n_tiles[1] : u.n_tiles[0], both = min(u.n_tiles[0], u.n_tiles[1]);
+      // Key tiles before this one need no mask in any row of the warp.
+      const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
+      // P V number i of the half is done (two buffers: the last of its unit i).  With three buffers S of a tile
+      // may be there before its last three P V are done, but no more: with a barrier for every third one,
+      // none is two phases off.
+      auto product_done = [&](int i) {
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kPvDone + 3 * x + i % 3], (i / 3) & 1, s.status));
+        tc::fence_after_sync();
+      };
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < mine; ++j) {
+        const int job = kBuffers == 2 ? 2 * (done + j) + x : jobs + (j < both ? 2 * j + x : both + j);
+        const int buffer = job % kBuffers;
+        const uint32_t s_addr = lane_addr + buffer * 128;
+        // (A warp whose wait gave up goes on without waiting; the status word has the error.)
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kSFull + buffer], (job / kBuffers) & 1, s.status));
+        tc::fence_after_sync();
+        uint32_t z[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
-      tc::wait_ld();
-      if (j >= whole) {
-        const int keep = limit - j * 128;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) z[i] = i < keep ? z[i] : 0xff800000u;   // -inf
-      }
-      float t[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(z[i]);
-#pragma unroll
-      for (int i = 4; i < 128; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(z[i]));
-      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * s.scale2;
-      // S of tile j was issued after P V of tile j - 1, so x may be rescaled now.
-      const bool move = top > m + kLazy;
-      if (__any_sync(0xffffffffu, move)) {
-        const float alpha = move ? fast_exp2(m - top) : 1.f;   // 0 the first time
-        if (move) {
-          m = top;
-          l *= alpha;
-        }
-        if (j > 0) {
-#pragma unroll 1
-          for (int c = 0; c < kD / 32; ++c) {
-            uint32_t w[32];
-            tc::ld32(o_addr + 32 * c, w);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-            tc::st32(o_addr + 32 * c, w);
-          }
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m - kTop<kFp16>;   // (a row that attends no key yet)
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t p[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(fmaf(__uint_as_float(z[64 * c + 2 * i]), s.scale2, -base));
-          const float d = fast_exp2(fmaf(__uint_as_float(z[64 * c + 2 * i + 1]), s.scale2, -base));
-          sum[0] += a;
-          sum[1] += d;
-          p[i] = packed::pack2<kFp16>(a, d);
-        }
-        tc::st32(s_addr + 32 * c, p);
-      }
-      l += sum[0] + sum[1];
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kPFull + x]);
-    }
-    // (kSplit: of both halves, whose products read the ring that is written next.)
-    for (int y = 0; y < 2; ++y)
-      if ((kSplit || y == x) && n_tiles[y] > 0 && ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kODone + y], 0, s.status));
-    tc::fence_after_sync();
-    // ---- x / l and the log sum ----
-    const float inv = 1.f / l;
-    const int head = h * s.G + r % s.G;
-    const long long row = seq.q0 + token;
-    const bool none = before + token < 0;   // the row attends no key
-    uint16_t* out = static_cast<uint16_t*>(o.out) + row * o.st.token + head * o.st.head;
-    const uint16_t* q_row = static_cast<const uint16_t*>(in.q) + row * in.q_st.token + head * in.q_st.head;
-    uint32_t cleared = 0u;   // P V of the last tile is done, so every tile has been looked through
-    for (int j = looked; j < mine && ok; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kChecked + j - partial], 0, s.status));
-      for (int i = 0; i < 4; ++i) cleared |= flags[4 * (j - partial) + i];
-    }
-#pragma unroll 1
-    for (int c = 0; c < kD / 32; ++c) {
-      uint32_t w[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0u;
-      if (mine > 0) {
-        tc::ld32(o_addr + 32 * c, w);
+        for (int c = 0; c < 4; ++c) tc::ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
         tc::wait_ld();
-      }
-      if (cleared && active) {
-#pragma unroll 1
-        for (int key = looked * 128; key < min(limit, mine * 128); ++key) {
-          const int bit = key - partial * 128;
-          if (!((flags[bit >> 5] >> (bit & 31)) & 1)) continue;
-          const long long at = seq.k0 + j0 * 128 + key;
-          const uint16_t* k_row = static_cast<const uint16_t*>(in.k) + at * in.k_st.token + h * in.k_st.head;
-          const uint16_t* v_row = static_cast<const uint16_t*>(in.v) + at * in.v_st.token + h * in.v_st.head + 32 * c;
-          const float p = fast_exp2(fmaf(dot<kD, kFp16>(q_row, k_row), s.scale2, kTop<kFp16> - m));
+        if (j >= whole) {
+          const int keep = limit - j * 128;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 v = packed::unpack2<kFp16>(reinterpret_cast<const uint32_t*>(v_row)[i]);
-            w[2 * i] = __float_as_uint(fmaf(p, v.x, __uint_as_float(w[2 * i])));
-            w[2 * i + 1] = __float_as_uint(fmaf(p, v.y, __uint_as_float(w[2 * i + 1])));
-          }
+          for (int i = 0; i < 128; ++i) z[i] = i < keep ? z[i] : 0xff800000u;   // -inf
         }
-      }
-      if (kSplit) {   // into this CTA's ring, which is free now
+        float t[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          parts[packed::swizzled<kD>(x * 128 + r, 8 * c + i)] =
-              make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
-                          __uint_as_float(w[4 * i + 3]));
-      } else if (active) {
+        for (int i = 0; i < 4; ++i) t[i] = fmaxf(__uint_as_float(z[i]), __uint_as_float(z[i + 4]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[4];
+        for (int i = 8; i < 128; i += 8) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            p[e] = !none ? packed::pack2<kFp16>(__uint_as_float(w[8 * i + 2 * e]) * inv,
-                                                    __uint_as_float(w[8 * i + 2 * e + 1]) * inv)
-                             : 0u;
-          *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
+            t[e] = packed::max3(t[e], __uint_as_float(z[i + e]), __uint_as_float(z[i + e + 4]));
+        }
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * s.scale2;
+        const bool move = top > m + kLazy;
+        if (__any_sync(0xffffffffu, move)) {
+          const float alpha = move ? fast_exp2(m - top) : 1.f;   // 0 the first time
+          if (move) {
+            m = top;
+            l *= alpha;
+          }
+          if (j > 0) {   // x of the tiles before, once their P V is done
+            // (Two buffers: S of this tile was issued after that P V.)
+            if (kBuffers == 3) product_done(done + j - 1);
+#pragma unroll 1
+            for (int c = 0; c < kD / 32; ++c) {
+              uint32_t w[32];
+              tc::ld32(o_addr + 32 * c, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tc::st32(o_addr + 32 * c, w);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m - kTop<kFp16>;   // (a row that attends no key yet)
+        const uint64_t down = packed::pair(-base, -base);
+        uint64_t sum = 0ull;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int at = 64 * c + 2 * i;
+            const float2 e = packed::unpair(
+                packed::fma2(packed::pair(__uint_as_float(z[at]), __uint_as_float(z[at + 1])), scale2, down));
+            const float a = fast_exp2(e.x), d = fast_exp2(e.y);
+            sum = packed::add2(sum, packed::pair(a, d));
+            p[i] = packed::pack2<kFp16>(a, d);
+          }
+          tc::st32(s_addr + 32 * c, p);
+        }
+        const float2 halves = packed::unpair(sum);
+        l += halves.x + halves.y;
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kPFull + buffer]);
+      }
+      // ---- x / l and the log sum ----
+      if (mine > 0) product_done(kBuffers == 3 ? done + mine - 1 : used);
+      if (kSplit && ok)   // the other half's too: they read the ring, which is written next
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kAllDone], 0, s.status));
+      tc::fence_after_sync();
+      const float inv = 1.f / l;
+      const int head = u.h * s.G + r % s.G;
+      const long long row = u.seq.q0 + token;
+      const bool none = u.before + token < 0;   // the row attends no key
+      uint16_t* out = static_cast<uint16_t*>(o.out) + row * o.st.token + head * o.st.head;
+      const uint16_t* q_row = static_cast<const uint16_t*>(in.q) + row * in.q_st.token + head * in.q_st.head;
+      // Rows that were cleared.  (P V of each tile is done, so each has been looked through.)
+      const uint32_t* gone = flags + (k & 1) * kMaxPartial * 4;
+      uint32_t cleared = 0u;
+      for (int j = u.looked; j < mine && ok; ++j)
+        for (int i = 0; i < 4; ++i) cleared |= gone[4 * (j - u.looked) + i];
+#pragma unroll 1
+      for (int c = 0; c < kD / 32; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = 0u;
+        if (mine > 0) {
+          tc::ld32(o_addr + 32 * c, w);
+          tc::wait_ld();
+        }
+        if (cleared && active) {
+#pragma unroll 1
+          for (int key = u.looked * 128; key < min(limit, mine * 128); ++key) {
+            const int bit = key - u.looked * 128;
+            if (!((gone[bit >> 5] >> (bit & 31)) & 1)) continue;
+            const long long at = u.seq.k0 + u.j0 * 128 + key;
+            const uint16_t* k_row = static_cast<const uint16_t*>(in.k) + at * in.k_st.token + u.h * in.k_st.head;
+            const uint16_t* v_row =
+                static_cast<const uint16_t*>(in.v) + at * in.v_st.token + u.h * in.v_st.head + 32 * c;
+            const float p = fast_exp2(fmaf(dot<kD, kFp16>(q_row, k_row), s.scale2, kTop<kFp16> - m));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = packed::unpack2<kFp16>(reinterpret_cast<const uint32_t*>(v_row)[i]);
+              w[2 * i] = __float_as_uint(fmaf(p, v.x, __uint_as_float(w[2 * i])));
+              w[2 * i + 1] = __float_as_uint(fmaf(p, v.y, __uint_as_float(w[2 * i + 1])));
+            }
+          }
+        }
+        if (kSplit) {   // into this CTA's ring, which is free now
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            parts[packed::swizzled<kD>(x * 128 + r, 8 * c + i)] =
+                make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
+                            __uint_as_float(w[4 * i + 3]));
+        } else if (active) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = !none ? packed::pack2<kFp16>(__uint_as_float(w[8 * i + 2 * e]) * inv,
+                                                  __uint_as_float(w[8 * i + 2 * e + 1]) * inv)
+                           : 0u;
+            *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
         }
       }
-    }
-    if (kSplit) {
-      sums[x * 128 + r] = make_float2(m, l);
-    } else if (active && o.lse) {
-      o.lse[row * (s.Hkv * s.G) + head] =
-          !none ? (m - kTop<kFp16> + fast_log2(l)) * 0.69314718055994531f : -INFINITY;
+      if (mine > 0) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kOFree + x]);
+      }
+      if (kSplit) {
+        sums[x * 128 + r] = make_float2(m, l);
+      } else if (active && o.lse) {
+        o.lse[row * (s.Hkv * s.G) + head] =
+            !none ? (m - kTop<kFp16> + fast_log2(l)) * 0.69314718055994531f : -INFINITY;
+      }
+      jobs += u.n_tiles[0] + u.n_tiles[1];
+      done += mine;
+      used += mine > 0;
+      unit_done(k);
+      if (kSplit) break;
     }
   }
   if (kSplit) {
@@ -399,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // out = sum 2^(m - M) x / sum 2^(m - M) l ----
     __syncwarp();
     cluster_sync();
-    if (warp < 8) {   // (the others have given registers away)
+    if (any) {   // (the softmax warps: the others have given registers away)
       const int share = 256 / ctas, row0 = rank * share;
       for (int e = tid; e < share; e += 256) {   // a row: its weights, over l, and log sum
         const int row = row0 + e, rr = row & 127;
-        const int token = t0 + (row >> 7) * tile_tokens + rr / s.G;
+        const int token = u.t0 + (row >> 7) * tile_tokens + rr / s.G;
         float top = -INFINITY, l = 0.f;
         for (int c = 0; c < ctas; ++c) top = fmaxf(top, ld_dsmem_f32(dsmem_addr(&sums[row].x, c)));
         const float base = top == -INFINITY ? 0.f : top;
@@ -413,17 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           weights[e * 16 + c] = weight;
           l = fmaf(weight, ml.y, l);
         }
-        const bool active = rr < tile_tokens * s.G && token < seq.n_q, none = before + token < 0;
+        const bool active = rr < tile_tokens * s.G && token < u.seq.n_q, none = u.before + token < 0;
         for (int c = 0; c < ctas; ++c) weights[e * 16 + c] *= none ? 0.f : 1.f / l;
         if (active && o.lse)
-          o.lse[static_cast<long long>(seq.q0 + token) * (s.Hkv * s.G) + h * s.G + rr % s.G] =
+          o.lse[static_cast<long long>(u.seq.q0 + token) * (s.Hkv * s.G) + u.h * s.G + rr % s.G] =
               !none ? (top - kTop<kFp16> + fast_log2(l)) * 0.69314718055994531f : -INFINITY;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       for (int e = tid; e < share * (kD / 4); e += 256) {
         const int local = e / (kD / 4), c4 = e % (kD / 4), row = row0 + local, rr = row & 127;
-        const int token = t0 + (row >> 7) * tile_tokens + rr / s.G;
-        if (rr >= tile_tokens * s.G || token >= seq.n_q) continue;
+        const int token = u.t0 + (row >> 7) * tile_tokens + rr / s.G;
+        if (rr >= tile_tokens * s.G || token >= u.seq.n_q) continue;
         const float4* mine = parts + packed::swizzled<kD>(row, c4);
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   #pragma unroll 4
@@ -435,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum.z = fmaf(weight, v.z, sum.z);
           sum.w = fmaf(weight, v.w, sum.w);
         }
-        uint16_t* out = static_cast<uint16_t*>(o.out) + static_cast<long long>(seq.q0 + token) * o.st.token +
-                        (h * s.G + rr % s.G) * o.st.head + 4 * c4;
+        uint16_t* out = static_cast<uint16_t*>(o.out) + static_cast<long long>(u.seq.q0 + token) * o.st.token +
+                        (u.h * s.G + rr % s.G) * o.st.head + 4 * c4;
         *reinterpret_cast<uint2*>(out) =
             make_uint2(packed::pack2<kFp16>(sum.x, sum.y), packed::pack2<kFp16>(sum.z, sum.w));
       }
@@ -514,7 +738,9 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kD>::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * s.Hkv * ctas), 1, 1);
+  // A CTA per SM, or a cluster per unit.
+  const long long grid = ctas > 1 ? units * s.Hkv * ctas : std::min<long long>(units * s.Hkv, device_sm_count());
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Layout<kD>::kBytes;
   cfg.stream = st;

@@ -99,6 +99,64 @@ __device__ __forceinline__ bool find_tile(const PackedAttnShape& s, int i, int s
   return scratch[0] != 0;
 }
 
+// The same order for one warp that asks for one tile after another (i rising).  Up
+// to 32 sequences: by level, as above, from counts kept in registers.  More: the
+// sequences in turn, each from its last tile down, walked once (there is nothing to
+// balance among so many, and a search by level would read them all each time).
+struct Walker {
+  int count;     // of sequence base + lane
+  int base;      // more than 32: the 32 sequences at hand, and the tiles before them
+  int before;
+
+  __device__ __forceinline__ void load(const PackedAttnShape& s, int step, bool of_keys, bool* bad) {
+    const int b = base + static_cast<int>(threadIdx.x & 31);
+    count = b < s.B ? tile_count(s, b, step, of_keys, bad) : 0;
+  }
+
+  __device__ __forceinline__ void start(const PackedAttnShape& s, int step, bool of_keys, bool* bad) {
+    base = before = 0;
+    load(s, step, of_keys, bad);
+  }
+
+  // All lanes: the sequence and level of tile i; false past the last one.
+  __device__ __forceinline__ bool find(const PackedAttnShape& s, int i, int step, bool of_keys, int* b, int* level,
+                                       bool* bad) {
+    const int lane = threadIdx.x & 31;
+    if (s.B > 32) {
+      for (;;) {
+        const int incl = warp_inclusive_scan(count), all = __shfl_sync(0xffffffffu, incl, 31);
+        if (i < before + all) {
+          const unsigned mask = __ballot_sync(0xffffffffu, i < before + incl);
+          const int at = __ffs(mask) - 1;
+          *b = base + at;
+          *level = __shfl_sync(0xffffffffu, incl, at) - 1 - (i - before);   // from its last tile down
+          return true;
+        }
+        before += all;
+        base += 32;
+        if (base >= s.B) return false;
+        load(s, step, of_keys, bad);
+      }
+    }
+    auto at_least = [&](int t) {   // tiles of level t and up
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(max(count - t, 0))));
+    };
+    if (at_least(0) <= i) return false;
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, count);
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at_least(mid) > i) lo = mid; else hi = mid;
+    }
+    // Among the sequences that have a tile of this level, number `rank`.
+    const int rank = i - at_least(lo + 1);
+    const unsigned mask = __ballot_sync(0xffffffffu, count > lo);
+    const unsigned here = __ballot_sync(0xffffffffu, ((mask >> lane) & 1) && __popc(mask & ((1u << lane) - 1)) == rank);
+    *b = __ffs(here) - 1;
+    *level = lo;
+    return true;
+  }
+};
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -114,6 +172,38 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 template <bool kFp16>
