@@ -18,15 +18,17 @@
 //              runs, the other's P V and next Q K^T keep the tensor cores busy.
 //   warp 9     finds the units; TMA: both Q tiles, then K_0, V_0, K_1, V_1, ...
 //              through a ring that goes on from unit to unit.
-//   warps 10, 11  look through the V tiles that some row attends in part (at most
+//   warps 10, 11 (D = 64: 11; 10 issues the scores, 8 the P V)  look through the V tiles that some row attends in part (at most
 //              three): a zero probability must meet no infinity or NaN.  Rows behind
 //              the sequence's end are cleared; a row of the sequence that holds one is
 //              cleared too, and the rows that attend it add it at the end, one by one.
 // Jobs (a tile's scores for one tile of keys, then P V) go through the score buffers
 // in tensor memory in turn, columns of 128: two for D = 128 and three for D = 64,
-// beside two accumulators of D.  S of job k goes out right after P V of job k - 2 or
-// k - 3, whose P it overwrites; with three the next scores of a tile are done before
-// its softmax is, which is what bounds D = 64.
+// beside two accumulators of D.  S of job k overwrites P of job k - 2 or k - 3, so it goes
+// out behind that P V.  With three buffers the next scores of a tile are there before
+// its softmax ends.  An issuer that waits or computes addresses leaves the tensor
+// cores idle (their queue is short): the jobs of D = 64 are so small that two warps
+// share them, and the loop of D = 128 has its halves unrolled.
 // Few queries against many keys (drafted tokens, a short chunk after a long past)
 // leave most SMs without a unit: its key tiles are then divided over a cluster,
 // whose CTAs join their (m, l, x) through distributed shared memory.
@@ -60,11 +62,13 @@ struct Layout {
   static constexpr int kBars = 2 * kTile + kRing;
   // Barriers: a unit found and done with; Q of each tile full and free; ring full and empty; V tiles
   // attended in part, before and after they were looked through; of each score buffer S and P; of each
-  // tile P V (three, in turn) and x read; kSplit: all products.
+  // tile P V (three, in turn) and x read; kSplit: all products; of each
+  // score buffer P V once more, for who issues scores.
   static constexpr int kUnit = 0, kUnitFree = kUnit + 2, kQFull = kUnitFree + 2, kQFree = kQFull + 2,
                        kFull = kQFree + 2, kEmpty = kFull + kStages, kPartial = kEmpty + kStages,
                        kChecked = kPartial + kMaxPartial, kSFull = kChecked + kMaxPartial,
-                       kPFull = kSFull + kBuffers, kPvDone = kPFull + kBuffers, kOFree = kPvDone + 6, kAllDone = kOFree + 2, kNumBars = kAllDone + 1;
+                       kPFull = kSFull + kBuffers, kPvDone = kPFull + kBuffers, kOFree = kPvDone + 6, kAllDone = kOFree + 2, kReused = kAllDone + 1,
+                       kNumBars = kReused + kBuffers;
   static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 32 bytes each
   static constexpr int kFlags = kUnits + 2 * 32;   // of each unit [kMaxPartial][4]: rows that were cleared
   static constexpr int kSlot = kFlags + 2 * kMaxPartial * 16;
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int count = 1;
       if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
       if ((i >= L::kPFull && i < L::kPFull + kBuffers) || (i >= L::kOFree && i < L::kOFree + 2)) count = 4;
-      if (i >= L::kChecked && i < L::kChecked + kMaxPartial) count = 2;
+      if (i >= L::kChecked && i < L::kChecked + kMaxPartial) count = kBuffers == 2 ? 2 : 1;
       mbar_init(&bars[i], count);
     }
     fence_barrier_init();
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bars[L::kPartial + i % kMaxPartial], (i / kMaxPartial) & 1, s.status);
       for (int x = 0; x < 2; ++x)
         if (q_uses[x] > 0) mbar_wait(&bars[L::kQFull + x], (q_uses[x] - 1) & 1, s.status);
-    } else if (warp >= kCheckWarp) {
+    } else if (warp > kCheckWarp || (kBuffers == 2 && warp == kCheckWarp)) {
       // ---------------------------------------------- V attended in part
       bool ok = true;
       int copies = 0, seen = 0;
@@ -268,16 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kPartial + seen % kMaxPartial], (seen / kMaxPartial) & 1,
                                                  s.status));
           if (!ok) break;
-          packed::check_rows<kD, kFp16>(ring + (copies + 2 * j + 1) % kStages * kTile, warp - kCheckWarp,
-                                        u.seq.n_k - (u.j0 + j) * 128,
-                                        flags + ((k & 1) * kMaxPartial + j - u.looked) * 4);
+          for (int half = 0; half < 2; ++half)   // (two warps share a tile, or one has all of it)
+            if (kBuffers == 3 || half == warp - kCheckWarp)
+              packed::check_rows<kD, kFp16>(ring + (copies + 2 * j + 1) % kStages * kTile, half,
+                                            u.seq.n_k - (u.j0 + j) * 128,
+                                            flags + ((k & 1) * kMaxPartial + j - u.looked) * 4);
           if (lane == 0) mbar_arrive(&bars[L::kChecked + seen % kMaxPartial]);
         }
         copies += 2 * u.n;
         unit_done(k);
       }
-    } else if (warp == kMmaWarp) {
-      // --------------------------------------------------------- products
+    } else {
+      // ----------------- products (three buffers: scores by warp 10, P V by warp 8)
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
       const uint64_t q_desc = packed::desc_rows(smem_u32(smem));
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Of each half: its units and its P V barrier's turn; and V tiles looked through.  (After a wait that
       // gave up nothing waits any more; what is issued then stays within this CTA's memory.)
-      int used[2] = {0, 0}, turn[2] = {0, 0}, look = 0, look_phase = 0;
+      int used[2] = {0, 0}, turn[2] = {0, 0}, look = 0, look_phase = 0, jobs = 0;
       auto next_turn = [&](int& t) { t = t == 2 ? 0 : t + 1; };
       auto values = [&](bool checked) {   // this tile's V is there
         if (!checked) {
@@ -389,27 +395,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             x = j < both ? 0 : longer;
             return true;
           };
-          bool fresh = true;   // a tile of keys that no scores have been issued for
-          auto scores = [&](bool last) {
+          for (int i = 0; i < total && warp == kCheckWarp; ++i) {
             const int x = xs, j = js;
             if (j == 0) wait(L::kQFull + x, x ? used[1] : used[0]);
-            if (fresh) wait(L::kFull + ss.stage, ss.stage_phase);
+            if (i == 0 || x == 0 || j >= both) wait(L::kFull + ss.stage, ss.stage_phase);
             const bool q_free = j + 1 == (x ? n1 : n0);
-            fresh = next_job(xs, js) || last;   // K's last reader
+            const bool changes = next_job(xs, js) || i + 1 == total;   // K's last reader
+            if (jobs >= kBuffers) wait(L::kReused + ss.buffer, ss.buffer_phase ^ 1);
+            ++jobs;
             if (issuer) {
               packed::mma_rows<kD>(tmem + ss.buffer * 128, q_desc + (x ? kTile >> 4 : 0),
                                    k_desc + static_cast<uint64_t>(ss.stage * (kTile >> 4)), kIdS);
               tc::commit(&bars[L::kSFull + ss.buffer]);
-              if (fresh) tc::commit(&bars[L::kEmpty + ss.stage]);
+              if (changes) tc::commit(&bars[L::kEmpty + ss.stage]);
               if (q_free) tc::commit(&bars[L::kQFree + x]);
             }
             __syncwarp();
             next_buffer(ss);
-            if (fresh) next_tile(ss);
-          };
-          for (int i = 0; i < min(total, kBuffers); ++i) scores(i + 1 == total);
+            if (changes) next_tile(ss);
+          }
           bool opens = true;   // a tile whose V has not been waited for
-          for (int i = 0; i < total; ++i) {
+          for (int i = 0; i < total && warp == kMmaWarp; ++i) {
             const int x = xv, j = jv;
             if (opens) values(j >= looked);
             opens = next_job(xv, jv) || i + 1 == total;   // V's last reader
@@ -418,11 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issuer) {
               packed::mma_cols(tmem + kColO + (x ? kD : 0), tmem + sv.buffer * 128,
                                v_desc + static_cast<uint64_t>(sv.stage * (kTile >> 4)), kIdO, j > 0);
+              tc::commit(&bars[L::kReused + sv.buffer]);
               tc::commit(&bars[L::kPvDone + (x ? 3 + turn[1] : turn[0])]);
               if (opens) tc::commit(&bars[L::kEmpty + sv.stage]);
             }
             __syncwarp();
-            if (i + kBuffers < total) scores(i + kBuffers + 1 == total);
             next_buffer(sv);
             if (x) {
               next_turn(turn[1]);
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (opens) next_tile(sv);
           }
         }
-        if (kSplit && issuer) tc::commit(&bars[L::kAllDone]);
+        if (kSplit && issuer && warp == kMmaWarp) tc::commit(&bars[L::kAllDone]);
         __syncwarp();
         used[0] += n0 > 0;
         used[1] += n1 > 0;
@@ -448,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t o_addr = lane_addr + kColO + x * kD;
     const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
+    const bool wide = packed::wide_rows(o.out, o.st);
     bool ok = true;
     int jobs = 0, done = 0, used = 0;   // of all units before: jobs, this half's, and its units
     for (int k = 0; next_unit(k, &ok, &u); ++k) {
@@ -588,16 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
                             __uint_as_float(w[4 * i + 3]));
         } else if (active) {
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = !none ? packed::pack2<kFp16>(__uint_as_float(w[8 * i + 2 * e]) * inv,
-                                                  __uint_as_float(w[8 * i + 2 * e + 1]) * inv)
-                           : 0u;
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
-          }
+          for (int i = 0; i < 16; ++i)
+            p[i] = !none ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv)
+                         : 0u;
+          packed::store_row(out + 32 * c, p, wide);
         }
       }
       if (mine > 0) {

@@ -221,6 +221,28 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// 32 consecutive 16-bit values (16 words) to global memory: in whole 32-byte sectors
+// where `wide` (every row starts on one), which halves the store instructions.
+__device__ __forceinline__ void store_row(uint16_t* to, const uint32_t (&w)[16], bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * i), "r"(w[8 * i]),
+                   "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                   "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+
+// Whether every row of a tensor starts on 32 bytes.
+__device__ __forceinline__ bool wide_rows(const void* x, const PackedStride& st) {
+  return reinterpret_cast<uint64_t>(x) % 32 == 0 && st.token % 16 == 0 && st.head % 16 == 0;
+}
+
 template <bool kFp16>
 constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
   return kFp16 ? tc::idesc_fp16(M, N, a_mn, b_mn) : tc::idesc_bf16(M, N, a_mn, b_mn);
