@@ -273,6 +273,19 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b
   }
 }
 
+// The same with A in tensor memory, two values to a 32-bit column.
+template <int kD>
+__device__ __forceinline__ void mma_rows_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id) {
+#pragma unroll
+  for (int k = 0; k < kD / 16; ++k) {
+    const uint64_t off = static_cast<uint64_t>(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+    tc::mma_ts(d_tmem, a_tmem + 8 * k, b + off, id, k > 0 ? 1u : 0u);
+  }
+}
+
+__device__ __forceinline__ void st_words(uint32_t addr, const uint32_t (&w)[32]) { tc::st32(addr, w); }
+__device__ __forceinline__ void st_words(uint32_t addr, const uint32_t (&w)[16]) { tc::st16(addr, w); }
+
 // D += A B over 128 rows of B: A [128 x 128] two to a 32-bit column of tensor
 // memory, the columns of its second half kHalf behind the first's, B the
 // [128][kD] tile read along its rows (MN-major).

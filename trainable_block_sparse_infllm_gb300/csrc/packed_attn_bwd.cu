@@ -23,6 +23,7 @@
 // operand in tensor memory: no product's input passes through shared memory but
 // the tiles that TMA brought.  Two warpgroups share a tile's columns.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "packed_attn.cuh"
@@ -32,7 +33,8 @@ namespace infllmv2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kRowsWarp = 10;
+constexpr int kPairWarp = 8, kTmaWarp = 9, kSumWarp = 10;   // dq
+constexpr int kMmaWarp = 8, kRowsWarp = 10;                 // dk and dv (and kTmaWarp)
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 of what P is multiplied by on its way to dv.  A probability of a long row is
 // among fp16's subnormal numbers, where it would lose bits.
@@ -42,63 +44,70 @@ constexpr int kUp = kFp16 ? 8 : 0;
 constexpr int kExactTiles = 8;
 
 // ------------------------------------------------------------------- dq ----
+//
+// A CTA takes one tile of rows after another.  For step j (a tile of keys) the tensor
+// cores form S and dout . v, the threads P and dS, the tensor cores add dS K.  The
+// threads work on two steps at once: dS of step j - 1, which is multiplications, and P
+// of step j, which is exponentials, in one pass over the registers.  So S of step j
+// and dout . v of step j - 1 are issued together, and the next pair as soon as they
+// have been read, while the threads still compute.
 
 template <int kD>
 struct DqLayout {
   static constexpr int kTile = kD / 64 * 16384;
-  static constexpr int kStages = 163840 / kTile;
-  static constexpr int kRing = 2 * kTile;   // Q and dout before it
-  static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kQFull = 0, kFull = 1, kEmpty = kFull + kStages, kCleared = kEmpty + kStages,
-                       kSFull = kCleared + 1, kDpFull = kSFull + 1, kFree = kDpFull + 1, kDsFull = kFree + 1,
-                       kDqDone = kDsFull + 2, kNumBars = kDqDone + 2;
-  static constexpr int kScratch = kBars + 8 * kNumBars;
-  static constexpr int kSum = kScratch + 32;   // [2][128]: sums over the halves of a row
+  static constexpr int kKs = 4 * 128 / kD, kVs = 2 * 128 / kD;   // stages of the K and the V ring
+  static constexpr int kK = kTile, kV = kK + kKs * kTile;        // behind dout
+  static constexpr int kBars = kV + kVs * kTile;
+  static constexpr int kUnit = 0, kUnitFree = 2, kDoFull = 4, kDoFree = 5, kKFull = 6, kKEmpty = kKFull + kKs,
+                       kVFull = kKEmpty + kKs, kVEmpty = kVFull + kVs, kTail = kVEmpty + kVs, kCleared = kTail + 1,
+                       kPair = kCleared + 1, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
+                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kNumBars = kQIn + 1;
+  static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 16 bytes each
+  static constexpr int kSlot = kUnits + 32;
+  static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
   static constexpr int kBytes = kSum + 1024 + 1024;
 };
-// Tensor memory: S, dout . v, two buffers of dS, dq.
-constexpr uint32_t kDqS = 0, kDqDp = 128, kDqDs = 256, kDqAcc = 384;
+// Tensor memory: S, dout . v, dS, Q (16 bits: the A operand of S), dq.  Q comes through
+// the K ring, as the element before K_0, and makes room there: a tile of K is read
+// until its dS K is done, almost two steps after its S, and with three stages the
+// next K came too late.
+constexpr uint32_t kDqS = 0, kDqDp = 128, kDqDs = 256, kDqQ = 320, kDqAcc = 384;
+
+struct DqUnit {
+  packed::Sequence seq;
+  int t0, h, before;   // its first query, its KV head; query t attends keys 0 .. before + t
+  int n;               // tiles of keys
+  bool exact, clears;  // D from the scores; the last tile runs past the sequence
+  int steps, back;     // tiles walked (twice where exact), the first of the walk that sums dq
+};
 
 template <int kD, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnGrads g) {
   using L = DqLayout<kD>;
-  constexpr int kTile = L::kTile, kStages = L::kStages;
+  constexpr int kTile = L::kTile, kKs = L::kKs, kVs = L::kVs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  int* scratch = reinterpret_cast<int*>(smem + L::kScratch);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
-  uint8_t* ring = smem + L::kRing;
+  int4* units = reinterpret_cast<int4*>(smem + L::kUnits);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
-
-  pdl_wait();
-  pdl_trigger();
   const int tile_tokens = packed_tile_tokens(s.G);
-  const int h = static_cast<int>(blockIdx.x) % s.Hkv;
-  int b, tile;
-  if (!packed::find_tile(s, static_cast<int>(blockIdx.x) / s.Hkv, tile_tokens, false, scratch, &b, &tile)) return;
-  bool bad = false;
-  const packed::Sequence seq = packed::sequence(s, b, &bad);
-  const int t0 = tile * tile_tokens;
-  const int before = seq.n_k - seq.n_q;
-  const int last = min(t0 + tile_tokens, seq.n_q) - 1;
-  const int n = (max(before + last + 1, 0) + 127) / 128;   // key tiles
-  const bool clears = n * 128 > seq.n_k;
-  const bool exact = n <= kExactTiles;
-  const int steps = exact && n > 1 ? 2 * n : n;   // walks the keys twice, or once
-  const int back = steps - n;                     // the first step of the walk that sums dq
 
   if (tid == 0) {
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
     prefetch_tensormap(&maps.dout);
-    for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(&bars[i], i == L::kFree || i == L::kDsFull || i == L::kDsFull + 1 ? 8 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) {
+      int count = 1;
+      if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
+      if (i == L::kFree || i == L::kDsFull || i == L::kAccFree || i == L::kQIn) count = 8;
+      mbar_init(&bars[i], count);
+    }
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kPairWarp) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
@@ -106,226 +115,457 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  auto unit_of = [&](int4 at) {
+    DqUnit u;
+    bool bad = false;
+    u.seq = packed::sequence(s, at.x, &bad);
+    u.t0 = at.y * tile_tokens;
+    u.h = at.z;
+    u.before = u.seq.n_k - u.seq.n_q;
+    const int last = min(u.t0 + tile_tokens, u.seq.n_q) - 1;
+    u.n = (max(u.before + last + 1, 0) + 127) / 128;
+    u.clears = u.n * 128 > u.seq.n_k;
+    u.exact = u.n <= kExactTiles;
+    u.steps = u.exact && u.n > 1 ? 2 * u.n : u.n;
+    u.back = u.steps - u.n;
+    return u;
+  };
+  auto next_unit = [&](int k, bool* ok, DqUnit* u) {
+    if (*ok) *ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnit + (k & 1)], (k >> 1) & 1, s.status));
+    if (!*ok) return false;
+    int4 at = units[k & 1];
+    at.x = __shfl_sync(0xffffffffu, at.x, 0);   // (uniform for the compiler, so that the roles' loops are)
+    if (at.x < 0) return false;
+    at.y = __shfl_sync(0xffffffffu, at.y, 0);
+    at.z = __shfl_sync(0xffffffffu, at.z, 0);
+    *u = unit_of(at);
+    return true;
+  };
+  auto unit_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[L::kUnitFree + (k & 1)]);
+  };
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  // Stage and phase of a ring, or a phase alone.
+  struct Place {
+    int stage, phase;
+  };
+  auto next = [](Place& p, int stages) {
+    if (++p.stage == stages) {
+      p.stage = 0;
+      p.phase ^= 1;
+    }
+  };
+  DqUnit u;
+  bool ok = true;
+  auto wait = [&](int bar, int phase) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
+    tc::fence_after_sync();
+  };
 
   if (warp >= 8) {
     packed::regs_down<72>();
-    if (warp == kTmaWarp && n > 0) {
-      int issued = 0;   // K_0, V_0, K_1, V_1, ...
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars[L::kQFull], 2 * tile_tokens * s.G * kD * 2);
-        for (int c = 0; c < kD / 64; ++c) {
-          packed::tma_load_4d(smem_u32(smem + c * 16384), &maps.q, c * 64, 0, h, seq.q0 + t0, &bars[L::kQFull]);
-          packed::tma_load_4d(smem_u32(smem + kTile + c * 16384), &maps.dout, c * 64, 0, h, seq.q0 + t0,
-                              &bars[L::kQFull]);
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------ units and loads
+      packed::Walker walker;
+      bool bad = false;
+      walker.start(s, tile_tokens, false, &bad);
+      const int stride = static_cast<int>(gridDim.x);
+      int k_copies = 0, v_copies = 0, tails = 0, uses = 0;
+      // The next stage of the K ring, with a copy of `bytes` announced on `bar` (null: the stage's own).
+      auto k_stage = [&](uint32_t bytes, uint64_t* bar) {
+        const int st = k_copies % kKs;
+        if (k_copies >= kKs) wait(L::kKEmpty + st, k_copies / kKs - 1);
+        if (ok && lane == 0) {
+          if (bar) mbar_arrive(&bars[L::kKFull + st]);   // only counts the turn
+          mbar_arrive_expect_tx(bar ? bar : &bars[L::kKFull + st], bytes);
         }
-        for (; issued < 2 * steps; ++issued) {
-          const int st = issued % kStages;
-          if (issued >= kStages && !mbar_wait(&bars[L::kEmpty + st], (issued / kStages - 1) & 1, s.status)) break;
-          mbar_arrive_expect_tx(&bars[L::kFull + st], kTile);
-          for (int c = 0; c < kD / 64; ++c)
-            packed::tma_load_3d(smem_u32(ring + st * kTile + c * 16384), issued & 1 ? &maps.v : &maps.k, c * 64,
-                                seq.k0 + (issued >> 1) % n * 128, h, &bars[L::kFull + st]);
+        if (ok) ++k_copies;
+        return st;
+      };
+      for (int k = 0;; ++k) {
+        // Down the order of all units and back, so that no CTA gets the longest of each round.
+        int i = static_cast<int>(blockIdx.x);
+        i = k * stride + (k & 1 ? stride - 1 - i : i);
+        int4 at = make_int4(-1, 0, i % s.Hkv, 0);
+        int b, level;
+        if (walker.find(s, i / s.Hkv, tile_tokens, false, &b, &level, &bad)) {
+          at.x = b;
+          at.y = level;
         }
+        if (k >= 2 && ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnitFree + (k & 1)], ((k >> 1) - 1) & 1, s.status));
+        if (!ok) at.x = -1;
+        if (lane == 0) {
+          units[k & 1] = at;
+          mbar_arrive(&bars[L::kUnit + (k & 1)]);
+        }
+        __syncwarp();
+        if (at.x < 0) break;
+        u = unit_of(at);
+        const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
+        if (u.n > 0) {
+          const int st = k_stage(row_bytes, nullptr);
+          if (ok && lane == 0)
+            for (int c = 0; c < kD / 64; ++c)
+              packed::tma_load_4d(smem_u32(smem + L::kK + st * kTile + c * 16384), &maps.q, c * 64, 0, u.h,
+                                  u.seq.q0 + u.t0, &bars[L::kKFull + st]);
+        }
+        for (int j = 0; j < u.steps && ok; ++j) {
+          const int row = u.seq.k0 + (j < u.back ? j : j - u.back) * 128;
+          // The tile of K that is to be cleared behind the sequence lands on a barrier of its own.
+          const bool tail = u.clears && j == u.steps - 1;
+          const int st = k_stage(kTile, tail ? &bars[L::kTail] : nullptr);
+          if (!ok) break;
+          if (lane == 0)
+            for (int c = 0; c < kD / 64; ++c)
+              packed::tma_load_3d(smem_u32(smem + L::kK + st * kTile + c * 16384), &maps.k, c * 64, row, u.h,
+                                  tail ? &bars[L::kTail] : &bars[L::kKFull + st]);
+          tails += tail;
+          if (j == 0) {
+            if (uses > 0) wait(L::kDoFree, uses - 1);
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars[L::kDoFull], row_bytes);
+              for (int c = 0; c < kD / 64; ++c)
+                packed::tma_load_4d(smem_u32(smem + c * 16384), &maps.dout, c * 64, 0, u.h, u.seq.q0 + u.t0,
+                                    &bars[L::kDoFull]);
+            }
+            ++uses;
+          }
+          const int vs = v_copies % kVs;
+          if (v_copies >= kVs) wait(L::kVEmpty + vs, v_copies / kVs - 1);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars[L::kVFull + vs], kTile);
+            for (int c = 0; c < kD / 64; ++c)
+              packed::tma_load_3d(smem_u32(smem + L::kV + vs * kTile + c * 16384), &maps.v, c * 64, row, u.h,
+                                  &bars[L::kVFull + vs]);
+          }
+          ++v_copies;
+        }
+        __syncwarp();
       }
-      issued = __shfl_sync(0xffffffffu, issued, 0);
-      // The last copy of each stage: here its phase is the barrier's newest.  The
-      // CTA outlives its copies, also after a wait that gave up.
-      for (int i = max(0, issued - kStages); i < issued; ++i)
-        mbar_wait(&bars[L::kFull + i % kStages], (i / kStages) & 1, s.status);
-      if (clears && issued == 2 * steps) {   // K rows behind the sequence: they meet dS = 0
-        packed::clear_rows<kD>(ring + (2 * steps - 2) % kStages * kTile, seq.n_k - (n - 1) * 128);
-        if (lane == 0) mbar_arrive(&bars[L::kCleared]);
-      }
-      mbar_wait(&bars[L::kQFull], 0, s.status);
-    } else if (warp == kMmaWarp && n > 0) {
+      if (bad && blockIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
+      // The CTA outlives its copies, also after a wait that gave up.  (Each barrier's last copy is its
+      // newest phase here.)
+      for (int i = max(0, k_copies - kKs); i < k_copies; ++i)
+        mbar_wait(&bars[L::kKFull + i % kKs], (i / kKs) & 1, s.status);
+      for (int i = max(0, v_copies - kVs); i < v_copies; ++i)
+        mbar_wait(&bars[L::kVFull + i % kVs], (i / kVs) & 1, s.status);
+      if (tails > 0) mbar_wait(&bars[L::kTail], (tails - 1) & 1, s.status);
+      if (uses > 0) mbar_wait(&bars[L::kDoFull], (uses - 1) & 1, s.status);
+    } else if (warp == kPairWarp) {
+      // ----------------------- S of a step and dout . v of the one before it
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
-      constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
-      const uint64_t q_desc = packed::desc_rows(smem_u32(smem));
-      const uint64_t do_desc = packed::desc_rows(smem_u32(smem + kTile));
-      const uint64_t rows_desc = packed::desc_rows(smem_u32(ring));
-      const uint64_t cols_desc = packed::desc_cols(smem_u32(ring));
+      const uint64_t do_desc = packed::desc_rows(smem_u32(smem));
+      const uint64_t k_desc = packed::desc_rows(smem_u32(smem + L::kK));
+      const uint64_t v_desc = packed::desc_rows(smem_u32(smem + L::kV));
       const bool issuer = packed::elect_one();
-      bool ok = true;
-      auto wait = [&](int bar, int phase) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
-        tc::fence_after_sync();
-      };
-      auto stage = [&](int i) { return static_cast<uint64_t>((i % kStages * kTile) >> 4); };
-      auto scores = [&](int j) {   // S and dout . v of step j
-        wait(L::kFull + (2 * j) % kStages, 2 * j / kStages);
-        if (clears && j == steps - 1) wait(L::kCleared, 0);
-        if (!ok) return;
-        if (issuer) {
-          packed::mma_rows<kD>(tmem + kDqS, q_desc, rows_desc + stage(2 * j), kIdS);
-          tc::commit(&bars[L::kSFull]);
+      Place pk = {0, 0}, pv = {0, 0};
+      int pairs = 0, tails = 0, uses = 0;
+      for (int k = 0; next_unit(k, &ok, &u); ++k) {
+        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
+        if (steps > 0) {
+          wait(L::kQIn, uses);
+          if (issuer) mbar_arrive(&bars[L::kKEmpty + pk.stage]);   // Q's stage has been read
+          __syncwarp();
+          next(pk, kKs);
         }
-        __syncwarp();
-        wait(L::kFull + (2 * j + 1) % kStages, (2 * j + 1) / kStages);
-        if (!ok) return;
-        if (issuer) {
-          packed::mma_rows<kD>(tmem + kDqDp, do_desc, rows_desc + stage(2 * j + 1), kIdS);
-          tc::commit(&bars[L::kDpFull]);
-          tc::commit(&bars[L::kEmpty + (2 * j + 1) % kStages]);
+        for (int t = 0; steps > 0 && t <= steps; ++t) {
+          if (t < steps) {
+            if (t == tail) {
+              wait(L::kTail, tails++);
+            } else {
+              wait(L::kKFull + pk.stage, pk.phase);
+            }
+          }
+          if (t == 1) wait(L::kDoFull, uses++);
+          if (t > 0) wait(L::kVFull + pv.stage, pv.phase);
+          if (pairs > 0) wait(L::kFree, pairs - 1);   // both have been read
+          ++pairs;
+          if (t > 0) {
+            if (issuer) {
+              packed::mma_rows<kD>(tmem + kDqDp, do_desc, v_desc + static_cast<uint64_t>(pv.stage * (kTile >> 4)),
+                                   kIdS);
+              tc::commit(&bars[L::kVEmpty + pv.stage]);
+            }
+            __syncwarp();
+            next(pv, kVs);
+          }
+          if (t < steps) {
+            if (issuer) {
+              packed::mma_rows_ts<kD>(tmem + kDqS, tmem + kDqQ,
+                                      k_desc + static_cast<uint64_t>(pk.stage * (kTile >> 4)), kIdS);
+              if (t < back) tc::commit(&bars[L::kKEmpty + pk.stage]);   // (otherwise dS K is its last reader)
+            }
+            __syncwarp();
+            next(pk, kKs);
+          }
+          if (issuer) {
+            tc::commit(&bars[L::kPair]);
+            if (t == steps) tc::commit(&bars[L::kDoFree]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      wait(L::kQFull, 0);
-      if (ok) scores(0);
-      for (int j = 0; j < steps && ok; ++j) {
-        if (j < back && issuer) tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
-        __syncwarp();
-        if (j + 1 < steps) {
-          wait(L::kFree, j);   // both score buffers are in registers
-          if (ok) scores(j + 1);
+        unit_done(k);
+      }
+    } else if (warp == kSumWarp) {
+      // ---------------------------------------------------------- dq += dS K
+      constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
+      const uint64_t k_desc = packed::desc_cols(smem_u32(smem + L::kK));
+      const bool issuer = packed::elect_one();
+      Place pk = {0, 0};
+      int tails = 0, used = 0, made = 0;
+      for (int k = 0; next_unit(k, &ok, &u); ++k) {
+        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
+        if (steps > 0) next(pk, kKs);   // Q's stage
+        for (int j = 0; j < steps; ++j) {
+          if (j >= back) {
+            if (j == tail) wait(L::kCleared, tails++);   // (dS says that the other tiles are there)
+            if (j == back && used++ > 0) wait(L::kAccFree, used - 2);   // the last unit's dq has been read
+            wait(L::kDsFull, made++);
+            if (issuer) {
+              packed::mma_cols(tmem + kDqAcc, tmem + kDqDs,
+                               k_desc + static_cast<uint64_t>(pk.stage * (kTile >> 4)), kIdO, j > back);
+              tc::commit(&bars[L::kDqDone]);
+              tc::commit(&bars[L::kKEmpty + pk.stage]);
+            }
+            __syncwarp();
+          }
+          next(pk, kKs);
         }
-        if (j < back) continue;
-        const int i = j - back;
-        wait(L::kDsFull + (i & 1), i >> 1);
-        if (!ok) break;
-        if (issuer) {
-          packed::mma_cols(tmem + kDqAcc, tmem + kDqDs + (i & 1) * 64, cols_desc + stage(2 * j), kIdO, i > 0);
-          tc::commit(&bars[L::kDqDone + (i & 1)]);
-          tc::commit(&bars[L::kEmpty + (2 * j) % kStages]);
+        unit_done(k);
+      }
+    } else {
+      // ----------------------- K rows behind the sequence: they meet dS = 0
+      Place pk = {0, 0};
+      int tails = 0;
+      for (int k = 0; next_unit(k, &ok, &u); ++k) {
+        if (u.steps > 0) next(pk, kKs);   // Q's stage
+        for (int j = 0; j < u.steps; ++j) {
+          if (u.clears && j == u.steps - 1) {
+            wait(L::kTail, tails++);
+            packed::clear_rows<kD>(smem + L::kK + pk.stage * kTile, u.seq.n_k - (u.n - 1) * 128);
+            if (lane == 0) mbar_arrive(&bars[L::kCleared]);
+          }
+          next(pk, kKs);
         }
-        __syncwarp();
+        unit_done(k);
       }
     }
     __syncwarp();
   } else {
+    // ------------------------------------------------------------ P and dS
     packed::regs_up<216>();
     const int half = warp >> 2;   // columns 64 half .. 64 half + 63
     const int r = tid & 127;
-    const int token = t0 + r / s.G;
-    const bool active = r < tile_tokens * s.G && token < seq.n_q;
-    const int limit = active ? before + token + 1 : 0;
-    const int head = h * s.G + r % s.G;
-    const long long row = seq.q0 + token;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_addr + kDqS + 64 * half, dp_addr = lane_addr + kDqDp + 64 * half;
     float* part = reinterpret_cast<float*>(smem + L::kSum);
-
-    // The sum of the row's two halves, in both threads that share it.
+    const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
+    const bool wide = packed::wide_rows(g.dq, g.dq_st);
+    // The sum of a row's two halves, in both threads that share it.
     auto both = [&](float v) {
       asm volatile("bar.sync 1, 256;" ::: "memory");
       part[half * 128 + r] = v;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       return part[r] + part[128 + r];
     };
-    float D = 0.f, lse2 = 0.f, rest = 0.f;
-    if (active) {
-      if (!exact) {
-        const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.out) + row * g.out_st.token +
-                                                        head * g.out_st.head + half * (kD / 2));
-        const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + row * g.dout_st.token +
-                                                        head * g.dout_st.head + half * (kD / 2));
+    int pairs = 0, summed = 0;   // in all: pairs of scores read, dS written
+    Place pk = {0, 0};
+    for (int k = 0; next_unit(k, &ok, &u); ++k) {
+      const int token = u.t0 + r / s.G;
+      const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
+      const int limit = active ? u.before + token + 1 : 0;
+      const int head = u.h * s.G + r % s.G;
+      const long long row = u.seq.q0 + token;
+      if (u.steps > 0) {
+        // Q into tensor memory: S of the last unit has been read, so its Q has been.
+        wait(L::kKFull + pk.stage, pk.phase);
+        const uint8_t* q = smem + L::kK + pk.stage * kTile + r * 128;
+        uint32_t w[kD / 4];   // half of the row's columns
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
-          const uint4 u = __ldg(a + i), w = __ldg(c + i);
-          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+          const int c = half * (kD / 16) + i;
+          const uint4 v = *reinterpret_cast<const uint4*>(q + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4));
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+        packed::st_words(lane_addr + kDqQ + half * (kD / 4), w);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kQIn]);
+        for (int i = 0; i <= u.steps; ++i) next(pk, kKs);
+      }
+      float D = 0.f, lse2 = 0.f;
+      if (active) {
+        // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
+        lse2 = limit > 0 ? __ldg(g.lse + row * (s.Hkv * s.G) + head) * kLog2e : INFINITY;
+        if (!u.exact) {   // each warpgroup half of the columns
+          const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.out) + row * g.out_st.token +
+                                                          head * g.out_st.head + half * (kD / 2));
+          const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) +
+                                                          row * g.dout_st.token + head * g.dout_st.head +
+                                                          half * (kD / 2));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 p = packed::unpack2<kFp16>(us[e]), q = packed::unpack2<kFp16>(ws[e]);
-            D = fmaf(p.x, q.x, fmaf(p.y, q.y, D));
+          for (int i = 0; i < kD / 16; ++i) {
+            const uint4 v = __ldg(a + i), w = __ldg(c + i);
+            const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 p = packed::unpack2<kFp16>(vs[e]), q = packed::unpack2<kFp16>(ws[e]);
+              D = fmaf(p.x, q.x, fmaf(p.y, q.y, D));
+            }
           }
         }
       }
-      // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
-      lse2 = __ldg(g.lse + row * (s.Hkv * s.G) + head) * kLog2e;
-      if (limit <= 0) lse2 = INFINITY;
-    }
-    if (!exact) D = both(D);
-
-    const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
-    bool ok = true;
-    auto wait = [&](int bar, int phase) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
-      tc::fence_after_sync();
-    };
-    for (int j = 0; j < steps; ++j) {
-      const int tile_j = j < back ? j : j - back;
-      uint32_t z[64], dp[64];
-      wait(L::kSFull, j);
+      if (!u.exact) D = both(D);
+      const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
+      const uint64_t down = packed::pair(-lse2, -lse2);
+      // Columns of tile j that the row attends, of this half's 64; 64 where no row of the warp needs a mask.
+      auto attended = [&](int j) { return j >= whole ? limit - j * 128 - 64 * half : 64; };
+      uint64_t p[32], rest = 0ull;   // P of a step, two to a register pair; the sum of dS
+      auto read_done = [&] {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kFree]);
+      };
+      auto probs = [&](uint32_t (&z)[32], int c, int keep) {   // P of 32 columns
+        if (keep < 64) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        tc::ld32(lane_addr + kDqS + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
-      tc::wait_ld();
-      const int keep = limit - tile_j * 128 - 64 * half;
-      if (tile_j >= whole) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) z[i] = i < keep ? z[i] : 0xff800000u;
-      }
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        z[i] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(z[i]), s.scale2, -lse2)));
-      wait(L::kDpFull, j);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        tc::ld32(lane_addr + kDqDp + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&dp[32 * c]));
-      tc::wait_ld();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kFree]);
-      if (tile_j >= whole) {   // a hidden value's infinity meets P = 0
-#pragma unroll
-        for (int i = 0; i < 64; ++i) dp[i] = i < keep ? dp[i] : 0u;
-      }
-      if (j < back || (exact && n == 1)) {
-        float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          d0 = fmaf(__uint_as_float(z[i]), __uint_as_float(dp[i]), d0);
-          d1 = fmaf(__uint_as_float(z[i + 1]), __uint_as_float(dp[i + 1]), d1);
+          for (int i = 0; i < 32; ++i) z[i] = 32 * c + i < keep ? z[i] : 0xff800000u;
         }
-        D += d0 + d1;
-        if (tile_j == n - 1) D = both(D);
-        if (j < back) continue;
-      }
-      uint32_t ds[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float a = __uint_as_float(z[2 * i]) * (__uint_as_float(dp[2 * i]) - D);
-        const float c = __uint_as_float(z[2 * i + 1]) * (__uint_as_float(dp[2 * i + 1]) - D);
-        rest += a + c;
-        ds[i] = packed::pack2<kFp16>(a, c);
+        for (int i = 0; i < 16; ++i) {
+          const float2 e = packed::unpair(packed::fma2(
+              packed::pair(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), scale2, down));
+          p[16 * c + i] = packed::pair(fast_exp2(e.x), fast_exp2(e.y));
+        }
+      };
+      auto visible = [&](uint32_t (&dp)[32], int c, int keep) {   // (a hidden value may be infinite)
+        if (keep < 64) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dp[i] = 32 * c + i < keep ? dp[i] : 0u;
+        }
+      };
+      auto sum_d = [&](int keep) {   // D += sum P (dout . v)
+        uint64_t d = 0ull;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[32];
+          tc::ld32(dp_addr + 32 * c, dp);
+          tc::wait_ld();
+          visible(dp, c, keep);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            d = packed::fma2(p[16 * c + i], packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), d);
+        }
+        const float2 halves = packed::unpair(d);
+        D += halves.x + halves.y;
+      };
+      // One pair: dS of the step before from its P, and (kMore) P of this step.
+      auto body = [&](auto more, int was, int here) {
+        constexpr bool kMore = decltype(more)::value;
+        const int keep_was = attended(was), keep = kMore ? attended(here) : 64;
+        const uint64_t minus_d = packed::pair(-D, -D);
+        uint32_t ds[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t z[32], dp[32];
+          tc::ld32(dp_addr + 32 * c, dp);
+          if (kMore) tc::ld32(s_addr + 32 * c, z);
+          tc::wait_ld();
+          if (c == 1) read_done();
+          visible(dp, c, keep_was);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t v = packed::mul2(
+                p[16 * c + i],
+                packed::add2(packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), minus_d));
+            rest = packed::add2(rest, v);
+            const float2 w = packed::unpair(v);
+            ds[16 * c + i] = packed::pack2<kFp16>(w.x, w.y);
+          }
+          if (kMore) probs(z, c, keep);
+        }
+        if (summed > 0) wait(L::kDqDone, summed - 1);   // the last dS has been read
+        ++summed;
+        tc::st32(lane_addr + kDqDs + 32 * half, ds);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
+      };
+      if (u.steps > 0) {
+        // The first walk, where there are two: P of step t, D of step t - 1.
+        for (int t = 0; t <= u.back; ++t) {
+          wait(L::kPair, pairs++);
+          if (t > 0) sum_d(attended(t - 1));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t z[32];
+            tc::ld32(s_addr + 32 * c, z);
+            tc::wait_ld();
+            if (c == 1) read_done();
+            probs(z, c, attended(t < u.back ? t : 0));
+          }
+        }
+        if (u.back > 0) D = both(D);
+        for (int j = 1; j < u.n; ++j) {
+          wait(L::kPair, pairs++);
+          body(std::true_type(), j - 1, j);
+        }
+        wait(L::kPair, pairs++);
+        if (u.n == 1) {   // the only tile: D and dS from the same registers
+          sum_d(attended(0));
+          D = both(D);
+        }
+        body(std::false_type(), u.n - 1, 0);
       }
-      if (tile_j >= 2) wait(L::kDqDone + (tile_j & 1), (tile_j - 2) >> 1);   // this buffer's last reader
-      tc::st32(lane_addr + kDqDs + (tile_j & 1) * 64 + 32 * half, ds);
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kDsFull + (tile_j & 1)]);
-    }
-    // sum P (dout . v - D) is what D lacks.
-    D += both(rest);
-    if (half == 0 && active) g.rows[row * (s.Hkv * s.G) + head] = make_float2(lse2, D);
-    if (n > 0) wait(L::kDqDone + ((n - 1) & 1), (n - 1) >> 1);
-    uint16_t* dq = static_cast<uint16_t*>(g.dq) + row * g.dq_st.token + head * g.dq_st.head;
+      // sum P (dout . v - D) is what D lacks.
+      const float2 halves = packed::unpair(rest);
+      D += both(halves.x + halves.y);
+      if (half == 0 && active) g.rows[row * (s.Hkv * s.G) + head] = make_float2(lse2, D);
+      if (u.n > 0) wait(L::kDqDone, summed - 1);
+      uint16_t* dq = static_cast<uint16_t*>(g.dq) + row * g.dq_st.token + head * g.dq_st.head;
 #pragma unroll 1
-    for (int c = 0; c < kD / 64; ++c) {
-      const int col = half * (kD / 2) + 32 * c;
-      uint32_t w[32];
+      for (int c = 0; c < kD / 64; ++c) {
+        const int col = half * (kD / 2) + 32 * c;
+        uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0u;
-      if (n > 0) {
-        tc::ld32(lane_addr + kDqAcc + col, w);
-        tc::wait_ld();
-      }
-      if (active) {
+        for (int i = 0; i < 32; ++i) w[i] = 0u;
+        if (u.n > 0) {
+          tc::ld32(lane_addr + kDqAcc + col, w);
+          tc::wait_ld();
+        }
+        if (active) {
+          uint32_t v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = limit > 0 ? packed::pack2<kFp16>(__uint_as_float(w[8 * i + 2 * e]) * s.scale,
-                                                    __uint_as_float(w[8 * i + 2 * e + 1]) * s.scale)
+          for (int i = 0; i < 16; ++i)
+            v[i] = limit > 0 ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * s.scale,
+                                                    __uint_as_float(w[2 * i + 1]) * s.scale)
                              : 0u;
-          *reinterpret_cast<uint4*>(dq + col + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
+          packed::store_row(dq + col, v, wide);
         }
       }
+      if (u.n > 0) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kAccFree]);
+      }
+      unit_done(k);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kPairWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -336,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int kD>
 struct DkvLayout {
   static constexpr int kTile = kD / 64 * 16384;
-  static constexpr int kStages = 131072 / kTile;
+  static constexpr int kStages = 163840 / kTile;
   static constexpr int kRing = 2 * kTile;   // K and V before it
   static constexpr int kRows = kRing + kStages * kTile;   // two buffers of [128] lse log2(e), [128] D
   static constexpr int kBars = kRows + 2 * 1024;
@@ -345,7 +585,7 @@ struct DkvLayout {
                        kPFull = kSFull + 1, kDpFull = kPFull + 1, kDsFull = kDpFull + 1, kDone = kDsFull + 1,
                        kNumBars = kDone + 1;
   static constexpr int kScratch = kBars + 8 * kNumBars;
-  static constexpr int kBytes = kScratch + 32 + 1024;
+  static constexpr int kBytes = kScratch + 32;   // (no slack: where the base is not aligned the kernel says so)
 };
 // Tensor memory: S^T with P^T over it, (v . dout)^T with dS^T over it, dv, dk.  A
 // warpgroup's 16-bit values lie over its own 64 columns' first 32.
@@ -358,8 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = DkvLayout<kD>;
   constexpr int kTile = L::kTile, kStages = L::kStages;
   constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off again: from dout . v - D for dS, from dv
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) % 1024 != 0) {   // the whole grid: shared memory starts on 1024 bytes or it does not
+    if (threadIdx.x == 0) atomicOr(s.status, kStatusBounds);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int* scratch = reinterpret_cast<int*>(smem + L::kScratch);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
@@ -601,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t* to = static_cast<uint16_t*>(half ? g.dk : g.dv) + static_cast<long long>(seq.k0 + key) * st.token +
                    h * st.head;
     const float scale = half ? s.scale : kDown;
+    const bool wide = packed::wide_rows(half ? g.dk : g.dv, st);
 #pragma unroll 1
     for (int c = 0; c < kD / 32; ++c) {
       uint32_t w[32];
@@ -617,15 +861,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
                           __uint_as_float(w[4 * i + 3]));
       } else if (active) {
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = packed::pack2<kFp16>(__uint_as_float(w[8 * i + 2 * e]) * scale,
-                                        __uint_as_float(w[8 * i + 2 * e + 1]) * scale);
-          *reinterpret_cast<uint4*>(to + 32 * c + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
-        }
+        for (int i = 0; i < 16; ++i)
+          p[i] = packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * scale, __uint_as_float(w[2 * i + 1]) * scale);
+        packed::store_row(to + 32 * c, p, wide);
       }
     }
   }
@@ -695,9 +935,9 @@ long long most_tiles(int tokens, int step, int B) {
 
 template <int kD, bool kFp16>
 cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const PackedAttnGrads& g, cudaStream_t st) {
-  const cudaError_t e =
-      launch_one(packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
-                 most_tiles(s.Tq, packed_tile_tokens(s.G), s.B) * s.Hkv, 1, st, maps, s, g);
+  const long long tiles = most_tiles(s.Tq, packed_tile_tokens(s.G), s.B) * s.Hkv;
+  const cudaError_t e = launch_one(packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
+                                   std::min<long long>(tiles, device_sm_count()), 1, st, maps, s, g);
   if (e != cudaSuccess) return e;
   // CTAs per tile of keys.  Causal tiles differ by the whole length of the sequence, so
   // units that are few leave SMs idle behind the longest: one 8K sequence with 2 KV
