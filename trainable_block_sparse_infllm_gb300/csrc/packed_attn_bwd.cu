@@ -578,7 +578,7 @@ struct DkvLayout {
   static constexpr int kTile = kD / 64 * 16384;
   static constexpr int kStages = 163840 / kTile;
   static constexpr int kRing = 2 * kTile;   // K and V before it
-  static constexpr int kRows = kRing + kStages * kTile;   // two buffers of [128] lse log2(e), [128] D
+  static constexpr int kRows = kRing + kStages * kTile;   // two buffers of [128] -lse log2(e), [128] -D
   static constexpr int kBars = kRows + 2 * 1024;
   static constexpr int kKvFull = 0, kFull = 1, kEmpty = kFull + kStages, kRowsFull = kEmpty + kStages,
                        kRowsFree = kRowsFull + 2, kCleared = kRowsFree + 2, kSFull = kCleared + 2,
@@ -654,6 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  auto wait = [&](int bar, int phase) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
+    tc::fence_after_sync();
+  };
 
   if (warp >= 8) {
     packed::regs_down<72>();
@@ -686,21 +691,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_wait(&bars[L::kKvFull], 0, s.status);
     } else if (warp == kRowsWarp) {
-      // Each row tile's (lse, D), +inf for a row of no query: its P is 0.
-      for (int i = 0; i < n; ++i) {
-        const int buf = i & 1;
-        if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars[L::kRowsFree + buf], (i / 2 - 1) & 1, s.status))) break;
+      // Each row tile's (lse, D), +inf for a row of no query: its P is 0.  Two tiles are on their way in
+      // registers while a buffer is waited for.
+      int token_in[4];          // of rows lane, lane + 32, ...: their token in a tile
+      const float2* from[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = lane + 32 * k;
+        token_in[k] = r < tile_rows ? r / s.G : 0x40000000;   // (no such token)
+        from[k] = g.rows + static_cast<long long>(seq.q0 + t0 + r / s.G) * (s.Hkv * s.G) + h * s.G + r % s.G;
+      }
+      const long long step = static_cast<long long>(tile_tokens) * s.Hkv * s.G;
+      auto load = [&](int i, float2 (&v)[4]) {
+        const int tile = rank + i * ctas, left = seq.n_q - t0 - tile * tile_tokens;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = i < n && token_in[k] < left ? __ldg(from[k] + tile * step) : make_float2(INFINITY, 0.f);
+      };
+      auto put = [&](int i, const float2 (&v)[4]) {
+        float* to = rows + (i & 1) * 256 + lane;
+        if (i >= 2) wait(L::kRowsFree + (i & 1), i / 2 - 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = lane + 32 * k, token = tile_token(i) + r / s.G;
-          float2 v = make_float2(INFINITY, 0.f);
-          if (r < tile_rows && token < seq.n_q)
-            v = __ldg(g.rows + static_cast<long long>(seq.q0 + token) * (s.Hkv * s.G) + h * s.G + r % s.G);
-          rows[buf * 256 + r] = v.x - kUp<kFp16>;
-          rows[buf * 256 + 128 + r] = v.y * kDown;
+          to[32 * k] = kUp<kFp16> - v[k].x;   // negated: what is added
+          to[128 + 32 * k] = -kDown * v[k].y;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kRowsFull + buf]);
+        if (lane == 0) mbar_arrive(&bars[L::kRowsFull + (i & 1)]);
+      };
+      float2 even[4], odd[4];
+      load(0, even);
+      load(1, odd);
+      for (int i = 0; i < n && ok; i += 2) {
+        put(i, even);
+        load(i + 2, even);
+        if (i + 1 < n) put(i + 1, odd);
+        load(i + 3, odd);
       }
     } else if (warp == kMmaWarp && n > 0) {
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
@@ -710,11 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t rows_desc = packed::desc_rows(smem_u32(ring));
       const uint64_t cols_desc = packed::desc_cols(smem_u32(ring));
       const bool issuer = packed::elect_one();
-      bool ok = true;
-      auto wait = [&](int bar, int phase) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
-        tc::fence_after_sync();
-      };
       auto stage = [&](int i) { return static_cast<uint64_t>((i % kStages * kTile) >> 4); };
       auto loaded = [&](int i) {   // the i-th tile of the ring, cleared where it must be
         wait(L::kFull + i % kStages, i / kStages);
@@ -767,11 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = key0 + (tid & 127);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int warp_last = key0 + (warp & 3) * 32 + 31;
-    bool ok = true;
-    auto wait = [&](int bar, int phase) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
-      tc::fence_after_sync();
-    };
+    const uint64_t scale2 = packed::pair(s.scale2, s.scale2), down = packed::pair(kDown, kDown);
     for (int i = 0; i < n; ++i) {
       // Rows of tokens before key - before do not attend the key.
       const int token0 = tile_token(i);
@@ -789,10 +806,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const float4 m = lse2[c];
-        z[4 * c] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(z[4 * c]), s.scale2, -m.x)));
-        z[4 * c + 1] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(z[4 * c + 1]), s.scale2, -m.y)));
-        z[4 * c + 2] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(z[4 * c + 2]), s.scale2, -m.z)));
-        z[4 * c + 3] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(z[4 * c + 3]), s.scale2, -m.w)));
+        const float2 a = packed::unpair(packed::fma2(
+            packed::pair(__uint_as_float(z[4 * c]), __uint_as_float(z[4 * c + 1])), scale2, packed::pair(m.x, m.y)));
+        const float2 e = packed::unpair(packed::fma2(
+            packed::pair(__uint_as_float(z[4 * c + 2]), __uint_as_float(z[4 * c + 3])), scale2, packed::pair(m.z, m.w)));
+        z[4 * c] = __float_as_uint(fast_exp2(a.x));
+        z[4 * c + 1] = __float_as_uint(fast_exp2(a.y));
+        z[4 * c + 2] = __float_as_uint(fast_exp2(e.x));
+        z[4 * c + 3] = __float_as_uint(fast_exp2(e.y));
       }
       if (masked) {
 #pragma unroll
@@ -800,7 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t p[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) p[c] = packed::pack2<kFp16>(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1]));
+      for (int c = 0; c < 32; ++c)
+        p[c] = packed::pack2<kFp16>(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1]));
       tc::st32(lane_addr + kKvS + 64 * half, p);
       tc::wait_st();
       tc::fence_before_sync();
@@ -816,10 +838,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) {
           const float4 d = D[8 * c + e];
           const uint32_t* zz = &z[32 * c + 4 * e];
-          p[16 * c + 2 * e] = packed::pack2<kFp16>(__uint_as_float(zz[0]) * fmaf(__uint_as_float(dp[4 * e]), kDown, -d.x),
-                                                   __uint_as_float(zz[1]) * fmaf(__uint_as_float(dp[4 * e + 1]), kDown, -d.y));
-          p[16 * c + 2 * e + 1] = packed::pack2<kFp16>(__uint_as_float(zz[2]) * fmaf(__uint_as_float(dp[4 * e + 2]), kDown, -d.z),
-                                                       __uint_as_float(zz[3]) * fmaf(__uint_as_float(dp[4 * e + 3]), kDown, -d.w));
+          const uint64_t v0 = packed::pair(__uint_as_float(dp[4 * e]), __uint_as_float(dp[4 * e + 1]));
+          const uint64_t v1 = packed::pair(__uint_as_float(dp[4 * e + 2]), __uint_as_float(dp[4 * e + 3]));
+          const uint64_t d0 = packed::pair(d.x, d.y), d1 = packed::pair(d.z, d.w);
+          const float2 a = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[0]), __uint_as_float(zz[1])),
+                                                       kFp16 ? packed::fma2(v0, down, d0) : packed::add2(v0, d0)));
+          const float2 b = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[2]), __uint_as_float(zz[3])),
+                                                       kFp16 ? packed::fma2(v1, down, d1) : packed::add2(v1, d1)));
+          p[16 * c + 2 * e] = packed::pack2<kFp16>(a.x, a.y);
+          p[16 * c + 2 * e + 1] = packed::pack2<kFp16>(b.x, b.y);
         }
       }
       if (masked) {
