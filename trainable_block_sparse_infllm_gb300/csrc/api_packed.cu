@@ -310,16 +310,14 @@ int infllmv2_packed_attn_backward(const infllmv2_packed_attn_args* args, const v
         return rc;
     if ((rc = check_status(c))) return rc;
     PackedAttnMaps maps = {};
-    if ((rc = attn_maps(&maps, args, c)) || (rc = row_map(&maps.dout, c, dout, r[1], "dout"))) return rc;
+    if ((rc = attn_maps(&maps, args, c)) || (rc = row_map(&maps.out, c, out, r[0], "out")) ||
+        (rc = row_map(&maps.dout, c, dout, r[1], "dout")))
+      return rc;
     PackedAttnGrads g = {};
-    g.out = out;
-    g.dout = dout;
     g.lse = lse;
     g.dq = dq;
     g.dk = dk;
     g.dv = dv;
-    g.out_st = {r[0].token, r[0].head};
-    g.dout_st = {r[1].token, r[1].head};
     g.dq_st = {r[2].token, r[2].head};
     g.dk_st = {r[3].token, r[3].head};
     g.dv_st = {r[4].token, r[4].head};

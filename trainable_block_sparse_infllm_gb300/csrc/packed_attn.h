@@ -24,11 +24,11 @@ struct PackedAttnShape {
   uint32_t* status;
 };
 
-// Tensor maps.  q, dout: [d, group, KV head, token], one box of 64 columns = the
+// Tensor maps.  q, out, dout: [d, group, KV head, token], one box of 64 columns = the
 // rows (token, head of the group) of packed_tile_tokens(G) tokens; k, v: [d,
 // token, KV head], one box of 64 columns x 128 tokens.  128-byte swizzle.
 struct PackedAttnMaps {
-  CUtensorMap q, k, v, dout;
+  CUtensorMap q, k, v, out, dout;
 };
 
 // Tokens whose rows, one per head of the group, fill a tile of 128.
@@ -50,10 +50,9 @@ cudaError_t launch_packed_attn(const PackedAttnShape& s, int D, bool fp16, const
                                const PackedAttnIn& in, const PackedAttnOut& o, cudaStream_t st);
 
 struct PackedAttnGrads {
-  const void *out, *dout;
   const float* lse;
   void *dq, *dk, *dv;
-  PackedStride out_st, dout_st, dq_st, dk_st, dv_st;
+  PackedStride dq_st, dk_st, dv_st;
   float2* rows;   // workspace [Tq, Hkv * G]: (lse log2(e), D) of each row
 };
 

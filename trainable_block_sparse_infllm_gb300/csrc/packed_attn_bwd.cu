@@ -61,7 +61,7 @@ struct DqLayout {
   static constexpr int kUnit = 0, kUnitFree = 2, kDoFull = 4, kDoFree = 5, kKFull = 6, kKEmpty = kKFull + kKs,
                        kVFull = kKEmpty + kKs, kVEmpty = kVFull + kVs, kTail = kVEmpty + kVs, kCleared = kTail + 1,
                        kPair = kCleared + 1, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
-                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kNumBars = kQIn + 1;
+                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kNumBars = kOutRead + 1;
   static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 16 bytes each
   static constexpr int kSlot = kUnits + 32;
   static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kNumBars; ++i) {
       int count = 1;
       if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
-      if (i == L::kFree || i == L::kDsFull || i == L::kAccFree || i == L::kQIn) count = 8;
+      if (i == L::kFree || i == L::kDsFull || i == L::kAccFree || i == L::kQIn || i == L::kOutRead)
+        count = 8;
       mbar_init(&bars[i], count);
     }
     fence_barrier_init();
@@ -236,16 +237,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++uses;
           }
-          const int vs = v_copies % kVs;
-          if (v_copies >= kVs) wait(L::kVEmpty + vs, v_copies / kVs - 1);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars[L::kVFull + vs], kTile);
-            for (int c = 0; c < kD / 64; ++c)
-              packed::tma_load_3d(smem_u32(smem + L::kV + vs * kTile + c * 16384), &maps.v, c * 64, row, u.h,
-                                  &bars[L::kVFull + vs]);
+          // Through the V ring, before V_0 where D is rowsum(dout * out): out.
+          for (int first = j == 0 && !u.exact ? 0 : 1; first < 2; ++first) {
+            const int vs = v_copies % kVs;
+            if (v_copies >= kVs) wait(L::kVEmpty + vs, v_copies / kVs - 1);
+            if (!ok) break;
+            if (lane == 0) {
+              const uint32_t to = smem_u32(smem + L::kV + vs * kTile);
+              mbar_arrive_expect_tx(&bars[L::kVFull + vs], first ? kTile : row_bytes);
+              for (int c = 0; c < kD / 64; ++c) {
+                if (first) {
+                  packed::tma_load_3d(to + c * 16384, &maps.v, c * 64, row, u.h, &bars[L::kVFull + vs]);
+                } else {
+                  packed::tma_load_4d(to + c * 16384, &maps.out, c * 64, 0, u.h, u.seq.q0 + u.t0,
+                                      &bars[L::kVFull + vs]);
+                }
+              }
+            }
+            ++v_copies;
           }
-          ++v_copies;
+          if (!ok) break;
         }
         __syncwarp();
       }
@@ -266,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = packed::desc_rows(smem_u32(smem + L::kV));
       const bool issuer = packed::elect_one();
       Place pk = {0, 0}, pv = {0, 0};
-      int pairs = 0, tails = 0, uses = 0;
+      int pairs = 0, tails = 0, uses = 0, outs = 0;
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
+        const bool exact = uniform(u.exact);
         if (steps > 0) {
           wait(L::kQIn, uses);
           if (issuer) mbar_arrive(&bars[L::kKEmpty + pk.stage]);   // Q's stage has been read
@@ -283,7 +295,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               wait(L::kKFull + pk.stage, pk.phase);
             }
           }
-          if (t == 1) wait(L::kDoFull, uses++);
+          if (t == 1) {
+            wait(L::kDoFull, uses++);
+            if (!exact) {   // out's stage: read by the threads before their first pair
+              wait(L::kOutRead, outs++);
+              if (issuer) mbar_arrive(&bars[L::kVEmpty + pv.stage]);
+              __syncwarp();
+              next(pv, kVs);
+            }
+          }
           if (t > 0) wait(L::kVFull + pv.stage, pv.phase);
           if (pairs > 0) wait(L::kFree, pairs - 1);   // both have been read
           ++pairs;
@@ -375,14 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       return part[r] + part[128 + r];
     };
-    int pairs = 0, summed = 0;   // in all: pairs of scores read, dS written
-    Place pk = {0, 0};
+    int pairs = 0, summed = 0, uses = 0;   // in all: pairs of scores read, dS written, units with keys
+    Place pk = {0, 0}, pv = {0, 0};
     for (int k = 0; next_unit(k, &ok, &u); ++k) {
       const int token = u.t0 + r / s.G;
       const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 : 0;
       const int head = u.h * s.G + r % s.G;
       const long long row = u.seq.q0 + token;
+      // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
+      float D = 0.f, lse2 = 0.f;
+      if (active) lse2 = limit > 0 ? __ldg(g.lse + row * (s.Hkv * s.G) + head) * kLog2e : INFINITY;
       if (u.steps > 0) {
         // Q into tensor memory: S of the last unit has been read, so its Q has been.
         wait(L::kKFull + pk.stage, pk.phase);
@@ -403,30 +426,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kQIn]);
         for (int i = 0; i <= u.steps; ++i) next(pk, kKs);
-      }
-      float D = 0.f, lse2 = 0.f;
-      if (active) {
-        // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
-        lse2 = limit > 0 ? __ldg(g.lse + row * (s.Hkv * s.G) + head) * kLog2e : INFINITY;
-        if (!u.exact) {   // each warpgroup half of the columns
-          const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.out) + row * g.out_st.token +
-                                                          head * g.out_st.head + half * (kD / 2));
-          const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) +
-                                                          row * g.dout_st.token + head * g.dout_st.head +
-                                                          half * (kD / 2));
+        if (!u.exact) {   // D from dout and out, half of the columns each
+          wait(L::kDoFull, uses);
+          wait(L::kVFull + pv.stage, pv.phase);
+          const uint8_t* x = smem + r * 128;
+          const uint8_t* y = smem + L::kV + pv.stage * kTile + r * 128;
 #pragma unroll
           for (int i = 0; i < kD / 16; ++i) {
-            const uint4 v = __ldg(a + i), w = __ldg(c + i);
-            const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, ws[4] = {w.x, w.y, w.z, w.w};
+            const int c = half * (kD / 16) + i, at = (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4);
+            const uint4 v = *reinterpret_cast<const uint4*>(x + at), o = *reinterpret_cast<const uint4*>(y + at);
+            const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, os[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 p = packed::unpack2<kFp16>(vs[e]), q = packed::unpack2<kFp16>(ws[e]);
-              D = fmaf(p.x, q.x, fmaf(p.y, q.y, D));
+              const float2 a = packed::unpack2<kFp16>(vs[e]), b = packed::unpack2<kFp16>(os[e]);
+              D = fmaf(a.x, b.x, fmaf(a.y, b.y, D));
             }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[L::kOutRead]);
+          next(pv, kVs);
+          D = both(D);
         }
+        for (int i = 0; i < u.steps; ++i) next(pv, kVs);
+        ++uses;
       }
-      if (!u.exact) D = both(D);
       const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
       const uint64_t down = packed::pair(-lse2, -lse2);
       // Columns of tile j that the row attends, of this half's 64; 64 where no row of the warp needs a mask.
