@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // kSplit, at the end, over the ring: x of this CTA's 256 rows, their (m, l), and the weights of the share it joins.
   float4* parts = reinterpret_cast<float4*>(ring);
   float2* sums = reinterpret_cast<float2*>(ring + 256 * kD * 4);
-  float* weights = reinterpret_cast<float*>(sums + 256);   // [256 / ctas][16]
+  float* weights = reinterpret_cast<float*>(sums + 256);   // [rows of the share][16]
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
   const int tile_tokens = packed_tile_tokens(s.G);
   const int rank = kSplit ? static_cast<int>(blockIdx.x) % ctas : 0;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();
     if (any) {   // (the softmax warps: the others have given registers away)
-      const int share = 256 / ctas, row0 = rank * share;
+      const int row0 = rank * 256 / ctas, share = (rank + 1) * 256 / ctas - row0;
       for (int e = tid; e < share; e += 256) {   // a row: its weights, over l, and log sum
         const int row = row0 + e, rr = row & 127;
         const int token = u.t0 + (row >> 7) * tile_tokens + rr / s.G;
@@ -685,10 +685,10 @@ constexpr int kMaxSplit = 16;
 template <int kD, bool kFp16>
 int clusters_at_once(int ctas) {
   static std::mutex mu;
-  static int known[64][5];   // by log2 of ctas; what it is plus 1
-  int dev = 0, i = 0;
+  static int known[64][kMaxSplit + 1];   // what it is plus 1
+  const int i = ctas;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  while ((1 << i) < ctas) ++i;
   std::lock_guard<std::mutex> lock(mu);
   if (!known[dev][i]) {
     const auto kernel = packed_attn_kernel<kD, kFp16, true>;
@@ -725,7 +725,7 @@ int split(const PackedAttnShape& s, int step) {
   const long long tiles = s.Tk / s.B / 128;
   if (2 * units > device_sm_count()) return 1;
   int ctas = kMaxSplit;
-  while (ctas > 1 && (tiles / ctas < 4 || clusters_at_once<kD, kFp16>(ctas) < units)) ctas /= 2;
+  while (ctas > 1 && (tiles / ctas < 4 || clusters_at_once<kD, kFp16>(ctas) < units)) --ctas;
   return ctas;
 }
 
