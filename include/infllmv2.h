@@ -501,11 +501,24 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
  *           step is empty.
  * Page sizes, batch and pool as for the paged cache (any page size from 1 on).
  */
-int infllmv2_paged_reserve(int32_t page_size, int32_t num_pages, int32_t batch, int32_t max_pages,
-                           int32_t* page_table, int32_t* held, int32_t* free_pages, int32_t* n_free,
-                           const int32_t* kv_lens, const int32_t* n_new, const int32_t* seq_lens, int32_t* new_lens,
-                           int32_t* starts, int32_t max_tokens, int32_t* slots, int32_t* positions, int32_t* missing,
-                           void* stream);
+typedef struct infllmv2_reserve_args {
+  int32_t page_size, num_pages, batch, max_pages, max_tokens;
+  int32_t reserved;        /* 0 */
+  int32_t* page_table;
+  int32_t* held;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* missing;
+  const int32_t* kv_lens;
+  const int32_t* n_new;
+  const int32_t* seq_lens;
+  int32_t* new_lens;
+  int32_t* starts;
+  int32_t* slots;
+  int32_t* positions;
+} infllmv2_reserve_args;
+
+int infllmv2_paged_reserve(const infllmv2_reserve_args* args, void* stream);
 
 /*
  * Write the tokens of a packed step into the pages: row t of k_new and v_new
@@ -576,9 +589,9 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* 
  *     scale (x cos a - y sin a, x sin a + y cos a),  a = 2 pi positions[t] turns[i] / 2^64,
  * with transpose = 1 the same with -a: the gradient of the inputs from that of
  * the outputs.  The other head_dim - rotary_dim values are copied.
- *   q, k    INFLLMV2_BF16, INFLLMV2_FP16 or INFLLMV2_FP32 (dtype); k may be NULL.
- *           Strides in elements between tokens and heads.  out may be in, with the
- *           same strides; otherwise the two must not overlap.
+ *   q, k    INFLLMV2_BF16, INFLLMV2_FP16 or INFLLMV2_FP32 (dtype); no k where
+ *           k_heads is 0.  Strides in elements between tokens and heads.  q_out may be
+ *           q, with the same strides; otherwise the two must not overlap; k likewise.
  *   positions  int32 [tokens], any value.
  *   turns   device memory, [rotary_dim / 2], from infllmv2_rotary_frequencies.
  * head_dim and rotary_dim: multiples of 16, rotary_dim <= head_dim <= 512.
@@ -586,18 +599,20 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* 
  */
 #define INFLLMV2_FP32 2
 
-typedef struct infllmv2_rotary_rows {
-  const void* in;
-  void* out;
-  int64_t in_strides[2];   /* elements between tokens and heads */
-  int64_t out_strides[2];
-  int32_t heads;
+typedef struct infllmv2_rotary_args {
+  int32_t dtype, tokens, head_dim, rotary_dim, q_heads, k_heads, interleaved, transpose;
+  float scale;
   int32_t reserved;        /* 0 */
-} infllmv2_rotary_rows;
+  const int32_t* positions;
+  const uint64_t* turns;
+  const void* q;           /* [tokens, q_heads, head_dim] */
+  void* q_out;
+  const void* k;           /* [tokens, k_heads, head_dim] */
+  void* k_out;
+  int64_t q_strides[2], q_out_strides[2], k_strides[2], k_out_strides[2];
+} infllmv2_rotary_args;
 
-int infllmv2_rotary(int32_t dtype, int32_t tokens, int32_t head_dim, const infllmv2_rotary_rows* q,
-                    const infllmv2_rotary_rows* k, const int32_t* positions, int32_t rotary_dim,
-                    const uint64_t* turns, float scale, int32_t interleaved, int32_t transpose, void* stream);
+int infllmv2_rotary(const infllmv2_rotary_args* args, void* stream);
 
 /*
  * Causal attention over packed sequences with grouped heads.  Sequence b has the

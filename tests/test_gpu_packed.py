@@ -511,6 +511,9 @@ def test_reserve_reuses_what_the_call_gives_back(dev):
     assert step([64, 0], [0, 17]) == (2, [64, 0], [4, 0], 0)           # none free: as it was
     assert step([0, 0], [0, 33]) == (0, [0, 33], [0, 3], 1)            # the first finishes: its pages serve
     assert tables.page_table[1].tolist()[:3] == [0, 1, 2] and tables.free_pages.tolist()[0] == 3
+    assert step([0, 33], [60, 0]) == (3, [0, 33], [0, 3], 1) and step([0, 33], [64, 31]) == (4, [0, 33], [0, 3], 1)
+    assert step([0, 0], [64, 64]) == (4, [0, 0], [0, 3], 1)            # more than the pool has
+    assert _status() == 0
     assert step([0, 33], [0, -1])[0] == -1 and _status() == T.DEVICE_BAD_KV_LEN
 
 

@@ -104,59 +104,61 @@ def test_frequencies_refuse(L):
         T.rotary_frequencies(64, scaling=T.ROTARY_FACTORS, factors=[1.0] * 31, original_len=4096)
 
 
-def _rotary(L, rows=None, k=None, dtype=None, tokens=4, dim=64, positions=FAKE, part=64, turns=FAKE, scale=1.0,
-            interleaved=0, transpose=0, no_q=False):
-    rows = dict(dict(x_in=FAKE, x_out=FAKE, in_token=128, in_head=64, out_token=128, out_head=64, heads=2), **(rows or {}))
-    k_rows = None if k is None else ctypes.byref(L.RotaryRows(**dict(
-        dict(x_in=FAKE, x_out=FAKE, in_token=128, in_head=64, out_token=128, out_head=64, heads=2), **k)))
-    return L.lib.infllmv2_rotary(L.BF16 if dtype is None else dtype, tokens, dim,
-                                 None if no_q else ctypes.byref(L.RotaryRows(**rows)), k_rows, positions, part, turns,
-                                 scale, interleaved, transpose, None)
+def _rotary(L, **kw):
+    fields = dict(dtype=L.BF16, tokens=4, head_dim=64, rotary_dim=64, q_heads=2, k_heads=2, interleaved=0, transpose=0,
+                  scale=1.0, positions=FAKE, turns=FAKE)
+    for name in ("q", "q_out", "k", "k_out"):
+        fields.update({name: FAKE, name + "_token": 128, name + "_head": 64})
+    fields.update(kw)
+    return L.lib.infllmv2_rotary(ctypes.byref(L.RotaryArgs(**fields)), None)
 
 
 def test_rotary_refuses(L):
     bad, no = L.INVALID_ARGUMENT, L.UNSUPPORTED
-    for kw, code in ((dict(dtype=3), no), (dict(tokens=0), bad), (dict(tokens=-1), bad), (dict(dim=8, part=8), no),
-                     (dict(dim=72, part=64), no), (dict(dim=528), no), (dict(part=0), no), (dict(part=24), no),
-                     (dict(part=80), no), (dict(no_q=True), bad), (dict(positions=None), bad), (dict(turns=None), bad),
-                     (dict(scale=0.0), bad), (dict(scale=math.inf), bad), (dict(scale=math.nan), bad),
-                     (dict(interleaved=2), bad), (dict(transpose=-1), bad)):
+    assert L.lib.infllmv2_rotary(None, None) == bad
+    for kw, code in ((dict(dtype=3), no), (dict(tokens=0), bad), (dict(tokens=-1), bad),
+                     (dict(head_dim=8, rotary_dim=8), no), (dict(head_dim=72), no), (dict(head_dim=528), no),
+                     (dict(rotary_dim=0), no), (dict(rotary_dim=24), no), (dict(rotary_dim=80), no),
+                     (dict(q_heads=0), bad), (dict(k_heads=-1), bad), (dict(positions=None), bad),
+                     (dict(turns=None), bad), (dict(scale=0.0), bad), (dict(scale=math.inf), bad),
+                     (dict(scale=math.nan), bad), (dict(interleaved=2), bad), (dict(transpose=-1), bad)):
         assert _rotary(L, **kw) == code, kw
-    for rows, code in ((dict(heads=0), bad), (dict(heads=5000), no), (dict(x_in=None), bad), (dict(x_out=None), bad),
-                       (dict(x_in=ODD, x_out=ODD), no), (dict(in_token=-128), bad), (dict(in_token=130), no),
-                       (dict(in_token=1 << 58), no), (dict(x_out=FAKE + 4096, out_token=64), bad),
-                       (dict(x_out=FAKE + 4096, out_head=0), bad), (dict(out_token=256), bad)):
-        assert _rotary(L, rows=rows) == code, rows
-        assert _rotary(L, k=rows) == code, rows
+    for x in ("q", "k"):
+        other = {x + "_out": FAKE + 4096}
+        for kw, code in (({x + "_heads": 5000}, no), ({x: None}, bad), ({x + "_out": None}, bad),
+                         ({x: ODD, x + "_out": ODD}, no), ({x + "_token": -128}, bad), ({x + "_token": 130}, no),
+                         ({x + "_token": 1 << 58}, no), (dict(other, **{x + "_out_token": 64}), bad),
+                         (dict(other, **{x + "_out_head": 0}), bad), ({x + "_out_token": 256}, bad)):
+            assert _rotary(L, **kw) == code, kw
     # fp32 rows of 4 elements are 16 bytes.
-    assert _rotary(L, rows=dict(in_token=132), dtype=L.BF16) == no
-    assert _rotary(L, rows=dict(in_token=130), dtype=L.FP32) == no
+    assert _rotary(L, q_token=132) == no
+    assert _rotary(L, q_token=130, dtype=L.FP32) == no
 
 
 # ------------------------------------------------------------------ reserve
 
-def _reserve(L, page=16, pages=10, batch=2, max_pages=4, tokens=8, arrays=None, seq=None):
-    names = ("table", "held", "free", "n_free", "kv", "new", "lens", "starts", "slots", "positions", "missing")
-    a = {n: FAKE + 4096 * i for i, n in enumerate(names)}
-    a.update(arrays or {})
-    return L.lib.infllmv2_paged_reserve(page, pages, batch, max_pages, a["table"], a["held"], a["free"], a["n_free"],
-                                        a["kv"], a["new"], seq, a["lens"], a["starts"], tokens, a["slots"],
-                                        a["positions"], a["missing"], None)
+def _reserve(L, **kw):
+    names = ("page_table", "held", "free_pages", "n_free", "kv_lens", "n_new", "new_lens", "starts", "slots",
+             "positions", "missing")
+    fields = dict({n: FAKE + 4096 * i for i, n in enumerate(names)}, page_size=16, num_pages=10, batch=2, max_pages=4,
+                  max_tokens=8)
+    fields.update(kw)
+    return L.lib.infllmv2_paged_reserve(ctypes.byref(L.ReserveArgs(**fields)), None)
 
 
 def test_reserve_refuses(L):
     bad, no = L.INVALID_ARGUMENT, L.UNSUPPORTED
-    for kw, code in ((dict(page=0), bad), (dict(pages=0), bad), (dict(batch=0), bad), (dict(max_pages=0), bad),
-                     (dict(batch=4097), no), (dict(page=65537), no), (dict(page=1 << 15, max_pages=1 << 16), no),
-                     (dict(page=1 << 15, pages=1 << 16), no), (dict(tokens=-1), bad), (dict(tokens=(1 << 30) + 1), no)):
+    assert L.lib.infllmv2_paged_reserve(None, None) == bad
+    for kw, code in ((dict(page_size=0), bad), (dict(num_pages=0), bad), (dict(batch=0), bad),
+                     (dict(max_pages=0), bad), (dict(batch=4097), no), (dict(page_size=65537), no),
+                     (dict(page_size=1 << 15, max_pages=1 << 16), no), (dict(page_size=1 << 15, num_pages=1 << 16), no),
+                     (dict(max_tokens=-1), bad), (dict(max_tokens=(1 << 30) + 1), no)):
         assert _reserve(L, **kw) == code, kw
-    for name in ("table", "held", "free", "n_free", "kv", "new", "lens", "starts", "missing"):
-        assert _reserve(L, arrays={name: None}) == bad, name
-    assert _reserve(L, arrays=dict(lens=FAKE), seq=FAKE) == bad
-    assert _reserve(L, arrays=dict(lens=FAKE, held=FAKE)) == bad
-    for other in ("kv", "new"):
-        assert _reserve(L, arrays={"starts": FAKE, other: FAKE}) == bad
-    assert _reserve(L, arrays=dict(starts=FAKE), seq=FAKE) == bad
+    for name in ("page_table", "held", "free_pages", "n_free", "kv_lens", "n_new", "new_lens", "starts", "missing"):
+        assert _reserve(L, **{name: None}) == bad, name
+    for a, b in (("new_lens", "seq_lens"), ("new_lens", "held"), ("starts", "kv_lens"), ("starts", "n_new"),
+                 ("starts", "seq_lens"), ("starts", "new_lens"), ("starts", "held")):
+        assert _reserve(L, **{a: FAKE, b: FAKE}) == bad, (a, b)
 
 
 # ------------------------------------------------------------ packed append
@@ -213,7 +215,8 @@ def _backward(L, args, strides=GRAD_STRIDES, ws=FAKE, ws_bytes=640, **kw):
 
 def test_structs_match_the_header(L):
     assert ctypes.sizeof(L.PackedAttnArgs) == 8 * 4 + 3 * 8 + 6 * 8 + 2 * 8
-    assert ctypes.sizeof(L.RotaryRows) == 2 * 8 + 4 * 8 + 2 * 4
+    assert ctypes.sizeof(L.RotaryArgs) == 10 * 4 + 6 * 8 + 8 * 8
+    assert ctypes.sizeof(L.ReserveArgs) == 6 * 4 + 12 * 8
     assert ctypes.sizeof(L.RotaryConfig) == 2 * 4 + 2 * 8 + 2 * 4 + 2 * 8 + 8
 
 

@@ -108,19 +108,24 @@ class RotaryConfig(ctypes.Structure):
     ]
 
 
-class RotaryRows(ctypes.Structure):
-    """Mirror of ``infllmv2_rotary_rows``."""
+class RotaryArgs(ctypes.Structure):
+    """Mirror of ``infllmv2_rotary_args``."""
 
-    _fields_ = [
-        ("x_in", ctypes.c_void_p),
-        ("x_out", ctypes.c_void_p),
-        ("in_token", ctypes.c_int64),
-        ("in_head", ctypes.c_int64),
-        ("out_token", ctypes.c_int64),
-        ("out_head", ctypes.c_int64),
-        ("heads", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
-    ]
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "tokens", "head_dim", "rotary_dim", "q_heads", "k_heads",
+                                              "interleaved", "transpose")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("positions", "turns", "q", "q_out", "k", "k_out")] + \
+               [(n, ctypes.c_int64) for n in ("q_token", "q_head", "q_out_token", "q_out_head", "k_token", "k_head",
+                                              "k_out_token", "k_out_head")]
+
+
+class ReserveArgs(ctypes.Structure):
+    """Mirror of ``infllmv2_reserve_args``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("page_size", "num_pages", "batch", "max_pages", "max_tokens",
+                                              "reserved")] + \
+               [(n, ctypes.c_void_p) for n in ("page_table", "held", "free_pages", "n_free", "missing", "kv_lens",
+                                               "n_new", "seq_lens", "new_lens", "starts", "slots", "positions")]
 
 
 class PackedAttnArgs(ctypes.Structure):
@@ -206,24 +211,22 @@ lib.infllmv2_paged_attn_decode.argtypes = [_C, _i32, _i32, _i32, _vp, _vp, _vp, 
 lib.infllmv2_paged_attn_decode.restype = ctypes.c_int
 lib.infllmv2_paged_evict.argtypes = [_C, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 lib.infllmv2_paged_evict.restype = ctypes.c_int
-lib.infllmv2_paged_reserve.argtypes = [_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
-                                       _vp, _vp, _vp]
+# Argument structures of the packed step go in as bytes (struct.pack in the order of the fields above, which a
+# call fills in a sixth of the time) or by reference.
+lib.infllmv2_paged_reserve.argtypes = [_vp, _vp]
 lib.infllmv2_paged_reserve.restype = ctypes.c_int
-lib.infllmv2_paged_append_packed.argtypes = [_C, _i32, _vp, _vp, ctypes.POINTER(ctypes.c_int64), _vp, _vp, _vp]
+lib.infllmv2_paged_append_packed.argtypes = [_C, _i32, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.infllmv2_paged_append_packed.restype = ctypes.c_int
 lib.infllmv2_rotary_frequencies.argtypes = [ctypes.POINTER(RotaryConfig), ctypes.POINTER(ctypes.c_uint64),
                                             ctypes.POINTER(ctypes.c_float)]
 lib.infllmv2_rotary_frequencies.restype = ctypes.c_int
-_R = ctypes.POINTER(RotaryRows)
-lib.infllmv2_rotary.argtypes = [_i32, _i32, _i32, _R, _R, _vp, _i32, _vp, ctypes.c_float, _i32, _i32, _vp]
+lib.infllmv2_rotary.argtypes = [_vp, _vp]
 lib.infllmv2_rotary.restype = ctypes.c_int
-_A = ctypes.POINTER(PackedAttnArgs)
-lib.infllmv2_packed_attn.argtypes = [_A, _vp, ctypes.POINTER(ctypes.c_int64), _vp, _vp]
+lib.infllmv2_packed_attn.argtypes = [_vp, _vp, _vp, _vp, _vp]
 lib.infllmv2_packed_attn.restype = ctypes.c_int
-lib.infllmv2_packed_workspace_size.argtypes = [_A]
+lib.infllmv2_packed_workspace_size.argtypes = [_vp]
 lib.infllmv2_packed_workspace_size.restype = ctypes.c_size_t
-lib.infllmv2_packed_attn_backward.argtypes = [_A, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int64), _vp,
-                                              ctypes.c_size_t, _vp]
+lib.infllmv2_packed_attn_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 lib.infllmv2_packed_attn_backward.restype = ctypes.c_int
 lib.infllmv2_status_string.argtypes = [ctypes.c_int]
 lib.infllmv2_status_string.restype = ctypes.c_char_p

@@ -37,23 +37,22 @@ int check_apart(const PackedRows& r, int64_t tokens, int64_t heads, int d, const
   return ok ? INFLLMV2_OK : fail(INFLLMV2_INVALID_ARGUMENT, "%s: rows overlap (strides)", what);
 }
 
-int check_rotary_rows(const infllmv2_rotary_rows* r, int64_t tokens, int d, int bytes, const char* what,
-                      PackedRows* in, PackedRows* out, int* heads) {
-  if (r->heads < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "%s: heads must be >= 1", what);
-  if (r->heads > 4096) return fail(INFLLMV2_UNSUPPORTED, "%s: at most 4096 heads (got %d)", what, r->heads);
-  if (!r->in || !r->out) return fail(INFLLMV2_INVALID_ARGUMENT, "%s: in or out is NULL", what);
-  if (!aligned16(r->in) || !aligned16(r->out))
+int check_rotary_rows(const void* in, void* out, const int64_t in_strides[2], const int64_t out_strides[2],
+                      int64_t tokens, int64_t heads, int d, int bytes, const char* what, PackedRows* from,
+                      PackedRows* to) {
+  if (heads > 4096) return fail(INFLLMV2_UNSUPPORTED, "%s: at most 4096 heads (got %d)", what, (int)heads);
+  if (!in || !out) return fail(INFLLMV2_INVALID_ARGUMENT, "%s or its output is NULL", what);
+  if (!aligned16(in) || !aligned16(out))
     return fail(INFLLMV2_UNSUPPORTED, "%s: pointers must be 16-byte aligned", what);
   int rc;
-  if ((rc = check_rows(r->in_strides, tokens, r->heads, bytes, what, in)) ||
-      (rc = check_rows(r->out_strides, tokens, r->heads, bytes, what, out)) ||
-      (rc = check_apart(*out, tokens, r->heads, d, what)))
+  if ((rc = check_rows(in_strides, tokens, heads, bytes, what, from)) ||
+      (rc = check_rows(out_strides, tokens, heads, bytes, what, to)) ||
+      (rc = check_apart(*to, tokens, heads, d, what)))
     return rc;
-  if (r->in == r->out && (in->token != out->token || in->head != out->head))
-    return fail(INFLLMV2_INVALID_ARGUMENT, "%s: in place takes the same strides for in and out", what);
-  in->x = const_cast<void*>(r->in);
-  out->x = r->out;
-  *heads = r->heads;
+  if (in == out && (from->token != to->token || from->head != to->head))
+    return fail(INFLLMV2_INVALID_ARGUMENT, "%s: in place takes the same strides for input and output", what);
+  from->x = const_cast<void*>(in);
+  to->x = out;
   return INFLLMV2_OK;
 }
 
@@ -216,38 +215,46 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* c, uint64_t* turns
   });
 }
 
-int infllmv2_rotary(int32_t dtype, int32_t tokens, int32_t head_dim, const infllmv2_rotary_rows* q,
-                    const infllmv2_rotary_rows* k, const int32_t* positions, int32_t rotary_dim,
-                    const uint64_t* turns, float scale, int32_t interleaved, int32_t transpose, void* stream) {
+int infllmv2_rotary(const infllmv2_rotary_args* r, void* stream) {
   INFLLMV2_GUARD({
-    if (dtype != INFLLMV2_BF16 && dtype != INFLLMV2_FP16 && dtype != INFLLMV2_FP32)
-      return fail(INFLLMV2_UNSUPPORTED, "dtype must be bf16, fp16 or fp32 (got %d)", dtype);
-    if (tokens < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "tokens must be >= 1 (got %d)", tokens);
-    if (head_dim < 16 || head_dim % 16 != 0 || head_dim > kMaxRotary)
-      return fail(INFLLMV2_UNSUPPORTED, "head_dim must be a multiple of 16 up to %d (got %d)", kMaxRotary, head_dim);
-    if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
-      return fail(INFLLMV2_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to head_dim (got %d)", rotary_dim);
-    if (!q || !positions || !turns) return fail(INFLLMV2_INVALID_ARGUMENT, "q, positions or turns is NULL");
-    if (!(std::isfinite(scale) && scale > 0.f)) return fail(INFLLMV2_INVALID_ARGUMENT, "scale must be > 0 and finite");
-    if ((interleaved != 0 && interleaved != 1) || (transpose != 0 && transpose != 1))
+    if (!r) return fail(INFLLMV2_INVALID_ARGUMENT, "args is NULL");
+    if (r->dtype != INFLLMV2_BF16 && r->dtype != INFLLMV2_FP16 && r->dtype != INFLLMV2_FP32)
+      return fail(INFLLMV2_UNSUPPORTED, "dtype must be bf16, fp16 or fp32 (got %d)", r->dtype);
+    if (r->tokens < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "tokens must be >= 1 (got %d)", r->tokens);
+    if (r->q_heads < 1 || r->k_heads < 0)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "q_heads must be >= 1 and k_heads >= 0");
+    const int d = r->head_dim;
+    if (d < 16 || d % 16 != 0 || d > kMaxRotary)
+      return fail(INFLLMV2_UNSUPPORTED, "head_dim must be a multiple of 16 up to %d (got %d)", kMaxRotary, d);
+    if (r->rotary_dim < 16 || r->rotary_dim % 16 != 0 || r->rotary_dim > d)
+      return fail(INFLLMV2_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to head_dim (got %d)", r->rotary_dim);
+    if (!r->positions || !r->turns) return fail(INFLLMV2_INVALID_ARGUMENT, "positions or turns is NULL");
+    if (!(std::isfinite(r->scale) && r->scale > 0.f))
+      return fail(INFLLMV2_INVALID_ARGUMENT, "scale must be > 0 and finite");
+    if ((r->interleaved != 0 && r->interleaved != 1) || (r->transpose != 0 && r->transpose != 1))
       return fail(INFLLMV2_INVALID_ARGUMENT, "interleaved and transpose must be 0 or 1");
     RotaryArgs a = {};
-    const int bytes = dtype == INFLLMV2_FP32 ? 4 : 2;
-    int rc = check_rotary_rows(q, tokens, head_dim, bytes, "q", &a.q_in, &a.q_out, &a.q_heads);
+    const int bytes = r->dtype == INFLLMV2_FP32 ? 4 : 2;
+    int rc = check_rotary_rows(r->q, r->q_out, r->q_strides, r->q_out_strides, r->tokens, r->q_heads, d, bytes, "q",
+                               &a.q_in, &a.q_out);
     if (rc) return rc;
-    if (k && (rc = check_rotary_rows(k, tokens, head_dim, bytes, "k", &a.k_in, &a.k_out, &a.k_heads))) return rc;
-    a.positions = positions;
-    a.turns = turns;
-    a.scale = scale;
-    a.tokens = tokens;
-    a.dim = head_dim;
-    a.part = rotary_dim;
-    a.interleaved = interleaved != 0;
-    a.transpose = transpose != 0;
-    a.in_place = q->in == q->out && (!k || k->in == k->out);
-    const RotaryType type = dtype == INFLLMV2_BF16   ? RotaryType::kBf16
-                            : dtype == INFLLMV2_FP16 ? RotaryType::kFp16
-                                                     : RotaryType::kFp32;
+    if (r->k_heads > 0 && (rc = check_rotary_rows(r->k, r->k_out, r->k_strides, r->k_out_strides, r->tokens,
+                                                  r->k_heads, d, bytes, "k", &a.k_in, &a.k_out)))
+      return rc;
+    a.positions = r->positions;
+    a.turns = r->turns;
+    a.scale = r->scale;
+    a.tokens = r->tokens;
+    a.q_heads = r->q_heads;
+    a.k_heads = r->k_heads;
+    a.dim = d;
+    a.part = r->rotary_dim;
+    a.interleaved = r->interleaved != 0;
+    a.transpose = r->transpose != 0;
+    a.in_place = r->q == r->q_out && (r->k_heads == 0 || r->k == r->k_out);
+    const RotaryType type = r->dtype == INFLLMV2_BF16   ? RotaryType::kBf16
+                            : r->dtype == INFLLMV2_FP16 ? RotaryType::kFp16
+                                                        : RotaryType::kFp32;
     const cudaError_t e = launch_rotary(a, type, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rotary");
     return INFLLMV2_OK;

@@ -306,31 +306,32 @@ int infllmv2_paged_append_packed(const infllmv2_paged_cache* cache, int32_t toke
   });
 }
 
-int infllmv2_paged_reserve(int32_t page_size, int32_t num_pages, int32_t batch, int32_t max_pages,
-                           int32_t* page_table, int32_t* held, int32_t* free_pages, int32_t* n_free,
-                           const int32_t* kv_lens, const int32_t* n_new, const int32_t* seq_lens, int32_t* new_lens,
-                           int32_t* starts, int32_t max_tokens, int32_t* slots, int32_t* positions, int32_t* missing,
-                           void* stream) {
+int infllmv2_paged_reserve(const infllmv2_reserve_args* r, void* stream) {
   INFLLMV2_GUARD({
-    if (page_size < 1 || num_pages < 1 || batch < 1 || max_pages < 1)
+    if (!r) return fail(INFLLMV2_INVALID_ARGUMENT, "args is NULL");
+    if (r->page_size < 1 || r->num_pages < 1 || r->batch < 1 || r->max_pages < 1)
       return fail(INFLLMV2_INVALID_ARGUMENT, "page_size, num_pages, batch and max_pages must be >= 1");
-    if (batch > kPagedMaxBatch)
-      return fail(INFLLMV2_UNSUPPORTED, "at most %d sequences (got %d)", kPagedMaxBatch, batch);
-    if (page_size > 65536) return fail(INFLLMV2_UNSUPPORTED, "page_size must be <= 65536 (got %d)", page_size);
-    if (static_cast<int64_t>(max_pages) * page_size > kMaxCap)
+    if (r->batch > kPagedMaxBatch)
+      return fail(INFLLMV2_UNSUPPORTED, "at most %d sequences (got %d)", kPagedMaxBatch, r->batch);
+    if (r->page_size > 65536) return fail(INFLLMV2_UNSUPPORTED, "page_size must be <= 65536 (got %d)", r->page_size);
+    if (static_cast<int64_t>(r->max_pages) * r->page_size > kMaxCap)
       return fail(INFLLMV2_UNSUPPORTED, "max_pages * page_size must be <= 2^30");
-    if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL)
+    if (static_cast<int64_t>(r->num_pages) * r->page_size > 0x7fffffffLL)
       return fail(INFLLMV2_UNSUPPORTED, "num_pages * page_size must be < 2^31");
-    if (max_tokens < 0) return fail(INFLLMV2_INVALID_ARGUMENT, "max_tokens must be >= 0 (got %d)", max_tokens);
-    if (max_tokens > kMaxCap) return fail(INFLLMV2_UNSUPPORTED, "max_tokens must be <= 2^30 (got %d)", max_tokens);
-    if (!page_table || !held || !free_pages || !n_free || !kv_lens || !n_new || !new_lens || !starts || !missing)
+    if (r->max_tokens < 0) return fail(INFLLMV2_INVALID_ARGUMENT, "max_tokens must be >= 0 (got %d)", r->max_tokens);
+    if (r->max_tokens > kMaxCap)
+      return fail(INFLLMV2_UNSUPPORTED, "max_tokens must be <= 2^30 (got %d)", r->max_tokens);
+    if (!r->page_table || !r->held || !r->free_pages || !r->n_free || !r->kv_lens || !r->n_new || !r->new_lens ||
+        !r->starts || !r->missing)
       return fail(INFLLMV2_INVALID_ARGUMENT, "a required array is NULL");
-    if (new_lens == seq_lens || new_lens == held || starts == kv_lens || starts == n_new || starts == seq_lens)
+    if (r->new_lens == r->seq_lens || r->new_lens == r->held || r->starts == r->kv_lens || r->starts == r->n_new ||
+        r->starts == r->seq_lens || r->starts == r->new_lens || r->starts == r->held)
       return fail(INFLLMV2_INVALID_ARGUMENT, "new_lens and starts must be apart from seq_lens, held and the lengths");
     uint32_t* status = status_ptr();
     if (!status) return fail(INFLLMV2_CUDA_ERROR, "no device status word (no current CUDA device?)");
-    const ReserveArgs a{batch, max_pages, page_size, num_pages, max_tokens, page_table, held, free_pages, n_free,
-                        kv_lens, n_new, seq_lens, new_lens, starts, slots, positions, missing, status};
+    const ReserveArgs a{r->batch, r->max_pages, r->page_size, r->num_pages, r->max_tokens, r->page_table, r->held,
+                        r->free_pages, r->n_free, r->kv_lens, r->n_new, r->seq_lens, r->new_lens, r->starts,
+                        r->slots, r->positions, r->missing, status};
     const cudaError_t e = launch_paged_reserve(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged_reserve");
     return INFLLMV2_OK;

@@ -100,7 +100,7 @@ __device__ __forceinline__ float dot(const uint16_t* q, const uint16_t* k) {
 template <int kD, bool kFp16, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnIn in,
-                       const PackedAttnOut o, const int ctas) {
+                       const PackedAttnOut o, const int ctas, const int halves) {
   using L = Layout<kD>;
   constexpr int kTile = L::kTile, kStages = L::kStages, kBuffers = L::kBuffers;
   constexpr uint32_t kColO = L::kColO;
@@ -119,18 +119,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile_tokens = packed_tile_tokens(s.G);
   const int rank = kSplit ? static_cast<int>(blockIdx.x) % ctas : 0;
 
-  if (tid == 0) {
+  if (tid < L::kNumBars) {
+    int count = 1;
+    if (tid == L::kUnitFree || tid == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
+    if ((tid >= L::kPFull && tid < L::kPFull + kBuffers) || (tid >= L::kOFree && tid < L::kOFree + 2)) count = 4;
+    if (tid >= L::kChecked && tid < L::kChecked + kMaxPartial) count = kBuffers == 2 ? 2 : 1;
+    mbar_init(&bars[tid], count);
+    fence_barrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
-    for (int i = 0; i < L::kNumBars; ++i) {
-      int count = 1;
-      if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
-      if ((i >= L::kPFull && i < L::kPFull + kBuffers) || (i >= L::kOFree && i < L::kOFree + 2)) count = 4;
-      if (i >= L::kChecked && i < L::kChecked + kMaxPartial) count = kBuffers == 2 ? 2 : 1;
-      mbar_init(&bars[i], count);
-    }
-    fence_barrier_init();
   }
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit u;
     bool bad = false;
     u.seq = packed::sequence(s, at.x, &bad);
-    u.t0 = at.y * 2 * tile_tokens;
+    u.t0 = at.y * halves * tile_tokens;
     u.h = at.z;
     u.before = u.seq.n_k - u.seq.n_q;
     u.j0 = 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {   // each half: up to its last query's own key
       const int first = u.t0 + x * tile_tokens, last = min(first + tile_tokens, u.seq.n_q) - 1;
-      u.n_tiles[x] = last < first ? 0 : (max(u.before + last + 1, 0) + 127) / 128;
+      u.n_tiles[x] = x >= halves || last < first ? 0 : (max(u.before + last + 1, 0) + 127) / 128;
     }
     if (kSplit) {
       const int all = max(u.n_tiles[0], u.n_tiles[1]), j1 = (rank + 1) * all / ctas;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------- units and loads
       packed::Walker walker;
       bool bad = false, ok = true;
-      walker.start(s, 2 * tile_tokens, false, &bad);
+      walker.start(s, halves * tile_tokens, false, &bad);
       int issued = 0, seen = 0, q_uses[2] = {0, 0};   // ring copies, V tiles looked through, Q tiles
       const int stride = kSplit ? 1 : static_cast<int>(gridDim.x);
       for (int k = 0;; ++k) {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kSplit) i = k * stride + (k & 1 ? stride - 1 - i : i);
         int4 at = make_int4(-1, 0, i % s.Hkv, 0);
         int b, level;
-        if (!(kSplit && k > 0) && walker.find(s, i / s.Hkv, 2 * tile_tokens, false, &b, &level, &bad)) {
+        if (!(kSplit && k > 0) && walker.find(s, i / s.Hkv, halves * tile_tokens, false, &b, &level, &bad)) {
           at.x = b;
           at.y = level;
         }
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; next_unit(k, &ok, &u); ++k) {
       any = true;
       const int token = u.t0 + x * tile_tokens + r / s.G;   // in the sequence
-      const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
+      const bool active = x < halves && r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 - u.j0 * 128 : 0;   // keys 0 .. limit - 1, from tile j0 on
       const int mine = x ? u.n_tiles[1] : u.n_tiles[0], both = min(u.n_tiles[0], u.n_tiles[1]);
       // Key tiles before this one need no mask in any row of the warp.
@@ -733,12 +733,16 @@ template <int kD, bool kFp16>
 cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const PackedAttnIn& in, const PackedAttnOut& o,
                    cudaStream_t st) {
   // Units of two tiles: at most one partly filled one per sequence.
-  const int step = 2 * packed_tile_tokens(s.G);
-  const long long units = std::min<long long>(s.Tq, static_cast<long long>(s.Tq) / step + s.B);
-  const int ctas = split<kD, kFp16>(s, step);
+  // While single tiles fill no more than the SMs, each is a unit of its own: its softmax then shares the SM
+  // with no other (one prompt of 301 tokens, 38 units or 76: 12.4 or 11.3 us).
+  const int one = packed_tile_tokens(s.G);
+  auto most = [&](int step) { return std::min<long long>(s.Tq, static_cast<long long>(s.Tq) / step + s.B); };
+  const int ctas = split<kD, kFp16>(s, 2 * one);
+  const int halves = ctas == 1 && most(one) * s.Hkv <= device_sm_count() ? 1 : 2;
+  const long long units = most(halves * one);
   const auto kernel = ctas > 1 ? packed_attn_kernel<kD, kFp16, true> : packed_attn_kernel<kD, kFp16, false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kD>::kBytes);
+  static packed::SharedMemory shared[2];   // of each of the two kernels
+  const cudaError_t e = shared[ctas > 1].allow(kernel, Layout<kD>::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // A CTA per SM, or a cluster per unit.
@@ -756,7 +760,7 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
   attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, maps, s, in, o, ctas);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, s, in, o, ctas, halves);
 }
 
 }  // namespace

@@ -4,12 +4,34 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "packed_attn.h"
 #include "tc.cuh"
 
 namespace infllmv2 {
 namespace packed {
+
+// Asks once per device for the dynamic shared memory that a kernel needs.
+class SharedMemory {
+ public:
+  template <typename Kernel>
+  cudaError_t allow(Kernel kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevices;
+    if (known && done_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done_[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<bool> done_[kDevices] = {};
+};
 
 // A sequence's rows.  One whose starts are out of range or descend is empty.
 struct Sequence {

@@ -94,19 +94,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
   const int tile_tokens = packed_tile_tokens(s.G);
 
-  if (tid == 0) {
+  if (tid < L::kNumBars) {
+    int count = 1;
+    if (tid == L::kUnitFree || tid == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
+    if (tid == L::kFree || tid == L::kDsFull || tid == L::kAccFree || tid == L::kQIn || tid == L::kOutRead) count = 8;
+    mbar_init(&bars[tid], count);
+    fence_barrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
+    prefetch_tensormap(&maps.out);
     prefetch_tensormap(&maps.dout);
-    for (int i = 0; i < L::kNumBars; ++i) {
-      int count = 1;
-      if (i == L::kUnitFree || i == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
-      if (i == L::kFree || i == L::kDsFull || i == L::kAccFree || i == L::kQIn || i == L::kOutRead)
-        count = 8;
-      mbar_init(&bars[i], count);
-    }
-    fence_barrier_init();
   }
   if (warp == kPairWarp) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -654,16 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int last_rows = (seq.n_q - tile_token(n - 1)) * s.G;
   const bool clears = n > 0 && last_rows < tile_rows;
 
-  if (tid == 0) {
+  if (tid < L::kNumBars) {
+    const bool by_warps = tid == L::kPFull || tid == L::kDsFull || tid == L::kRowsFree || tid == L::kRowsFree + 1;
+    mbar_init(&bars[tid], by_warps ? 8 : 1);
+    fence_barrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
     prefetch_tensormap(&maps.dout);
-    for (int i = 0; i < L::kNumBars; ++i) {
-      const bool by_warps = i == L::kPFull || i == L::kDsFull || i == L::kRowsFree || i == L::kRowsFree + 1;
-      mbar_init(&bars[i], by_warps ? 8 : 1);
-    }
-    fence_barrier_init();
   }
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -958,8 +958,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename Kernel, typename... More>
-cudaError_t launch_one(Kernel kernel, int bytes, long long units, int ctas, cudaStream_t st, const More&... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t launch_one(packed::SharedMemory& shared, Kernel kernel, int bytes, long long units, int ctas,
+                       cudaStream_t st, const More&... args) {
+  const cudaError_t e = shared.allow(kernel, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * ctas), 1, 1);
@@ -986,7 +987,8 @@ long long most_tiles(int tokens, int step, int B) {
 template <int kD, bool kFp16>
 cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const PackedAttnGrads& g, cudaStream_t st) {
   const long long tiles = most_tiles(s.Tq, packed_tile_tokens(s.G), s.B) * s.Hkv;
-  const cudaError_t e = launch_one(packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
+  static packed::SharedMemory shared[2];   // of each kernel
+  const cudaError_t e = launch_one(shared[0], packed_dq_kernel<kD, kFp16>, DqLayout<kD>::kBytes,
                                    std::min<long long>(tiles, device_sm_count()), 1, st, maps, s, g);
   if (e != cudaSuccess) return e;
   // CTAs per tile of keys.  Causal tiles differ by the whole length of the sequence, so
@@ -1000,7 +1002,7 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
   int ctas = 1;
   while (ctas < 4 && units * ctas < 2 * sms && row_tiles >= 12 * ctas) ctas *= 2;
   if (ctas == 4 && units * 8 <= sms && row_tiles >= 48) ctas = 8;
-  return launch_one(packed_dkv_kernel<kD, kFp16>, DkvLayout<kD>::kBytes, most_tiles(s.Tk, 128, s.B) * s.Hkv, ctas, st,
+  return launch_one(shared[1], packed_dkv_kernel<kD, kFp16>, DkvLayout<kD>::kBytes, most_tiles(s.Tk, 128, s.B) * s.Hkv, ctas, st,
                     maps, s, g, ctas);
 }
 

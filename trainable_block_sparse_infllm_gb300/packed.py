@@ -19,6 +19,7 @@ allocates (but for the ``alloc_`` functions) or synchronises.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -33,8 +34,15 @@ _rotary = _lib.lib.infllmv2_rotary
 _attn = _lib.lib.infllmv2_packed_attn
 _backward = _lib.lib.infllmv2_packed_attn_backward
 _byref = ctypes.byref
-_Strides4 = ctypes.c_int64 * 4
-_Strides10 = ctypes.c_int64 * 10
+_int32 = torch.int32
+# The C argument structures (_lib.py names their fields).
+_reserve_args = struct.Struct("=6i12Q").pack
+_rotary_args = struct.Struct("=8ifi6Q8q").pack
+_attn_args = struct.Struct("=7if3Q6q2Q").pack
+_strides2, _strides4, _strides10 = (struct.Struct("=%dq" % n).pack for n in (2, 4, 10))
+
+# As in paged.py each call's arguments are looked at in one expression, and only
+# where it fails do the functions named _refuse_* find out what is wrong.
 
 
 def _on(index: int, stream) -> int:
@@ -47,7 +55,13 @@ def _on(index: int, stream) -> int:
 
 
 def _is_ints(t, index: int, n: int) -> bool:
-    return t.dtype is torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == index
+    return t.dtype is _int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == index
+
+
+def _refuse_ints(index: int, **ints) -> None:
+    for name, (t, n) in ints.items():
+        if t is not None and not _is_ints(t, index, n):
+            raise _bad(f"{name} must be contiguous int32 [{n}] on cuda:{index}")
 
 
 # ------------------------------------------------------------ pages and slots
@@ -76,9 +90,10 @@ class PageTables:
                 raise _bad(f"{name} must be contiguous int32 [{n}] on cuda:{self.index}")
         self.page_table, self.held, self.free_pages = page_table, held, free_pages
         self.n_free, self.missing = n_free, missing
-        self._head = (self.page_size, self.num_pages, self.batch, self.max_pages, page_table.data_ptr(),
-                      held.data_ptr(), free_pages.data_ptr(), n_free.data_ptr())
-        self._missing = missing.data_ptr()
+        self._sizes = (self.page_size, self.num_pages, self.batch, self.max_pages)
+        self._arrays = (page_table.data_ptr(), held.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+                        missing.data_ptr())
+        self._lens_shape, self._starts_shape = held.shape, torch.Size([self.batch + 1])
 
 
 def alloc_page_tables(cache: PagedCache, batch: int, max_pages: int) -> PageTables:
@@ -101,19 +116,33 @@ def paged_reserve(tables: PageTables, kv_lens: torch.Tensor, n_new: torch.Tensor
     sequence has seen before (default kv_lens).  Where pages lack,
     ``tables.missing`` says how many and the step is empty.
     """
-    index, batch = tables.index, tables.batch
-    if not (_is_ints(kv_lens, index, batch) and _is_ints(n_new, index, batch) and _is_ints(new_lens, index, batch) and
-            _is_ints(starts, index, batch + 1) and (seq_lens is None or _is_ints(seq_lens, index, batch))):
-        raise _bad(f"kv_lens, n_new, new_lens and seq_lens must be contiguous int32 [{batch}] and starts [{batch + 1}] "
-                   f"on cuda:{index}")
-    tokens = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
-    for t in (slots, positions):
-        if t is not None and not _is_ints(t, index, tokens):
-            raise _bad(f"slots and positions must be contiguous int32 of one length on cuda:{index}")
-    rc = _reserve(*tables._head, kv_lens.data_ptr(), n_new.data_ptr(),
-                  None if seq_lens is None else seq_lens.data_ptr(), new_lens.data_ptr(), starts.data_ptr(), tokens,
-                  None if slots is None else slots.data_ptr(), None if positions is None else positions.data_ptr(),
-                  tables._missing, _on(index, stream))
+    index, shape = tables.index, tables._lens_shape
+    if not (kv_lens.dtype is _int32 and n_new.dtype is _int32 and new_lens.dtype is _int32 and
+            starts.dtype is _int32 and kv_lens.shape == shape and n_new.shape == shape and new_lens.shape == shape and
+            starts.shape == tables._starts_shape and kv_lens.is_contiguous() and n_new.is_contiguous() and
+            new_lens.is_contiguous() and starts.is_contiguous() and kv_lens.get_device() == index and
+            n_new.get_device() == index and new_lens.get_device() == index and starts.get_device() == index):
+        _refuse_ints(index, kv_lens=(kv_lens, tables.batch), n_new=(n_new, tables.batch),
+                     new_lens=(new_lens, tables.batch), starts=(starts, tables.batch + 1))
+    seen = map_slots = map_positions = tokens = 0
+    if seq_lens is not None:
+        if not (seq_lens.dtype is _int32 and seq_lens.shape == shape and seq_lens.is_contiguous() and
+                seq_lens.get_device() == index):
+            _refuse_ints(index, seq_lens=(seq_lens, tables.batch))
+        seen = seq_lens.data_ptr()
+    if slots is not None:
+        tokens = slots.numel()
+        if not (slots.dtype is _int32 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == index):
+            _refuse_ints(index, slots=(slots, tokens))
+        map_slots = slots.data_ptr()
+    if positions is not None:
+        tokens = tokens if slots is not None else positions.numel()
+        if not (positions.dtype is _int32 and positions.dim() == 1 and positions.numel() == tokens and
+                positions.is_contiguous() and positions.get_device() == index):
+            _refuse_ints(index, positions=(positions, tokens))
+        map_positions = positions.data_ptr()
+    rc = _reserve(_reserve_args(*tables._sizes, tokens, 0, *tables._arrays, kv_lens.data_ptr(), n_new.data_ptr(), seen,
+                                new_lens.data_ptr(), starts.data_ptr(), map_slots, map_positions), _on(index, stream))
     if rc:
         _lib.check(rc)
     return tables
@@ -127,21 +156,27 @@ def paged_append_packed(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Ten
     where the cache has positions.  Any strides with consecutive values;
     pinned host tensors are accepted.
     """
-    index, shape = cache.index, k_new.shape
-    tokens = shape[0] if len(shape) == 3 else -1
-    if tokens < 0 or shape != v_new.shape or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim:
+    index, dtype, shape = cache.index, cache.dtype, k_new.shape
+    if len(shape) != 3 or shape != v_new.shape or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim:
         raise _bad("k_new and v_new must be [tokens, n_kv_heads, head_dim]")
-    k_st, v_st = k_new.stride(), v_new.stride()
-    if k_new.dtype is not cache.dtype or v_new.dtype is not cache.dtype or k_st[2] != 1 or v_st[2] != 1:
+    tokens, k_st, v_st = shape[0], k_new.stride(), v_new.stride()
+    if k_new.dtype is not dtype or v_new.dtype is not dtype or k_st[2] != 1 or v_st[2] != 1:
         raise _bad("k_new and v_new must have the cache's type and rows of consecutive values")
-    for t in (k_new, v_new):
-        if t.get_device() != index and (t.is_cuda or not t.is_pinned()):
-            raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
-    if not _is_ints(slots, index, tokens) or not (positions is None or _is_ints(positions, index, tokens)):
-        raise _bad(f"slots and positions must be contiguous int32 [{tokens}] on {cache.device}")
+    if k_new.get_device() != index or v_new.get_device() != index:
+        for t in (k_new, v_new):
+            if t.get_device() != index and (t.is_cuda or not t.is_pinned()):
+                raise _bad(f"k_new and v_new must live on {cache.device} or in pinned host memory")
+    if not (slots.dtype is _int32 and slots.dim() == 1 and slots.numel() == tokens and slots.is_contiguous() and
+            slots.get_device() == index):
+        _refuse_ints(index, slots=(slots, tokens))
+    where = None
+    if positions is not None:
+        if not (positions.dtype is _int32 and positions.dim() == 1 and positions.numel() == tokens and
+                positions.is_contiguous() and positions.get_device() == index):
+            _refuse_ints(index, positions=(positions, tokens))
+        where = positions.data_ptr()
     rc = _append(cache._ref, tokens, k_new.data_ptr(), v_new.data_ptr(),
-                 _Strides4(k_st[0], k_st[1], v_st[0], v_st[1]), slots.data_ptr(),
-                 None if positions is None else positions.data_ptr(), _cache_stream(cache, stream))
+                 _strides4(k_st[0], k_st[1], v_st[0], v_st[1]), slots.data_ptr(), where, _cache_stream(cache, stream))
     if rc:
         _lib.check(rc)
     return cache
@@ -156,6 +191,7 @@ class RotaryPlan:
         if not turns.is_cuda or turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
             raise _bad("turns must be contiguous int64 [rotary_dim / 2] on a CUDA device")
         self.turns, self.scale, self.rotary_dim, self.index = turns, scale, 2 * turns.numel(), turns.get_device()
+        self._ptr = turns.data_ptr()
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = _lib.ROTARY_PLAIN, factor: float = 1.0,
@@ -186,15 +222,14 @@ def alloc_rotary_plan(rotary_dim: int, base: float = 10000.0, scaling: int = _li
     return RotaryPlan(torch.tensor(signed, dtype=torch.int64, device=device or "cuda"), scale)
 
 
-def _rotary_rows(x: torch.Tensor, out: torch.Tensor, name: str, dtype, index: int, tokens: int, dim: int):
-    shape, st, so = x.shape, x.stride(), out.stride()
-    if len(shape) != 3 or out.shape != shape or shape[0] != tokens or shape[2] != dim:
+def _refuse_rotary(x: torch.Tensor, out: torch.Tensor, name: str, q: torch.Tensor) -> None:
+    if x.dim() != 3 or out.shape != x.shape or x.shape[0] != q.shape[0] or x.shape[2] != q.shape[2]:
         raise _bad(f"{name} and its output must be [tokens, heads, head_dim], of one head_dim and count of tokens")
-    if x.dtype is not dtype or out.dtype is not dtype or x.get_device() != index or out.get_device() != index:
+    if x.dtype is not q.dtype or out.dtype is not q.dtype or x.get_device() != q.get_device() or \
+            out.get_device() != q.get_device():
         raise _bad(f"{name} and its output must have q's type and live on its device")
-    if st[2] != 1 or so[2] != 1:
+    if x.stride(2) != 1 or out.stride(2) != 1:
         raise _bad(f"{name}: the values of a head must be consecutive")
-    return _lib.RotaryRows(x.data_ptr(), out.data_ptr(), st[0], st[1], so[0], so[1], shape[1], 0)
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, plan: RotaryPlan,
@@ -207,20 +242,34 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, pla
     ``interleaved``: pairs are neighbours instead of half the dimension apart.
     ``transpose``: the gradient of the inputs from that of the outputs.
     """
-    index, dtype = q.get_device(), q.dtype
-    if dtype not in _DTYPES or index < 0 or q.dim() != 3:
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    kind = _DTYPES.get(dtype)
+    if kind is None or index < 0 or len(shape) != 3:
         raise _bad("q must be bf16, fp16 or fp32 [tokens, heads, head_dim] on a CUDA device")
-    tokens, _, dim = q.shape
-    if plan.index != index or not _is_ints(positions, index, tokens):
+    tokens, heads, dim = shape
+    if plan.index != index or not (positions.dtype is _int32 and positions.dim() == 1 and
+                                   positions.numel() == tokens and positions.is_contiguous() and
+                                   positions.get_device() == index):
         raise _bad(f"positions must be contiguous int32 [{tokens}], and the plan's frequencies, on cuda:{index}")
     q_out = q if q_out is None else q_out
-    rows = _rotary_rows(q, q_out, "q", dtype, index, tokens, dim)
-    k_rows = None
+    st, so = q.stride(), q_out.stride()
+    if q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != index or st[2] != 1 or so[2] != 1:
+        _refuse_rotary(q, q_out, "q", q)
+    k_in = k_to = k_heads = 0
+    kt = ko = (0, 0)
     if k is not None:
         k_out = k if k_out is None else k_out
-        k_rows = _byref(_rotary_rows(k, k_out, "k", dtype, index, tokens, dim))
-    rc = _rotary(_DTYPES[dtype], tokens, dim, _byref(rows), k_rows, positions.data_ptr(), plan.rotary_dim,
-                 plan.turns.data_ptr(), plan.scale, 1 if interleaved else 0, 1 if transpose else 0,
+        k_shape, kt, ko = k.shape, k.stride(), k_out.stride()
+        if len(k_shape) != 3 or k_out.shape != k_shape or k_shape[0] != tokens or k_shape[2] != dim or \
+                k.dtype is not dtype or k_out.dtype is not dtype or k.get_device() != index or \
+                k_out.get_device() != index or kt[2] != 1 or ko[2] != 1:
+            _refuse_rotary(k, k_out, "k", q)
+        k_in, k_to, k_heads = k.data_ptr(), k_out.data_ptr(), k_shape[1]
+        if k_heads == 0:
+            raise _bad("k has no heads")
+    rc = _rotary(_rotary_args(kind, tokens, dim, plan.rotary_dim, heads, k_heads, 1 if interleaved else 0,
+                              1 if transpose else 0, plan.scale, 0, positions.data_ptr(), plan._ptr, q.data_ptr(),
+                              q_out.data_ptr(), k_in, k_to, st[0], st[1], so[0], so[1], kt[0], kt[1], ko[0], ko[1]),
                  _on(index, stream))
     if rc:
         _lib.check(rc)
@@ -229,7 +278,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, pla
 
 # ------------------------------------------------------------------ attention
 
-def _attn_args(q, k, v, q_starts, k_starts, scale):
+def _inputs(q, k, v, q_starts, k_starts, scale):
+    """The argument structure of an attention call."""
     q_shape, k_shape, dtype, index = q.shape, k.shape, q.dtype, q.get_device()
     if len(q_shape) != 3 or len(k_shape) != 3 or v.shape != k_shape or q_shape[2] != k_shape[2] or \
             k_shape[1] == 0 or q_shape[1] == 0 or q_shape[1] % k_shape[1] != 0:
@@ -245,11 +295,10 @@ def _attn_args(q, k, v, q_starts, k_starts, scale):
     if batch < 1 or not _is_ints(q_starts, index, batch + 1) or \
             not (k_starts is None or _is_ints(k_starts, index, batch + 1)):
         raise _bad(f"q_starts and k_starts must be contiguous int32 [batch + 1] on cuda:{index}")
-    return _lib.PackedAttnArgs(
-        _DTYPES[dtype], batch, k_shape[1], q_shape[1] // k_shape[1], q_shape[2], q_shape[0], k_shape[0],
-        q_shape[2] ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], q_starts.data_ptr(),
-        None if k_starts is None else k_starts.data_ptr())
+    return _attn_args(_DTYPES[dtype], batch, k_shape[1], q_shape[1] // k_shape[1], q_shape[2], q_shape[0], k_shape[0],
+                      q_shape[2] ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], q_starts.data_ptr(),
+                      0 if k_starts is None else k_starts.data_ptr())
 
 
 def _like(x: torch.Tensor, y: torch.Tensor, name: str):
@@ -279,9 +328,9 @@ def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: tor
     gradient needs.  ``scale`` defaults to 1 / sqrt(head_dim).  Rows of no
     sequence are left as they were.
     """
-    args = _attn_args(q, k, v, q_starts, k_starts, scale)
+    args = _inputs(q, k, v, q_starts, k_starts, scale)
     st = _like(out, q, "out")
-    rc = _attn(_byref(args), out.data_ptr(), (ctypes.c_int64 * 2)(st[0], st[1]),
+    rc = _attn(args, out.data_ptr(), _strides2(st[0], st[1]),
                None if lse is None else _sums(lse, q), _on(q.get_device(), stream))
     if rc:
         _lib.check(rc)
@@ -306,13 +355,13 @@ def packed_attn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_st
 
     ``out`` and ``lse`` are the forward call's on the same arguments.
     """
-    args = _attn_args(q, k, v, q_starts, k_starts, scale)
-    strides = _Strides10(*_like(out, q, "out")[:2], *_like(dout, q, "dout")[:2], *_like(dq, q, "dq")[:2],
+    args = _inputs(q, k, v, q_starts, k_starts, scale)
+    strides = _strides10(*_like(out, q, "out")[:2], *_like(dout, q, "dout")[:2], *_like(dq, q, "dq")[:2],
                          *_like(dk, k, "dk")[:2], *_like(dv, v, "dv")[:2])
     index = q.get_device()
     if not workspace.is_contiguous() or workspace.get_device() != index:
         raise _bad(f"workspace must be contiguous on cuda:{index}")
-    rc = _backward(_byref(args), out.data_ptr(), _sums(lse, q), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+    rc = _backward(args, out.data_ptr(), _sums(lse, q), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                    dv.data_ptr(), strides, workspace.data_ptr(), workspace.nbytes, _on(index, stream))
     if rc:
         _lib.check(rc)
