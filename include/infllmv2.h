@@ -637,6 +637,7 @@ int infllmv2_rotary(const infllmv2_rotary_args* args, void* stream);
  *           range or descend sets INFLLMV2_DEVICE_BAD_KV_LEN and counts as empty.
  *   scale   > 0, and finite in fp32 also times log2(e).
  * lse is contiguous fp32 [q_tokens, heads] and may be NULL in the forward call.
+ * Outputs must not overlap inputs or each other.
  */
 typedef struct infllmv2_packed_attn_args {
   int32_t dtype, batch, n_kv_heads, group_size, head_dim, q_tokens, k_tokens;

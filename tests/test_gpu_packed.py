@@ -54,6 +54,13 @@ SHAPES = [
     (64, "fp16", 2, 1, [5, 300], [1300, 301], "heads"),
     (128, "bf16", 1, 4, [50, 300, 7], [20, 0, 300], "own"),        # fewer keys than queries: rows that attend none
     (64, "bf16", 1, 2, [300], [129], "own"),
+    (128, "fp16", 2, 4, [0, 30, 0], [50, 40, 129], "own"),          # keys that no query attends
+    # Few queries against many keys: divided over clusters.
+    (128, "bf16", 2, 16, [12, 12], [4000, 1000], "own"),
+    (64, "fp16", 1, 5, [1, 60, 0], [5000, 3001, 77], "heads"),
+    (128, "fp16", 3, 4, [7], [2000], "own"),
+    (64, "bf16", 1, 32, [2, 9], [6000, 20], "own"),
+    (128, "bf16", 1, 1, [200], [3500], "own"),
 ]
 
 
@@ -88,6 +95,24 @@ def test_attention_of_many_sequences(dev):
     assert _status() == 0
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "fp16")])
+@pytest.mark.parametrize("count", [30, 64])
+def test_units_one_after_another(dev, dim, dtype, count):
+    """Far more tiles than SMs: short and long ones, whole and partly filled, follow each other on one SM."""
+    import trainable_block_sparse_infllm_gb300 as T
+    from packed_helpers import Step, check, plain
+    lens = [1 + (i * 389) % 1000 for i in range(count)]
+    step = Step(dev, dtype, dim, 4, 4, lens, layout="fused", seed=count)
+    want = plain(step)
+    out, lse = step.forward(T)
+    assert _status() == 0
+    check("out", out, want)
+    check("lse", lse, want)
+    for name, grad in zip(("dq", "dk", "dv"), step.backward(T, out, lse)):
+        assert _status() == 0
+        check(name, grad, want)
+
+
 def test_attention_of_4096_sequences_of_one_token(dev):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
@@ -99,6 +124,37 @@ def test_attention_of_4096_sequences_of_one_token(dev):
     z = (step.q[:n].double() * step.k[:n].double()).sum(dim=2) * step.scale
     tol = 2 * 2.0 ** -24 * 67 * step.scale * (step.q[:n].double() * step.k[:n].double()).abs().sum(dim=2) + 2.0 ** -19
     assert ((lse[:n].double() - z).abs() <= tol + 2.0 ** -20 * z.abs()).all()
+    assert _status() == 0
+
+
+def test_gradient_of_4096_short_sequences(dev):
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from packed_helpers import Step
+    step = Step(dev, "fp16", 64, 1, 2, [1, 2] * 2048)
+    out, lse = step.forward(T)
+    dq, dk, dv = step.backward(T, out, lse)
+    n = 3 * 2048
+    # Sequences of one token: P = 1 + d with |d| <= e_p (packed_helpers.py), so |dS| <= (e_p + 2^-23) |dout . v|, and
+    # half the type's smallest step.
+    one = torch.arange(0, n, 3, device=dev)
+    q, k, v, g = (x[one].double() for x in (step.q, step.k, step.v, step.dout))
+    e_p = 4 * 2.0 ** -24 * 67 * step.scale * (q * k).abs().sum(2, keepdim=True) + 2.0 ** -21 + 2.0 ** -23
+    ds = 1.001 * e_p * (g * v).abs().sum(2, keepdim=True) + 2.0 ** -25
+    assert (dq[one].double().abs() <= step.scale * ds * k.abs() + 2.0 ** -25).all()
+    assert (dk[one].double().abs() <= (step.scale * ds * q.abs()).sum(1, keepdim=True) + 2.0 ** -25).all()
+    want = step.dout[one].double().sum(dim=1, keepdim=True)
+    # Two rounded probabilities of 1 (exact), an fp32 sum, and the rounding of the result.
+    assert ((dv[one].double() - want).abs() <= 2.0 ** -11 * 1.001 * want.abs() + 2.0 ** -19 *
+            step.dout[one].double().abs().sum(dim=1, keepdim=True) + 2.0 ** -25).all()
+    last = one + 2                                              # the second token's key: only its own query attends it
+    q, k = step.q[last].double(), step.k[:n].double()
+    z = torch.stack([(q * k[last - 1]).sum(2), (q * k[last]).sum(2)]) * step.scale
+    p = torch.softmax(z, dim=0)[1][..., None]
+    want = (p * step.dout[last].double()).sum(dim=1, keepdim=True)
+    size = (p * step.dout[last].double().abs()).sum(dim=1, keepdim=True)
+    assert ((dv[last].double() - want).abs() <= (2.0 ** -11 + 2.0 ** -15) * size + 2.0 ** -11 * 1.001 * want.abs() +
+            2.0 ** -24).all()
     assert _status() == 0
 
 
@@ -231,17 +287,19 @@ def test_other_stream_and_graph(dev):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
     from packed_helpers import Step, check, plain
-    steps = [Step(dev, "bf16", 128, 2, 4, [130, 70], layout="fused", seed=i) for i in range(2)]
+    shapes = [dict(q_lens=[130, 70], layout="fused"), dict(q_lens=[9, 3], k_lens=[1200, 900])]   # (one over clusters)
+    steps = [Step(dev, "bf16", 128, 2, 4, seed=i, **shapes[i]) for i in range(2)]
     captured = []
     for step in steps:
         out, lse = torch.full_like(step.q, 7.0), torch.full(step.q.shape[:2], 7.0, device=dev)
         grads = [torch.full_like(x, 7.0) for x in (step.q, step.k, step.v)]
         ws, starts = T.alloc_packed_workspace(step.q).fill_(0xff), step.ints(step.q_starts)
+        k_starts = step.ints(step.k_starts) if step.own_keys else None
 
         def call():
-            T.packed_attn(step.q, step.k, step.v, starts, out, lse, scale=step.scale)
+            T.packed_attn(step.q, step.k, step.v, starts, out, lse, k_starts=k_starts, scale=step.scale)
             T.packed_attn_backward(step.q, step.k, step.v, starts, out, lse, step.dout, *grads, workspace=ws,
-                                   scale=step.scale)
+                                   k_starts=k_starts, scale=step.scale)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
@@ -250,10 +308,10 @@ def test_other_stream_and_graph(dev):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             call()
-        captured.append((graph, step, out, lse, grads, ws, starts))     # (a graph holds no tensors)
+        captured.append((graph, step, out, lse, grads, ws, starts, k_starts))     # (a graph holds no tensors)
     for seed in (5, 6):                          # new contents, replayed in both orders
         for i, (graph, step, out, lse, grads, *_) in enumerate(captured):
-            fresh = Step(dev, "bf16", 128, 2, 4, [130, 70], layout="fused", seed=10 * seed + i)
+            fresh = Step(dev, "bf16", 128, 2, 4, seed=10 * seed + i, **shapes[i])
             for name in ("q", "k", "v", "dout"):
                 getattr(step, name).copy_(getattr(fresh, name))
             for t in (out, lse, *grads):

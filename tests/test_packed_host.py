@@ -197,7 +197,7 @@ def _args(L, **kw):
     return L.PackedAttnArgs(**fields)
 
 
-def _forward(L, args, out=FAKE, strides=(1024, 128), lse=FAKE):
+def _forward(L, args, out=FAKE + 65536, strides=(1024, 128), lse=FAKE):
     return L.lib.infllmv2_packed_attn(None if args is None else ctypes.byref(args), out,
                                       None if strides is None else _ints64(*strides), lse, None)
 
@@ -206,7 +206,7 @@ GRAD_STRIDES = (1024, 128) * 3 + (256, 128) * 2
 
 
 def _backward(L, args, strides=GRAD_STRIDES, ws=FAKE, ws_bytes=640, **kw):
-    a = dict(out=FAKE, lse=FAKE, dout=FAKE, dq=FAKE, dk=FAKE, dv=FAKE)
+    a = {name: FAKE + 65536 * i for i, name in enumerate(("out", "lse", "dout", "dq", "dk", "dv"), 1)}
     a.update(kw)
     return L.lib.infllmv2_packed_attn_backward(None if args is None else ctypes.byref(args), a["out"], a["lse"],
                                                a["dout"], a["dq"], a["dk"], a["dv"],
@@ -235,13 +235,17 @@ def test_attention_refuses(L):
                          (dict(k_head=0), bad), (dict(k_token=128), bad), (dict(v_token=1 << 40), no),
                          (dict(v_head=132), no), (dict(k_starts=None, k_tokens=11), bad)):
             assert call(L, _args(L, **kw)) == code, (call.__name__, kw)
-    for kw, code in ((dict(out=None), bad), (dict(out=ODD), no), (dict(strides=None), bad), (dict(strides=(1024, 0)), bad),
+    for kw, code in ((dict(out=None), bad), (dict(out=ODD), no), (dict(out=FAKE), bad), (dict(strides=None), bad), (dict(strides=(1024, 0)), bad),
                      (dict(strides=(1024, 132)), no), (dict(strides=(512, 128)), bad)):
         assert _forward(L, _args(L), **kw) == code, kw
     for name in ("out", "lse", "dout", "dq", "dk", "dv"):
         assert _backward(L, _args(L), **{name: None}) == bad, name
         if name != "lse":
             assert _backward(L, _args(L), **{name: ODD}) == no, name
+    for name in ("dq", "dk", "dv"):
+        for other in (FAKE, FAKE + 65536, FAKE + 2 * 65536, FAKE + 3 * 65536):
+            assert _backward(L, _args(L), **{name: other}) == bad, name
+    assert _backward(L, _args(L), dq=FAKE + 5 * 65536) == bad and _backward(L, _args(L), dv=FAKE + 4 * 65536) == bad
     assert _backward(L, _args(L), strides=None) == bad
     for i in range(5):
         strides = list(GRAD_STRIDES)

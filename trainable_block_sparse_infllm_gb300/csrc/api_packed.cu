@@ -269,6 +269,8 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
     if (rc) return rc;
     if (!out || !out_strides) return fail(INFLLMV2_INVALID_ARGUMENT, "out or out_strides is NULL");
     if (!aligned16(out)) return fail(INFLLMV2_UNSUPPORTED, "out must be 16-byte aligned");
+    if (out == args->q || out == args->k || out == args->v)
+      return fail(INFLLMV2_INVALID_ARGUMENT, "out must be apart from q, k and v");
     PackedRows o = {};
     if ((rc = check_tensor(out_strides, c.s.Tq, static_cast<int64_t>(c.s.Hkv) * c.s.G, c.D, "out", &o))) return rc;
     if ((rc = check_status(c))) return rc;
@@ -304,6 +306,13 @@ int infllmv2_packed_attn_backward(const infllmv2_packed_attn_args* args, const v
       return fail(INFLLMV2_INVALID_ARGUMENT, "out, lse, dout, a gradient or grad_strides is NULL");
     if (!aligned16(out) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
       return fail(INFLLMV2_UNSUPPORTED, "out, dout and the gradients must be 16-byte aligned");
+    const void* read[6] = {args->q, args->k, args->v, out, lse, dout};
+    const void* written[3] = {dq, dk, dv};
+    for (int i = 0; i < 3; ++i) {
+      bool apart = written[i] != written[(i + 1) % 3];
+      for (const void* x : read) apart = apart && x != written[i];
+      if (!apart) return fail(INFLLMV2_INVALID_ARGUMENT, "the gradients must be apart from each other and the inputs");
+    }
     const int64_t heads = static_cast<int64_t>(c.s.Hkv) * c.s.G;
     const size_t need = sizeof(float2) * c.s.Tq * heads;
     if (!workspace || workspace_bytes < need)

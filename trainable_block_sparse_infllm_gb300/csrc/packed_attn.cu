@@ -58,17 +58,20 @@ struct Layout {
   static constexpr int kTile = kD / 64 * 16384;   // 128 rows of kD
   static constexpr int kStages = kRing / kTile;
   static constexpr int kBuffers = kD == 64 ? 3 : 2;   // of scores
+  // V tiles that may be looked through at once, as many as the ring holds: each has barriers of its own, so
+  // that none is two phases ahead of who waits for it.
+  static constexpr int kLooks = (kStages + 1) / 2;
   static constexpr uint32_t kColO = 128 * kBuffers;
   static constexpr int kBars = 2 * kTile + kRing;
   // Barriers: a unit found and done with; Q of each tile full and free; ring full and empty; V tiles
-  // attended in part, before and after they were looked through; of each score buffer S and P; of each
-  // tile P V (three, in turn) and x read; kSplit: all products; of each
-  // score buffer P V once more, for who issues scores.
+  // attended in part, before and after they were looked through; of each tile S (three buffers: three, in
+  // turn); of each score buffer P; of each tile P V (three, in turn) and x read; kSplit: all products; of each
+  // score buffer P V once more, for who issues scores; and all that each issuer issued.
   static constexpr int kUnit = 0, kUnitFree = kUnit + 2, kQFull = kUnitFree + 2, kQFree = kQFull + 2,
                        kFull = kQFree + 2, kEmpty = kFull + kStages, kPartial = kEmpty + kStages,
-                       kChecked = kPartial + kMaxPartial, kSFull = kChecked + kMaxPartial,
-                       kPFull = kSFull + kBuffers, kPvDone = kPFull + kBuffers, kOFree = kPvDone + 6, kAllDone = kOFree + 2, kReused = kAllDone + 1,
-                       kNumBars = kReused + kBuffers;
+                       kChecked = kPartial + kLooks, kSFull = kChecked + kLooks,
+                       kPFull = kSFull + (kBuffers == 3 ? 6 : 2), kPvDone = kPFull + kBuffers, kOFree = kPvDone + 6, kAllDone = kOFree + 2, kReused = kAllDone + 1,
+                       kEnd = kReused + kBuffers, kNumBars = kEnd + 2;
   static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 32 bytes each
   static constexpr int kFlags = kUnits + 2 * 32;   // of each unit [kMaxPartial][4]: rows that were cleared
   static constexpr int kSlot = kFlags + 2 * kMaxPartial * 16;
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int count = 1;
     if (tid == L::kUnitFree || tid == L::kUnitFree + 1) count = 11;   // the warps but the one that finds units
     if ((tid >= L::kPFull && tid < L::kPFull + kBuffers) || (tid >= L::kOFree && tid < L::kOFree + 2)) count = 4;
-    if (tid >= L::kChecked && tid < L::kChecked + kMaxPartial) count = kBuffers == 2 ? 2 : 1;
+    if (tid >= L::kChecked && tid < L::kChecked + L::kLooks) count = kBuffers == 2 ? 2 : 1;
     mbar_init(&bars[tid], count);
     fence_barrier_init();
   }
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             if (looks) {
               mbar_arrive(bar);
-              bar = &bars[L::kPartial + seen % kMaxPartial];
+              bar = &bars[L::kPartial + seen % L::kLooks];
             }
             mbar_arrive_expect_tx(bar, kTile);
             for (int c = 0; c < kD / 64; ++c)
@@ -259,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // newest phase here.)
       for (int i = max(0, issued - kStages); i < issued; ++i)
         mbar_wait(&bars[L::kFull + i % kStages], (i / kStages) & 1, s.status);
-      for (int i = max(0, seen - kMaxPartial); i < seen; ++i)
-        mbar_wait(&bars[L::kPartial + i % kMaxPartial], (i / kMaxPartial) & 1, s.status);
+      for (int i = max(0, seen - L::kLooks); i < seen; ++i)
+        mbar_wait(&bars[L::kPartial + i % L::kLooks], (i / L::kLooks) & 1, s.status);
       for (int x = 0; x < 2; ++x)
         if (q_uses[x] > 0) mbar_wait(&bars[L::kQFull + x], (q_uses[x] - 1) & 1, s.status);
     } else if (warp > kCheckWarp || (kBuffers == 2 && warp == kCheckWarp)) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int copies = 0, seen = 0;
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         for (int j = u.looked; j < u.n && ok; ++j, ++seen) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kPartial + seen % kMaxPartial], (seen / kMaxPartial) & 1,
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kPartial + seen % L::kLooks], (seen / L::kLooks) & 1,
                                                  s.status));
           if (!ok) break;
           for (int half = 0; half < 2; ++half)   // (two warps share a tile, or one has all of it)
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               packed::check_rows<kD, kFp16>(ring + (copies + 2 * j + 1) % kStages * kTile, half,
                                             u.seq.n_k - (u.j0 + j) * 128,
                                             flags + ((k & 1) * kMaxPartial + j - u.looked) * 4);
-          if (lane == 0) mbar_arrive(&bars[L::kChecked + seen % kMaxPartial]);
+          if (lane == 0) mbar_arrive(&bars[L::kChecked + seen % L::kLooks]);
         }
         copies += 2 * u.n;
         unit_done(k);
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.buffer_phase ^= 1;
         }
       };
-      // Of each half: its units and its P V barrier's turn; and V tiles looked through.  (After a wait that
+      // Of each half: its units and the turn of its barriers (of P V, or of S); and V tiles looked through.  (After a wait that
       // gave up nothing waits any more; what is issued then stays within this CTA's memory.)
       int used[2] = {0, 0}, turn[2] = {0, 0}, look = 0, look_phase = 0, jobs = 0;
       auto next_turn = [&](int& t) { t = t == 2 ? 0 : t + 1; };
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
         wait(L::kChecked + look, look_phase);
-        if (++look == kMaxPartial) {
+        if (++look == L::kLooks) {
           look = 0;
           look_phase ^= 1;
         }
@@ -406,12 +409,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issuer) {
               packed::mma_rows<kD>(tmem + ss.buffer * 128, q_desc + (x ? kTile >> 4 : 0),
                                    k_desc + static_cast<uint64_t>(ss.stage * (kTile >> 4)), kIdS);
-              tc::commit(&bars[L::kSFull + ss.buffer]);
+              tc::commit(&bars[L::kSFull + (x ? 3 + turn[1] : turn[0])]);
               if (changes) tc::commit(&bars[L::kEmpty + ss.stage]);
               if (q_free) tc::commit(&bars[L::kQFree + x]);
             }
             __syncwarp();
             next_buffer(ss);
+            if (x) {
+              next_turn(turn[1]);
+            } else {
+              next_turn(turn[0]);
+            }
             if (changes) next_tile(ss);
           }
           bool opens = true;   // a tile whose V has not been waited for
@@ -444,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         used[1] += n1 > 0;
         unit_done(k);
       }
+      // Nothing that was issued outlives the CTA, also after a wait that gave up.
+      packed::products_end(&bars[L::kEnd + (warp == kMmaWarp ? 0 : 1)], issuer, s.status);
     }
     __syncwarp();
   } else {
@@ -478,8 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int job = kBuffers == 2 ? 2 * (done + j) + x : jobs + (j < both ? 2 * j + x : both + j);
         const int buffer = job % kBuffers;
         const uint32_t s_addr = lane_addr + buffer * 128;
+        // S of the half's tile number done + j.  (Not by buffer: a half without tiles in a unit is a unit ahead,
+        // and a buffer's barrier may then be any number of phases behind.)
+        const int full = kBuffers == 2 ? L::kSFull + x : L::kSFull + 3 * x + (done + j) % 3;
+        const int phase = kBuffers == 2 ? done + j : (done + j) / 3;
         // (A warp whose wait gave up goes on without waiting; the status word has the error.)
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kSFull + buffer], (job / kBuffers) & 1, s.status));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[full], phase & 1, s.status));
         tc::fence_after_sync();
         uint32_t z[128];
 #pragma unroll
@@ -626,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // out = sum 2^(m - M) x / sum 2^(m - M) l ----
     __syncwarp();
     cluster_sync();
-    if (any) {   // (the softmax warps: the others have given registers away)
+    if (warp < 8 && packed::all_agree(any)) {   // (the softmax warps: the others have given registers away)
       const int row0 = rank * 256 / ctas, share = (rank + 1) * 256 / ctas - row0;
       for (int e = tid; e < share; e += 256) {   // a row: its weights, over l, and log sum
         const int row = row0 + e, rr = row & 127;

@@ -54,75 +54,15 @@ __device__ __forceinline__ Sequence sequence(const PackedAttnShape& s, int b, bo
 
 // Tiles of `step` tokens cut from the sequences' queries (of_keys: keys).  A
 // tile's level is its index among the queries' tiles, or that of the keys' tiles
-// counted from the last: either way causal work grows with it.  The order of all
-// tiles goes down the levels, sequence by sequence within one, so that the CTAs
-// that start last have the least to do.  Finds the sequence and level of tile `i`
-// of that order, the same for all threads of the CTA; false past the last tile.
-// `scratch`: 4 ints of shared memory.
+// counted from the last: either way causal work grows with it.
 __device__ __forceinline__ int tile_count(const PackedAttnShape& s, int b, int step, bool of_keys, bool* bad) {
   const Sequence q = sequence(s, b, bad);
   return ((of_keys ? q.n_k : q.n_q) + step - 1) / step;
 }
 
-__device__ __forceinline__ bool find_tile(const PackedAttnShape& s, int i, int step, bool of_keys, int* scratch,
-                                          int* b_out, int* level_out) {
-  const int lane = threadIdx.x & 31;
-  bool bad = false;
-  if (s.B == 1) {
-    const int n = tile_count(s, 0, step, of_keys, &bad);
-    if (bad && i == 0 && threadIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
-    *b_out = 0;
-    *level_out = n - 1 - i;
-    return i < n;
-  }
-  // One warp: lane l holds the counts of sequences l, l + 32, ... (the first in a
-  // register).  at_least(t) = tiles with index >= t.
-  if (threadIdx.x < 32) {
-    const int first = lane < s.B ? tile_count(s, lane, step, of_keys, &bad) : 0;
-    auto at_least = [&](int t) {
-      unsigned sum = max(first - t, 0);
-      for (int b = lane + 32; b < s.B; b += 32) sum += max(tile_count(s, b, step, of_keys, &bad) - t, 0);
-      return static_cast<int>(__reduce_add_sync(0xffffffffu, sum));
-    };
-    int most = first;
-    for (int b = lane + 32; b < s.B; b += 32) most = max(most, tile_count(s, b, step, of_keys, &bad));
-    most = __reduce_max_sync(0xffffffffu, most);
-    int lo = 0, hi = most;   // at_least(lo) > i >= at_least(hi), if there is such a tile
-    const bool found = at_least(0) > i;
-    while (found && hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (at_least(mid) > i) lo = mid; else hi = mid;
-    }
-    int b = 0;
-    if (found) {
-      int rank = i - at_least(lo + 1);   // among the sequences that have a tile of level `lo`
-      for (int base = 0; base < s.B; base += 32) {
-        const bool has = base + lane < s.B &&
-                         (base == 0 ? first : tile_count(s, base + lane, step, of_keys, &bad)) > lo;
-        const unsigned mask = __ballot_sync(0xffffffffu, has);
-        const int n = __popc(mask);
-        if (rank < n) {
-          b = base + static_cast<int>(__fns(mask, 0, rank + 1));
-          break;
-        }
-        rank -= n;
-      }
-    }
-    if (bad && i == 0) atomicOr(s.status, kStatusBadKvLen);
-    if (lane == 0) {
-      scratch[0] = found;
-      scratch[1] = b;
-      scratch[2] = lo;
-    }
-  }
-  __syncthreads();
-  *b_out = scratch[1];
-  *level_out = scratch[2];
-  return scratch[0] != 0;
-}
-
-// The same order for one warp that asks for one tile after another (i rising).  Up
-// to 32 sequences: by level, as above, from counts kept in registers.  More: the
+// The order of all tiles, for one warp that asks for one after another (i rising).  Up
+// to 32 sequences: down the levels, sequence by sequence within one, so that what
+// starts last has the least to do; the counts stay in registers.  More: the
 // sequences in turn, each from its last tile down, walked once (there is nothing to
 // balance among so many, and a search by level would read them all each time).
 struct Walker {
@@ -178,6 +118,74 @@ struct Walker {
     return true;
   }
 };
+
+// Tile `i` of the same order, once, for a whole CTA; false past the last one.  (More
+// than 32 sequences: every thread sums a run of them.)  `scratch`: 40 ints of shared
+// memory.  The CTA that has tile 0 flags bad starts.
+__device__ __forceinline__ bool find_tile(const PackedAttnShape& s, int i, int step, bool of_keys, int* scratch, int* b,
+                                          int* level) {
+  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x / 32;
+  bool bad = false;
+  int* found = scratch + 32;   // whether, sequence, level
+  if (tid == 0) found[0] = 0;
+  if (s.B <= 32) {
+    __syncthreads();
+    if (tid < 32) {
+      Walker w;
+      w.start(s, step, of_keys, &bad);
+      int at = 0, its = 0;
+      const bool ok = w.find(s, i, step, of_keys, &at, &its, &bad);
+      if (lane == 0) {
+        found[0] = ok;
+        found[1] = at;
+        found[2] = its;
+      }
+    }
+  } else {
+    const int per = (s.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    const int b0 = min(tid * per, s.B), b1 = min(b0 + per, s.B);
+    int mine = 0;
+    for (int x = b0; x < b1; ++x) mine += tile_count(s, x, step, of_keys, &bad);
+    const int incl = warp_inclusive_scan(mine);
+    if (lane == 31) scratch[tid >> 5] = incl;
+    __syncthreads();
+    int first = incl - mine;   // the tiles before this thread's
+    for (int w = 0; w < warps; ++w) first += w < (tid >> 5) ? scratch[w] : 0;
+    if (i >= first && i < first + mine) {
+      for (int x = b0; x < b1; ++x) {
+        const int n = tile_count(s, x, step, of_keys, &bad);
+        if (i < first + n) {
+          found[0] = 1;
+          found[1] = x;
+          found[2] = n - 1 - (i - first);
+          break;
+        }
+        first += n;
+      }
+    }
+  }
+  if (bad && i == 0) atomicOr(s.status, kStatusBadKvLen);
+  __syncthreads();
+  *b = found[1];
+  *level = found[2];
+  return found[0] != 0;
+}
+
+// Whether all of the 256 threads of the first eight warps say so (barrier 1).  They go
+// on to the next unit together or not at all: a warp whose wait gave up would leave
+// the others at a barrier.
+__device__ __forceinline__ bool all_agree(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(mine ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -283,6 +291,13 @@ __device__ __forceinline__ bool elect_one() {
 
 // The warp's index, uniform for the compiler too.
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
+// A converged warp that issued products: waits until all of them are done.
+__device__ __forceinline__ void products_end(uint64_t* bar, bool issuer, uint32_t* status) {
+  if (issuer) tc::commit(bar);
+  __syncwarp();
+  mbar_wait(bar, 0, status);
+}
 
 // One product of a 128-row A by D-step K extent: both operands K-major tiles of
 // [rows][kD] in boxes of 64 columns x 128 rows.

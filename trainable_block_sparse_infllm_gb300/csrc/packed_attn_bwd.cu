@@ -59,9 +59,10 @@ struct DqLayout {
   static constexpr int kK = kTile, kV = kK + kKs * kTile;        // behind dout
   static constexpr int kBars = kV + kVs * kTile;
   static constexpr int kUnit = 0, kUnitFree = 2, kDoFull = 4, kDoFree = 5, kKFull = 6, kKEmpty = kKFull + kKs,
-                       kVFull = kKEmpty + kKs, kVEmpty = kVFull + kVs, kTail = kVEmpty + kVs, kCleared = kTail + 1,
-                       kPair = kCleared + 1, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
-                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kNumBars = kOutRead + 1;
+                       kVFull = kKEmpty + kKs, kVEmpty = kVFull + kVs, kTail = kVEmpty + kVs, kCleared = kTail + 2,
+                       kPair = kCleared + 2, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
+                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kEnd = kOutRead + 1,
+                       kNumBars = kEnd + 2;
   static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 16 bytes each
   static constexpr int kSlot = kUnits + 32;
   static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false;
       walker.start(s, tile_tokens, false, &bad);
       const int stride = static_cast<int>(gridDim.x);
-      int k_copies = 0, v_copies = 0, tails = 0, uses = 0;
+      int k_copies = 0, v_copies = 0, tails[2] = {0, 0}, uses = 0;   // (tails: of units of each parity)
       // The next stage of the K ring, with a copy of `bytes` announced on `bar` (null: the stage's own).
       auto k_stage = [&](uint32_t bytes, uint64_t* bar) {
         const int st = k_copies % kKs;
@@ -217,15 +218,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < u.steps && ok; ++j) {
           const int row = u.seq.k0 + (j < u.back ? j : j - u.back) * 128;
-          // The tile of K that is to be cleared behind the sequence lands on a barrier of its own.
+          // The tile of K that is to be cleared behind the sequence lands on a barrier of its own (of two in
+          // turn: the unit after next waits for this one's end).
           const bool tail = u.clears && j == u.steps - 1;
-          const int st = k_stage(kTile, tail ? &bars[L::kTail] : nullptr);
+          uint64_t* own = tail ? &bars[L::kTail + (k & 1)] : nullptr;
+          const int st = k_stage(kTile, own);
           if (!ok) break;
           if (lane == 0)
             for (int c = 0; c < kD / 64; ++c)
               packed::tma_load_3d(smem_u32(smem + L::kK + st * kTile + c * 16384), &maps.k, c * 64, row, u.h,
-                                  tail ? &bars[L::kTail] : &bars[L::kKFull + st]);
-          tails += tail;
+                                  own ? own : &bars[L::kKFull + st]);
+          tails[0] += tail && !(k & 1);
+          tails[1] += tail && (k & 1);
           if (j == 0) {
             if (uses > 0) wait(L::kDoFree, uses - 1);
             if (!ok) break;
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&bars[L::kKFull + i % kKs], (i / kKs) & 1, s.status);
       for (int i = max(0, v_copies - kVs); i < v_copies; ++i)
         mbar_wait(&bars[L::kVFull + i % kVs], (i / kVs) & 1, s.status);
-      if (tails > 0) mbar_wait(&bars[L::kTail], (tails - 1) & 1, s.status);
+      for (int i = 0; i < 2; ++i)
+        if (tails[i] > 0) mbar_wait(&bars[L::kTail + i], (tails[i] - 1) & 1, s.status);
       if (uses > 0) mbar_wait(&bars[L::kDoFull], (uses - 1) & 1, s.status);
     } else if (warp == kPairWarp) {
       // ----------------------- S of a step and dout . v of the one before it
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = packed::desc_rows(smem_u32(smem + L::kV));
       const bool issuer = packed::elect_one();
       Place pk = {0, 0}, pv = {0, 0};
-      int pairs = 0, tails = 0, uses = 0, outs = 0;
+      int pairs = 0, even = 0, odd = 0, uses = 0, outs = 0;   // (tails of units of each parity)
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
         const bool exact = uniform(u.exact);
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; steps > 0 && t <= steps; ++t) {
           if (t < steps) {
             if (t == tail) {
-              wait(L::kTail, tails++);
+              wait(L::kTail + (k & 1), k & 1 ? odd++ : even++);
             } else {
               wait(L::kKFull + pk.stage, pk.phase);
             }
@@ -333,19 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         unit_done(k);
       }
+      packed::products_end(&bars[L::kEnd], issuer, s.status);   // (nothing outlives the CTA)
     } else if (warp == kSumWarp) {
       // ---------------------------------------------------------- dq += dS K
       constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
       const uint64_t k_desc = packed::desc_cols(smem_u32(smem + L::kK));
       const bool issuer = packed::elect_one();
       Place pk = {0, 0};
-      int tails = 0, used = 0, made = 0;
+      int even = 0, odd = 0, used = 0, made = 0;
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
         if (steps > 0) next(pk, kKs);   // Q's stage
         for (int j = 0; j < steps; ++j) {
           if (j >= back) {
-            if (j == tail) wait(L::kCleared, tails++);   // (dS says that the other tiles are there)
+            if (j == tail) wait(L::kCleared + (k & 1), k & 1 ? odd++ : even++);   // (dS says that the other tiles are there)
             if (j == back && used++ > 0) wait(L::kAccFree, used - 2);   // the last unit's dq has been read
             wait(L::kDsFull, made++);
             if (issuer) {
@@ -360,17 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         unit_done(k);
       }
+      packed::products_end(&bars[L::kEnd + 1], issuer, s.status);
     } else {
       // ----------------------- K rows behind the sequence: they meet dS = 0
       Place pk = {0, 0};
-      int tails = 0;
+      int even = 0, odd = 0;
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         if (u.steps > 0) next(pk, kKs);   // Q's stage
         for (int j = 0; j < u.steps; ++j) {
           if (u.clears && j == u.steps - 1) {
-            wait(L::kTail, tails++);
+            wait(L::kTail + (k & 1), k & 1 ? odd++ : even++);
             packed::clear_rows<kD>(smem + L::kK + pk.stage * kTile, u.seq.n_k - (u.n - 1) * 128);
-            if (lane == 0) mbar_arrive(&bars[L::kCleared]);
+            if (lane == 0) mbar_arrive(&bars[L::kCleared + (k & 1)]);
           }
           next(pk, kKs);
         }
@@ -397,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int pairs = 0, summed = 0, uses = 0;   // in all: pairs of scores read, dS written, units with keys
     Place pk = {0, 0}, pv = {0, 0};
-    for (int k = 0; next_unit(k, &ok, &u); ++k) {
+    for (int k = 0; packed::all_agree(next_unit(k, &ok, &u)); ++k) {
       const int token = u.t0 + r / s.G;
       const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 : 0;
@@ -606,9 +613,9 @@ struct DkvLayout {
   static constexpr int kKvFull = 0, kFull = 1, kEmpty = kFull + kStages, kRowsFull = kEmpty + kStages,
                        kRowsFree = kRowsFull + 2, kCleared = kRowsFree + 2, kSFull = kCleared + 2,
                        kPFull = kSFull + 1, kDpFull = kPFull + 1, kDsFull = kDpFull + 1, kDone = kDsFull + 1,
-                       kNumBars = kDone + 1;
+                       kEnd = kDone + 1, kNumBars = kEnd + 1;
   static constexpr int kScratch = kBars + 8 * kNumBars;
-  static constexpr int kBytes = kScratch + 32;   // (no slack: where the base is not aligned the kernel says so)
+  static constexpr int kBytes = kScratch + 160 + 16;   // (no slack: where the base is not aligned the kernel says so)
 };
 // Tensor memory: S^T with P^T over it, (v . dout)^T with dS^T over it, dv, dk.  A
 // warpgroup's 16-bit values lie over its own 64 columns' first 32.
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int* scratch = reinterpret_cast<int*>(smem + L::kScratch);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 40);
   uint8_t* ring = smem + L::kRing;
   float* rows = reinterpret_cast<float*>(smem + L::kRows);
   float4* parts = reinterpret_cast<float4*>(ring);   // at the end: this CTA's dv and dk, 2 x 128 rows of kD
@@ -803,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 < n) inner(i + 1);
       }
       if (ok && issuer) tc::commit(&bars[L::kDone]);
+      packed::products_end(&bars[L::kEnd], issuer, s.status);
     }
     __syncwarp();
   } else {
