@@ -46,11 +46,10 @@ constexpr int kExactTiles = 8;
 // ------------------------------------------------------------------- dq ----
 //
 // A CTA takes one tile of rows after another.  For step j (a tile of keys) the tensor
-// cores form S and dout . v, the threads P and dS, the tensor cores add dS K.  The
-// threads work on two steps at once: dS of step j - 1, which is multiplications, and P
-// of step j, which is exponentials, in one pass over the registers.  So S of step j
-// and dout . v of step j - 1 are issued together, and the next pair as soon as they
-// have been read, while the threads still compute.
+// cores form S and dout . v, the threads P and dS, the tensor cores add dS K.  Both
+// scores go into registers at once and are replaced while the threads compute: S and
+// dout . v of step j + 1 run beside P and dS of step j, whose exponentials and
+// products overlap in turn.
 
 template <int kD>
 struct DqLayout {
@@ -70,8 +69,7 @@ struct DqLayout {
 };
 // Tensor memory: S, dout . v, dS, Q (16 bits: the A operand of S), dq.  Q comes through
 // the K ring, as the element before K_0, and makes room there: a tile of K is read
-// until its dS K is done, almost two steps after its S, and with three stages the
-// next K came too late.
+// until its dS K is done, more than a step after its S.
 constexpr uint32_t kDqS = 0, kDqDp = 128, kDqDs = 256, kDqQ = 320, kDqAcc = 384;
 
 struct DqUnit {
@@ -275,32 +273,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tails[i] > 0) mbar_wait(&bars[L::kTail + i], (tails[i] - 1) & 1, s.status);
       if (uses > 0) mbar_wait(&bars[L::kDoFull], (uses - 1) & 1, s.status);
     } else if (warp == kPairWarp) {
-      // ----------------------- S of a step and dout . v of the one before it
+      // ------------------------------------------------- S and dout . v of a step
       constexpr uint32_t kIdS = packed::idesc<kFp16>(128, 128, 0, 0);
       const uint64_t do_desc = packed::desc_rows(smem_u32(smem));
       const uint64_t k_desc = packed::desc_rows(smem_u32(smem + L::kK));
       const uint64_t v_desc = packed::desc_rows(smem_u32(smem + L::kV));
       const bool issuer = packed::elect_one();
       Place pk = {0, 0}, pv = {0, 0};
-      int pairs = 0, even = 0, odd = 0, uses = 0, outs = 0;   // (tails of units of each parity)
+      int pairs = 0, even = 0, odd = 0, ins = 0, uses = 0, outs = 0;   // (tails of units of each parity)
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
         const bool exact = uniform(u.exact);
         if (steps > 0) {
-          wait(L::kQIn, uses);
+          wait(L::kQIn, ins++);
           if (issuer) mbar_arrive(&bars[L::kKEmpty + pk.stage]);   // Q's stage has been read
           __syncwarp();
           next(pk, kKs);
         }
-        for (int t = 0; steps > 0 && t <= steps; ++t) {
-          if (t < steps) {
-            if (t == tail) {
-              wait(L::kTail + (k & 1), k & 1 ? odd++ : even++);
-            } else {
-              wait(L::kKFull + pk.stage, pk.phase);
-            }
+        for (int t = 0; t < steps; ++t) {
+          if (t == tail) {
+            wait(L::kTail + (k & 1), k & 1 ? odd++ : even++);
+          } else {
+            wait(L::kKFull + pk.stage, pk.phase);
           }
-          if (t == 1) {
+          if (t > 0) wait(L::kVFull + pv.stage, pv.phase);
+          if (pairs > 0) wait(L::kFree, pairs - 1);   // both have been read
+          ++pairs;
+          if (issuer) {
+            packed::mma_rows_ts<kD>(tmem + kDqS, tmem + kDqQ,
+                                    k_desc + static_cast<uint64_t>(pk.stage * (kTile >> 4)), kIdS);
+            if (t < back) tc::commit(&bars[L::kKEmpty + pk.stage]);   // (otherwise dS K is its last reader)
+          }
+          __syncwarp();
+          next(pk, kKs);
+          if (t == 0) {
             wait(L::kDoFull, uses++);
             if (!exact) {   // out's stage: read by the threads before their first pair
               wait(L::kOutRead, outs++);
@@ -308,33 +314,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               next(pv, kVs);
             }
-          }
-          if (t > 0) wait(L::kVFull + pv.stage, pv.phase);
-          if (pairs > 0) wait(L::kFree, pairs - 1);   // both have been read
-          ++pairs;
-          if (t > 0) {
-            if (issuer) {
-              packed::mma_rows<kD>(tmem + kDqDp, do_desc, v_desc + static_cast<uint64_t>(pv.stage * (kTile >> 4)),
-                                   kIdS);
-              tc::commit(&bars[L::kVEmpty + pv.stage]);
-            }
-            __syncwarp();
-            next(pv, kVs);
-          }
-          if (t < steps) {
-            if (issuer) {
-              packed::mma_rows_ts<kD>(tmem + kDqS, tmem + kDqQ,
-                                      k_desc + static_cast<uint64_t>(pk.stage * (kTile >> 4)), kIdS);
-              if (t < back) tc::commit(&bars[L::kKEmpty + pk.stage]);   // (otherwise dS K is its last reader)
-            }
-            __syncwarp();
-            next(pk, kKs);
+            wait(L::kVFull + pv.stage, pv.phase);
           }
           if (issuer) {
+            packed::mma_rows<kD>(tmem + kDqDp, do_desc, v_desc + static_cast<uint64_t>(pv.stage * (kTile >> 4)), kIdS);
             tc::commit(&bars[L::kPair]);
-            if (t == steps) tc::commit(&bars[L::kDoFree]);
+            tc::commit(&bars[L::kVEmpty + pv.stage]);
+            if (t == steps - 1) tc::commit(&bars[L::kDoFree]);
           }
           __syncwarp();
+          next(pv, kVs);
         }
         unit_done(k);
       }
@@ -461,69 +450,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t down = packed::pair(-lse2, -lse2);
       // Columns of tile j that the row attends, of this half's 64; 64 where no row of the warp needs a mask.
       auto attended = [&](int j) { return j >= whole ? limit - j * 128 - 64 * half : 64; };
-      uint64_t p[32], rest = 0ull;   // P of a step, two to a register pair; the sum of dS
-      auto read_done = [&] {
+      uint64_t rest = 0ull;   // the sum of dS
+      uint32_t z[64], dp[64];
+      // P and dout . v of the next step, 64 columns each, of which the tensor cores then form the next.
+      auto probs = [&](int j) {
+        wait(L::kPair, pairs++);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tc::ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
+          tc::ld32(dp_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&dp[32 * c]));
+        }
+        tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kFree]);
-      };
-      auto probs = [&](uint32_t (&z)[32], int c, int keep) {   // P of 32 columns
-        if (keep < 64) {
+        const int keep = attended(j);
+        if (keep < 64) {   // (a hidden value may be infinite)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = 32 * c + i < keep ? z[i] : 0xff800000u;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 e = packed::unpair(packed::fma2(
-              packed::pair(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), scale2, down));
-          p[16 * c + i] = packed::pair(fast_exp2(e.x), fast_exp2(e.y));
+          for (int i = 0; i < 64; ++i) {
+            z[i] = i < keep ? z[i] : 0xff800000u;
+            dp[i] = i < keep ? dp[i] : 0u;
+          }
         }
       };
-      auto visible = [&](uint32_t (&dp)[32], int c, int keep) {   // (a hidden value may be infinite)
-        if (keep < 64) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) dp[i] = 32 * c + i < keep ? dp[i] : 0u;
-        }
+      auto prob2 = [&](int i) {   // P of columns 2 i and 2 i + 1
+        const float2 e = packed::unpair(
+            packed::fma2(packed::pair(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), scale2, down));
+        return packed::pair(fast_exp2(e.x), fast_exp2(e.y));
       };
-      auto sum_d = [&](int keep) {   // D += sum P (dout . v)
+      auto value2 = [&](int i) { return packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])); };
+      auto sum_d = [&] {   // D += sum P (dout . v)
         uint64_t d = 0ull;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t dp[32];
-          tc::ld32(dp_addr + 32 * c, dp);
-          tc::wait_ld();
-          visible(dp, c, keep);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            d = packed::fma2(p[16 * c + i], packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), d);
-        }
+        for (int i = 0; i < 32; ++i) d = packed::fma2(prob2(i), value2(i), d);
         const float2 halves = packed::unpair(d);
         D += halves.x + halves.y;
       };
-      // One pair: dS of the step before from its P, and (kMore) P of this step.
-      auto body = [&](auto more, int was, int here) {
-        constexpr bool kMore = decltype(more)::value;
-        const int keep_was = attended(was), keep = kMore ? attended(here) : 64;
+      for (int t = 0; t < u.back; ++t) {   // the first walk, where there are two
+        probs(t);
+        sum_d();
+      }
+      if (u.back > 0) D = both(D);
+      for (int j = 0; j < u.n; ++j) {
+        probs(j);
+        if (u.n == 1) {   // the only tile: D and dS from the same registers
+          sum_d();
+          D = both(D);
+        }
         const uint64_t minus_d = packed::pair(-D, -D);
         uint32_t ds[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t z[32], dp[32];
-          tc::ld32(dp_addr + 32 * c, dp);
-          if (kMore) tc::ld32(s_addr + 32 * c, z);
-          tc::wait_ld();
-          if (c == 1) read_done();
-          visible(dp, c, keep_was);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t v = packed::mul2(
-                p[16 * c + i],
-                packed::add2(packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), minus_d));
-            rest = packed::add2(rest, v);
-            const float2 w = packed::unpair(v);
-            ds[16 * c + i] = packed::pack2<kFp16>(w.x, w.y);
-          }
-          if (kMore) probs(z, c, keep);
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t v = packed::mul2(prob2(i), packed::add2(value2(i), minus_d));
+          rest = packed::add2(rest, v);
+          const float2 w = packed::unpair(v);
+          ds[i] = packed::pack2<kFp16>(w.x, w.y);
         }
         if (summed > 0) wait(L::kDqDone, summed - 1);   // the last dS has been read
         ++summed;
@@ -532,32 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
-      };
-      if (u.steps > 0) {
-        // The first walk, where there are two: P of step t, D of step t - 1.
-        for (int t = 0; t <= u.back; ++t) {
-          wait(L::kPair, pairs++);
-          if (t > 0) sum_d(attended(t - 1));
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t z[32];
-            tc::ld32(s_addr + 32 * c, z);
-            tc::wait_ld();
-            if (c == 1) read_done();
-            probs(z, c, attended(t < u.back ? t : 0));
-          }
-        }
-        if (u.back > 0) D = both(D);
-        for (int j = 1; j < u.n; ++j) {
-          wait(L::kPair, pairs++);
-          body(std::true_type(), j - 1, j);
-        }
-        wait(L::kPair, pairs++);
-        if (u.n == 1) {   // the only tile: D and dS from the same registers
-          sum_d(attended(0));
-          D = both(D);
-        }
-        body(std::false_type(), u.n - 1, 0);
       }
       // sum P (dout . v - D) is what D lacks.
       const float2 halves = packed::unpair(rest);
@@ -932,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();
     if (warp < 8) {   // (the others have given registers away)
-      const int share = 2 * 128 / ctas;   // rows of dv, then of dk
+      const int row0 = rank * 256 / ctas, share = (rank + 1) * 256 / ctas - row0;   // rows of dv, then of dk
       for (int e = tid; e < share * (kD / 4); e += 256) {
-        const int row = rank * share + e / (kD / 4), c4 = e % (kD / 4);
+        const int row = row0 + e / (kD / 4), c4 = e % (kD / 4);
         const int which = row >> 7, key = key0 + (row & 127);
         if (key >= seq.n_k) continue;
         const float4* mine = parts + packed::swizzled<kD>(row, c4);
