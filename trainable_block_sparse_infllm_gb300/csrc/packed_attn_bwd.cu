@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kPairWarp = 8, kTmaWarp = 9, kSumWarp = 10;   // dq
-constexpr int kMmaWarp = 8, kRowsWarp = 10;                 // dk and dv (and kTmaWarp)
+constexpr int kMmaWarp = 8, kRowsWarp = 10, kKvSumWarp = 11;   // dk and dv (and kTmaWarp)
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 of what P is multiplied by on its way to dv.  A probability of a long row is
 // among fp16's subnormal numbers, where it would lose bits.
@@ -557,6 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // -------------------------------------------------------------- dk and dv ----
+//
+// A CTA (or a cluster, each CTA every ctas-th tile of rows) takes one tile of keys.
+// D = 128: two scores and two accumulators fill tensor memory, so P^T lies over S^T
+// and dS^T over (v . dout)^T, and the products go round: dv += P^T dout, the next S^T,
+// dk += dS^T Q, the next (v . dout)^T, each pair beside the threads' other half step.
+// D = 64 leaves room for P^T and dS^T of their own: both scores go into registers at
+// once and the next ones are formed while the threads compute, as for dq.
 
 template <int kD>
 struct DkvLayout {
@@ -568,13 +575,16 @@ struct DkvLayout {
   static constexpr int kKvFull = 0, kFull = 1, kEmpty = kFull + kStages, kRowsFull = kEmpty + kStages,
                        kRowsFree = kRowsFull + 2, kCleared = kRowsFree + 2, kSFull = kCleared + 2,
                        kPFull = kSFull + 1, kDpFull = kPFull + 1, kDsFull = kDpFull + 1, kDone = kDsFull + 1,
-                       kEnd = kDone + 1, kNumBars = kEnd + 1;
+                       kUsed = kDone + 1, kEnd = kUsed + 1, kNumBars = kEnd + 2;
   static constexpr int kScratch = kBars + 8 * kNumBars;
   static constexpr int kBytes = kScratch + 160 + 16;   // (no slack: where the base is not aligned the kernel says so)
 };
-// Tensor memory: S^T with P^T over it, (v . dout)^T with dS^T over it, dv, dk.  A
+// Tensor memory: S^T, (v . dout)^T, dv, dk and (D = 64) P^T and dS^T.  Over the scores a
 // warpgroup's 16-bit values lie over its own 64 columns' first 32.
-constexpr uint32_t kKvS = 0, kKvDp = 128, kKvDv = 256, kKvDk = 384;
+constexpr uint32_t kKvS = 0, kKvDp = 128, kKvDv = 256;
+template <int kD>
+constexpr uint32_t kKvDk = kKvDv + kD;
+constexpr uint32_t kKvP = 384, kKvDs = 448;
 
 template <int kD, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -582,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const int ctas) {
   using L = DkvLayout<kD>;
   constexpr int kTile = L::kTile, kStages = L::kStages;
+  constexpr bool kOwn = kD == 64;   // P^T and dS^T have columns of their own
   constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off again: from dout . v - D for dS, from dv
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) % 1024 != 0) {   // the whole grid: shared memory starts on 1024 bytes or it does not
@@ -617,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool clears = n > 0 && last_rows < tile_rows;
 
   if (tid < L::kNumBars) {
+    // (D = 64: kSFull is both scores, kPFull that they have been read, kDsFull both of P^T and dS^T.)
     const bool by_warps = tid == L::kPFull || tid == L::kDsFull || tid == L::kRowsFree || tid == L::kRowsFree + 1;
     mbar_init(&bars[tid], by_warps ? 8 : 1);
     fence_barrier_init();
@@ -744,28 +756,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       wait(L::kKvFull, 0);
-      if (ok) scores(0);
-      if (ok) inner(0);
-      for (int i = 0; i < n && ok; ++i) {
-        wait(L::kPFull, i);
-        if (!ok) break;
-        if (issuer) {
-          packed::mma_cols<64>(tmem + kKvDv, tmem + kKvS, cols_desc + stage(2 * i + 1), kIdO, i > 0);
-          tc::commit(&bars[L::kEmpty + (2 * i + 1) % kStages]);
+      if constexpr (kOwn) {
+        for (int i = 0; i < n && ok; ++i) {
+          if (!loaded(2 * i) || !loaded(2 * i + 1)) break;
+          if (i > 0) wait(L::kPFull, i - 1);   // both scores have been read
+          if (issuer) {
+            packed::mma_rows<kD>(tmem + kKvS, k_desc, rows_desc + stage(2 * i), kIdS);
+            packed::mma_rows<kD>(tmem + kKvDp, v_desc, rows_desc + stage(2 * i + 1), kIdS);
+            tc::commit(&bars[L::kSFull]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (i + 1 < n) scores(i + 1);
+        packed::products_end(&bars[L::kEnd], issuer, s.status);
+      } else {
+        if (ok) scores(0);
+        if (ok) inner(0);
+        for (int i = 0; i < n && ok; ++i) {
+          wait(L::kPFull, i);
+          if (!ok) break;
+          if (issuer) {
+            packed::mma_cols<64>(tmem + kKvDv, tmem + kKvS, cols_desc + stage(2 * i + 1), kIdO, i > 0);
+            tc::commit(&bars[L::kEmpty + (2 * i + 1) % kStages]);
+          }
+          __syncwarp();
+          if (i + 1 < n) scores(i + 1);
+          wait(L::kDsFull, i);
+          if (!ok) break;
+          if (issuer) {
+            packed::mma_cols<64>(tmem + kKvDk<kD>, tmem + kKvDp, cols_desc + stage(2 * i), kIdO, i > 0);
+            tc::commit(&bars[L::kEmpty + (2 * i) % kStages]);
+          }
+          __syncwarp();
+          if (i + 1 < n) inner(i + 1);
+        }
+        if (ok && issuer) tc::commit(&bars[L::kDone]);
+        packed::products_end(&bars[L::kEnd], issuer, s.status);
+      }
+    } else if (kOwn && warp == kKvSumWarp && n > 0) {
+      constexpr uint32_t kIdO = packed::idesc<kFp16>(128, kD, 0, 1);
+      const uint64_t cols_desc = packed::desc_cols(smem_u32(ring));
+      const bool issuer = packed::elect_one();
+      int at = 0;   // the stage of Q_i; dout_i is in the next
+      for (int i = 0; i < n && ok; ++i) {
+        const uint64_t q = cols_desc + static_cast<uint64_t>(at * (kTile >> 4));
+        const uint64_t dout = cols_desc + static_cast<uint64_t>((at + 1) * (kTile >> 4));
         wait(L::kDsFull, i);
         if (!ok) break;
         if (issuer) {
-          packed::mma_cols<64>(tmem + kKvDk, tmem + kKvDp, cols_desc + stage(2 * i), kIdO, i > 0);
-          tc::commit(&bars[L::kEmpty + (2 * i) % kStages]);
+          packed::mma_cols(tmem + kKvDv, tmem + kKvP, dout, kIdO, i > 0);
+          packed::mma_cols(tmem + kKvDk<kD>, tmem + kKvDs, q, kIdO, i > 0);
+          tc::commit(&bars[L::kUsed]);
+          tc::commit(&bars[L::kEmpty + at]);
+          tc::commit(&bars[L::kEmpty + at + 1]);
         }
         __syncwarp();
-        if (i + 1 < n) inner(i + 1);
+        at += 2;   // (an even number of stages)
+        if (at == kStages) at = 0;
       }
       if (ok && issuer) tc::commit(&bars[L::kDone]);
-      packed::products_end(&bars[L::kEnd], issuer, s.status);
+      packed::products_end(&bars[L::kEnd + 1], issuer, s.status);
     }
     __syncwarp();
   } else {
@@ -782,73 +831,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = warp_last - before > token0;
       const float4* lse2 = reinterpret_cast<const float4*>(rows + (i & 1) * 256 + 64 * half);
       const float4* D = reinterpret_cast<const float4*>(rows + (i & 1) * 256 + 128 + 64 * half);
-      uint32_t z[64];
       wait(L::kRowsFull + (i & 1), i >> 1);
-      wait(L::kSFull, i);
+      if constexpr (kOwn) {
+        uint32_t z[64], dp[64];
+        wait(L::kSFull, i);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        tc::ld32(lane_addr + kKvS + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
-      tc::wait_ld();
+        for (int c = 0; c < 2; ++c) {
+          tc::ld32(lane_addr + kKvS + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
+          tc::ld32(lane_addr + kKvDp + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&dp[32 * c]));
+        }
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kPFull]);
+        uint32_t p[32], ds[32];
+        auto compute = [&](auto masks) {
+          constexpr bool kMasks = decltype(masks)::value;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 m = lse2[c];
-        const float2 a = packed::unpair(packed::fma2(
-            packed::pair(__uint_as_float(z[4 * c]), __uint_as_float(z[4 * c + 1])), scale2, packed::pair(m.x, m.y)));
-        const float2 e = packed::unpair(packed::fma2(
-            packed::pair(__uint_as_float(z[4 * c + 2]), __uint_as_float(z[4 * c + 3])), scale2, packed::pair(m.z, m.w)));
-        z[4 * c] = __float_as_uint(fast_exp2(a.x));
-        z[4 * c + 1] = __float_as_uint(fast_exp2(a.y));
-        z[4 * c + 2] = __float_as_uint(fast_exp2(e.x));
-        z[4 * c + 3] = __float_as_uint(fast_exp2(e.y));
-      }
-      if (masked) {
+          for (int c = 0; c < 16; ++c) {
+            const float4 m = lse2[c], d = D[c];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) z[c] = c >= from ? z[c] : 0u;
-      }
-      uint32_t p[32];
+            for (int e = 0; e < 2; ++e) {
+              const int at = 4 * c + 2 * e;
+              const uint64_t minus_m = e ? packed::pair(m.z, m.w) : packed::pair(m.x, m.y);
+              const uint64_t minus_d = e ? packed::pair(d.z, d.w) : packed::pair(d.x, d.y);
+              float2 x = packed::unpair(packed::fma2(
+                  packed::pair(__uint_as_float(z[at]), __uint_as_float(z[at + 1])), scale2, minus_m));
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              if (kMasks) {
+                x.x = at >= from ? x.x : 0.f;
+                x.y = at + 1 >= from ? x.y : 0.f;
+              }
+              p[at / 2] = packed::pack2<kFp16>(x.x, x.y);
+              const uint64_t v = packed::pair(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1]));
+              const float2 y = packed::unpair(packed::mul2(
+                  packed::pair(x.x, x.y), kFp16 ? packed::fma2(v, down, minus_d) : packed::add2(v, minus_d)));
+              ds[at / 2] = packed::pack2<kFp16>(y.x, y.y);
+              if (kMasks) {   // a hidden row's 0 stays 0 beside an infinity
+                if (at + 1 < from) ds[at / 2] = 0u;
+                if (at < from) ds[at / 2] &= 0xffff0000u;
+              }
+            }
+          }
+        };
+        if (masked) {
+          compute(std::true_type());
+        } else {
+          compute(std::false_type());
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kRowsFree + (i & 1)]);
+        if (i > 0) wait(L::kUsed, i - 1);   // the last P^T and dS^T have been read
+        tc::st32(lane_addr + kKvP + 32 * half, p);
+        tc::st32(lane_addr + kKvDs + 32 * half, ds);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
+      } else {
+        uint32_t z[64];
+        wait(L::kSFull, i);
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        p[c] = packed::pack2<kFp16>(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1]));
-      tc::st32(lane_addr + kKvS + 64 * half, p);
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kPFull]);
-      wait(L::kDpFull, i);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t dp[32];
-        tc::ld32(lane_addr + kKvDp + 64 * half + 32 * c, dp);
+        for (int c = 0; c < 2; ++c)
+          tc::ld32(lane_addr + kKvS + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&z[32 * c]));
         tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 d = D[8 * c + e];
-          const uint32_t* zz = &z[32 * c + 4 * e];
-          const uint64_t v0 = packed::pair(__uint_as_float(dp[4 * e]), __uint_as_float(dp[4 * e + 1]));
-          const uint64_t v1 = packed::pair(__uint_as_float(dp[4 * e + 2]), __uint_as_float(dp[4 * e + 3]));
-          const uint64_t d0 = packed::pair(d.x, d.y), d1 = packed::pair(d.z, d.w);
-          const float2 a = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[0]), __uint_as_float(zz[1])),
-                                                       kFp16 ? packed::fma2(v0, down, d0) : packed::add2(v0, d0)));
-          const float2 b = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[2]), __uint_as_float(zz[3])),
-                                                       kFp16 ? packed::fma2(v1, down, d1) : packed::add2(v1, d1)));
-          p[16 * c + 2 * e] = packed::pack2<kFp16>(a.x, a.y);
-          p[16 * c + 2 * e + 1] = packed::pack2<kFp16>(b.x, b.y);
+        for (int c = 0; c < 16; ++c) {
+          const float4 m = lse2[c];
+          const float2 a = packed::unpair(packed::fma2(
+              packed::pair(__uint_as_float(z[4 * c]), __uint_as_float(z[4 * c + 1])), scale2, packed::pair(m.x, m.y)));
+          const float2 e = packed::unpair(packed::fma2(
+              packed::pair(__uint_as_float(z[4 * c + 2]), __uint_as_float(z[4 * c + 3])), scale2, packed::pair(m.z, m.w)));
+          z[4 * c] = __float_as_uint(fast_exp2(a.x));
+          z[4 * c + 1] = __float_as_uint(fast_exp2(a.y));
+          z[4 * c + 2] = __float_as_uint(fast_exp2(e.x));
+          z[4 * c + 3] = __float_as_uint(fast_exp2(e.y));
         }
-      }
-      if (masked) {
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (2 * c + 1 < from) p[c] = 0u;
-          if (2 * c < from) p[c] &= 0xffff0000u;
+          for (int c = 0; c < 64; ++c) z[c] = c >= from ? z[c] : 0u;
         }
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          p[c] = packed::pack2<kFp16>(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1]));
+        tc::st32(lane_addr + kKvS + 64 * half, p);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kPFull]);
+        wait(L::kDpFull, i);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[32];
+          tc::ld32(lane_addr + kKvDp + 64 * half + 32 * c, dp);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 d = D[8 * c + e];
+            const uint32_t* zz = &z[32 * c + 4 * e];
+            const uint64_t v0 = packed::pair(__uint_as_float(dp[4 * e]), __uint_as_float(dp[4 * e + 1]));
+            const uint64_t v1 = packed::pair(__uint_as_float(dp[4 * e + 2]), __uint_as_float(dp[4 * e + 3]));
+            const uint64_t d0 = packed::pair(d.x, d.y), d1 = packed::pair(d.z, d.w);
+            const float2 a = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[0]), __uint_as_float(zz[1])),
+                                                         kFp16 ? packed::fma2(v0, down, d0) : packed::add2(v0, d0)));
+            const float2 b = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[2]), __uint_as_float(zz[3])),
+                                                         kFp16 ? packed::fma2(v1, down, d1) : packed::add2(v1, d1)));
+            p[16 * c + 2 * e] = packed::pack2<kFp16>(a.x, a.y);
+            p[16 * c + 2 * e + 1] = packed::pack2<kFp16>(b.x, b.y);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (2 * c + 1 < from) p[c] = 0u;
+            if (2 * c < from) p[c] &= 0xffff0000u;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kRowsFree + (i & 1)]);
+        tc::st32(lane_addr + kKvDp + 64 * half, p);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kRowsFree + (i & 1)]);
-      tc::st32(lane_addr + kKvDp + 64 * half, p);
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
     }
     if (n > 0) wait(L::kDone, 0);
     // ---- the first warpgroup has dv, the second dk ----
@@ -864,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = 0u;
       if (n > 0) {
-        tc::ld32(lane_addr + (half ? kKvDk : kKvDv) + 32 * c, w);
+        tc::ld32(lane_addr + (half ? kKvDk<kD> : kKvDv) + 32 * c, w);
         tc::wait_ld();
       }
       if (ctas > 1) {   // into this CTA's ring, which is free now
