@@ -146,11 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // A unit from where it lies: (sequence, index of its two tiles, KV head).
-  auto unit_of = [&](int4 at) {
+  // A unit from where it lies, (whether there is one, index of its two tiles, KV head), and its sequence.
+  auto unit_of = [&](int4 at, int4 rows) {
     Unit u;
-    bool bad = false;
-    u.seq = packed::sequence(s, at.x, &bad);
+    u.seq = {rows.x, rows.y, rows.z, rows.w};
     u.t0 = at.y * halves * tile_tokens;
     u.h = at.z;
     u.before = u.seq.n_k - u.seq.n_q;
@@ -176,11 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*ok) *ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnit + (k & 1)], (k >> 1) & 1, s.status));
     if (!*ok) return false;
     int4 at = units[2 * (k & 1)];
+    const int4 rows = units[2 * (k & 1) + 1];
     at.x = __shfl_sync(0xffffffffu, at.x, 0);   // (uniform for the compiler, so that the roles' loops are)
     if (at.x < 0) return false;
-    at.y = __shfl_sync(0xffffffffu, at.y, 0);
-    at.z = __shfl_sync(0xffffffffu, at.z, 0);
-    *u = unit_of(at);
+    *u = unit_of(at, rows);
     return true;
   };
   auto unit_done = [&](int k) {
@@ -203,22 +201,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Unit number k of this CTA: down the order of all and back, so that none gets the longest of each round.
         int i = kSplit ? static_cast<int>(blockIdx.x) / ctas : static_cast<int>(blockIdx.x);
         if (!kSplit) i = k * stride + (k & 1 ? stride - 1 - i : i);
-        int4 at = make_int4(-1, 0, i % s.Hkv, 0);
+        int4 at = make_int4(-1, 0, i % s.Hkv, 0), rows = make_int4(0, 0, 0, 0);
         int b, level;
         if (!(kSplit && k > 0) && walker.find(s, i / s.Hkv, halves * tile_tokens, false, &b, &level, &bad)) {
-          at.x = b;
+          at.x = 0;
           at.y = level;
+          const packed::Sequence seq = packed::sequence(s, b, &bad);
+          rows = make_int4(seq.q0, seq.n_q, seq.k0, seq.n_k);
         }
         if (k >= 2 && ok)
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnitFree + (k & 1)], ((k >> 1) - 1) & 1, s.status));
         if (!ok) at.x = -1;
         if (lane == 0) {
           units[2 * (k & 1)] = at;
+          units[2 * (k & 1) + 1] = rows;
           mbar_arrive(&bars[L::kUnit + (k & 1)]);
         }
         __syncwarp();
         if (at.x < 0) break;
-        u = unit_of(at);
+        u = unit_of(at, rows);
         const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {

@@ -62,8 +62,8 @@ struct DqLayout {
                        kPair = kCleared + 2, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
                        kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kEnd = kOutRead + 1,
                        kNumBars = kEnd + 2;
-  static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 16 bytes each
-  static constexpr int kSlot = kUnits + 32;
+  static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 32 bytes each
+  static constexpr int kSlot = kUnits + 64;
   static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
   static constexpr int kBytes = kSum + 1024 + 1024;
 };
@@ -118,10 +118,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  auto unit_of = [&](int4 at) {
+  // A unit from where it lies, (whether there is one, its tile, KV head), and its sequence.
+  auto unit_of = [&](int4 at, int4 rows) {
     DqUnit u;
-    bool bad = false;
-    u.seq = packed::sequence(s, at.x, &bad);
+    u.seq = {rows.x, rows.y, rows.z, rows.w};
     u.t0 = at.y * tile_tokens;
     u.h = at.z;
     u.before = u.seq.n_k - u.seq.n_q;
@@ -136,12 +136,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto next_unit = [&](int k, bool* ok, DqUnit* u) {
     if (*ok) *ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnit + (k & 1)], (k >> 1) & 1, s.status));
     if (!*ok) return false;
-    int4 at = units[k & 1];
+    int4 at = units[2 * (k & 1)];
+    const int4 rows = units[2 * (k & 1) + 1];
     at.x = __shfl_sync(0xffffffffu, at.x, 0);   // (uniform for the compiler, so that the roles' loops are)
     if (at.x < 0) return false;
-    at.y = __shfl_sync(0xffffffffu, at.y, 0);
-    at.z = __shfl_sync(0xffffffffu, at.z, 0);
-    *u = unit_of(at);
+    *u = unit_of(at, rows);
     return true;
   };
   auto unit_done = [&](int k) {
@@ -190,22 +189,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Down the order of all units and back, so that no CTA gets the longest of each round.
         int i = static_cast<int>(blockIdx.x);
         i = k * stride + (k & 1 ? stride - 1 - i : i);
-        int4 at = make_int4(-1, 0, i % s.Hkv, 0);
+        int4 at = make_int4(-1, 0, i % s.Hkv, 0), rows = make_int4(0, 0, 0, 0);
         int b, level;
         if (walker.find(s, i / s.Hkv, tile_tokens, false, &b, &level, &bad)) {
-          at.x = b;
+          at.x = 0;
           at.y = level;
+          const packed::Sequence seq = packed::sequence(s, b, &bad);
+          rows = make_int4(seq.q0, seq.n_q, seq.k0, seq.n_k);
         }
         if (k >= 2 && ok)
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnitFree + (k & 1)], ((k >> 1) - 1) & 1, s.status));
         if (!ok) at.x = -1;
         if (lane == 0) {
-          units[k & 1] = at;
+          units[2 * (k & 1)] = at;
+          units[2 * (k & 1) + 1] = rows;
           mbar_arrive(&bars[L::kUnit + (k & 1)]);
         }
         __syncwarp();
         if (at.x < 0) break;
-        u = unit_of(at);
+        u = unit_of(at, rows);
         const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
         if (u.n > 0) {
           const int st = k_stage(row_bytes, nullptr);
