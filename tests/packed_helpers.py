@@ -48,7 +48,8 @@ class Step:
             whole = self.full(tq, hq + 2 * heads, dim)
             self.q, self.k, self.v = whole.split([hq, heads, heads], dim=1)
         elif layout == "heads":                      # head-major storage
-            self.q, self.k, self.v = (self.full(h, t, dim).transpose(0, 1) for h, t in ((hq, tq), (heads, tk), (heads, tk)))
+            self.q, self.k, self.v = (self.full(h, t, dim).transpose(0, 1)
+                                      for h, t in ((hq, tq), (heads, tk), (heads, tk)))
         else:
             self.q, self.k, self.v = self.full(tq, hq, dim), self.full(tk, heads, dim), self.full(tk, heads, dim)
         self.q[:self.q_starts[-1]] = self.normal(self.q_starts[-1], hq, dim)
@@ -92,7 +93,8 @@ def plain(step, with_grads=True):
         return torch.full(x.shape, float("nan"), dtype=torch.float64, device=step.dev)
     names = dict(out=step.q, dq=step.q, dk=step.k, dv=step.v)
     result = {n: (empty(x), empty(x)) for n, x in names.items()}
-    result["lse"] = tuple(torch.full(step.q.shape[:2], float("nan"), dtype=torch.float64, device=step.dev) for _ in range(2))
+    result["lse"] = tuple(torch.full(step.q.shape[:2], float("nan"), dtype=torch.float64, device=step.dev)
+                          for _ in range(2))
 
     def put(name, at, heads_at, value, tol):
         result[name][0][at, heads_at], result[name][1][at, heads_at] = value, tol

@@ -384,8 +384,8 @@ def _turn(x, positions, freq, scale, part, interleaved, transpose):
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("dim,part,heads,tokens", [(128, 128, 3, 5), (64, 32, 40, 700), (512, 512, 1, 3), (80, 48, 2, 33),
-                                                   (128, 16, 17, 1), (16, 16, 1, 2000), (256, 128, 9, 1300)])
+@pytest.mark.parametrize("dim,part,heads,tokens", [(128, 128, 3, 5), (64, 32, 40, 700), (512, 512, 1, 3),
+                                                   (80, 48, 2, 33), (128, 16, 17, 1), (16, 16, 1, 2000), (256, 128, 9, 1300)])
 def test_rotary(dev, dtype, interleaved, dim, part, heads, tokens):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
@@ -393,7 +393,8 @@ def test_rotary(dev, dtype, interleaved, dim, part, heads, tokens):
     gen = torch.Generator(device=dev).manual_seed(dim + tokens)
     whole = torch.randn((tokens, heads + 2, dim), device=dev, generator=gen).to(dtype)   # q and k of one projection
     q, k = whole[:, :heads], whole[:, heads:]
-    positions = torch.randint(-100, 2 ** 31 - 1, (tokens,), device=dev, generator=gen, dtype=torch.int64).to(torch.int32)
+    positions = torch.randint(-100, 2 ** 31 - 1, (tokens,), device=dev, generator=gen,
+                              dtype=torch.int64).to(torch.int32)
     positions[::2] %= 5000
     positions[-1] = 0
     plan = T.alloc_rotary_plan(part, base=50000.0, device=dev)
@@ -666,7 +667,8 @@ def test_packed_append_from_pinned_memory_and_a_slot_past_the_pool(dev):
     slots = torch.tensor([31, 32, 0], dtype=torch.int32, device=dev)
     T.paged_append_packed(cache, *new, slots, torch.tensor([4, 5, 6], dtype=torch.int32, device=dev))
     assert _status() == T.DEVICE_BAD_PAGE
-    assert torch.equal(cache.k_pages[1, :, 15].cpu(), new[0][0]) and torch.equal(cache.v_pages[0, :, 0].cpu(), new[1][2])
+    assert torch.equal(cache.k_pages[1, :, 15].cpu(), new[0][0])
+    assert torch.equal(cache.v_pages[0, :, 0].cpu(), new[1][2])
     assert cache.positions[1, :, 15].tolist() == [4, 4] and cache.positions[0, :, 0].tolist() == [6, 6]
     assert int((cache.positions == -5).sum()) == 2 * 2 * 16 - 4 and int((cache.weights == 0).sum()) == 4
     for bad in ((new[0][:2], new[1], slots), (new[0], new[1], slots[:2]), (new[0].clone(), new[1], slots),

@@ -235,8 +235,8 @@ def test_attention_refuses(L):
                          (dict(k_head=0), bad), (dict(k_token=128), bad), (dict(v_token=1 << 40), no),
                          (dict(v_head=132), no), (dict(k_starts=None, k_tokens=11), bad)):
             assert call(L, _args(L, **kw)) == code, (call.__name__, kw)
-    for kw, code in ((dict(out=None), bad), (dict(out=ODD), no), (dict(out=FAKE), bad), (dict(strides=None), bad), (dict(strides=(1024, 0)), bad),
-                     (dict(strides=(1024, 132)), no), (dict(strides=(512, 128)), bad)):
+    for kw, code in ((dict(out=None), bad), (dict(out=ODD), no), (dict(out=FAKE), bad), (dict(strides=None), bad),
+                     (dict(strides=(1024, 0)), bad), (dict(strides=(1024, 132)), no), (dict(strides=(512, 128)), bad)):
         assert _forward(L, _args(L), **kw) == code, kw
     for name in ("out", "lse", "dout", "dq", "dk", "dv"):
         assert _backward(L, _args(L), **{name: None}) == bad, name
