@@ -237,6 +237,20 @@ def test_bad_starts_are_flagged_and_skipped(dev):
         assert (out[rest] == 7.0).all() and all((g[rest] == 7.0).all() for g in grads)
 
 
+def test_bad_starts_behind_many_good_ones_are_flagged(dev):
+    """40 sequences of one query, each with more than a thousand keys: few units, divided over clusters."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from packed_helpers import Step
+    step = Step(dev, "bf16", 64, 1, 1, [1] * 40, [1100] * 40)
+    good, good_lse = step.forward(T)
+    assert _status() == 0
+    step.q_starts = [*range(38), 38, 12, 40]       # sequence 38 descends; the last one has rows 12 .. 39
+    out, lse = step.forward(T)
+    assert _status() == T.DEVICE_BAD_KV_LEN
+    assert torch.equal(out[:12], good[:12]) and torch.equal(lse[:12], good_lse[:12])
+
+
 def test_same_bits_every_time(dev):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
@@ -350,6 +364,8 @@ def test_binding_refuses(dev):
     refused(q, k, v, starts, out, k_starts=starts[:-1])
     refused(q, k.expand(-1, 2, -1)[:, :1].expand(-1, 2, -1), v, starts, out)   # one row for two heads
     refused(q, k, v, starts, out, scale=0.0)
+    refused(q, k, v, starts, out, scale=float("nan"))
+    refused(q, k, v, starts, out, scale=1e39)                 # past fp32
     refused(q[:10], k, v, starts, out[:10])                   # no k_starts, other counts of tokens
     lse = torch.empty(q.shape[:2], device=dev)
     grads = [torch.empty_like(x) for x in (q, k, v)]

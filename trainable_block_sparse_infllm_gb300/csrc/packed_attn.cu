@@ -146,6 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
   }
+  // Tensor memory is taken once the kernel before has ended and before the next one may start: neither ever
+  // waits for columns that the other holds.
+  pdl_wait();
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
@@ -154,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
   pdl_trigger();
 
   // A unit from where it lies, (whether there is one, index of its two tiles, KV head), and its sequence.
@@ -268,6 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         __syncwarp();
+      }
+      if (kSplit && blockIdx.x == 0) {   // (its only unit is behind it: on to the end, where bad starts may be)
+        int b, level;
+        walker.find(s, 0x7fffffff, halves * tile_tokens, false, &b, &level, &bad);
       }
       if (bad && blockIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
       // The CTA outlives its copies, also after a wait that gave up.  (Each barrier's last copy is its

@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&maps.out);
     prefetch_tensormap(&maps.dout);
   }
+  // Tensor memory is taken once the kernel before has ended and before the next one may start: neither ever
+  // waits for columns that the other holds.
+  pdl_wait();
   if (warp == kPairWarp) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
@@ -122,7 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
   pdl_trigger();
 
   // A unit from where it lies, (whether there is one, its tile, KV head), and its sequence.
@@ -618,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
-  pdl_trigger();
   const int tile_tokens = packed_tile_tokens(s.G), tile_rows = tile_tokens * s.G;
   const int rank = static_cast<int>(blockIdx.x) % ctas, unit = static_cast<int>(blockIdx.x) / ctas;
   const int h = unit % s.Hkv;
@@ -661,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
   bool ok = true;
   auto wait = [&](int bar, int phase) {
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
