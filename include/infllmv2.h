@@ -494,7 +494,8 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
  *           step its slot in the pool, page * page_size + row, and its position,
  *           seq_lens[b] + t; past the last token -1 and 0.
  *   missing int32 [1]: 0, or the number of free pages that lack, or -1: a length,
- *           held[b] or n_free is out of range (a row has max_pages entries), or
+ *           held[b] or n_free is out of range (a row has max_pages entries; the
+ *           pages given back and the free ones are at most num_pages), or
  *           the step has more than max_tokens tokens; then also
  *           INFLLMV2_DEVICE_BAD_KV_LEN.  Where it is not 0 nothing is taken or
  *           given back, new_lens is kv_lens, every start 0 and every slot -1: the
@@ -592,6 +593,7 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* 
  *   q, k    INFLLMV2_BF16, INFLLMV2_FP16 or INFLLMV2_FP32 (dtype); no k where
  *           k_heads is 0.  Strides in elements between tokens and heads.  q_out may be
  *           q, with the same strides; otherwise the two must not overlap; k likewise.
+ *           q_out must be apart from k and k_out, and k_out from q.
  *   positions  int32 [tokens], any value.
  *   turns   device memory, [rotary_dim / 2], from infllmv2_rotary_frequencies.
  * head_dim and rotary_dim: multiples of 16, rotary_dim <= head_dim <= 512.

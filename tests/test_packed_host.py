@@ -133,6 +133,11 @@ def test_rotary_refuses(L):
     # fp32 rows of 4 elements are 16 bytes.
     assert _rotary(L, q_token=132) == no
     assert _rotary(L, q_token=130, dtype=L.FP32) == no
+    # An output that the other tensor is read from or written to.
+    assert _rotary(L) == bad
+    for q_out, k, k_out in ((FAKE + 4096, FAKE + 8192, FAKE), (FAKE + 4096, FAKE + 4096, FAKE + 8192),
+                            (FAKE + 4096, FAKE + 8192, FAKE + 4096)):
+        assert _rotary(L, q_out=q_out, k=k, k_out=k_out) == bad, (q_out, k, k_out)
 
 
 # ------------------------------------------------------------------ reserve

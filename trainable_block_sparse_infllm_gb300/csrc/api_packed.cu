@@ -241,6 +241,8 @@ int infllmv2_rotary(const infllmv2_rotary_args* r, void* stream) {
     if (r->k_heads > 0 && (rc = check_rotary_rows(r->k, r->k_out, r->k_strides, r->k_out_strides, r->tokens,
                                                   r->k_heads, d, bytes, "k", &a.k_in, &a.k_out)))
       return rc;
+    if (r->k_heads > 0 && (r->k_out == r->q_out || r->k_out == r->q || r->q_out == r->k))
+      return fail(INFLLMV2_INVALID_ARGUMENT, "q and k must be apart from each other's output");
     a.positions = r->positions;
     a.turns = r->turns;
     a.scale = r->scale;

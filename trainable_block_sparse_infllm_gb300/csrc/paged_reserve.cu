@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kMost) paged_reserve_kernel(const ReserveArgs 
   const long long reused = total.take - on_stack;                         // takes of what is given back
   const long long lacking = reused - total.give;
   const long long most = a.slots || a.positions ? a.max_tokens : 0x7fffffffll;
-  const bool refuse = bad_any || total.give > a.pages || kept + total.give - reused > a.pages || total.tokens > most;
+  const bool refuse = bad_any || n_free + total.give > a.pages || total.tokens > most;
   const bool go = !refuse && lacking <= 0;
   at = {at.take + incl.take - mine.take, at.give + incl.give - mine.give, at.tokens + incl.tokens - mine.tokens};
   if (go) {

@@ -35,6 +35,7 @@ _attn = _lib.lib.infllmv2_packed_attn
 _backward = _lib.lib.infllmv2_packed_attn_backward
 _byref = ctypes.byref
 _int32 = torch.int32
+_MAX = torch.finfo(torch.float32).max
 # The C argument structures (_lib.py names their fields).
 _reserve_args = struct.Struct("=6i12Q").pack
 _rotary_args = struct.Struct("=8ifi6Q8q").pack
@@ -190,6 +191,8 @@ class RotaryPlan:
     def __init__(self, turns: torch.Tensor, scale: float):
         if not turns.is_cuda or turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
             raise _bad("turns must be contiguous int64 [rotary_dim / 2] on a CUDA device")
+        if not abs(scale) < _MAX:
+            raise _bad("scale must be finite in fp32")
         self.turns, self.scale, self.rotary_dim, self.index = turns, scale, 2 * turns.numel(), turns.get_device()
         self._ptr = turns.data_ptr()
 
@@ -291,6 +294,8 @@ def _inputs(q, k, v, q_starts, k_starts, scale):
     qs, ks, vs = q.stride(), k.stride(), v.stride()
     if qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
         raise _bad("the values of a head must be consecutive")
+    if scale is not None and not abs(scale) < _MAX:
+        raise _bad("scale must be finite in fp32")
     batch = q_starts.numel() - 1
     if batch < 1 or not _is_ints(q_starts, index, batch + 1) or \
             not (k_starts is None or _is_ints(k_starts, index, batch + 1)):
