@@ -11,12 +11,16 @@
 // keys' gradients inside the product.
 //
 // D from the rounded `out` is off by up to half a step of |out| |dout|.  Where a row
-// attends few keys, dout . v - D is a small difference of such numbers and the
-// error shows in dq and dk (2% of them for documents of 7 tokens in bf16, against
-// 0.3% past a thousand).  So rows of up to kExactTiles tiles of keys walk them twice
-// and sum D = sum P (dout . v) first (one tile: it is all in registers); and every
-// row ends with sum P (dout . v - D), which is what its D lacks, before D goes to
-// the dk and dv kernel.
+// attends few keys, or one key takes most of its weight, dout . v - D is a small
+// difference of such numbers and the error shows in dq and dk (2% of them for
+// documents of 7 tokens in bf16).  So rows of up to kExactTiles tiles of keys walk them
+// twice and sum D = sum P (dout . v) first (one tile: it is all in registers).  Longer
+// ones walk them once, from the last to the first: then sum P (dout . v - D) of all
+// tiles is what D lacked, and the first tile's dS (the first tokens are what draws much of
+// the attention in trained models) and the dk and dv kernel have D exactly.  Left is dS's
+// rounding to 16 bits: dq and dk 0.24% off in bf16, the rounding of the result being
+// 0.17%; with a heavy key amid 1000 to 4000 others dq 0.25 to 0.26%.  Two walks up to 4 or
+// 2 tiles only made 16 documents 3 and 7% faster, and the latter error 0.32 and 0.35%.
 //
 // In both kernels the operand that the second products take from the scores, dS (dq), or
 // P^T and dS^T (dk, dv: scores are computed transposed, keys in rows), is the A
@@ -226,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   u.seq.q0 + u.t0, &bars[L::kKFull + st]);
         }
         for (int j = 0; j < u.steps && ok; ++j) {
-          const int row = u.seq.k0 + (j < u.back ? j : j - u.back) * 128;
+          const int row = u.seq.k0 + (j < u.back ? j : u.steps - 1 - j) * 128;
           // The tile of K that is to be cleared behind the sequence lands on a barrier of its own (of two in
           // turn: the unit after next waits for this one's end).
-          const bool tail = u.clears && j == u.steps - 1;
+          const bool tail = u.clears && j == u.back;
           uint64_t* own = tail ? &bars[L::kTail + (k & 1)] : nullptr;
           const int st = k_stage(kTile, own);
           if (!ok) break;
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place pk = {0, 0}, pv = {0, 0};
       int pairs = 0, even = 0, odd = 0, ins = 0, uses = 0, outs = 0;   // (tails of units of each parity)
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
-        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
+        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? back : -1;
         const bool exact = uniform(u.exact);
         if (steps > 0) {
           wait(L::kQIn, ins++);
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place pk = {0, 0};
       int even = 0, odd = 0, used = 0, made = 0;
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
-        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? steps - 1 : -1;
+        const int steps = uniform(u.steps), back = uniform(u.back), tail = uniform(u.clears) ? back : -1;
         if (steps > 0) next(pk, kKs);   // Q's stage
         for (int j = 0; j < steps; ++j) {
           if (j >= back) {
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
         if (u.steps > 0) next(pk, kKs);   // Q's stage
         for (int j = 0; j < u.steps; ++j) {
-          if (u.clears && j == u.steps - 1) {
+          if (u.clears && j == u.back) {
             wait(L::kTail + (k & 1), k & 1 ? odd++ : even++);
             packed::clear_rows<kD>(smem + L::kK + pk.stage * kTile, u.seq.n_k - (u.n - 1) * 128);
             if (lane == 0) mbar_arrive(&bars[L::kCleared + (k & 1)]);
@@ -491,23 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         return packed::pair(fast_exp2(e.x), fast_exp2(e.y));
       };
       auto value2 = [&](int i) { return packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])); };
-      auto sum_d = [&] {   // D += sum P (dout . v)
+      // Of the columns in registers: sum P (dout . v - x).
+      auto sum_p = [&](float x) {
+        const uint64_t minus_x = packed::pair(-x, -x);
         uint64_t d = 0ull;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) d = packed::fma2(prob2(i), value2(i), d);
+        for (int i = 0; i < 32; ++i) d = packed::fma2(prob2(i), packed::add2(value2(i), minus_x), d);
         const float2 halves = packed::unpair(d);
-        D += halves.x + halves.y;
+        return halves.x + halves.y;
       };
       for (int t = 0; t < u.back; ++t) {   // the first walk, where there are two
         probs(t);
-        sum_d();
+        D += sum_p(0.f);
       }
       if (u.back > 0) D = both(D);
-      for (int j = 0; j < u.n; ++j) {
+      for (int j = u.n - 1; j >= 0; --j) {
         probs(j);
-        if (u.n == 1) {   // the only tile: D and dS from the same registers
-          sum_d();
-          D = both(D);
+        if (j == 0 && u.back == 0) {   // all of D is known now (one tile: D and dS are from the same registers)
+          const float2 halves = packed::unpair(rest);
+          D += both(halves.x + halves.y + sum_p(D));
         }
         const uint64_t minus_d = packed::pair(-D, -D);
         uint32_t ds[32];
@@ -526,9 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
       }
-      // sum P (dout . v - D) is what D lacks.
-      const float2 halves = packed::unpair(rest);
-      D += both(halves.x + halves.y);
       if (half == 0 && active) g.rows[row * (s.Hkv * s.G) + head] = make_float2(lse2, D);
       if (u.n > 0) wait(L::kDqDone, summed - 1);
       uint16_t* dq = static_cast<uint16_t*>(g.dq) + row * g.dq_st.token + head * g.dq_st.head;
