@@ -278,7 +278,9 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
     if ((rc = check_status(c))) return rc;
     PackedAttnMaps maps = {};
     if ((rc = attn_maps(&maps, args, c))) return rc;
-    const PackedAttnOut to{out, {o.token, o.head}, lse};
+    const bool by_tile = packed_attn_by_tile(c.s, c.D);
+    if (by_tile && (rc = row_map(&maps.out, c, out, o, "out"))) return rc;
+    const PackedAttnOut to{out, {o.token, o.head}, lse, by_tile};
     const PackedAttnIn in{args->q, args->k, args->v, {c.q.token, c.q.head}, {c.k.token, c.k.head},
                           {c.v.token, c.v.head}};
     const cudaError_t e = launch_packed_attn(c.s, c.D, c.fp16, maps, in, to, static_cast<cudaStream_t>(stream));

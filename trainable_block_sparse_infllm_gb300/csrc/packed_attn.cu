@@ -72,7 +72,8 @@ struct Layout {
   // that none is two phases ahead of who waits for it.
   static constexpr int kLooks = (kStages + 1) / 2;
   static constexpr uint32_t kColO = 128 * kBuffers;
-  static constexpr int kBars = 2 * kTile + kRing;
+  static constexpr int kOut = 2 * kTile + kRing;   // by_tile: a tile of out for each half
+  static constexpr int kBars = kOut + (kD == 64 ? 2 * kTile : 0);
   // Barriers: a unit found and done with; Q of each tile full and free; ring full and empty; V tiles
   // attended in part, before and after they were looked through; of each tile S (three buffers: three, in
   // turn); of each score buffer P; of each tile P V (three, in turn) and x read; kSplit: all products; of each
@@ -478,16 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax
     packed::regs_up<216>();
     const int x = warp >> 2;
-    const int r = tid & 127;
+    const int r = tid & 127, row_token = r / s.G, row_head = r % s.G;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t o_addr = lane_addr + kColO + x * kD;
     const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
-    const bool wide = packed::wide_rows(o.out, o.st);
+    const bool wide = packed::wide_rows(o.out, o.st), by_tile = kD == 64 && !kSplit && o.by_tile;
     bool ok = true;
     int jobs = 0, done = 0, used = 0;   // of all units before: jobs, this half's, and its units
-    for (int k = 0; next_unit(k, &ok, &u); ++k) {
+    for (int k = 0;; ++k) {
+      const bool more = next_unit(k, &ok, &u);
+      if (by_tile ? !packed::all_agree(more, 2 + x, 128) : !more) break;
       any = true;
-      const int token = u.t0 + x * tile_tokens + r / s.G;   // in the sequence
+      const int token = u.t0 + x * tile_tokens + row_token;   // in the sequence
       const bool active = x < halves && r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 - u.j0 * 128 : 0;   // keys 0 .. limit - 1, from tile j0 on
       const int mine = x ? u.n_tiles[1] : u.n_tiles[0], both = min(u.n_tiles[0], u.n_tiles[1]);
@@ -583,37 +586,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kAllDone], 0, s.status));
       tc::fence_after_sync();
       const float inv = 1.f / l;
-      const int head = u.h * s.G + r % s.G;
+      const int head = u.h * s.G + row_head;
       const long long row = u.seq.q0 + token;
       const bool none = u.before + token < 0;   // the row attends no key
       uint16_t* out = static_cast<uint16_t*>(o.out) + row * o.st.token + head * o.st.head;
-      const uint16_t* q_row = static_cast<const uint16_t*>(in.q) + row * in.q_st.token + head * in.q_st.head;
       // Rows that were cleared.  (P V of each tile is done, so each has been looked through.)
       const uint32_t* gone = flags + (k & 1) * kMaxPartial * 4;
       uint32_t cleared = 0u;
-      for (int j = u.looked; j < mine && ok; ++j)
-        for (int i = 0; i < 4; ++i) cleared |= gone[4 * (j - u.looked) + i];
+      for (int j = u.looked; j < mine && ok; ++j) {
+        const uint4 four = *reinterpret_cast<const uint4*>(gone + 4 * (j - u.looked));
+        cleared |= four.x | four.y | four.z | four.w;
+      }
+      // D = 64 at once, so that the next unit's P V can start; 128 columns in registers beside their stores cost
+      // more than that gives (48 prompts of 512, 8 KV heads of 4: 149 or 158 us).
+      constexpr int kPart = kD == 64 ? 64 : 32;
 #pragma unroll 1
-      for (int c = 0; c < kD / 32; ++c) {
-        uint32_t w[32];
+      for (int c0 = 0; c0 < kD; c0 += kPart) {
+        uint32_t w[kPart];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = 0u;
+        for (int i = 0; i < kPart; ++i) w[i] = 0u;
         if (mine > 0) {
-          tc::ld32(o_addr + 32 * c, w);
+#pragma unroll
+          for (int c = 0; c < kPart; c += 32) tc::ld32(o_addr + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&w[c]));
           tc::wait_ld();
+          if (c0 + kPart == kD) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::kOFree + x]);
+          }
         }
         if (cleared && active) {
+          const uint16_t* q_row = static_cast<const uint16_t*>(in.q) + row * in.q_st.token + head * in.q_st.head;
 #pragma unroll 1
           for (int key = u.looked * 128; key < min(limit, mine * 128); ++key) {
             const int bit = key - u.looked * 128;
             if (!((gone[bit >> 5] >> (bit & 31)) & 1)) continue;
             const long long at = u.seq.k0 + u.j0 * 128 + key;
             const uint16_t* k_row = static_cast<const uint16_t*>(in.k) + at * in.k_st.token + u.h * in.k_st.head;
-            const uint16_t* v_row =
-                static_cast<const uint16_t*>(in.v) + at * in.v_st.token + u.h * in.v_st.head + 32 * c;
+            const uint16_t* v_row = static_cast<const uint16_t*>(in.v) + at * in.v_st.token + u.h * in.v_st.head + c0;
             const float p = fast_exp2(fmaf(dot<kD, kFp16>(q_row, k_row), s.scale2, kTop<kFp16> - m));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kPart / 2; ++i) {
               const float2 v = packed::unpack2<kFp16>(reinterpret_cast<const uint32_t*>(v_row)[i]);
               w[2 * i] = __float_as_uint(fmaf(p, v.x, __uint_as_float(w[2 * i])));
               w[2 * i + 1] = __float_as_uint(fmaf(p, v.y, __uint_as_float(w[2 * i + 1])));
@@ -622,23 +635,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kSplit) {   // into this CTA's ring, which is free now
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            parts[packed::swizzled<kD>(x * 128 + r, 8 * c + i)] =
-                make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]), __uint_as_float(w[4 * i + 2]),
-                            __uint_as_float(w[4 * i + 3]));
-        } else if (active) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            p[i] = !none ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv)
-                         : 0u;
-          packed::store_row(out + 32 * c, p, wide);
+          for (int i = 0; i < kPart; i += 4)
+            parts[packed::swizzled<kD>(x * 128 + r, (c0 + i) / 4)] =
+                make_float4(__uint_as_float(w[i]), __uint_as_float(w[i + 1]), __uint_as_float(w[i + 2]),
+                            __uint_as_float(w[i + 3]));
+          continue;
         }
-      }
-      if (mine > 0) {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kOFree + x]);
+        uint32_t p[kPart / 2];
+#pragma unroll
+        for (int i = 0; i < kPart / 2; ++i)
+          p[i] = !none ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv)
+                       : 0u;
+        if (kPart == kD && by_tile && x < halves && u.t0 + (x + 1) * tile_tokens <= u.seq.n_q) {
+          // Every row of the tile is a query's.
+          uint8_t* tile = smem + L::kOut + x * kTile;
+          if (r == 0) packed::stores_read();
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + x) : "memory");
+#pragma unroll
+          for (int c = 0; c < kPart / 8; ++c)
+            *reinterpret_cast<uint4*>(tile + r * 128 + ((c ^ (r & 7)) << 4)) =
+                make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+          fence_proxy_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + x) : "memory");
+          if (r == 0)
+            packed::tma_store_4d(&maps.out, smem_u32(tile), 0, 0, u.h, u.seq.q0 + u.t0 + x * tile_tokens);
+        } else if (active) {
+#pragma unroll
+          for (int c = 0; c < kPart; c += 32)
+            packed::store_row(out + c0 + c, *reinterpret_cast<uint32_t(*)[16]>(&p[c / 2]), wide);
+        }
       }
       if (kSplit) {
         sums[x * 128 + r] = make_float2(m, l);
@@ -652,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unit_done(k);
       if (kSplit) break;
     }
+    if (by_tile && r == 0) packed::stores_done();
   }
   if (kSplit) {
     // ---- each CTA joins its share of the rows over the cluster: with M the largest m,
@@ -796,6 +822,13 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
 }
 
 }  // namespace
+
+// Where a CTA has more than one unit, and shared memory has room (D = 64): a thread's row
+// is 128 bytes, and a warp's stores of 32 rows at once take twice the time of
+// whole lines.
+bool packed_attn_by_tile(const PackedAttnShape& s, int D) {
+  return D == 64 && static_cast<long long>(s.Tq) * s.Hkv > 2ll * packed_tile_tokens(s.G) * device_sm_count();
+}
 
 cudaError_t launch_packed_attn(const PackedAttnShape& s, int D, bool fp16, const PackedAttnMaps& maps,
                                const PackedAttnIn& in, const PackedAttnOut& o, cudaStream_t st) {

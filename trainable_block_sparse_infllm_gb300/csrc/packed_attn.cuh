@@ -171,18 +171,18 @@ __device__ __forceinline__ bool find_tile(const PackedAttnShape& s, int i, int s
   return found[0] != 0;
 }
 
-// Whether all of the 256 threads of the first eight warps say so (barrier 1).  They go
-// on to the next unit together or not at all: a warp whose wait gave up would leave
-// the others at a barrier.
-__device__ __forceinline__ bool all_agree(bool mine) {
+// Whether all `threads` that meet at barrier `bar` say so (all of the first eight warps).
+// They go on to the next unit together or not at all: a warp whose wait gave up would
+// leave the others at a barrier.
+__device__ __forceinline__ bool all_agree(bool mine, int bar = 1, int threads = 256) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.and.pred p, 1, 256, q;\n\t"
+      "barrier.cta.red.and.pred p, %2, %3, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(mine ? 1u : 0u)
+      : "r"(mine ? 1u : 0u), "r"(bar), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -203,6 +203,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// The thread's stores have read shared memory; have been done.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Two fp32 operations at once.
 __device__ __forceinline__ uint64_t pair(float x, float y) {

@@ -24,7 +24,7 @@ struct PackedAttnShape {
   uint32_t* status;
 };
 
-// Tensor maps.  q, out, dout: [d, group, KV head, token], one box of 64 columns = the
+// Tensor maps.  q, out (in the forward pass only where by_tile), dout: [d, group, KV head, token], one box of 64 columns = the
 // rows (token, head of the group) of packed_tile_tokens(G) tokens; k, v: [d,
 // token, KV head], one box of 64 columns x 128 tokens.  128-byte swizzle.
 struct PackedAttnMaps {
@@ -38,7 +38,11 @@ struct PackedAttnOut {
   void* out;
   PackedStride st;
   float* lse;   // [Tq, Hkv * G] or null
+  bool by_tile;   // whole tiles through maps.out (head dim 64)
 };
+
+// Whether the forward pass writes whole tiles by TMA.
+bool packed_attn_by_tile(const PackedAttnShape& s, int D);
 
 // The inputs behind the maps, for single rows.
 struct PackedAttnIn {
