@@ -278,7 +278,7 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
     if ((rc = check_status(c))) return rc;
     PackedAttnMaps maps = {};
     if ((rc = attn_maps(&maps, args, c))) return rc;
-    const bool by_tile = packed_attn_by_tile(c.s, c.D);
+    const bool by_tile = packed_attn_by_tile(c.s);
     if (by_tile && (rc = row_map(&maps.out, c, out, o, "out"))) return rc;
     const PackedAttnOut to{out, {o.token, o.head}, lse, by_tile};
     const PackedAttnIn in{args->q, args->k, args->v, {c.q.token, c.q.head}, {c.k.token, c.k.head},

@@ -56,24 +56,29 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kCheckWarp = 10;
 constexpr int kMaxPartial = 3;   // V tiles that rows attend in part: 256 queries' own keys lie in three tiles at most
-constexpr int kRing = 163840;   // bytes of the K / V ring
 constexpr float kLazy = 8.0f;   // log2 of how far scores may pass the running maximum
 // log2 of P at the running maximum.  fp16 loses what is below 2^-25, which many
 // small probabilities could add up to; its largest value leaves room for 2^(6 + 8).
 template <bool kFp16>
 constexpr float kTop = kFp16 ? 6.0f : 0.0f;
 
-template <int kD>
+// kFew: few units, whose code each SM meets once.  kTiles: CTAs have more than one, and
+// whole tiles of out are written by TMA.  kSplit: one unit per cluster, among whose
+// CTAs its key tiles are divided.
+enum class Form { kFew, kTiles, kSplit };
+
+template <int kD, Form kForm>
 struct Layout {
   static constexpr int kTile = kD / 64 * 16384;   // 128 rows of kD
+  static constexpr int kRing = kD == 128 && kForm == Form::kTiles ? 131072 : 163840;   // bytes of the K / V ring
   static constexpr int kStages = kRing / kTile;
   static constexpr int kBuffers = kD == 64 ? 3 : 2;   // of scores
   // V tiles that may be looked through at once, as many as the ring holds: each has barriers of its own, so
   // that none is two phases ahead of who waits for it.
   static constexpr int kLooks = (kStages + 1) / 2;
   static constexpr uint32_t kColO = 128 * kBuffers;
-  static constexpr int kOut = 2 * kTile + kRing;   // by_tile: a tile of out for each half
-  static constexpr int kBars = kOut + (kD == 64 ? 2 * kTile : 0);
+  static constexpr int kOut = 2 * kTile + kRing;   // kTiles: 64 columns of out for each half
+  static constexpr int kBars = kOut + (kForm == Form::kTiles ? 2 * 16384 : 0);
   // Barriers: a unit found and done with; Q of each tile full and free; ring full and empty; V tiles
   // attended in part, before and after they were looked through; of each tile S (three buffers: three, in
   // turn); of each score buffer P; of each tile P V (three, in turn) and x read; kSplit: all products; of each
@@ -111,12 +116,12 @@ __device__ __forceinline__ float dot(const uint16_t* q, const uint16_t* k) {
   return z;
 }
 
-// kSplit: one unit per cluster of `ctas` CTAs, among which its key tiles are divided.
-template <int kD, bool kFp16, bool kSplit>
+template <int kD, bool kFp16, Form kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attn_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnIn in,
                        const PackedAttnOut o, const int ctas, const int halves) {
-  using L = Layout<kD>;
+  using L = Layout<kD, kForm>;
+  constexpr bool kSplit = kForm == Form::kSplit, kTiles = kForm == Form::kTiles;
   constexpr int kTile = L::kTile, kStages = L::kStages, kBuffers = L::kBuffers;
   constexpr uint32_t kColO = L::kColO;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -483,12 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t o_addr = lane_addr + kColO + x * kD;
     const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
-    const bool wide = packed::wide_rows(o.out, o.st), by_tile = kD == 64 && !kSplit && o.by_tile;
+    const bool wide = packed::wide_rows(o.out, o.st);
     bool ok = true;
     int jobs = 0, done = 0, used = 0;   // of all units before: jobs, this half's, and its units
     for (int k = 0;; ++k) {
       const bool more = next_unit(k, &ok, &u);
-      if (by_tile ? !packed::all_agree(more, 2 + x, 128) : !more) break;
+      if (kTiles ? !packed::all_agree(more, 2 + x, 128) : !more) break;
       any = true;
       const int token = u.t0 + x * tile_tokens + row_token;   // in the sequence
       const bool active = x < halves && r < tile_tokens * s.G && token < u.seq.n_q;
@@ -597,9 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4 four = *reinterpret_cast<const uint4*>(gone + 4 * (j - u.looked));
         cleared |= four.x | four.y | four.z | four.w;
       }
-      // D = 64 at once, so that the next unit's P V can start; 128 columns in registers beside their stores cost
-      // more than that gives (48 prompts of 512, 8 KV heads of 4: 149 or 158 us).
-      constexpr int kPart = kD == 64 ? 64 : 32;
+      constexpr int kPart = kTiles ? 64 : 32;   // columns at a time
 #pragma unroll 1
       for (int c0 = 0; c0 < kD; c0 += kPart) {
         uint32_t w[kPart];
@@ -646,9 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kPart / 2; ++i)
           p[i] = !none ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv)
                        : 0u;
-        if (kPart == kD && by_tile && x < halves && u.t0 + (x + 1) * tile_tokens <= u.seq.n_q) {
+        if (kTiles && x < halves && u.t0 + (x + 1) * tile_tokens <= u.seq.n_q) {
           // Every row of the tile is a query's.
-          uint8_t* tile = smem + L::kOut + x * kTile;
+          uint8_t* tile = smem + L::kOut + x * 16384;
           if (r == 0) packed::stores_read();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + x) : "memory");
 #pragma unroll
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + x) : "memory");
           if (r == 0)
-            packed::tma_store_4d(&maps.out, smem_u32(tile), 0, 0, u.h, u.seq.q0 + u.t0 + x * tile_tokens);
+            packed::tma_store_4d(&maps.out, smem_u32(tile), c0, 0, u.h, u.seq.q0 + u.t0 + x * tile_tokens);
         } else if (active) {
 #pragma unroll
           for (int c = 0; c < kPart; c += 32)
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unit_done(k);
       if (kSplit) break;
     }
-    if (by_tile && r == 0) packed::stores_done();
+    if (kTiles && r == 0) packed::stores_done();
   }
   if (kSplit) {
     // ---- each CTA joins its share of the rows over the cluster: with M the largest m,
@@ -749,12 +752,12 @@ int clusters_at_once(int ctas) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (!known[dev][i]) {
-    const auto kernel = packed_attn_kernel<kD, kFp16, true>;
+    const auto kernel = packed_attn_kernel<kD, kFp16, Form::kSplit>;
     int n = 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Layout<kD>::kBytes;
+    cfg.dynamicSmemBytes = Layout<kD, Form::kSplit>::kBytes;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = ctas;
@@ -762,7 +765,7 @@ int clusters_at_once(int ctas) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kD>::kBytes) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kD, Form::kSplit>::kBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
@@ -798,16 +801,21 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
   const int ctas = split<kD, kFp16>(s, 2 * one);
   const int halves = ctas == 1 && most(one) * s.Hkv <= device_sm_count() ? 1 : 2;
   const long long units = most(halves * one);
-  const auto kernel = ctas > 1 ? packed_attn_kernel<kD, kFp16, true> : packed_attn_kernel<kD, kFp16, false>;
-  static packed::SharedMemory shared[2];   // of each of the two kernels
-  const cudaError_t e = shared[ctas > 1].allow(kernel, Layout<kD>::kBytes);
+  const auto kernel = ctas > 1    ? packed_attn_kernel<kD, kFp16, Form::kSplit>
+                      : o.by_tile ? packed_attn_kernel<kD, kFp16, Form::kTiles>
+                                  : packed_attn_kernel<kD, kFp16, Form::kFew>;
+  const int bytes = ctas > 1    ? Layout<kD, Form::kSplit>::kBytes
+                    : o.by_tile ? Layout<kD, Form::kTiles>::kBytes
+                                : Layout<kD, Form::kFew>::kBytes;
+  static packed::SharedMemory shared[3];   // of each of the three kernels
+  const cudaError_t e = shared[ctas > 1 ? 2 : o.by_tile].allow(kernel, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // A CTA per SM, or a cluster per unit.
   const long long grid = ctas > 1 ? units * s.Hkv * ctas : std::min<long long>(units * s.Hkv, device_sm_count());
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Layout<kD>::kBytes;
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -823,11 +831,11 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
 
 }  // namespace
 
-// Where a CTA has more than one unit, and shared memory has room (D = 64): a thread's row
-// is 128 bytes, and a warp's stores of 32 rows at once take twice the time of
-// whole lines.
-bool packed_attn_by_tile(const PackedAttnShape& s, int D) {
-  return D == 64 && static_cast<long long>(s.Tq) * s.Hkv > 2ll * packed_tile_tokens(s.G) * device_sm_count();
+// Where a CTA has more than one unit: a warp's stores of 32 rows at once, 32 bytes of each,
+// take twice the time of whole lines (24 prompts of up to 2047 tokens, d 64: 177 or 170
+// us; 48 of 512, d 128: 149 or 140).
+bool packed_attn_by_tile(const PackedAttnShape& s) {
+  return static_cast<long long>(s.Tq) * s.Hkv > 2ll * packed_tile_tokens(s.G) * device_sm_count();
 }
 
 cudaError_t launch_packed_attn(const PackedAttnShape& s, int D, bool fp16, const PackedAttnMaps& maps,

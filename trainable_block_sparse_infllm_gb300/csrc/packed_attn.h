@@ -38,11 +38,11 @@ struct PackedAttnOut {
   void* out;
   PackedStride st;
   float* lse;   // [Tq, Hkv * G] or null
-  bool by_tile;   // whole tiles through maps.out (head dim 64)
+  bool by_tile;   // whole tiles through maps.out
 };
 
 // Whether the forward pass writes whole tiles by TMA.
-bool packed_attn_by_tile(const PackedAttnShape& s, int D);
+bool packed_attn_by_tile(const PackedAttnShape& s);
 
 // The inputs behind the maps, for single rows.
 struct PackedAttnIn {
