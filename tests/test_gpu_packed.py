@@ -113,6 +113,34 @@ def test_units_one_after_another(dev, dim, dtype, count):
         check(name, grad, want)
 
 
+@pytest.mark.parametrize("dim,dtype,group,layout", [(64, "fp16", 5, "heads"), (128, "bf16", 7, "heads"),
+                                                    (128, "fp16", 16, "own"), (64, "bf16", 32, "fused")])
+def test_many_units_of_odd_groups(dev, dim, dtype, group, layout):
+    """More than two tiles for every SM, so whole tiles are written at once: rows behind each, and of none, stay."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from packed_helpers import Step, check, plain
+    q_lens = [700, 1, 0, 640, 333, 411, 25, 128, 256]
+    k_lens = [700, 1, 40, 500, 900, 411, 25, 129, 256]           # the fourth: rows that attend no key
+    step = Step(dev, dtype, dim, 4, group, q_lens, None if layout == "fused" else k_lens, layout, seed=group)
+    assert step.q_starts[-1] * 4 > 2 * (128 // group) * torch.cuda.get_device_properties(0).multi_processor_count
+    want = plain(step)
+    out, lse = step.forward(T)
+    check("out", out, want)
+    check("lse", lse, want)
+    for name, grad in zip(("dq", "dk", "dv"), step.backward(T, out, lse)):
+        check(name, grad, want)
+    assert (out[step.q_starts[-1]:] == 7.0).all() and (lse[step.q_starts[-1]:] == 7.0).all()
+    first = 300
+    step.v[first, 2, 5] = math.inf                               # of the first sequence
+    odd, _ = step.forward(T)
+    hit = odd[first:700, 2 * group:3 * group, 5]
+    assert (hit == math.inf).all()
+    odd[first:700, 2 * group:3 * group] = out[first:700, 2 * group:3 * group]
+    assert torch.equal(odd, out)                                 # the rest, bit for bit
+    assert _status() == 0
+
+
 def test_attention_of_4096_sequences_of_one_token(dev):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
