@@ -71,12 +71,13 @@ struct DqLayout {
   static constexpr int kUnit = 0, kUnitFree = 2, kDoFull = 4, kDoFree = 5, kKFull = 6, kKEmpty = kKFull + kKs,
                        kVFull = kKEmpty + kKs, kVEmpty = kVFull + kVs, kTail = kVEmpty + kVs, kCleared = kTail + 2,
                        kPair = kCleared + 2, kFree = kPair + 1, kDsFull = kFree + 1, kDqDone = kDsFull + 1,
-                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kEnd = kOutRead + 1,
-                       kNumBars = kEnd + 2;
+                       kAccFree = kDqDone + 1, kQIn = kAccFree + 1, kOutRead = kQIn + 1, kLse = kOutRead + 1,
+                       kEnd = kLse + 2, kNumBars = kEnd + 2;
   static constexpr int kUnits = kBars + (8 * kNumBars + 15) / 16 * 16;   // two units, 32 bytes each
   static constexpr int kSlot = kUnits + 64;
   static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
-  static constexpr int kBytes = kSum + 1024 + 1024;
+  static constexpr int kLses = kSum + 1024;   // of two units [128]: lse log2(e)
+  static constexpr int kBytes = kLses + 1024;   // (no slack: where the base is not aligned the kernel says so)
 };
 // Tensor memory: S, dout . v, dS, Q (16 bits: the A operand of S), dq.  Q comes through
 // the K ring, as the element before K_0, and makes room there: a tile of K is read
@@ -96,8 +97,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const __grid_constant__ PackedAttnMaps maps, const PackedAttnShape s, const PackedAttnGrads g) {
   using L = DqLayout<kD>;
   constexpr int kTile = L::kTile, kKs = L::kKs, kVs = L::kVs;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) % 1024 != 0) {   // the whole grid: shared memory starts on 1024 bytes or it does not
+    if (threadIdx.x == 0) atomicOr(s.status, kStatusBounds);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   int4* units = reinterpret_cast<int4*>(smem + L::kUnits);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlot);
@@ -373,10 +377,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       packed::products_end(&bars[L::kEnd + 1], issuer, s.status);
     } else {
-      // ----------------------- K rows behind the sequence: they meet dS = 0
+      // ----------- the rows' lse, and K rows behind the sequence: they meet dS = 0
       Place pk = {0, 0};
       int even = 0, odd = 0;
+      float* lses = reinterpret_cast<float*>(smem + L::kLses);
       for (int k = 0; next_unit(k, &ok, &u); ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // a unit ahead of who needs it
+          const int r = lane + 32 * i, token = u.t0 + r / s.G;
+          const long long at = (u.seq.q0 + token) * static_cast<long long>(s.Hkv * s.G) + u.h * s.G + r % s.G;
+          // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
+          float lse2 = 0.f;
+          if (r < tile_tokens * s.G && token < u.seq.n_q)
+            lse2 = u.before + token >= 0 ? __ldg(g.lse + at) * kLog2e : INFINITY;
+          lses[(k & 1) * 128 + r] = lse2;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kLse + (k & 1)]);
         if (u.steps > 0) next(pk, kKs);   // Q's stage
         for (int j = 0; j < u.steps; ++j) {
           if (u.clears && j == u.back) {
@@ -394,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ P and dS
     packed::regs_up<216>();
     const int half = warp >> 2;   // columns 64 half .. 64 half + 63
-    const int r = tid & 127;
+    const int r = tid & 127, row_token = r / s.G, row_head = r % s.G;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + kDqS + 64 * half, dp_addr = lane_addr + kDqDp + 64 * half;
     float* part = reinterpret_cast<float*>(smem + L::kSum);
@@ -410,14 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int pairs = 0, summed = 0, uses = 0;   // in all: pairs of scores read, dS written, units with keys
     Place pk = {0, 0}, pv = {0, 0};
     for (int k = 0; packed::all_agree(next_unit(k, &ok, &u)); ++k) {
-      const int token = u.t0 + r / s.G;
+      const int token = u.t0 + row_token;
       const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 : 0;
-      const int head = u.h * s.G + r % s.G;
+      const int head = u.h * s.G + row_head;
       const long long row = u.seq.q0 + token;
-      // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
-      float D = 0.f, lse2 = 0.f;
-      if (active) lse2 = limit > 0 ? __ldg(g.lse + row * (s.Hkv * s.G) + head) * kLog2e : INFINITY;
+      float D = 0.f;
       if (u.steps > 0) {
         // Q into tensor memory: S of the last unit has been read, so its Q has been.
         wait(L::kKFull + pk.stage, pk.phase);
@@ -463,6 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++uses;
       }
       const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
+      wait(L::kLse + (k & 1), k >> 1);
+      const float lse2 = reinterpret_cast<const float*>(smem + L::kLses)[(k & 1) * 128 + r];
       const uint64_t down = packed::pair(-lse2, -lse2);
       // Columns of tile j that the row attends, of this half's 64; 64 where no row of the warp needs a mask.
       auto attended = [&](int j) { return j >= whole ? limit - j * 128 - 64 * half : 64; };
@@ -610,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kOwn = kD == 64;   // P^T and dS^T have columns of their own
   constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off again: from dout . v - D for dS, from dv
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) % 1024 != 0) {   // the whole grid: shared memory starts on 1024 bytes or it does not
+  if (smem_u32(smem) % 1024 != 0) {   // (as above)
     if (threadIdx.x == 0) atomicOr(s.status, kStatusBounds);
     return;
   }
