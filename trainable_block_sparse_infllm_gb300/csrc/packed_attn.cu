@@ -155,6 +155,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Tensor memory is taken once the kernel before has ended and before the next one may start: neither ever
   // waits for columns that the other holds.
   pdl_wait();
+  packed::Walker walker;   // of the warp that finds the units
+  bool bad = false;
+  if (warp == kTmaWarp) walker.start(s, halves * tile_tokens, false, &bad);
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
@@ -211,9 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed::regs_down<72>();
     if (warp == kTmaWarp) {
       // ---------------------------------------------------- units and loads
-      packed::Walker walker;
-      bool bad = false, ok = true;
-      walker.start(s, halves * tile_tokens, false, &bad);
+      bool ok = true;
       int issued = 0, seen = 0, q_uses[2] = {0, 0};   // ring copies, V tiles looked through, Q tiles
       const int stride = kSplit ? 1 : static_cast<int>(gridDim.x);
       for (int k = 0;; ++k) {

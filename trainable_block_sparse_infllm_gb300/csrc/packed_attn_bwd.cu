@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Tensor memory is taken once the kernel before has ended and before the next one may start: neither ever
   // waits for columns that the other holds.
   pdl_wait();
+  packed::Walker walker;   // of the warp that finds the units
+  bool bad = false;
+  if (warp == kTmaWarp) walker.start(s, tile_tokens, false, &bad);
   if (warp == kPairWarp) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
@@ -186,9 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed::regs_down<72>();
     if (warp == kTmaWarp) {
       // ------------------------------------------------------ units and loads
-      packed::Walker walker;
-      bool bad = false;
-      walker.start(s, tile_tokens, false, &bad);
       const int stride = static_cast<int>(gridDim.x);
       int k_copies = 0, v_copies = 0, tails[2] = {0, 0}, uses = 0;   // (tails: of units of each parity)
       // The next stage of the K ring, with a copy of `bytes` announced on `bar` (null: the stage's own).
