@@ -429,7 +429,8 @@ def _turn(x, positions, freq, scale, part, interleaved, transpose):
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dim,part,heads,tokens", [(128, 128, 3, 5), (64, 32, 40, 700), (512, 512, 1, 3),
-                                                   (80, 48, 2, 33), (128, 16, 17, 1), (16, 16, 1, 2000), (256, 128, 9, 1300)])
+                                                   (80, 48, 2, 33), (128, 16, 17, 1), (16, 16, 1, 2000),
+                                                   (256, 128, 9, 1300)])
 def test_rotary(dev, dtype, interleaved, dim, part, heads, tokens):
     import torch
     import trainable_block_sparse_infllm_gb300 as T

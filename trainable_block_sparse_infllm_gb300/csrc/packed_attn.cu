@@ -36,12 +36,13 @@
 //
 // Measured (GB300): one prompt of 16,384 tokens, 2 KV heads of 16, d 128, 1.24 to 1.34 ms,
 // 1.64 to 1.78 PFLOP/s, 86 to 93% of the measured library product: the tensor cores
-// (72% busy at 8K, the rest goes to the handing over of S and P).  24 prompts of up to 2047 tokens, 8 heads
-// of 4, d 64, 190 us: exponentials (16 of 32 a cycle and SM are issued) and the start
-// and end of units of five tiles.  12 tokens after 32,000 in 4 sequences 48 us: the 8
-// units' clusters have 12 CTAs, 96 SMs.  One prompt of 301 tokens 9 us in a graph.
-// With the products issued by lane 0 of a diverged warp the first took 1.92 ms, with a
-// CTA for each unit the second took 283 us.
+// (72% busy at 8K, the rest goes to the handing over of S and P).  24 prompts of up to
+// 2047 tokens, 8 heads of 4, d 64, 170 us: the softmax warps' chain of a tile (1.9
+// thousand cycles, two warps of a scheduler, a quarter of it waiting for S) and 2.2
+// thousand cycles at the end of units of five tiles.  12 tokens after 32,000 in 4
+// sequences 47 us: the 8 units' clusters have 12 CTAs, 96 SMs.  One prompt of 301
+// tokens 8.7 us in a graph.  With the products issued by lane 0 of a diverged warp the
+// first took 1.92 ms, with a CTA for each unit the second took 283 us.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -62,9 +63,12 @@ constexpr float kLazy = 8.0f;   // log2 of how far scores may pass the running m
 template <bool kFp16>
 constexpr float kTop = kFp16 ? 6.0f : 0.0f;
 
-// kFew: few units, whose code each SM meets once.  kTiles: CTAs have more than one, and
-// whole tiles of out are written by TMA.  kSplit: one unit per cluster, among whose
-// CTAs its key tiles are divided.
+// kTiles: CTAs have more than one unit; whole tiles of out go through shared memory and
+// TMA, since a warp's stores of 32 rows at once, 32 bytes of each, take twice the time
+// of whole lines (24 prompts of up to 2047 tokens, d 64: 177 us or 170; 48 of 512,
+// d 128: 149 or 142).  kFew: they have one, and leave that out, for each SM meets the code
+// only once (one prompt of 301 tokens: 11.3 us or 10.6).  kSplit: one unit per cluster,
+// among whose CTAs its key tiles are divided.
 enum class Form { kFew, kTiles, kSplit };
 
 template <int kD, Form kForm>
@@ -766,7 +770,8 @@ int clusters_at_once(int ctas) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kD, Form::kSplit>::kBytes) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<kD, Form::kSplit>::kBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();

@@ -24,7 +24,8 @@ struct PackedAttnShape {
   uint32_t* status;
 };
 
-// Tensor maps.  q, out (in the forward pass only where by_tile), dout: [d, group, KV head, token], one box of 64 columns = the
+// Tensor maps.  q, out (the forward pass's only where by_tile), dout: [d, group, KV
+// head, token], one box of 64 columns = the
 // rows (token, head of the group) of packed_tile_tokens(G) tokens; k, v: [d,
 // token, KV head], one box of 64 columns x 128 tokens.  128-byte swizzle.
 struct PackedAttnMaps {
