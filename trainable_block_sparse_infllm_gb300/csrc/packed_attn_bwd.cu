@@ -28,10 +28,10 @@
 // the tiles that TMA brought.  Two warpgroups share a tile's columns.
 //
 // Measured (GB300): one sequence of 8192 tokens, 2 KV heads of 16, d 128, 1.06 ms
-// (dq 465 us, tensor cores 81% busy; dk and dv 595, 87%): 1.30 PFLOP/s of five products,
+// (dq 461 us, tensor cores 82% busy; dk and dv 604, 87%): 1.30 PFLOP/s of five products,
 // 1.82 of the seven that are issued, 96% of the measured library product.  16
-// documents of 17 to 2500 tokens, 4 heads of 5, d 64, fp16, 400 us (dq 228, 37%; dk and dv
-// 172, 54%): the exponentials, the second walk of the rows that attend up to 1024 keys and
+// documents of 17 to 2500 tokens, 4 heads of 5, d 64, fp16, 400 us (dq 229, 37%; dk and dv
+// 175, 54%): the exponentials, the second walk of the rows that attend up to 1024 keys and
 // the start and end of short units.
 #include <algorithm>
 #include <type_traits>
