@@ -367,6 +367,32 @@ def test_other_stream_and_graph(dev):
     assert _status() == 0
 
 
+def test_two_calls_at_once(dev):
+    """Forward and backward passes of two batches on two streams give what they give one after the other."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from packed_helpers import Step
+    steps = [Step(dev, "bf16", 128, 2, 4, [900, 31, 1700]), Step(dev, "fp16", 64, 4, 5, [64] * 40 + [700, 1100])]
+    want = []
+    for step in steps:
+        out, lse = step.forward(T)
+        want.append((out, lse, *step.backward(T, out, lse)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, step in enumerate(steps):
+            with torch.cuda.stream(streams[i]):
+                out, lse = step.forward(T)
+                got[i].append((out, lse, *step.backward(T, out, lse)))
+    torch.cuda.synchronize()
+    for once, many in zip(want, got):
+        for result in many:
+            for a, b in zip(once, result):
+                assert torch.equal(a.nan_to_num(9.0), b.nan_to_num(9.0))
+    assert _status() == 0
+
+
 def test_binding_refuses(dev):
     import torch
     import trainable_block_sparse_infllm_gb300 as T
