@@ -664,7 +664,9 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
  * run to run; keys that no query attends get 0.
  *   out, lse  as the forward call on the same arguments wrote them.
  *   grad_strides (host memory): between tokens and heads of out, dout, dq, dk, dv.
- *   P and dS enter the sums in the type of q: a non-finite dout or q row reaches every
+ *   P and dS enter the sums in the type of q, in fp16 times powers of two (of a row, and of the
+ *           rows that share keys), so that neither small nor large upstream gradients leave
+ *           its range.  A non-finite dout or q row reaches every
  *           key row of its own sequence and KV head, a non-finite key every query row.
  * Workspace: infllmv2_packed_workspace_size(args) bytes (D and lse of each row).  Written before
  * it is read in every call: calls that may overlap on the GPU need their own.

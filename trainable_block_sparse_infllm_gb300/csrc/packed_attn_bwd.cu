@@ -54,6 +54,30 @@ constexpr int kUp = kFp16 ? 8 : 0;
 // Rows that attend at most so many tiles of keys get D from their scores.
 constexpr int kExactTiles = 8;
 
+// fp16's dS.  Upstream gradients of 10^-3 to 10^-4 are ordinary (a mean over tokens), and dS, a probability times
+// them, is then among fp16's subnormal numbers or below; with large ones it passes 65504.  So dS is formed times
+// a power of two, which comes off the fp32 sums.  |dS| <= max |dout . v| + |D|, and what a bound is above the truth
+// only costs bits of a range of 2^40, so norms will do.
+//   * dq: one power per row, in the exponent of P.  Rows of up to kExactTiles tiles know |dout . v| and D before they
+//     form dS: 8 times their sum, at most, goes to 2^15.  Longer ones take |dout| |out|, which is about |dS| where
+//     a few keys have the weight and far above it where many have: at most 4 times that goes to 2^10.  A row whose
+//     dS passes 2^15.5 all the same (values that cancel in out; by the sum of squares) has its unit done once more,
+//     with the power from that sum.
+//   * dk: one power per tile of keys, from the largest |dS| that dq found among the rows that attend it.
+// 3000 keys, d 64, dout of 10^-3 (10^-4): dq 0.094% (0.90%) off without the powers, 0.034% (0.20%) with them, which
+// is the rounding of the results; dout of 1000 and values of 50 gave infinities.  It costs 8% of the time of 16
+// documents of 17 to 2500 tokens, d 64 (429 or 460 us), and 5% of a sequence of 8192's.
+constexpr int kNoTop = -1000;   // of a row without a finite dS
+
+// The power for values below 2^top: `to` is log2 of where they go.  From 2^-30 to 2^20, which is beyond what
+// results in fp16 show, and keeps fp32 sums of squares finite.
+__device__ __forceinline__ int power_for(int top, int to) { return top == kNoTop ? 0 : min(max(to - top, -30), 20); }
+// The least `top` with 0 <= x < 2^top.
+__device__ __forceinline__ int top_of(float x) {
+  return x < INFINITY ? static_cast<int>(__float_as_uint(x) >> 23) - 126 : kNoTop;
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // ------------------------------------------------------------------- dq ----
 //
 // A CTA takes one tile of rows after another.  For step j (a tile of keys) the tensor
@@ -77,8 +101,12 @@ struct DqLayout {
   static constexpr int kSlot = kUnits + 64;
   static constexpr int kSum = kSlot + 16;   // [2][128]: sums over the halves of a row
   static constexpr int kLses = kSum + 1024;   // of two units [128]: lse log2(e)
-  static constexpr int kBytes = kLses + 1024;   // (no slack: where the base is not aligned the kernel says so)
+  static constexpr int kMost = kLses + 1024;   // [2][128] 16 bits: the larger of two halves
+  static constexpr int kTops = kMost + 512;    // of two units: the largest top_of of their rows; and the first row
+  static constexpr int kAgain = kTops + 16;    // a bit for each of kAgainUnits of the CTA's units: once more
+  static constexpr int kBytes = kAgain + 128;   // (no slack: where the base is not aligned the kernel says so)
 };
+constexpr int kAgainUnits = 1024;   // (further units share the bits: some are done once more for nothing)
 // Tensor memory: S, dout . v, dS, Q (16 bits: the A operand of S), dq.  Q comes through
 // the K ring, as the element before K_0, and makes room there: a tile of K is read
 // until its dS K is done, more than a step after its S.
@@ -88,8 +116,10 @@ struct DqUnit {
   packed::Sequence seq;
   int t0, h, before;   // its first query, its KV head; query t attends keys 0 .. before + t
   int n;               // tiles of keys
-  bool exact, clears;  // D from the scores; the last tile runs past the sequence
-  int steps, back;     // tiles walked (twice where exact), the first of the walk that sums dq
+  bool again;          // it has been done: D and the power of its dS are known
+  bool exact, clears;  // D not from out; the last tile runs past the sequence
+  int steps, back;     // tiles walked (twice where D comes from the scores), the first of the walk that sums dq
+  int number;          // among the CTA's, modulo kAgainUnits
 };
 
 template <int kD, bool kFp16>
@@ -132,13 +162,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
+  int* tops = reinterpret_cast<int*>(smem + L::kTops);
+  uint32_t* again = reinterpret_cast<uint32_t*>(smem + L::kAgain);
+  if (tid < 2) tops[tid] = kNoTop;
+  if (tid < kAgainUnits / 32) again[tid] = 0u;
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
 
-  // A unit from where it lies, (whether there is one, its tile, KV head), and its sequence.
+  // A unit from where it lies, (0, or 1 once more; -1: there is none; its tile, KV head and number), and its
+  // sequence.
   auto unit_of = [&](int4 at, int4 rows) {
     DqUnit u;
     u.seq = {rows.x, rows.y, rows.z, rows.w};
@@ -148,9 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int last = min(u.t0 + tile_tokens, u.seq.n_q) - 1;
     u.n = (max(u.before + last + 1, 0) + 127) / 128;
     u.clears = u.n * 128 > u.seq.n_k;
-    u.exact = u.n <= kExactTiles;
-    u.steps = u.exact && u.n > 1 ? 2 * u.n : u.n;
+    u.again = at.x > 0;
+    u.exact = u.again || u.n <= kExactTiles;
+    u.steps = u.exact && !u.again && u.n > 1 ? 2 * u.n : u.n;
     u.back = u.steps - u.n;
+    u.number = at.w;
     return u;
   };
   auto next_unit = [&](int k, bool* ok, DqUnit* u) {
@@ -202,17 +239,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ++k_copies;
         return st;
       };
-      for (int k = 0;; ++k) {
+      // Unit number n of the CTA.
+      auto find_unit = [&](int n, int4* at, int4* rows) {
         // Down the order of all units and back, so that no CTA gets the longest of each round.
         int i = static_cast<int>(blockIdx.x);
-        i = k * stride + (k & 1 ? stride - 1 - i : i);
-        int4 at = make_int4(-1, 0, i % s.Hkv, 0), rows = make_int4(0, 0, 0, 0);
+        i = n * stride + (n & 1 ? stride - 1 - i : i);
         int b, level;
-        if (walker.find(s, i / s.Hkv, tile_tokens, false, &b, &level, &bad)) {
-          at.x = 0;
-          at.y = level;
-          const packed::Sequence seq = packed::sequence(s, b, &bad);
-          rows = make_int4(seq.q0, seq.n_q, seq.k0, seq.n_k);
+        if (!walker.find(s, i / s.Hkv, tile_tokens, false, &b, &level, &bad)) return false;
+        *at = make_int4(0, level, i % s.Hkv, n % kAgainUnits);
+        const packed::Sequence seq = packed::sequence(s, b, &bad);
+        *rows = make_int4(seq.q0, seq.n_q, seq.k0, seq.n_k);
+        return true;
+      };
+      bool repeats = false, may_repeat = false;   // past the last unit; there was one that may be done once more
+      uint32_t wanted = 0u;                       // the lane's 32 bits of those that are
+      for (int k = 0, number = 0;; ++k) {
+        int4 at = make_int4(-1, 0, 0, 0), rows = make_int4(0, 0, 0, 0);
+        bool found = !repeats && find_unit(number, &at, &rows);
+        if (found) {
+          ++number;
+        } else if (!repeats && may_repeat) {
+          // Once more: each unit says so before it is done with.
+          repeats = true;
+          for (int d = k >= 2 ? 2 : 1; d > 0 && ok; --d)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&bars[L::kUnitFree + ((k - d) & 1)], ((k - d) >> 1) & 1, s.status));
+          wanted = again[lane];
+          number = 0;
+          walker.start(s, tile_tokens, false, &bad);
+        }
+        if (repeats && __any_sync(0xffffffffu, wanted != 0u)) {
+          while ((found = find_unit(number, &at, &rows))) {
+            ++number;
+            if ((__shfl_sync(0xffffffffu, wanted, at.w >> 5) >> (at.w & 31)) & 1) break;
+          }
+          at.x = found ? 1 : -1;
         }
         if (k >= 2 && ok)
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[L::kUnitFree + (k & 1)], ((k >> 1) - 1) & 1, s.status));
@@ -225,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (at.x < 0) break;
         u = unit_of(at, rows);
+        may_repeat |= kFp16 && !u.exact;
         const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
         if (u.n > 0) {
           const int st = k_stage(row_bytes, nullptr);
@@ -415,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + kDqS + 64 * half, dp_addr = lane_addr + kDqDp + 64 * half;
     float* part = reinterpret_cast<float*>(smem + L::kSum);
+    uint16_t* larger = reinterpret_cast<uint16_t*>(smem + L::kMost);
     const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
     const bool wide = packed::wide_rows(g.dq, g.dq_st);
     // The sum of a row's two halves, in both threads that share it.
@@ -424,15 +487,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       return part[r] + part[128 + r];
     };
+    // The same, and top_of of sqrt((x + x')(y + y')), rounded up, with other values x and y >= 0 of the two.  (Once
+    // in a unit: no barrier keeps a second one from `larger`.)
+    auto both_and_top = [&](float v, float x, float y, int* top) {
+      larger[half * 128 + r] = static_cast<uint16_t>((__float_as_uint(x) >> 23) << 8 | __float_as_uint(y) >> 23);
+      const float sum = both(v);
+      const uint32_t both_tops = __vmaxu4(larger[r], larger[128 + r]);   // (biased exponents)
+      const int tx = static_cast<int>(both_tops >> 8) - 125, ty = static_cast<int>(both_tops & 0xffu) - 125;
+      *top = max(tx, ty) > 128 ? kNoTop : (tx + ty + 1) >> 1;   // (a sum is at most twice the larger)
+      return sum;
+    };
+    // fp16: the largest top_of of a unit's rows lies beside its first row's, once all warps are past the unit.
+    // (Thread 0 alone knows of it, and keeps the row's number and its own top_of beside the tops.)
+    if (tid == 0) tops[2] = -1;
+    auto tops_put = [&](int k) {
+      if (tid != 0 || tops[2] < 0) return;
+      g.rows[tops[2]].x =
+          __uint_as_float((static_cast<uint32_t>(tops[k & 1]) << 16) | (static_cast<uint32_t>(tops[3]) & 0xffffu));
+      tops[k & 1] = kNoTop;
+      tops[2] = -1;
+    };
     int pairs = 0, summed = 0, uses = 0;   // in all: pairs of scores read, dS written, units with keys
     Place pk = {0, 0}, pv = {0, 0};
-    for (int k = 0; packed::all_agree(next_unit(k, &ok, &u)); ++k) {
+    for (int k = 0;; ++k) {
+      const bool more = packed::all_agree(next_unit(k, &ok, &u));
+      if (kFp16) tops_put(k - 1);
+      if (!more) break;
       const int token = u.t0 + row_token;
       const bool active = r < tile_tokens * s.G && token < u.seq.n_q;
       const int limit = active ? u.before + token + 1 : 0;
       const int head = u.h * s.G + row_head;
       const long long row = u.seq.q0 + token;
       float D = 0.f;
+      int top = kNoTop;   // fp16: the row's |dS| < 2^top
       if (u.steps > 0) {
         // Q into tensor memory: S of the last unit has been read, so its Q has been.
         wait(L::kKFull + pk.stage, pk.phase);
@@ -453,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kQIn]);
         for (int i = 0; i <= u.steps; ++i) next(pk, kKs);
-        if (!u.exact) {   // D from dout and out, half of the columns each
+        if (!u.exact) {   // D from dout and out, half of the columns each; fp16: |dout| |out| for the power
+          float dd = 0.f, oo = 0.f;
           wait(L::kDoFull, uses);
           wait(L::kVFull + pv.stage, pv.phase);
           const uint8_t* x = smem + r * 128;
@@ -467,12 +555,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) {
               const float2 a = packed::unpack2<kFp16>(vs[e]), b = packed::unpack2<kFp16>(os[e]);
               D = fmaf(a.x, b.x, fmaf(a.y, b.y, D));
+              if (kFp16) {
+                dd = fmaf(a.x, a.x, fmaf(a.y, a.y, dd));
+                oo = fmaf(b.x, b.x, fmaf(b.y, b.y, oo));
+              }
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[L::kOutRead]);
           next(pv, kVs);
-          D = both(D);
+          D = kFp16 ? both_and_top(D, dd, oo, &top) : both(D);
         }
         for (int i = 0; i < u.steps; ++i) next(pv, kVs);
         ++uses;
@@ -480,10 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, active ? max(limit, 0) : 0x7fffffff)) / 128;
       wait(L::kLse + (k & 1), k >> 1);
       const float lse2 = reinterpret_cast<const float*>(smem + L::kLses)[(k & 1) * 128 + r];
-      const uint64_t down = packed::pair(-lse2, -lse2);
+      uint64_t down = packed::pair(-lse2, -lse2);
       // Columns of tile j that the row attends, of this half's 64; 64 where no row of the warp needs a mask.
       auto attended = [&](int j) { return j >= whole ? limit - j * 128 - 64 * half : 64; };
-      uint64_t rest = 0ull;   // the sum of dS
+      uint64_t rest = 0ull, squares = 0ull;   // the sums of dS and of its square, times the row's power
+      int e = 0;                              // fp16: log2 of what P, and so dS, is multiplied by
       uint32_t z[64], dp[64];
       // P and dout . v of the next step, 64 columns each, of which the tensor cores then form the next.
       auto probs = [&](int j) {
@@ -521,25 +614,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 halves = packed::unpair(d);
         return halves.x + halves.y;
       };
-      for (int t = 0; t < u.back; ++t) {   // the first walk, where there are two
-        probs(t);
-        D += sum_p(0.f);
+      auto sum_values = [&](uint64_t d) {   // of the columns in registers: sum (dout . v)^2
+        uint64_t c = 0ull;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          d = packed::fma2(value2(i), value2(i), d);
+          c = packed::fma2(value2(i + 1), value2(i + 1), c);
+        }
+        return packed::add2(d, c);
+      };
+      // fp16: the row's D and top_of of its |dS|, for dk and for a unit that is done once more.
+      auto put_row = [&](int top) {
+        const int in_warp = __reduce_max_sync(0xffffffffu, active ? top : kNoTop);
+        if (half == 0 && lane == 0) atomicMax(&tops[k & 1], in_warp);
+        const int at = static_cast<int>(row) * (s.Hkv * s.G) + head;   // (heads * tokens < 2^31)
+        if (half == 0 && active) g.rows[at] = make_float2(__uint_as_float(static_cast<uint32_t>(top) & 0xffffu), D);
+        if (tid == 0) {
+          tops[2] = at;
+          tops[3] = top;
+        }
+      };
+      // fp16: the row's power, which takes 2^top to 2^to.
+      auto set_power = [&](int to) {
+        e = power_for(top, to);
+        down = packed::pair(e - lse2, e - lse2);
+      };
+      if (u.again) {
+        if (active) {
+          const float2 was = g.rows[row * (s.Hkv * s.G) + head];
+          D = was.y;
+          top = static_cast<int16_t>(__float_as_uint(was.x) & 0xffffu);
+        }
+        if (kFp16) set_power(14);
+      } else if (kFp16 && !u.exact) {
+        set_power(10);
       }
-      if (u.back > 0) D = both(D);
-      for (int j = u.n - 1; j >= 0; --j) {
-        probs(j);
-        if (j == 0 && u.back == 0) {   // all of D is known now (one tile: D and dS are from the same registers)
-          const float2 halves = packed::unpair(rest);
-          D += both(halves.x + halves.y + sum_p(D));
+      // Both walks in one loop: what a unit runs through is short (the instruction cache).
+      float part_of_d = 0.f, moved = 0.f;   // (moved: by how much the scores' D differs from that of out)
+      uint64_t values = 0ull;   // fp16: sum (dout . v)^2
+      for (int t = 0; t < u.steps; ++t) {
+        const bool first_walk = t < u.back;
+        probs(first_walk ? t : u.steps - 1 - t);
+        // The last tile's sums complete D, where there is one walk (one tile: D and dS are from the same registers).
+        const bool completes = t + 1 == u.steps && u.back == 0 && !u.again;
+        if (first_walk || completes) {
+          part_of_d += sum_p(D);   // (in the first walk D is 0)
+          if (kFp16) values = sum_values(values);
+          if (completes || t + 1 == u.back) {
+            const float2 sums = packed::unpair(rest), squares_of = packed::unpair(values);
+            part_of_d += sums.x + sums.y;
+            if (kFp16 && u.exact) {   // (the top from all dout . v)
+              D = both_and_top(part_of_d, squares_of.x + squares_of.y, 0.5f, &top);
+              if (top != kNoTop) top = max(top, top_of(fabsf(D))) + 1;
+              set_power(15);
+            } else {
+              moved = both(part_of_d) * (kFp16 ? power(-e) : 1.f);
+              D += moved;
+            }
+          }
+          if (first_walk) continue;
         }
         const uint64_t minus_d = packed::pair(-D, -D);
         uint32_t ds[32];
+        auto form = [&](auto squared) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint64_t v = packed::mul2(prob2(i), packed::add2(value2(i), minus_d));
-          rest = packed::add2(rest, v);
-          const float2 w = packed::unpair(v);
-          ds[i] = packed::pack2<kFp16>(w.x, w.y);
+          for (int i = 0; i < 32; ++i) {
+            const uint64_t v = packed::mul2(prob2(i), packed::add2(value2(i), minus_d));
+            rest = packed::add2(rest, v);
+            if (decltype(squared)::value) squares = packed::fma2(v, v, squares);
+            const float2 w = packed::unpair(v);
+            ds[i] = packed::pack2<kFp16>(w.x, w.y);
+          }
+        };
+        if (kFp16 && !u.exact) {
+          form(std::true_type());
+        } else {
+          form(std::false_type());
         }
         if (summed > 0) wait(L::kDqDone, summed - 1);   // the last dS has been read
         ++summed;
@@ -549,7 +699,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
       }
-      if (half == 0 && active) g.rows[row * (s.Hkv * s.G) + head] = make_float2(lse2, D);
+      if (kFp16 && !u.exact) {
+        const float2 halves = packed::unpair(squares);
+        const float sum = both(halves.x + halves.y);
+        top = top_of(sqrtf(sum) * power(-e) + fabsf(moved));   // (dk has D from the scores in all its tiles)
+        if (sum >= 0x1p31f && sum < INFINITY && active) atomicOr(&again[u.number >> 5], 1u << (u.number & 31));
+      }
+      if (kFp16 && !u.again) {
+        put_row(top);
+      } else if (!u.again && half == 0 && active) {
+        g.rows[row * (s.Hkv * s.G) + head] = make_float2(lse2, D);
+      }
+      const float off = kFp16 ? power(-e) : 1.f;
       if (u.n > 0) wait(L::kDqDone, summed - 1);
       uint16_t* dq = static_cast<uint16_t*>(g.dq) + row * g.dq_st.token + head * g.dq_st.head;
 #pragma unroll 1
@@ -566,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            v[i] = limit > 0 ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * s.scale,
-                                                    __uint_as_float(w[2 * i + 1]) * s.scale)
+            v[i] = limit > 0 ? packed::pack2<kFp16>(__uint_as_float(w[2 * i]) * off * s.scale,
+                                                    __uint_as_float(w[2 * i + 1]) * off * s.scale)
                              : 0u;
           packed::store_row(dq + col, v, wide);
         }
@@ -625,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = DkvLayout<kD>;
   constexpr int kTile = L::kTile, kStages = L::kStages;
   constexpr bool kOwn = kD == 64;   // P^T and dS^T have columns of their own
-  constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off again: from dout . v - D for dS, from dv
+  constexpr float kDown = 1.f / (1 << kUp<kFp16>);   // takes kUp off dv again
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) % 1024 != 0) {   // (as above)
     if (threadIdx.x == 0) atomicOr(s.status, kStatusBounds);
@@ -637,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + L::kRing;
   float* rows = reinterpret_cast<float*>(smem + L::kRows);
   float4* parts = reinterpret_cast<float4*>(ring);   // at the end: this CTA's dv and dk, 2 x 128 rows of kD
+  int* top = scratch + 41;   // fp16: the largest top_of of the rows that attend the tile
   const int tid = threadIdx.x, warp = packed::warp_index(), lane = tid & 31;
 
   pdl_wait();
@@ -658,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int last_rows = (seq.n_q - tile_token(n - 1)) * s.G;
   const bool clears = n > 0 && last_rows < tile_rows;
 
+  if (tid == 0) *top = kNoTop;
   if (tid < L::kNumBars) {
     // (D = 64: kSFull is both scores, kPFull that they have been read, kDsFull both of P^T and dS^T.)
     const bool by_warps = tid == L::kPFull || tid == L::kDsFull || tid == L::kRowsFree || tid == L::kRowsFree + 1;
@@ -687,6 +850,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](int bar, int phase) {
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[bar], phase & 1, s.status));
     tc::fence_after_sync();
+  };
+  // fp16: what dout . v - D is multiplied by for dS, beside P's 2^kUp, once the computing warps have found `top`.
+  auto dp_power = [&]() { return power_for(*top, 14) - kUp<kFp16>; };
+  auto top_found = [&]() {
+    if (kFp16) asm volatile("bar.sync 1, 288;" ::: "memory");   // (the computing warps and kRowsWarp)
   };
 
   if (warp >= 8) {
@@ -723,27 +891,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Each row tile's (lse, D), +inf for a row of no query: its P is 0.  Two tiles are on their way in
       // registers while a buffer is waited for.
       int token_in[4];          // of rows lane, lane + 32, ...: their token in a tile
-      const float2* from[4];
+      long long from[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = lane + 32 * k;
         token_in[k] = r < tile_rows ? r / s.G : 0x40000000;   // (no such token)
-        from[k] = g.rows + static_cast<long long>(seq.q0 + t0 + r / s.G) * (s.Hkv * s.G) + h * s.G + r % s.G;
+        from[k] = static_cast<long long>(seq.q0 + t0 + r / s.G) * (s.Hkv * s.G) + h * s.G + r % s.G;
       }
       const long long step = static_cast<long long>(tile_tokens) * s.Hkv * s.G;
       auto load = [&](int i, float2 (&v)[4]) {
         const int tile = rank + i * ctas, left = seq.n_q - t0 - tile * tile_tokens;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = i < n && token_in[k] < left ? __ldg(from[k] + tile * step) : make_float2(INFINITY, 0.f);
+        for (int k = 0; k < 4; ++k) {
+          v[k] = make_float2(INFINITY, 0.f);
+          if (i < n && token_in[k] < left) {
+            const long long at = from[k] + tile * step;
+            v[k] = kFp16 ? make_float2(g.lse[at], g.rows[at].y) : g.rows[at];   // (fp16: lse as it is, see put)
+          }
+        }
       };
+      float d_power = 1.f;
       auto put = [&](int i, const float2 (&v)[4]) {
         float* to = rows + (i & 1) * 256 + lane;
         if (i >= 2) wait(L::kRowsFree + (i & 1), i / 2 - 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          to[32 * k] = kUp<kFp16> - v[k].x;   // negated: what is added
-          to[128 + 32 * k] = -kDown * v[k].y;
+          to[32 * k] = kUp<kFp16> - (kFp16 ? v[k].x * kLog2e : v[k].x);   // negated: what is added
+          to[128 + 32 * k] = -v[k].y * d_power;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kRowsFull + (i & 1)]);
@@ -751,6 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 even[4], odd[4];
       load(0, even);
       load(1, odd);
+      if (kFp16 && n > 0) {
+        top_found();
+        d_power = power(dp_power());
+      }
       for (int i = 0; i < n && ok; i += 2) {
         put(i, even);
         load(i + 2, even);
@@ -855,7 +1033,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = key0 + (tid & 127);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int warp_last = key0 + (warp & 3) * 32 + 31;
-    const uint64_t scale2 = packed::pair(s.scale2, s.scale2), down = packed::pair(kDown, kDown);
+    const uint64_t scale2 = packed::pair(s.scale2, s.scale2);
+    float d_power = 1.f;
+    if (kFp16 && n > 0) {   // (while the first tiles are on their way)
+      const int tiles = (seq.n_q + tile_tokens - 1) / tile_tokens;
+      int mine = kNoTop;
+      for (int i = t0 / tile_tokens + tid; i < tiles; i += 256) {
+        const float2* first = g.rows + (seq.q0 + static_cast<long long>(i) * tile_tokens) * (s.Hkv * s.G) + h * s.G;
+        mine = max(mine, static_cast<int>(__float_as_uint(first->x)) >> 16);
+      }
+      mine = __reduce_max_sync(0xffffffffu, mine);
+      if (lane == 0) atomicMax(top, mine);
+      top_found();
+      d_power = power(dp_power());
+    }
+    const uint64_t up = packed::pair(d_power, d_power);
     for (int i = 0; i < n; ++i) {
       // Rows of tokens before key - before do not attend the key.
       const int token0 = tile_token(i);
@@ -898,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[at / 2] = packed::pack2<kFp16>(x.x, x.y);
               const uint64_t v = packed::pair(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1]));
               const float2 y = packed::unpair(packed::mul2(
-                  packed::pair(x.x, x.y), kFp16 ? packed::fma2(v, down, minus_d) : packed::add2(v, minus_d)));
+                  packed::pair(x.x, x.y), kFp16 ? packed::fma2(v, up, minus_d) : packed::add2(v, minus_d)));
               ds[at / 2] = packed::pack2<kFp16>(y.x, y.y);
               if (kMasks) {   // a hidden row's 0 stays 0 beside an infinity
                 if (at + 1 < from) ds[at / 2] = 0u;
@@ -968,9 +1160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t v1 = packed::pair(__uint_as_float(dp[4 * e + 2]), __uint_as_float(dp[4 * e + 3]));
             const uint64_t d0 = packed::pair(d.x, d.y), d1 = packed::pair(d.z, d.w);
             const float2 a = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[0]), __uint_as_float(zz[1])),
-                                                         kFp16 ? packed::fma2(v0, down, d0) : packed::add2(v0, d0)));
+                                                         kFp16 ? packed::fma2(v0, up, d0) : packed::add2(v0, d0)));
             const float2 b = packed::unpair(packed::mul2(packed::pair(__uint_as_float(zz[2]), __uint_as_float(zz[3])),
-                                                         kFp16 ? packed::fma2(v1, down, d1) : packed::add2(v1, d1)));
+                                                         kFp16 ? packed::fma2(v1, up, d1) : packed::add2(v1, d1)));
             p[16 * c + 2 * e] = packed::pack2<kFp16>(a.x, a.y);
             p[16 * c + 2 * e + 1] = packed::pack2<kFp16>(b.x, b.y);
           }
@@ -998,6 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t* to = static_cast<uint16_t*>(half ? g.dk : g.dv) + static_cast<long long>(seq.k0 + key) * st.token +
                    h * st.head;
     const float scale = half ? s.scale : kDown;
+    const float off = kFp16 && n > 0 ? power(-dp_power() - kUp<kFp16>) : 1.f;   // takes dS's power off dk
     const bool wide = packed::wide_rows(half ? g.dk : g.dv, st);
 #pragma unroll 1
     for (int c = 0; c < kD / 32; ++c) {
@@ -1007,6 +1200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0) {
         tc::ld32(lane_addr + (half ? kKvDk<kD> : kKvDv) + 32 * c, w);
         tc::wait_ld();
+        if (kFp16 && half) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * off);
+        }
       }
       if (ctas > 1) {   // into this CTA's ring, which is free now
 #pragma unroll
