@@ -663,6 +663,9 @@ int infllmv2_packed_attn(const infllmv2_packed_attn_args* args, void* out, const
  * Every row of a sequence is written, in an order of sums that does not change from
  * run to run; keys that no query attends get 0.
  *   out, lse  as the forward call on the same arguments wrote them.
+ *   D is summed from the scores where a row attends up to 1024 keys.  Longer rows take it
+ *           from out and correct it by the scores; a tile of rows whose dq the rounding of out has moved more than
+ *           the 16-bit rounding of dS may is done once more, which takes its time once more.
  *   grad_strides (host memory): between tokens and heads of out, dout, dq, dk, dv.
  *   P and dS enter the sums in the type of q, in fp16 times powers of two (of a row, and of the
  *           rows that share keys), so that neither small nor large upstream gradients leave

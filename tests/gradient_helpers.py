@@ -21,9 +21,9 @@ and e = eps / 2 of the tensors' type:
     2^-19 of P (dout . v) and of D, which moves dq by scale d_D sum P k, and a key's dk
     by scale P d_D q; the row's lse moves dq by e_p + 2^-19 of itself.
   * a row that attends more than 1024 keys may have D from the rounded out for
-    the keys from 128 on, as long as that moves the row's dq, by the size of its keys,
-    no more than 2 e sqrt(sum dS^2), and 32 neighbouring rows' no more than 2/3 of e
-    and the same: the square of that times the longest mean key of any row.
+    the keys from 128 on, as long as that moves the dq of a tile of rows, by the size
+    of their keys, no more than e sqrt(sum dS^2): the square of that times the longest
+    mean key of any row.
   * results are rounded: e of themselves and half the smallest step.
 """
 
@@ -88,7 +88,7 @@ def gradients(step):
             step_k = 2.0 ** -36 * most if half else least
             sums["dk"][1] = sums["dk"][1] + scale ** 2 * step_k ** 2 * steps
             for g, dq, square, square_far, lin in rows:
-                square = scale ** 2 * (square + (2 / 3 * e * longest) ** 2 * square_far / dim)
+                square = scale ** 2 * (square + (e * longest) ** 2 * square_far / dim)
                 for i, part in enumerate((dq, square + (e * dq) ** 2 + least ** 2, lin)):
                     result["dq"][i][at, g] = part
             for name in ("dk", "dv"):

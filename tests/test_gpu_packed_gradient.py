@@ -107,3 +107,80 @@ def test_values_that_outgrow_the_first_tile(dev, dim):
     grads, _ = _close(step, slice(1300, None))
     assert torch.isfinite(grads[0][:2400]).all()
     assert _status() == 0
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "fp16"), (64, "bf16"), (128, "fp16"), (128, "bf16")])
+@pytest.mark.parametrize("keys,at", [(1000, 0), (1000, 500), (1000, 940), (2000, 0), (2000, 100), (2000, 1500),
+                                     (2000, 1940), (2300, 128)])
+@pytest.mark.parametrize("weight", [0.5, 0.9, 0.99])
+def test_heavy_keys(dev, dim, dtype, keys, at, weight):
+    """One key, in the first, a middle or the last tile, has most of the weight of every row behind it."""
+    from gradient_helpers import close, heavy_key
+    from packed_helpers import Step
+    step = Step(dev, dtype, dim, 1, 2, [30, keys])
+    heavy_key(step, at, weight, seq=1)
+    grads, want = _close(step, slice(30 + at + 1, None))
+    close("dq", grads[0], want)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "fp16"), (64, "bf16"), (128, "fp16"), (128, "bf16")])
+def test_keys_and_values_with_means(dev, dim, dtype):
+    """D is many times dout . v - D, and dq is what is left when the keys' mean has gone."""
+    from packed_helpers import Step
+    step = Step(dev, dtype, dim, 2, 3, [3000, 1100, 200], [3000, 2100, 200])
+    step.k += 3
+    step.v += 3
+    _close(step)
+    assert _status() == 0
+
+
+def test_units_done_once_more_among_others(dev):
+    """Some sequences have heavy keys: the others' bits stay as they are, and all are the same every time."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from gradient_helpers import heavy_key
+    from packed_helpers import Step
+    lens = [1500 + 37 * i for i in range(12)]
+    step = Step(dev, "bf16", 64, 2, 4, lens)
+    out, lse = step.forward(T)
+    plain = step.backward(T, out, lse)
+    for seq in (0, 5, 11):
+        heavy_key(step, 700, 0.97, seq)
+    out, lse = step.forward(T)
+    grads = step.backward(T, out, lse)
+    again = step.backward(T, out, lse)
+    for a, b in zip(grads, again):
+        assert torch.equal(a, b)
+    for seq in range(12):
+        rows = slice(step.q_starts[seq], step.q_starts[seq + 1])
+        for a, b in zip(grads, plain):
+            assert torch.equal(a[rows], b[rows]) == (seq not in (0, 5, 11))
+    assert _status() == 0
+
+
+def test_more_units_than_marks(dev):
+    """A CTA marks 1024 units that it does once more; with more of them some share a mark, which changes no bit."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from gradient_helpers import heavy_key
+    from packed_helpers import Step
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    tiles = 1100 * sms // 4095 + 1                  # of 4 tokens with group 32
+    step = Step(dev, "bf16", 64, 1, 32, [1400, *[4 * tiles] * 4095])
+    heavy_key(step, 300, 0.97)
+    out, lse = step.forward(T)
+    grads = step.backward(T, out, lse)
+
+    def alone(first, last, lens):
+        """dq of the same rows as a batch of their own (dk and dv may be summed in another order)."""
+        rows = slice(first, last)
+        part = Step(dev, "bf16", 64, 1, 32, lens, gap=0)
+        for name in ("q", "k", "v", "dout"):
+            setattr(part, name, getattr(step, name)[rows].contiguous())
+        assert torch.equal(grads[0][rows], part.backward(T, out[rows].contiguous(), lse[rows].contiguous())[0])
+    alone(0, 1400, [1400])                          # its own marks
+    for first in range(1400, step.q_starts[-1], 500 * 4 * tiles):
+        last = min(first + 500 * 4 * tiles, step.q_starts[-1])
+        alone(first, last, [4 * tiles] * ((last - first) // (4 * tiles)))
+    assert _status() == 0

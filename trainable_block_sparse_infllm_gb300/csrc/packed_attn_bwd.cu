@@ -11,16 +11,21 @@
 // keys' gradients inside the product.
 //
 // D from the rounded `out` is off by up to half a step of |out| |dout|.  Where a row
-// attends few keys, or one key takes most of its weight, dout . v - D is a small
-// difference of such numbers and the error shows in dq and dk (2% of them for
-// documents of 7 tokens in bf16).  So rows of up to kExactTiles tiles of keys walk them
-// twice and sum D = sum P (dout . v) first (one tile: it is all in registers).  Longer
-// ones walk them once, from the last to the first: then sum P (dout . v - D) of all
-// tiles is what D lacked, and the first tile's dS (the first tokens are what draws much of
-// the attention in trained models) and the dk and dv kernel have D exactly.  Left is dS's
-// rounding to 16 bits: dq and dk 0.24% off in bf16, the rounding of the result being
-// 0.17%; with a heavy key amid 1000 to 4000 others dq 0.25 to 0.26%.  Two walks up to 4 or
-// 2 tiles only made 16 documents 3 and 7% faster, and the latter error 0.32 and 0.35%.
+// attends few keys, or one key takes most of its weight, or values and keys have large
+// means, dout . v - D is a small difference of such numbers and the error shows in dq and
+// dk.  So rows of up to kExactTiles tiles of keys walk them twice and sum
+// D = sum P (dout . v) first (one tile: it is all in registers).  Longer ones walk them
+// once, from the last to the first: sum P (dout . v - D) of all tiles is what D lacked
+// (`moved`), so that the first tile's dS (the first tokens are what draws much of the
+// attention in trained models) and the dk and dv kernel have D exactly.  dq of the other
+// tiles is off by scale moved sum P k: with W their weight by moved W times the size of
+// their keys at most, while rounding dS to 16 bits costs dq e sqrt(sum dS^2) times that size
+// at most (e: half a step of the type).  A tile of rows is done once more, with the D that
+// is known then, where the first passes the second (by sums of squares over the tile).  Where
+// none of the cases above holds, their ratio is about 0.4, and 0.73 was the largest among 900
+// tiles of 8192 keys with a sink at the first.  bf16, d 128, 2000 keys, key 1500 with
+// 0.97 of the weight: dq 6.0% off before, 0.23% now; 3000 keys and values with means of 3
+// deviations: 14.4% and 0.56%.  It costs those tiles twice their time.
 //
 // In both kernels the operand that the second products take from the scores, dS (dq), or
 // P^T and dS^T (dk, dv: scores are computed transposed, keys in rows), is the A
@@ -51,6 +56,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // among fp16's subnormal numbers, where it would lose bits.
 template <bool kFp16>
 constexpr int kUp = kFp16 ? 8 : 0;
+// Half a step of the type, the most that one rounding costs.
+template <bool kFp16>
+constexpr float kHalfStep = kFp16 ? 0x1p-11f : 0x1p-8f;
 // Rows that attend at most so many tiles of keys get D from their scores.
 constexpr int kExactTiles = 8;
 
@@ -65,8 +73,8 @@ constexpr int kExactTiles = 8;
 //     with the power from that sum.
 //   * dk: one power per tile of keys, from the largest |dS| that dq found among the rows that attend it.
 // 3000 keys, d 64, dout of 10^-3 (10^-4): dq 0.094% (0.90%) off without the powers, 0.034% (0.20%) with them, which
-// is the rounding of the results; dout of 1000 and values of 50 gave infinities.  It costs 8% of the time of 16
-// documents of 17 to 2500 tokens, d 64 (429 or 460 us), and 5% of a sequence of 8192's.
+// is the rounding of the results; dout of 1000 and values of 50 gave infinities.  It costs 7% of the time of 16
+// documents of 17 to 2500 tokens, d 64 (403 or 432 us), and 4% of a sequence of 8192's.
 constexpr int kNoTop = -1000;   // of a row without a finite dS
 
 // The power for values below 2^top: `to` is log2 of where they go.  From 2^-30 to 2^20, which is beyond what
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (at.x < 0) break;
         u = unit_of(at, rows);
-        may_repeat |= kFp16 && !u.exact;
+        may_repeat |= !u.exact;
         const uint32_t row_bytes = tile_tokens * s.G * kD * 2;
         if (u.n > 0) {
           const int st = k_stage(row_bytes, nullptr);
@@ -614,6 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 halves = packed::unpair(d);
         return halves.x + halves.y;
       };
+      auto sum_weights = [&]() {   // sum P
+        uint64_t d = 0ull;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d = packed::add2(prob2(i), d);
+        const float2 halves = packed::unpair(d);
+        return halves.x + halves.y;
+      };
       auto sum_values = [&](uint64_t d) {   // of the columns in registers: sum (dout . v)^2
         uint64_t c = 0ull;
 #pragma unroll
@@ -670,26 +685,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               moved = both(part_of_d) * (kFp16 ? power(-e) : 1.f);
               D += moved;
+              // (All have read `larger` before: products of several dS, which all warps wait for, are between.)
+              if (!u.exact)
+                larger[half * 128 + r] =
+                    static_cast<uint16_t>(__float_as_uint(sum_weights() * (kFp16 ? power(-e) : 1.f)) >> 16);
             }
           }
           if (first_walk) continue;
         }
         const uint64_t minus_d = packed::pair(-D, -D);
         uint32_t ds[32];
-        auto form = [&](auto squared) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint64_t v = packed::mul2(prob2(i), packed::add2(value2(i), minus_d));
-            rest = packed::add2(rest, v);
-            if (decltype(squared)::value) squares = packed::fma2(v, v, squares);
-            const float2 w = packed::unpair(v);
-            ds[i] = packed::pack2<kFp16>(w.x, w.y);
-          }
-        };
-        if (kFp16 && !u.exact) {
-          form(std::true_type());
-        } else {
-          form(std::false_type());
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t v = packed::mul2(prob2(i), packed::add2(value2(i), minus_d));
+          rest = packed::add2(rest, v);
+          squares = packed::fma2(v, v, squares);   // (only long rows need it; a loop without it costs the same)
+          const float2 w = packed::unpair(v);
+          ds[i] = packed::pack2<kFp16>(w.x, w.y);
         }
         if (summed > 0) wait(L::kDqDone, summed - 1);   // the last dS has been read
         ++summed;
@@ -699,11 +711,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kDsFull]);
       }
-      if (kFp16 && !u.exact) {
+      if (!u.exact) {   // whether it has to be done once more
         const float2 halves = packed::unpair(squares);
         const float sum = both(halves.x + halves.y);
-        top = top_of(sqrtf(sum) * power(-e) + fabsf(moved));   // (dk has D from the scores in all its tiles)
-        if (sum >= 0x1p31f && sum < INFINITY && active) atomicOr(&again[u.number >> 5], 1u << (u.number & 31));
+        const float size = sqrtf(sum) * (kFp16 ? power(-e) : 1.f);   // the norm of dS
+        if (kFp16) top = top_of(size + fabsf(moved));   // (dk has the scores' D in all its tiles)
+        const bool too_large = kFp16 && sum >= 0x1p31f && sum < INFINITY;
+        if (active && too_large) atomicOr(&again[u.number >> 5], 1u << (u.number & 31));
+        const float weight = 1.f - __uint_as_float(static_cast<uint32_t>(larger[r]) << 16) -
+                             __uint_as_float(static_cast<uint32_t>(larger[128 + r]) << 16);
+        float off_by = active ? moved * fmaxf(weight, 0.f) : 0.f, most = active ? size * kHalfStep<kFp16> : 0.f;
+        off_by *= off_by;
+        most *= most;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          off_by += __shfl_xor_sync(0xffffffffu, off_by, o);
+          most += __shfl_xor_sync(0xffffffffu, most, o);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // (`part` has been read)
+        if (half == 0 && lane == 0) {
+          part[2 * warp] = off_by;
+          part[2 * warp + 1] = most;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (tid == 0 && part[0] + part[2] + part[4] + part[6] > part[1] + part[3] + part[5] + part[7])
+          atomicOr(&again[u.number >> 5], 1u << (u.number & 31));
       }
       if (kFp16 && !u.again) {
         put_row(top);
