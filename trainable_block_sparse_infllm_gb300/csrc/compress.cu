@@ -21,9 +21,9 @@ constexpr int kKernelsPerCta = 32;
 constexpr int kThreads = 256;
 
 __global__ void __launch_bounds__(kThreads)
-    compress_kernel(const __nv_bfloat16* __restrict__ k, const int32_t* __restrict__ kv_lens,
+    compress_kernel(const __nv_bfloat16* k, const int32_t* kv_lens,
                     int Hkv, int Lmax, int ncmax, int kbegin, int kend,
-                    __nv_bfloat16* __restrict__ kc, uint32_t* status) {
+                    __nv_bfloat16* kc, uint32_t* status) {
   __shared__ __align__(16) float csum[kKernelsPerCta + 1][kHeadDim];
   const int b = blockIdx.z, h = blockIdx.y;
   pdl_wait();
@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kThreads)
 // sc a multiple of 16), as hi/lo bf16 planes like the fine kernels.  Sixteen
 // threads per window, 8 dims each, summing its 16-key chunks in order.
 __global__ void __launch_bounds__(kThreads)
-    coarse_kernel(const __nv_bfloat16* __restrict__ k, const int32_t* __restrict__ kv_lens, int Hkv, int Lmax,
-                  int nccmax, int sc, __nv_bfloat16* __restrict__ kcc, uint32_t* status) {
+    coarse_kernel(const __nv_bfloat16* k, const int32_t* kv_lens, int Hkv, int Lmax,
+                  int nccmax, int sc, __nv_bfloat16* kcc, uint32_t* status) {
   const int b = blockIdx.z, h = blockIdx.y;
   pdl_wait();
   pdl_trigger();

@@ -40,9 +40,9 @@ struct Sequence {
 
 __device__ __forceinline__ Sequence sequence(const PackedAttnShape& s, int b, bool* bad) {
   Sequence r;
-  r.q0 = __ldg(s.q_starts + b);
-  r.k0 = __ldg(s.k_starts + b);
-  const int q1 = __ldg(s.q_starts + b + 1), k1 = __ldg(s.k_starts + b + 1);
+  r.q0 = s.q_starts[b];
+  r.k0 = s.k_starts[b];
+  const int q1 = s.q_starts[b + 1], k1 = s.k_starts[b + 1];
   if (r.q0 < 0 || q1 < r.q0 || q1 > s.Tq || r.k0 < 0 || k1 < r.k0 || k1 > s.Tk) {
     *bad = true;
     return {0, 0, 0, 0};

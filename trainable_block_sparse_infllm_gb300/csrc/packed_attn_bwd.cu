@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A row that attends nothing has P = 0: no finite score reaches 2^+inf.
           float lse2 = 0.f;
           if (r < tile_tokens * s.G && token < u.seq.n_q)
-            lse2 = u.before + token >= 0 ? __ldg(g.lse + at) * kLog2e : INFINITY;
+            lse2 = u.before + token >= 0 ? g.lse[at] * kLog2e : INFINITY;
           lses[(k & 1) * 128 + r] = lse2;
         }
         __syncwarp();

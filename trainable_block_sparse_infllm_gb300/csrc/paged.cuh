@@ -12,7 +12,7 @@ constexpr uint32_t kStatusBadPage = 0x8u;
 
 // A sequence's length, or 0 (flagged) where it is outside [0, cap].
 __device__ __forceinline__ int paged_len(const int32_t* kv_lens, int b, int cap, uint32_t* status) {
-  const int n = __ldg(kv_lens + b);
+  const int n = kv_lens[b];
   if (n >= 0 && n <= cap) return n;
   atomicOr(status, kStatusBadKvLen);
   return 0;

@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
   const int which = blockIdx.y & 1;   // 0: keys, 1: values
   const int h = blockIdx.y >> 1;
   const int t0 = (blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes) * kRows;
-  const int n_new = a.n_new ? __ldg(a.n_new + b) : a.nq;
-  const int L = __ldg(s.kv_lens + b);
+  const int n_new = a.n_new ? a.n_new[b] : a.nq;
+  const int L = s.kv_lens[b];
   if (n_new < 0 || n_new > a.nq || L < n_new || L > s.cap) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(s.status, kStatusBadKvLen);
     return;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     page[i] = -1;
     if (t0 + i < n_new) {
       const int slot = L - n_new + t0 + i;
-      page[i] = __ldg(s.table + static_cast<long long>(b) * s.maxp + slot / s.ps);
+      page[i] = s.table[static_cast<long long>(b) * s.maxp + slot / s.ps];
       row[i] = slot % s.ps;
       x[i] = *reinterpret_cast<const uint4*>(src + (t0 + i) * sst[2]);
     }
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
       const long long m = paged_meta(page[i], h, row[i], s.Hkv, s.ps);
       if (which == 0 && s.weights) s.weights[m] = 0.f;
       if (which == 1 && s.positions)
-        s.positions[m] = (a.seq_lens ? __ldg(a.seq_lens + b) : L) - n_new + t0 + i;
+        s.positions[m] = (a.seq_lens ? a.seq_lens[b] : L) - n_new + t0 + i;
     }
   }
 }
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) packed_append_kernel(const PagedShap
   for (int i = 0; i < kRows; ++i) {
     slot[i] = -1;
     if (t0 + i < a.tokens) {
-      slot[i] = __ldg(a.slots + t0 + i);
+      slot[i] = a.slots[t0 + i];
       x[i] = *reinterpret_cast<const uint4*>(src + (t0 + i) * step);
     }
   }
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) packed_append_kernel(const PagedShap
     if (lane == 0) {
       const long long m = paged_meta(page, h, row, s.Hkv, s.ps);
       if (which == 0 && s.weights) s.weights[m] = 0.f;
-      if (which == 1 && s.positions) s.positions[m] = __ldg(a.positions + t0 + i);
+      if (which == 1 && s.positions) s.positions[m] = a.positions[t0 + i];
     }
   }
 }

@@ -406,7 +406,7 @@ __device__ __forceinline__ void add_weights(const PagedAttnArgs& a, long long un
                                             int step, const float2* ml) {
   const int32_t* table = a.table + static_cast<long long>(b) * a.maxp;
   for (int slot = first; slot < len; slot += step) {   // the four share a page (pages hold multiples of 16)
-    const int page = __ldg(table + slot / a.ps);
+    const int page = table[slot / a.ps];
     const float* z = a.scores + unit * a.G * a.cap64 + slot;
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
         // Lane i handles box i of a tile; its page is fetched one tile ahead.
         auto fetch = [&](int tile) {
           const int slot = tile * kTile + lane * a.box;
-          return (lane < boxes && tile < p.tile1 && slot < p.len) ? __ldg(row + slot / a.ps) : -1;
+          return (lane < boxes && tile < p.tile1 && slot < p.len) ? row[slot / a.ps] : -1;
         };
         int page_next = fetch(p.tile0);
         // The unit's queries, 16 bytes per lane and step, on their way while the
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kGroups, kStack>::kThreads, Attn
           const uint4* q = static_cast<const uint4*>(a.q) + static_cast<long long>(unit) * a.G * (kDim / 8);
 #pragma unroll
           for (int i = 0; i < kQSteps; ++i)
-            if (i * 32 + lane < a.G * (kDim / 8)) qv[i] = __ldg(q + i * 32 + lane);
+            if (i * 32 + lane < a.G * (kDim / 8)) qv[i] = q[i * 32 + lane];
         }
         const int place = a.cluster ? cta : piece_place(chunk, begin, tile_at(s, p, p.tile0));
         for (int t = p.tile0; t < p.tile1; ++t) {

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     if (writes_len) a.new_lens[b] = n;
     return;
   }
-  const int seen = a.seq_lens ? __ldg(a.seq_lens + b) : n;
+  const int seen = a.seq_lens ? a.seq_lens[b] : n;
   const int slot0 = (rank * kThreads + tid) * kKeys;
   // Slots at or past n get key 0.  They never stay: of equal keys the lower
   // slots do, and more than `budget` of those exist.
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       long long at = -1;
       place[c] = 0;
       if (first < n) {
-        const int page = __ldg(table + first / s.ps), row = first % s.ps;
+        const int page = table[first / s.ps], row = first % s.ps;
         if (page < 0 || page >= s.P) {
           bad = true;
         } else {

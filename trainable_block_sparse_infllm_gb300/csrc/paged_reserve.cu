@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kMost) paged_reserve_kernel(const ReserveArgs 
                                        : taken(take0[b] + c - held[b]);
           slot = slot_of(page, s - c * a.ps, a);
         }
-        position = (a.seq_lens ? __ldg(a.seq_lens + b) : kv[b]) + i;
+        position = (a.seq_lens ? a.seq_lens[b] : kv[b]) + i;
       }
       if (a.slots) a.slots[t] = slot;
       if (a.positions) a.positions[t] = position;

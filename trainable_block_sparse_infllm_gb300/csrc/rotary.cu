@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a)
       for (int i = me; i < n; i += blockDim.x * blockDim.y * blockDim.z) {
         const int t = i / half, pair = i - t * half;
         angles[t * half + (pair % group) * vectors + pair / group] =
-            turned(__ldg(a.positions + cta0 + t), __ldg(a.turns + pair), a.scale, a.transpose);
+            turned(a.positions[cta0 + t], a.turns[pair], a.scale, a.transpose);
       }
       __syncthreads();
     }

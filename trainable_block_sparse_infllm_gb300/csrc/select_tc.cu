@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kStThreads, 2)
       const uint4* src = reinterpret_cast<const uint4*>(p.q + row * 128 + 64 * hf);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint4 u = __ldg(src + i);
+        const uint4 u = src[i];
         qw[4 * i] = u.x;
         qw[4 * i + 1] = u.y;
         qw[4 * i + 2] = u.z;
