@@ -184,3 +184,24 @@ def test_more_units_than_marks(dev):
         last = min(first + 500 * 4 * tiles, step.q_starts[-1])
         alone(first, last, [4 * tiles] * ((last - first) // (4 * tiles)))
     assert _status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_heavy_key_beside_a_row_that_is_not_finite(dev, dtype, bad):
+    """A row of dout with an infinity or NaN keeps no other row of its tile from being done once more."""
+    import torch
+    import trainable_block_sparse_infllm_gb300 as T
+    from gradient_helpers import close, gradients, heavy_key
+    from packed_helpers import Step
+    step = Step(dev, dtype, 128, 1, 2, [2000])
+    heavy_key(step, 1500, 0.97)
+    step.dout[1501:2000:64, 1, 3] = bad            # one row of each tile
+    out, lse = step.forward(T)
+    dq, want = step.backward(T, out, lse)[0], gradients(step)
+    rows = torch.ones(step.q.shape[:2], dtype=torch.bool, device=dev)
+    rows[1501:2000:64, 1] = False
+    rows[:1501] = False
+    assert torch.isfinite(dq[rows]).all()
+    close("dq", dq, want, rows)
+    assert _status() == 0

@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float off_by = active ? moved * fmaxf(weight, 0.f) : 0.f, most = active ? size * kHalfStep<kFp16> : 0.f;
         off_by *= off_by;
         most *= most;
+        if (!(off_by < INFINITY && most < INFINITY)) off_by = most = 0.f;   // (a row with one in dout has no say)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           off_by += __shfl_xor_sync(0xffffffffu, off_by, o);
