@@ -529,6 +529,7 @@ int infllmv2_paged_reserve(const infllmv2_reserve_args* args, void* stream);
  *           heads of k_new, then of v_new.  Read with ordinary loads: they may be
  *           page-locked host memory mapped for the device.
  *   positions  int32 [tokens]; NULL only where the cache has none.
+ *   tokens  1 .. 2^30.
  * A slot past the pool is not written and sets INFLLMV2_DEVICE_BAD_PAGE.  The
  * slots written must be pairwise different, and k_new and v_new apart from them.
  */
@@ -594,6 +595,7 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* 
  *           k_heads is 0.  Strides in elements between tokens and heads.  q_out may be
  *           q, with the same strides; otherwise the two must not overlap; k likewise.
  *           q_out must be apart from k and k_out, and k_out from q.
+ *   tokens  1 .. 2^30.
  *   positions  int32 [tokens], any value.
  *   turns   device memory, [rotary_dim / 2], from infllmv2_rotary_frequencies.
  * head_dim and rotary_dim: multiples of 16, rotary_dim <= head_dim <= 512.

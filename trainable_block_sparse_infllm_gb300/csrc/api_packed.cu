@@ -221,6 +221,8 @@ int infllmv2_rotary(const infllmv2_rotary_args* r, void* stream) {
     if (r->dtype != INFLLMV2_BF16 && r->dtype != INFLLMV2_FP16 && r->dtype != INFLLMV2_FP32)
       return fail(INFLLMV2_UNSUPPORTED, "dtype must be bf16, fp16 or fp32 (got %d)", r->dtype);
     if (r->tokens < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "tokens must be >= 1 (got %d)", r->tokens);
+    if (r->tokens > kPackedMaxTokens)
+      return fail(INFLLMV2_UNSUPPORTED, "tokens must be <= 2^30 (got %d)", r->tokens);
     if (r->q_heads < 1 || r->k_heads < 0)
       return fail(INFLLMV2_INVALID_ARGUMENT, "q_heads must be >= 1 and k_heads >= 0");
     const int d = r->head_dim;

@@ -283,6 +283,7 @@ int infllmv2_paged_append_packed(const infllmv2_paged_cache* cache, int32_t toke
     int rc = check_cache(cache, 1, 1, &s);
     if (rc) return rc;
     if (tokens < 1) return fail(INFLLMV2_INVALID_ARGUMENT, "tokens must be >= 1 (got %d)", tokens);
+    if (tokens > kPackedMaxTokens) return fail(INFLLMV2_UNSUPPORTED, "tokens must be <= 2^30 (got %d)", tokens);
     if (!k_new || !v_new || !slots) return fail(INFLLMV2_INVALID_ARGUMENT, "k_new, v_new or slots is NULL");
     if (!aligned16(k_new) || !aligned16(v_new))
       return fail(INFLLMV2_UNSUPPORTED, "k_new and v_new must be 16-byte aligned");

@@ -10,6 +10,9 @@
 
 namespace infllmv2 {
 
+// Tokens of a rotary or append call (their rounding up to whole CTAs stays within 32 bits).
+constexpr int kPackedMaxTokens = 1 << 30;
+
 // One packed tensor [tokens, heads, d]; strides in elements.
 struct PackedRows {
   void* x;
