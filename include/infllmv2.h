@@ -492,7 +492,8 @@ int infllmv2_paged_evict(const infllmv2_paged_cache* cache, int32_t batch, int32
  *           starts[b + 1] - 1 of the step.
  *   slots, positions  int32 [max_tokens], each may be NULL: of every token of the
  *           step its slot in the pool, page * page_size + row, and its position,
- *           seq_lens[b] + t; past the last token -1 and 0.
+ *           seq_lens[b] + t; past the last token -1 and 0.  max_tokens counts where one of
+ *           the two is there.
  *   missing int32 [1]: 0, or the number of free pages that lack, or -1: a length,
  *           held[b] or n_free is out of range (a row has max_pages entries; the
  *           pages given back and the free ones are at most num_pages), or

@@ -135,13 +135,13 @@ def paged_reserve(tables: PageTables, kv_lens: torch.Tensor, n_new: torch.Tensor
         tokens = slots.numel()
         if not (slots.dtype is _int32 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == index):
             _refuse_ints(index, slots=(slots, tokens))
-        map_slots = slots.data_ptr()
+        map_slots = slots.data_ptr() or starts.data_ptr()   # (one of no tokens has no memory, but is there)
     if positions is not None:
         tokens = tokens if slots is not None else positions.numel()
         if not (positions.dtype is _int32 and positions.dim() == 1 and positions.numel() == tokens and
                 positions.is_contiguous() and positions.get_device() == index):
             _refuse_ints(index, positions=(positions, tokens))
-        map_positions = positions.data_ptr()
+        map_positions = positions.data_ptr() or starts.data_ptr()
     rc = _reserve(_reserve_args(*tables._sizes, tokens, 0, *tables._arrays, kv_lens.data_ptr(), n_new.data_ptr(), seen,
                                 new_lens.data_ptr(), starts.data_ptr(), map_slots, map_positions), _on(index, stream))
     if rc:
