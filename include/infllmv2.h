@@ -600,7 +600,7 @@ int infllmv2_rotary_frequencies(const infllmv2_rotary_config* config, uint64_t* 
  *   positions  int32 [tokens], any value.
  *   turns   device memory, [rotary_dim / 2], from infllmv2_rotary_frequencies.
  * head_dim and rotary_dim: multiples of 16, rotary_dim <= head_dim <= 512.
- * Angles are exact to 2^-32 turn whatever the position.
+ * Angles are exact to 2^-27 turn whatever the position.
  */
 #define INFLLMV2_FP32 2
 
@@ -634,7 +634,7 @@ int infllmv2_rotary(const infllmv2_rotary_args* args, void* stream);
  * does not reach it.
  *   dtype   INFLLMV2_BF16 or INFLLMV2_FP16: q, k, v, out and the gradients.
  *   head_dim 64 or 128; group_size 1 .. 32; up to 4096 sequences; fewer than
- *           2^31 / (n_kv_heads * group_size) tokens.
+ *           2^31 / (n_kv_heads * group_size) tokens, at least one of each.
  *   strides elements between tokens and heads, multiples of 8; rows of one tensor
  *           must not overlap.  Pointers 16-byte aligned.
  *   q_starts, k_starts  int32 [batch + 1], not descending, within [0, q_tokens] and

@@ -34,10 +34,10 @@
 // leave most SMs without a unit: its key tiles are then divided over a cluster,
 // whose CTAs join their (m, l, x) through distributed shared memory.
 //
-// Measured (GB300): one prompt of 16,384 tokens, 2 KV heads of 16, d 128, 1.24 to 1.34 ms,
-// 1.64 to 1.78 PFLOP/s, 86 to 93% of the measured library product: the tensor cores
+// Measured (GB300): one prompt of 16,384 tokens, 2 KV heads of 16, d 128, 1.24 to 1.36 ms,
+// 1.62 to 1.78 PFLOP/s, 85 to 93% of the measured library product: the tensor cores
 // (72% busy at 8K, the rest goes to the handing over of S and P).  24 prompts of up to
-// 2047 tokens, 8 heads of 4, d 64, 170 us: the softmax warps' chain of a tile (1.9
+// 2047 tokens, 8 heads of 4, d 64, 170 us (177 in turn with other work): the softmax warps' chain of a tile (1.9
 // thousand cycles, two warps of a scheduler, a quarter of it waiting for S) and 2.2
 // thousand cycles at the end of units of five tiles.  12 tokens after 32,000 in 4
 // sequences 47 us: the 8 units' clusters have 12 CTAs, 96 SMs.  One prompt of 301
@@ -837,9 +837,7 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
 
 }  // namespace
 
-// Where a CTA has more than one unit: a warp's stores of 32 rows at once, 32 bytes of each,
-// take twice the time of whole lines (24 prompts of up to 2047 tokens, d 64: 177 or 170
-// us; 48 of 512, d 128: 149 or 140).
+// Where a CTA has more than one unit (see Form::kTiles).
 bool packed_attn_by_tile(const PackedAttnShape& s) {
   return static_cast<long long>(s.Tq) * s.Hkv > 2ll * packed_tile_tokens(s.G) * device_sm_count();
 }

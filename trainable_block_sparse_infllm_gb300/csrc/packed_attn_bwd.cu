@@ -32,12 +32,13 @@
 // operand in tensor memory: no product's input passes through shared memory but
 // the tiles that TMA brought.  Two warpgroups share a tile's columns.
 //
-// Measured (GB300): one sequence of 8192 tokens, 2 KV heads of 16, d 128, 1.06 ms
-// (dq 461 us, tensor cores 82% busy; dk and dv 604, 87%): 1.30 PFLOP/s of five products,
-// 1.82 of the seven that are issued, 96% of the measured library product.  16
-// documents of 17 to 2500 tokens, 4 heads of 5, d 64, fp16, 400 us (dq 229, 37%; dk and dv
-// 175, 54%): the exponentials, the second walk of the rows that attend up to 1024 keys and
-// the start and end of short units.
+// Measured (GB300): one sequence of 8192 tokens, 2 KV heads of 16, d 128, 1.07 ms
+// (dq 475 us, tensor cores 79% busy; dk and dv 608, 86%; 1.19 ms in turn with other work):
+// 1.28 PFLOP/s of five products, 1.80 of the seven that are issued, 94% of the measured
+// library product.  16 documents of 17 to 2500 tokens, 4 heads of 5, d 64, fp16, 435 us (dq 262, 32%;
+// dk and dv 178, 53%): the exponentials, the second walk of the rows that attend up to 1024
+// keys and the start and end of short units.  96 sequences of 256, 4 heads of 5, d 64:
+// 230 us in bf16, 243 in fp16.
 #include <algorithm>
 #include <type_traits>
 
@@ -613,19 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return packed::pair(fast_exp2(e.x), fast_exp2(e.y));
       };
       auto value2 = [&](int i) { return packed::pair(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])); };
-      // Of the columns in registers: sum P (dout . v - x).
+      // Of the columns in registers: sum P (dout . v - x), and sum P into `weights`.
+      uint64_t weights = 0ull;
       auto sum_p = [&](float x) {
         const uint64_t minus_x = packed::pair(-x, -x);
         uint64_t d = 0ull;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) d = packed::fma2(prob2(i), packed::add2(value2(i), minus_x), d);
-        const float2 halves = packed::unpair(d);
-        return halves.x + halves.y;
-      };
-      auto sum_weights = [&]() {   // sum P
-        uint64_t d = 0ull;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) d = packed::add2(prob2(i), d);
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t p = prob2(i);
+          d = packed::fma2(p, packed::add2(value2(i), minus_x), d);
+          weights = packed::add2(p, weights);
+        }
         const float2 halves = packed::unpair(d);
         return halves.x + halves.y;
       };
@@ -685,10 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               moved = both(part_of_d) * (kFp16 ? power(-e) : 1.f);
               D += moved;
-              // (All have read `larger` before: products of several dS, which all warps wait for, are between.)
+              // The first tile's weight.  (All have read `larger` before: products of several dS, which all warps
+              // wait for, are between.)
+              const float2 weight = packed::unpair(weights);
               if (!u.exact)
-                larger[half * 128 + r] =
-                    static_cast<uint16_t>(__float_as_uint(sum_weights() * (kFp16 ? power(-e) : 1.f)) >> 16);
+                larger[half * 128 + r] = static_cast<uint16_t>(
+                    __float_as_uint((weight.x + weight.y) * (kFp16 ? power(-e) : 1.f)) >> 16);
             }
           }
           if (first_walk) continue;
@@ -1326,11 +1327,13 @@ cudaError_t launch(const PackedAttnShape& s, const PackedAttnMaps& maps, const P
                                    std::min<long long>(tiles, device_sm_count()), 1, st, maps, s, g);
   if (e != cudaSuccess) return e;
   // CTAs per tile of keys.  Causal tiles differ by the whole length of the sequence, so
-  // units that are few leave SMs idle behind the longest: the gradient of one 8K
-  // sequence with 2 KV heads took 1.13 ms with clusters of 4 (which find 144 of the 152
-  // SMs), 1.16 with 2, 1.35 with 7 (105 SMs) and 1.72 alone.  That of 16 documents (640
+  // units that are few leave SMs idle behind the longest: with kernels before these the gradient
+  // of one 8K sequence with 2 KV heads took 1.13 ms with clusters of 4 (which find 144 of the
+  // 152 SMs), 1.16 with 2, 1.35 with 7 (105 SMs) and 1.72 alone.  That of 16 documents (640
   // units) took 0.47 ms alone and 0.52 with 2: enough units, and the join costs a few row
-  // tiles.
+  // tiles.  Clusters of 8 where all their units run at once: both kernels 41 us instead of 50 (10 units
+  // of 1200 tokens, group 8, d 128), 45 instead of 58 (18 of 1100, group 16, d 64); with 32
+  // units (2000 tokens, group 4) 63 instead of 50.
   const long long units = ((s.Tk + s.B - 1) / s.B + 127) / 128 * static_cast<long long>(s.B) * s.Hkv;
   const long long row_tiles = static_cast<long long>(s.Tq) * s.G / 128 / s.B;
   const int sms = device_sm_count();

@@ -232,7 +232,9 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t st) {
   // Items of a head: in place, what stays need not be copied.
   const int items = (a.in_place ? a.part : a.dim) / (2 * Vec<T>::kN);
   const int heads = a.q_heads + a.k_heads;
-  // One token for a thread while the grid is small, where latency counts.
+  // One token for a thread while the grid is small, where latency counts: 34 heads of 128, bf16, in place, in a
+  // graph, one or four tokens: 1.9 or 3.0 us for 64 tokens, 4.1 or 4.6 for 963 (the border), 5.7 or 4.6 for 1500,
+  // 61.7 or 43.6 for 16,384.
   return static_cast<long long>(a.tokens) * items * heads < 1 << 18 ? launch_tokens<T, 1>(a, items, heads, st)
                                                                     : launch_tokens<T, 4>(a, items, heads, st);
 }
