@@ -16,7 +16,7 @@
 // Measured (GB300): 8 prompts of up to 8192 tokens, 4 KV heads, 37,700 tokens in
 // all, 25.9 us, 93% of the copy rate; one token of each of 64 sequences, 8 KV
 // heads, 2.4 us in a graph, 7.0 us a call from Python.  Packed: 40,000 tokens, 4 KV
-// heads, into token-major pages, 26.1 us, 94%; 64 tokens, 8 KV heads, 2.0 us in a graph,
+// heads, into token-major pages, 26.1 us in a graph, 93%; 64 tokens, 8 KV heads, 2.0 us in a graph,
 // 5.3 us a call from Python.
 #include "packed.h"
 #include "paged.cuh"
