@@ -88,8 +88,8 @@ def test_upstream_gradients_of_all_sizes(dev, dim, dtype):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-def test_values_that_outgrow_the_first_tile(dev, dim):
-    """fp16 rows that walk their keys from the last: neither the first tile nor D tells of the values before.
+def test_values_that_cancel_in_out(dev, dim):
+    """fp16 rows of many keys, whose |dS| is hundreds of times |dout| |out|.
 
     Keys 700 .. 999 and 1000 .. 1299 are alike in all that the queries look at and their values are opposite, so
     that they cancel in out and D, but not in dq.
@@ -204,4 +204,33 @@ def test_heavy_key_beside_a_row_that_is_not_finite(dev, dtype, bad):
     rows[:1501] = False
     assert torch.isfinite(dq[rows]).all()
     close("dq", dq, want, rows)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "fp16"), (128, "bf16")])
+@pytest.mark.parametrize("queries,keys", [([3000, 5], [2000, 5]), ([40, 2500], [4000, 1100]), ([1], [3000])])
+def test_heavy_keys_of_other_lengths(dev, dim, dtype, queries, keys):
+    """Rows that attend no key before rows of many, and many keys before the first query."""
+    from gradient_helpers import heavy_key
+    from packed_helpers import Step
+    step = Step(dev, dtype, dim, 2, 3, queries, keys)
+    for seq, m in enumerate(keys):
+        if m > 1024:
+            heavy_key(step, m // 3, 0.97, seq)
+    _close(step)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "fp16")])
+def test_heavy_keys_of_many_sequences(dev, dim, dtype):
+    """More than 32 sequences, a few of them long, some of those with a heavy key."""
+    from gradient_helpers import close, heavy_key
+    from packed_helpers import Step
+    lens = [1300 + i if i % 7 == 3 else (5 * i) % 40 for i in range(45)]
+    step = Step(dev, dtype, dim, 1, 5, lens)
+    for seq in (3, 17, 38):
+        heavy_key(step, 600, 0.97, seq)
+    grads, want = _close(step)
+    for seq in (3, 17, 38):
+        close("dq", grads[0], want, slice(step.q_starts[seq] + 601, step.q_starts[seq + 1]))
     assert _status() == 0

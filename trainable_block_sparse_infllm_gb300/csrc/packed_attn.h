@@ -58,7 +58,9 @@ struct PackedAttnGrads {
   const float* lse;
   void *dq, *dk, *dv;
   PackedStride dq_st, dk_st, dv_st;
-  float2* rows;   // workspace [Tq, Hkv * G]: (lse log2(e), D) of each row
+  // Workspace [Tq, Hkv * G]: of each row D and, before it, lse log2(e), or in fp16 two exponents of dS (its own, and
+  // in the first row of a tile that of the tile's rows).
+  float2* rows;
 };
 
 cudaError_t launch_packed_attn_bwd(const PackedAttnShape& s, int D, bool fp16, const PackedAttnMaps& maps,
